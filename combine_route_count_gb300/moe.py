@@ -40,13 +40,15 @@ MOE_OPT_COMBINE_SCHEDULE = 21
 MOE_OPT_ROUTE_VARIANT_FP8 = 22  # read only: the routing moe_dispatch_send_fp8 takes
 PACK_BULK, PACK_VECTOR = 0, 1
 
-# Every entry point of include/moe.h.
+# Every entry point of include/moe.h and include/moe_ffn.h.
 EXPORTS = ("moe_validate_config", "moe_workspace_bytes", "moe_recv_bound_rows", "moe_ctx_create",
            "moe_ctx_destroy", "moe_ctx_set_option", "moe_ctx_get_option", "moe_dispatch_send", "moe_dispatch_recv",
            "moe_combine_send", "moe_combine_recv", "moe_get_error", "moe_strerror",
            "moe_dispatch_send_noalloc", "moe_dispatch_send_fp8", "moe_combine_recv_two_level", "moe_partial_rows",
            "moe_dispatch_send_staged", "moe_kernel_times", "moe_dispatch_send_quantized",
-           "moe_dense_capacity", "moe_dispatch_send_dense", "moe_combine_recv_dense")
+           "moe_dense_capacity", "moe_dispatch_send_dense", "moe_combine_recv_dense",
+           # include/moe_ffn.h
+           "moe_add_rms_norm_fp8")
 
 
 class moe_config(ctypes.Structure):
@@ -104,6 +106,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_kernel_times": ([P, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)], I),
         "moe_get_error": ([P, P], I),
         "moe_strerror": ([I], ctypes.c_char_p),
+        "moe_add_rms_norm_fp8": ([P, P, P, I, I64, ctypes.c_int32, ctypes.c_float, P, P, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -286,6 +289,19 @@ def moe_dispatch_send_noalloc(cfg: moe_config, x: Any, topk_idx: Any, expert_x: 
         fn.restype = ctypes.c_int
     return int(fn(ctypes.byref(cfg), _ptr(x), _ptr(topk_idx), _ptr(expert_x), expert_x_rows, _ptr(expert_counts),
                   _ptr(expert_offsets), _ptr(status), _stream(stream)))
+
+
+# ---- feed-forward operators (include/moe_ffn.h); ffn.py calls them on tensors ----
+
+MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
+MOE_NORM_MAX_HIDDEN = 65536
+
+
+def moe_add_rms_norm_fp8(x: Any, residual: Any, weight: Any, weight_type: int, num_tokens: int, hidden: int,
+                         eps: float, residual_out: Any, y: Any, xq: Any, x_scales: Any, stream: Any = None) -> None:
+    _check(load_library().moe_add_rms_norm_fp8(_ptr(x), _ptr(residual), _ptr(weight), weight_type, num_tokens, hidden,
+                                               eps, _ptr(residual_out), _ptr(y), _ptr(xq), _ptr(x_scales),
+                                               _stream(stream)), "moe_add_rms_norm_fp8")
 
 
 # ---- convenience: one context with a torch-allocated workspace ---------------

@@ -1,0 +1,71 @@
+/*
+ * moe_ffn.h - the feed-forward operators around dispatch and combine (libmoe.so).
+ *
+ * A user of moe.h has token rows before the dispatch and expert rows between
+ * dispatch and combine.  These calls do that work on the same payload as
+ * moe_dispatch_send_fp8 / moe_dispatch_send_quantized: E4M3 codes with one
+ * float32 scale for each block of MOE_FP8_BLOCK consecutive elements of a row,
+ * weights with one float32 scale for each MOE_FP8_BLOCK x MOE_FP8_BLOCK block.
+ *
+ *   moe_add_rms_norm_fp8  x + residual -> RMS norm -> codes and scales
+ *
+ * Quantisation of a block with largest magnitude amax, in float32:
+ *   scale = max(amax, 2^-100) / 448 (1 for an all-zero block), inv = 1 / scale,
+ *   q = E4M3(v * inv), round to nearest even, saturating.
+ * For blocks that hold a bf16 value of at least 2^-100 this is the rule of
+ * moe_dispatch_send_fp8; below, the floor keeps 1 / scale finite.  A row that
+ * holds an infinity or a NaN, or whose squares leave the float32 range, has no
+ * defined outputs; other rows are not touched by it.
+ *
+ * Conventions as in moe.h: device pointers owned by the caller, no device
+ * allocation, no host synchronisation, `stream` is a cudaStream_t, argument
+ * errors are found on the host (MOE_EINVAL) before anything is enqueued,
+ * MOE_ECUDA if a launch fails.  Tensors are row-major and contiguous, and
+ * must not overlap unless a call says so.  None of these calls needs a moe_ctx.
+ */
+#ifndef MOE_FFN_H_
+#define MOE_FFN_H_
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of arguments that may have more than one. */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_F32 1
+
+/* Largest row of moe_add_rms_norm_fp8. */
+#define MOE_NORM_MAX_HIDDEN 65536
+
+/* Residual addition, root-mean-square norm and quantisation of token rows:
+ *   s = x + residual (float32; s = x without a residual)
+ *   v = s / sqrt(mean(s^2) + eps) * weight, float32
+ *   residual_out = bf16(s), y = bf16(v), (xq, x_scales) = v quantised
+ * The norm and the codes are taken from the float32 s and v, not from their
+ * roundings to bf16.  xq and x_scales are what moe_dispatch_send_quantized
+ * takes (it needs hidden % 512 == 0); y is what a router reads.
+ *   x             device bf16 [num_tokens, hidden], hidden % MOE_FP8_BLOCK == 0
+ *   residual      device bf16 [num_tokens, hidden], or NULL
+ *   weight        device [hidden], bf16 or float32 (weight_type MOE_TYPE_*)
+ *   eps           finite, > 0
+ *   residual_out  device bf16 [num_tokens, hidden]; NULL exactly when residual
+ *                 is.  May be x or residual itself (updated in place).
+ *   y             device bf16 [num_tokens, hidden], or NULL; may be x itself
+ *                 unless residual_out is
+ *   xq            device E4M3 bytes [num_tokens, hidden]
+ *   x_scales      device float32 [num_tokens, hidden / MOE_FP8_BLOCK]
+ * All but x_scales (4 bytes) are 16-byte aligned.  num_tokens == 0 is allowed. */
+int moe_add_rms_norm_fp8(const void* x, const void* residual, const void* weight, int weight_type,
+                         int64_t num_tokens, int32_t hidden, float eps, void* residual_out, void* y, void* xq,
+                         float* x_scales, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_FFN_H_ */

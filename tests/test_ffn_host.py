@@ -1,0 +1,44 @@
+"""Argument checks of the feed-forward operators that run before any CUDA
+call, through the C ABI; and the tests' own 64-bit forms.  No GPU is needed."""
+import numpy as np
+import pytest
+
+import ffn_ref as ref
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from combine_route_count_gb300 import build, moe as m
+    build.build()
+    m.load_library()
+    return m
+
+
+def refused(moe, fn, *args):
+    with pytest.raises(moe.MoEError) as e:
+        fn(*args, stream=0)
+    return e.value.code == moe.MOE_EINVAL
+
+
+def test_e4m3_grid():
+    torch = pytest.importorskip("torch")
+    codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy().astype(np.float64)
+    codes = codes[np.isfinite(codes)]
+    assert np.array_equal(ref.e4m3(codes), codes)
+    v = np.random.default_rng(0).standard_normal(20000) * 10.0 ** np.random.default_rng(1).uniform(-4, 2.6, 20000)
+    want = torch.from_numpy(np.clip(v, -448, 448)).to(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(ref.e4m3(v), want)
+
+
+def test_add_rms_norm_checks(moe):
+    A, bad = 0x1000, 0x1008  # addresses that are never read: every call below is refused on the host
+
+    def call(x=A, r=None, w=A, wt=0, T=4, H=256, eps=1e-6, ro=None, y=None, q=A, s=A):
+        return refused(moe, moe.moe_add_rms_norm_fp8, x, r, w, wt, T, H, eps, ro, y, q, s)
+
+    for kw in (dict(x=None), dict(w=None), dict(q=None), dict(s=None), dict(x=bad), dict(w=bad), dict(q=bad),
+               dict(y=bad), dict(s=0x1002), dict(r=A), dict(ro=A), dict(r=bad, ro=A), dict(r=A, ro=bad), dict(wt=2),
+               dict(T=-1), dict(T=2 ** 31), dict(H=0), dict(H=200), dict(H=65536 + 128), dict(eps=-1.0), dict(eps=0.0),
+               dict(eps=float("inf")), dict(eps=float("nan")), dict(r=A, ro=A, y=A)):
+        assert call(**kw), kw
+    moe.moe_add_rms_norm_fp8(None, None, None, 0, 0, 256, 1e-6, None, None, None, None, stream=0)  # no tokens: nothing to do
