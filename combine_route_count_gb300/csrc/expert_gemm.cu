@@ -1,0 +1,367 @@
+// The experts' products on grouped rows, block-scaled E4M3 operands, on the
+// 5th-generation tensor core:
+//
+//   P[i, n] = sum_b sa[i, b] * sw[e, n / 128, b] * sum_{k in block b} a[i, k] * w[e, n, k]
+//
+// for every row i of expert e (rows [offsets[e], offsets[e+1])), blocks b of
+// 128 along K.  Two epilogues: P itself as bf16 or float32 rows
+// (moe_expert_gemm_fp8), and, with w's rows the gate rows followed by the up
+// rows, h = SiLU(P_gate) * P_up quantised again by blocks of 128
+// (moe_expert_glu_fp8).
+//
+// The scales differ from block to block of K, so a block's product cannot be
+// left to accumulate in tensor memory: each block of K = 128 (four matrix
+// instructions) goes to one of two tensor-memory buffers of 256 columns, and
+// the epilogue warps add it, scaled, to float32 accumulators in registers
+// while the tensor core fills the other buffer.
+//
+// One CTA per SM, tile 128 rows x 256 columns (glu: 128 gate + 128 up
+// columns, 128 columns of h), 10 warps: 8 epilogue warps (two per quarter of
+// the tensor-memory lanes; a thread owns one row and half of the columns, 128
+// accumulators, two per fma.rn.f32x2), one TMA warp, one matrix warp.
+// Operands arrive by tiled TMA into kStages stages of 48 KiB with the 128-byte
+// swizzle that the matrix instruction reads.  At 256 columns the operands'
+// shared-memory reads (48 KiB per 512 cycles of matrix work) stay below the
+// shared-memory rate and the 2 x 256 columns use the whole tensor memory.
+// Rows past the end of an expert and columns past N are computed and not
+// stored: rows and columns do not mix.
+//
+// Tiles are dealt out statically (tile b, b+G, ...), rows fastest, so that the
+// CTAs at work at one time share weight columns in L2.  Waits are bounded (2 s)
+// and report MOE_ETIMEDOUT.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ffn_kernels.cuh"
+#include "fp8_quant.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTileM = 128, kTileN = 256, kBlockK = MOE_FP8_BLOCK;
+constexpr int kStages = 4;
+constexpr int kABytes = kTileM * kBlockK, kBBytes = kTileN * kBlockK;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kEpilogueWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemColumns = 512;
+constexpr int kCols = 128;  // accumulators of one epilogue thread
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t amax_ready[2];
+  uint64_t drained;
+  uint32_t tmem;
+  int gave_up;
+  float amax[2][2][kTileM];  // [tile parity][half of the columns][row]
+};
+
+// Per expert: where its rows begin and end, and how many row tiles come before it.
+struct Groups {
+  int32_t *lo, *hi, *start;
+};
+
+struct Tile {
+  int e, row0, rows, n;  // expert, first row, rows of the tile that exist, column tile
+};
+
+__device__ __forceinline__ Tile find_tile(const Groups& g, int E, int n_tiles, int64_t t) {
+  int lo = 0, hi = E;  // largest e with start[e] * n_tiles <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(g.start[mid]) * n_tiles <= t) lo = mid;
+    else hi = mid;
+  }
+  const int m_tiles = g.start[lo + 1] - g.start[lo];
+  const int local = static_cast<int>(t - static_cast<int64_t>(g.start[lo]) * n_tiles);
+  Tile r;
+  r.e = lo;
+  r.n = local / m_tiles;
+  r.row0 = g.lo[lo] + (local - r.n * m_tiles) * kTileM;
+  r.rows = min(kTileM, g.hi[lo] - r.row0);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <bool kGlu, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertGemmParams p) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ Shared s;
+  uint8_t* stages = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
+  Groups g;
+  g.lo = reinterpret_cast<int32_t*>(stages + kStages * kStageBytes);
+  g.hi = g.lo + p.E;
+  g.start = g.hi + p.E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&s.full[i], 1);
+      ptx::mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&s.acc_full[i], 1);
+      ptx::mbar_init(&s.acc_empty[i], kEpilogueWarps);
+      ptx::mbar_init(&s.amax_ready[i], kEpilogueWarps);
+    }
+    ptx::mbar_init(&s.drained, 1);
+    ptx::mbar_fence_init();
+    s.gave_up = 0;
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, kTmemColumns);
+  if (threadIdx.x == kTmaWarp * 32) {
+    tc::tma_prefetch_map(&p.a);
+    tc::tma_prefetch_map(&p.w);
+  }
+  ptx::wait_prerequisites();
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    const int rows = static_cast<int>(p.rows);
+    int lo = 0, hi = rows;
+    if (p.offsets) {  // clamped: a damaged table cannot lead outside the buffers
+      lo = min(max(p.offsets[e], 0), rows);
+      hi = min(max(p.offsets[e + 1], lo), rows);
+    }
+    g.lo[e] = lo;
+    g.hi[e] = hi;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int before = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int own = e < p.E ? (g.hi[e] - g.lo[e] + kTileM - 1) / kTileM : 0;
+      int sum = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      if (e < p.E) g.start[e] = before + sum - own;
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) g.start[p.E] = before;
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const int64_t tiles = static_cast<int64_t>(g.start[p.E]) * p.n_tiles;
+  const uint32_t tmem = s.tmem;
+  const int kblocks = p.kblocks;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const Tile tile = find_tile(g, p.E, p.n_tiles, t);
+        const int w0 = tile.e * p.w_rows + tile.n * (kGlu ? kTileN / 2 : kTileN);
+        const int w1 = kGlu ? w0 + p.N : w0 + kTileN / 2;
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+          const int st = it % kStages;
+          if (it >= kStages && !tc::wait(&s.empty[st], (it / kStages - 1) & 1, &s.gave_up)) {
+            ok = false;
+            break;
+          }
+          uint8_t* a = stages + st * kStageBytes;
+          ptx::mbar_arrive_expect_tx(&s.full[st], kStageBytes);
+          tc::tma_load_2d(a, &p.a, kb * kBlockK, tile.row0, &s.full[st]);
+          tc::tma_load_2d(a + kABytes, &p.w, kb * kBlockK, w0, &s.full[st]);
+          tc::tma_load_2d(a + kABytes + kBBytes / 2, &p.w, kb * kBlockK, w1, &s.full[st]);
+        }
+      }
+      if (!ok) {  // loads still in flight write to this CTA's shared memory: wait (bounded) for them
+        const uint32_t oldest = it > kStages ? it - kStages : 0;
+        const unsigned long long start = tc::now_ns();
+        for (uint32_t j = oldest; j < it; ++j)
+          while (!ptx::mbar_try_wait(&s.full[j % kStages], (j / kStages) & 1) &&
+                 tc::now_ns() - start < tc::kWaitLimitNs) {
+          }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t kInstr = tc::instr_desc_e4m3(kTileM, kTileN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+          const int st = it % kStages, buf = it & 1;
+          if (it >= 2 && !tc::wait(&s.acc_empty[buf], (it / 2 - 1) & 1, &s.gave_up)) {
+            ok = false;
+            break;
+          }
+          if (!tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+          const uint64_t a = tc::smem_desc(stages + st * kStageBytes);
+          const uint64_t b = tc::smem_desc(stages + st * kStageBytes + kABytes);
+#pragma unroll
+          for (int k = 0; k < kBlockK / 32; ++k)
+            tc::mma_e4m3(tmem + buf * kTileN, a + 2 * k, b + 2 * k, kInstr, k > 0);
+          tc::commit(&s.empty[st]);
+          tc::commit(&s.acc_full[buf]);
+        }
+      }
+      // Nothing may be in flight when the tensor memory is freed.
+      tc::commit(&s.drained);
+      tc::wait(&s.drained, 0, &s.gave_up);
+    }
+  } else {
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    uint32_t it = 0;
+    int parity = 0, round = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++round) {
+      const Tile tile = find_tile(g, p.E, p.n_tiles, t);
+      const bool act = r < tile.rows;
+      const int64_t row = tile.row0 + (act ? r : 0);
+      const float* sa = p.a_scales + row * kblocks;
+      // The block rows of w's scales that this thread's columns lie in.
+      const float* sw = p.w_scales + static_cast<int64_t>(tile.e) * p.w_blocks * kblocks;
+      const float *sw0, *sw1;
+      if (kGlu) {
+        sw0 = sw + static_cast<int64_t>(tile.n) * kblocks;
+        sw1 = sw0 + static_cast<int64_t>(p.N / kBlockK) * kblocks;
+      } else {
+        sw0 = sw1 = sw + static_cast<int64_t>(min(tile.n * 2 + half, p.w_blocks - 1)) * kblocks;
+      }
+      unsigned long long acc[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
+      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const float a = sa[kb];
+        const float f0 = a * sw0[kb], f1 = kGlu ? a * sw1[kb] : f0;
+        const unsigned long long scale0 = tc::pack2(f0, f0), scale1 = tc::pack2(f1, f1);
+        const int buf = it & 1;
+        ok = tc::wait(&s.acc_full[buf], (it / 2) & 1, &s.gave_up);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        // glu: 64 gate columns, then the 64 up columns of the same h.
+        const uint32_t c0 = lanes + buf * kTileN + half * (kGlu ? kCols / 2 : kCols);
+        const uint32_t c1 = c0 + (kGlu ? kTileN / 2 : kCols / 2);
+        uint32_t v[2][16];
+        tc::tmem_load_16(c0, v[0]);
+#pragma unroll
+        for (int c = 0; c < kCols / 16; ++c) {
+          tc::wait_loads();
+          if (c + 1 < kCols / 16)
+            tc::tmem_load_16((c + 1) * 16 < kCols / 2 ? c0 + (c + 1) * 16 : c1 + (c + 1) * 16 - kCols / 2,
+                             v[(c + 1) & 1]);
+          else {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+          }
+          const unsigned long long scale = c * 16 < kCols / 2 ? scale0 : scale1;
+          const uint32_t* d = v[c & 1];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            acc[c * 8 + j] = tc::fma2(tc::pack2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), scale,
+                                      acc[c * 8 + j]);
+        }
+      }
+      if (!ok) break;
+      if (kGlu) {
+        float h[kCols / 2];
+        float amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) {
+          const float gate = j & 1 ? tc::hi2(acc[j / 2]) : tc::lo2(acc[j / 2]);
+          const float up = j & 1 ? tc::hi2(acc[kCols / 4 + j / 2]) : tc::lo2(acc[kCols / 4 + j / 2]);
+          h[j] = gate / (1.0f + expf(-gate)) * up;
+          amax = fmaxf(amax, fabsf(h[j]));
+        }
+        // The other half of the row's 128 columns is another warp's.  The two
+        // copies alternate, so a warp one tile ahead does not overwrite.
+        parity = round & 1;
+        s.amax[parity][half][r] = amax;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s.amax_ready[parity]);
+        ok = tc::wait(&s.amax_ready[parity], (round >> 1) & 1, &s.gave_up);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        amax = fmaxf(amax, s.amax[parity][half ^ 1][r]);
+        const float scale = amax > 0.0f ? __fdiv_rn(fmaxf(amax, kTinyAmax), 448.0f) : 1.0f;
+        const float inv = __fdiv_rn(1.0f, scale);
+        if (act) {
+          uint8_t* dst = static_cast<uint8_t*>(p.out) + row * p.N + tile.n * kBlockK + half * (kCols / 2);
+#pragma unroll
+          for (int c = 0; c < kCols / 2; c += 16) {
+            uint4 q;
+            uint32_t* o = &q.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float* e = h + c + 4 * j;
+              o[j] = fp8q::e4m3x2(__fmul_rn(e[0], inv), __fmul_rn(e[1], inv)) |
+                     (fp8q::e4m3x2(__fmul_rn(e[2], inv), __fmul_rn(e[3], inv)) << 16);
+            }
+            ptx::st_v4(dst + c, q);
+          }
+          if (half == 0) p.h_scales[row * (p.N / kBlockK) + tile.n] = scale;
+        }
+      } else if (act) {
+        const int n0 = tile.n * kTileN + half * kCols;
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + (row * p.N + n0) * (kF32 ? 4 : 2);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 8) {
+          if (n0 + c < p.N) {  // N is a multiple of 8
+            const unsigned long long* v = acc + c / 2;
+            if (kF32) {
+              ptx::st_v4(dst + c * 4, make_uint4(v[0], v[0] >> 32, v[1], v[1] >> 32));
+              ptx::st_v4(dst + c * 4 + 16, make_uint4(v[2], v[2] >> 32, v[3], v[3] >> 32));
+            } else {
+              ptx::st_v4(dst + c * 2,
+                         make_uint4(bf16x2(tc::lo2(v[0]), tc::hi2(v[0])), bf16x2(tc::lo2(v[1]), tc::hi2(v[1])),
+                                    bf16x2(tc::lo2(v[2]), tc::hi2(v[2])), bf16x2(tc::lo2(v[3]), tc::hi2(v[3]))));
+            }
+          }
+        }
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (threadIdx.x == 0 && s.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
+  if (warp == kMmaWarp) tc::tmem_free(tmem, kTmemColumns);
+}
+
+template <bool kGlu, bool kF32>
+cudaError_t launch(const ExpertGemmParams& p, int sms, cudaStream_t stream) {
+  const size_t smem = 1024 + kStages * kStageBytes + (3 * static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
+  auto* kernel = expert_gemm_kernel<kGlu, kF32>;
+  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
+  if (err != cudaSuccess) return err;
+  // Every expert may add one partly filled row tile.
+  int64_t most = ((p.rows + kTileM - 1) / kTileM + (p.offsets ? p.E : 0)) * p.n_tiles;
+  if (most > sms) most = sms;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(most)), dim3(kThreads), smem, stream, true, p);
+}
+
+}  // namespace
+
+int expert_gemm_n_tile(bool glu) { return glu ? kTileN / 2 : kTileN; }
+
+cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool glu, bool f32, int sms, cudaStream_t stream) {
+  if (glu) return launch<true, false>(p, sms, stream);
+  return f32 ? launch<false, true>(p, sms, stream) : launch<false, false>(p, sms, stream);
+}
+
+}  // namespace moe

@@ -2,9 +2,11 @@
 // argument checks and launches.  Exceptions do not cross it: what can throw
 // in the host code below is the allocation of a per-device cache entry.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -53,6 +55,66 @@ int launched(cudaError_t err) {
   return MOE_ECUDA;
 }
 
+// E4M3 matrix [rows, cols] as a tensor map of 128 x 128 boxes, 128-byte
+// swizzle, zeros outside.  The encoder is the driver's, found through the
+// runtime (no link against libcuda).
+bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static std::atomic<Encode> known{nullptr};
+  Encode encode = known.load(std::memory_order_acquire);
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || !fn)
+      return false;
+    encode = reinterpret_cast<Encode>(fn);
+    known.store(encode, std::memory_order_release);
+  }
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+  const cuuint32_t box[2] = {128, 128}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What the two grouped products have in common; N: columns of the output.
+int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows, int32_t K, const void* w,
+                   const float* w_scales, int32_t N, int32_t E, const int32_t* offsets, void* out, float* h_scales,
+                   bool f32, int32_t* status, void* stream) {
+  const int64_t w_rows = glu ? 2 * static_cast<int64_t>(N) : N;
+  if (rows < 0 || rows > INT_MAX - 128 || K <= 0 || K % 16 != 0 || N <= 0 || E < 1 || E > MOE_MAX_EXPERTS)
+    return MOE_EINVAL;
+  if (w_rows * E > INT_MAX || (!offsets && E != 1)) return MOE_EINVAL;
+  if (rows == 0) return MOE_OK;
+  if (!a || !a_scales || !w || !w_scales || !out || (glu && !h_scales)) return MOE_EINVAL;
+  if (!aligned(a, 16) || !aligned(a_scales, 4) || !aligned(w, 16) || !aligned(w_scales, 4) || !aligned(offsets, 4) ||
+      !aligned(out, 16) || !aligned(h_scales, 4) || !aligned(status, 4))
+    return MOE_EINVAL;
+  return guarded([&] {
+    const int sms = sm_count();
+    if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    moe::ExpertGemmParams p = {};
+    if (!encode_map(&p.a, a, rows, K) || !encode_map(&p.w, w, w_rows * E, K)) return static_cast<int>(MOE_ECUDA);
+    p.a_scales = a_scales;
+    p.w_scales = w_scales;
+    p.offsets = offsets;
+    p.out = out;
+    p.h_scales = h_scales;
+    p.status = status;
+    p.rows = rows;
+    p.kblocks = (K + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
+    p.N = N;
+    p.n_tiles = (N + moe::expert_gemm_n_tile(glu) - 1) / moe::expert_gemm_n_tile(glu);
+    p.E = E;
+    p.w_rows = static_cast<int32_t>(w_rows);
+    p.w_blocks = static_cast<int32_t>((w_rows + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK);
+    return launched(moe::launch_expert_gemm(p, glu, f32, sms, static_cast<cudaStream_t>(stream)));
+  });
+}
+
 }  // namespace
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -88,4 +150,23 @@ MOE_API int moe_add_rms_norm_fp8(const void* x, const void* residual, const void
     p.eps = eps;
     return launched(moe::launch_add_norm_fp8(p, weight_type == MOE_TYPE_F32, sms, static_cast<cudaStream_t>(stream)));
   });
+}
+
+MOE_API int moe_expert_gemm_fp8(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,
+                                const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_offsets,
+                                void* out, int out_type, int32_t* status, void* stream) {
+  NvtxRange nvtx_range("moe_expert_gemm_fp8");
+  if (n % 8 != 0 || (out_type != MOE_TYPE_BF16 && out_type != MOE_TYPE_F32)) return MOE_EINVAL;
+  return expert_product(false, a, a_scales, rows, k, w, w_scales, n, num_experts, expert_offsets, out, nullptr,
+                        out_type == MOE_TYPE_F32, status, stream);
+}
+
+MOE_API int moe_expert_glu_fp8(const void* a, const float* a_scales, int64_t rows, int32_t hidden, const void* w13,
+                               const float* w13_scales, int32_t inter, int32_t num_experts,
+                               const int32_t* expert_offsets, void* hq, float* h_scales, int32_t* status,
+                               void* stream) {
+  NvtxRange nvtx_range("moe_expert_glu_fp8");
+  if (inter % MOE_FP8_BLOCK != 0) return MOE_EINVAL;
+  return expert_product(true, a, a_scales, rows, hidden, w13, w13_scales, inter, num_experts, expert_offsets, hq,
+                        h_scales, false, status, stream);
 }

@@ -78,3 +78,56 @@ def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, xq: torch.Tensor, x_
         py = _arg("y", y, _BF16, (T, H), dev)
     moe.moe_add_rms_norm_fp8(px, pr, pw, moe.MOE_TYPE_F32 if weight.dtype == torch.float32 else moe.MOE_TYPE_BF16,
                              T, H, eps, po, py, pq, ps, stream)
+
+
+def _blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _product_args(a, a_scales, w, w_scales, expert_offsets, status):
+    """The checks that the two products share; w may be [N, K] for one expert."""
+    dev = _device("a", a, 2)
+    rows, K = a.shape
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise _wrong("w must be a tensor of 3 dimensions, or 2 for one expert")
+    experts = () if w.dim() == 2 else (w.shape[0],)
+    E, N = (1, w.shape[0]) if w.dim() == 2 else w.shape[:2]
+    pa = _arg("a", a, _FP8, (rows, K), dev)
+    ps = _arg("a_scales", a_scales, _F32, (rows, _blocks(K)), dev)
+    pw = _arg("w", w, _FP8, (*experts, N, K), dev)
+    pv = _arg("w_scales", w_scales, _F32, (*experts, _blocks(N), _blocks(K)), dev)
+    po = None if expert_offsets is None else _arg("expert_offsets", expert_offsets, (torch.int32,), (E + 1,), dev)
+    pt = None if status is None else _arg("status", status, (torch.int32,), (1,), dev)
+    return dev, rows, K, N, E, pa, ps, pw, pv, po, pt
+
+
+def expert_gemm_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                    out: torch.Tensor, *, expert_offsets: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream: Any = None) -> None:
+    """out[i] = a[i] . w[e]^T for the rows i that expert_offsets gives expert e.
+
+    a E4M3 [rows, K] with a_scales float32 [rows, ceil(K/128)]; w E4M3
+    [E, N, K] with w_scales float32 [E, ceil(N/128), ceil(K/128)]; out bf16 or
+    float32 [rows, N].  expert_offsets int32 [E+1], e.g.
+    ``dispatch_recv()["expert_offsets"]``; None for one expert with all rows.
+    K % 16 == 0, N % 8 == 0."""
+    dev, rows, K, N, E, pa, ps, pw, pv, po, pt = _product_args(a, a_scales, w, w_scales, expert_offsets, status)
+    pout = _arg("out", out, _FLOAT, (rows, N), dev)
+    moe.moe_expert_gemm_fp8(pa, ps, rows, K, pw, pv, N, E, po, pout,
+                            moe.MOE_TYPE_F32 if out.dtype == torch.float32 else moe.MOE_TYPE_BF16, pt, stream)
+
+
+def expert_glu_fp8(a: torch.Tensor, a_scales: torch.Tensor, w13: torch.Tensor, w13_scales: torch.Tensor,
+                   hq: torch.Tensor, h_scales: torch.Tensor, *, expert_offsets: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream: Any = None) -> None:
+    """h = SiLU(a . gate^T) * (a . up^T), quantised: the rows of the second product.
+
+    As expert_gemm_fp8, with w13 [E, 2*I, H] (gate rows, then up rows; I a
+    multiple of 128); hq E4M3 [rows, I], h_scales float32 [rows, I/128]."""
+    dev, rows, H, N, E, pa, ps, pw, pv, po, pt = _product_args(a, a_scales, w13, w13_scales, expert_offsets, status)
+    if N % (2 * BLOCK):
+        raise _wrong(f"w13 has {N} rows, must be twice a multiple of {BLOCK}")
+    I = N // 2
+    ph = _arg("hq", hq, _FP8, (rows, I), dev)
+    pg = _arg("h_scales", h_scales, _F32, (rows, I // BLOCK), dev)
+    moe.moe_expert_glu_fp8(pa, ps, rows, H, pw, pv, I, E, po, ph, pg, pt, stream)

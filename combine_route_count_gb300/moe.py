@@ -48,7 +48,7 @@ EXPORTS = ("moe_validate_config", "moe_workspace_bytes", "moe_recv_bound_rows", 
            "moe_dispatch_send_staged", "moe_kernel_times", "moe_dispatch_send_quantized",
            "moe_dense_capacity", "moe_dispatch_send_dense", "moe_combine_recv_dense",
            # include/moe_ffn.h
-           "moe_add_rms_norm_fp8")
+           "moe_add_rms_norm_fp8", "moe_expert_gemm_fp8", "moe_expert_glu_fp8")
 
 
 class moe_config(ctypes.Structure):
@@ -107,6 +107,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_get_error": ([P, P], I),
         "moe_strerror": ([I], ctypes.c_char_p),
         "moe_add_rms_norm_fp8": ([P, P, P, I, I64, ctypes.c_int32, ctypes.c_float, P, P, P, P, P], I),
+        "moe_expert_gemm_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, I, P, P], I),
+        "moe_expert_glu_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -302,6 +304,21 @@ def moe_add_rms_norm_fp8(x: Any, residual: Any, weight: Any, weight_type: int, n
     _check(load_library().moe_add_rms_norm_fp8(_ptr(x), _ptr(residual), _ptr(weight), weight_type, num_tokens, hidden,
                                                eps, _ptr(residual_out), _ptr(y), _ptr(xq), _ptr(x_scales),
                                                _stream(stream)), "moe_add_rms_norm_fp8")
+
+
+def moe_expert_gemm_fp8(a: Any, a_scales: Any, rows: int, k: int, w: Any, w_scales: Any, n: int, num_experts: int,
+                        expert_offsets: Any, out: Any, out_type: int, status: Any = None, stream: Any = None) -> None:
+    _check(load_library().moe_expert_gemm_fp8(_ptr(a), _ptr(a_scales), rows, k, _ptr(w), _ptr(w_scales), n,
+                                              num_experts, _ptr(expert_offsets), _ptr(out), out_type, _ptr(status),
+                                              _stream(stream)), "moe_expert_gemm_fp8")
+
+
+def moe_expert_glu_fp8(a: Any, a_scales: Any, rows: int, hidden: int, w13: Any, w13_scales: Any, inter: int,
+                       num_experts: int, expert_offsets: Any, hq: Any, h_scales: Any, status: Any = None,
+                       stream: Any = None) -> None:
+    _check(load_library().moe_expert_glu_fp8(_ptr(a), _ptr(a_scales), rows, hidden, _ptr(w13), _ptr(w13_scales), inter,
+                                             num_experts, _ptr(expert_offsets), _ptr(hq), _ptr(h_scales),
+                                             _ptr(status), _stream(stream)), "moe_expert_glu_fp8")
 
 
 # ---- convenience: one context with a torch-allocated workspace ---------------

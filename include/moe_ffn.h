@@ -8,6 +8,8 @@
  * weights with one float32 scale for each MOE_FP8_BLOCK x MOE_FP8_BLOCK block.
  *
  *   moe_add_rms_norm_fp8  x + residual -> RMS norm -> codes and scales
+ *   moe_expert_glu_fp8    expert rows -> SiLU(gate) * up -> codes and scales
+ *   moe_expert_gemm_fp8   expert rows -> one product, bf16 or float32 rows
  *
  * Quantisation of a block with largest magnitude amax, in float32:
  *   scale = max(amax, 2^-100) / 448 (1 for an all-zero block), inv = 1 / scale,
@@ -63,6 +65,46 @@ extern "C" {
 int moe_add_rms_norm_fp8(const void* x, const void* residual, const void* weight, int weight_type,
                          int64_t num_tokens, int32_t hidden, float eps, void* residual_out, void* y, void* xq,
                          float* x_scales, void* stream);
+
+/* The experts' product on grouped rows (or one dense product):
+ *   out[i, j] = sum over blocks b of k:  a_scales[i, b] * w_scales[e, j / 128, b]
+ *               * sum over c in block b of  a[i, c] * w[e, j, c]
+ * for the rows i in [expert_offsets[e], expert_offsets[e+1]) of expert e,
+ * accumulated in float32 and rounded once.  With expert_offsets of
+ * moe_dispatch_recv this turns dispatched rows into the expert_y that
+ * moe_combine_send takes.
+ *   a               device E4M3 [rows, k], k % 16 == 0
+ *   a_scales        device float32 [rows, ceil(k / 128)]
+ *   w               device E4M3 [num_experts, n, k], n % 8 == 0,
+ *                   num_experts * n < 2^31
+ *   w_scales        device float32 [num_experts, ceil(n / 128), ceil(k / 128)]
+ *   expert_offsets  device int32 [num_experts + 1], non-decreasing; read on the
+ *                   device, values outside [0, rows] are taken as the nearest
+ *                   inside.  Rows that no expert owns are left untouched.
+ *                   NULL (num_experts 1 only): all rows.
+ *   out             device bf16 or float32 (out_type MOE_TYPE_*) [rows, n]
+ *   status          device int32 [1], or NULL; set to MOE_ETIMEDOUT from MOE_OK
+ *                   if a bounded wait inside the kernel gives up (the outputs
+ *                   are then incomplete), otherwise not touched
+ * a, w and out are 16-byte aligned.  rows == 0 is allowed; rows < 2^31 - 128. */
+int moe_expert_gemm_fp8(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,
+                        const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_offsets,
+                        void* out, int out_type, int32_t* status, void* stream);
+
+/* The experts' gated product with its activation and quantisation:
+ *   gate = a . w13[e, 0..inter), up = a . w13[e, inter..2 inter), each as in
+ *   moe_expert_gemm_fp8, left in float32;
+ *   h = gate / (1 + exp(-gate)) * up;  (hq, h_scales) = h quantised,
+ * which is what moe_expert_gemm_fp8 takes for the second product.
+ *   a, a_scales     device E4M3 [rows, hidden] and its scales, hidden % 16 == 0
+ *   w13             device E4M3 [num_experts, 2 * inter, hidden]: gate rows,
+ *                   then up rows; inter % 128 == 0
+ *   w13_scales      device float32 [num_experts, 2 * inter / 128, ceil(hidden / 128)]
+ *   hq, h_scales    device E4M3 [rows, inter], float32 [rows, inter / 128]
+ * Everything else as for moe_expert_gemm_fp8. */
+int moe_expert_glu_fp8(const void* a, const float* a_scales, int64_t rows, int32_t hidden, const void* w13,
+                       const float* w13_scales, int32_t inter, int32_t num_experts, const int32_t* expert_offsets,
+                       void* hq, float* h_scales, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -42,7 +42,8 @@ def dequantise(q, scales):
 
 def assert_codes_near(q, scales, v, rel):
     """q (code values) and scales against unquantised float64 rows v, where the
-    kernel's v may be off by a relative `rel` of its block's largest value:
+    kernel's v may be off by a relative `rel` of its block's largest value (one
+    number, or one for each block):
     scales within rel, and each code within half a step of E4M3 (at its
     binade) plus what `rel` moves it by."""
     b = v.reshape(v.shape[0], -1, BLOCK)
@@ -55,9 +56,47 @@ def assert_codes_near(q, scales, v, rel):
     # A value just below a binade may round up into it, where steps are twice
     # as wide; half a step of the own binade still bounds the distance.
     far = np.abs(q.reshape(b.shape) - u)
-    assert np.all(far <= 0.5 * step + 3 * rel * 448.0), np.max(far - 0.5 * step)
+    slack = 3 * np.broadcast_to(rel, want.shape)[..., None] * 448.0
+    assert np.all(far <= 0.5 * step + slack), np.max(far - 0.5 * step)
 
 
 def add_norm(x, residual, weight, eps):
     s = x + residual if residual is not None else x
     return s, s / np.sqrt((s * s).mean(-1, keepdims=True) + eps) * weight
+
+
+def product(a, a_scales, w, w_scales, offsets=None):
+    """Grouped product in float64 on the tensors' device, and the same sum over magnitudes.
+
+    a E4M3 [rows, K], w E4M3 [E, N, K]; returns (P, S) with P = 0 in rows no expert owns."""
+    import torch
+    rows, E = a.shape[0], w.shape[0]
+    off = [0, rows] if offsets is None else [min(max(int(o), 0), rows) for o in offsets]
+    P = torch.zeros(rows, w.shape[1], dtype=torch.float64, device=a.device)
+    S = torch.zeros_like(P)
+    k = torch.arange(a.shape[1], device=a.device) // BLOCK
+    n = torch.arange(w.shape[1], device=a.device) // BLOCK
+    for e in range(E):
+        lo, hi = off[e], max(off[e], off[e + 1])
+        if hi > lo:
+            x = a[lo:hi].float().double() * a_scales[lo:hi].double()[:, k]
+            y = w[e].float().double() * w_scales[e].double()[n][:, k]
+            P[lo:hi], S[lo:hi] = x @ y.t(), x.abs() @ y.abs().t()
+    return P, S
+
+
+def product_error(kblocks):
+    """Bound on a product's error over its sum of magnitudes: up to 128 additions
+    inside a block that may truncate (2^-23 each), one scaling and one
+    addition for each block in float32, and the product of the two scales."""
+    return (128 + kblocks + 3) * 2.0 ** -23
+
+
+def glu(P, S, rel):
+    """h from a gate/up product and a bound on its error: |silu'| < 1.1, float32 exp, division and products."""
+    import torch
+    I = P.shape[1] // 2
+    gate, up, sg, su = P[:, :I], P[:, I:], S[:, :I] * rel, S[:, I:] * rel
+    silu = gate * torch.sigmoid(gate)
+    h = silu * up
+    return h, 1.1 * sg * (up.abs() + su) + silu.abs() * su + 8 * 2.0 ** -23 * h.abs()

@@ -42,3 +42,21 @@ def test_add_rms_norm_checks(moe):
                dict(eps=float("inf")), dict(eps=float("nan")), dict(r=A, ro=A, y=A)):
         assert call(**kw), kw
     moe.moe_add_rms_norm_fp8(None, None, None, 0, 0, 256, 1e-6, None, None, None, None, stream=0)  # no tokens: nothing to do
+
+
+def test_product_checks(moe):
+    A, bad = 0x1000, 0x1008
+
+    def gemm(a=A, s=A, rows=4, k=256, w=A, ws=A, n=256, E=2, off=A, out=A, t=0, st=None):
+        return refused(moe, moe.moe_expert_gemm_fp8, a, s, rows, k, w, ws, n, E, off, out, t, st)
+
+    def glu(a=A, s=A, rows=4, k=256, w=A, ws=A, n=256, E=2, off=A, out=A, hs=A, st=None):
+        return refused(moe, moe.moe_expert_glu_fp8, a, s, rows, k, w, ws, n, E, off, out, hs, st)
+
+    for kw in (dict(a=None), dict(s=None), dict(w=None), dict(ws=None), dict(out=None), dict(a=bad), dict(w=bad),
+               dict(out=bad), dict(s=0x1002), dict(ws=0x1002), dict(off=0x1002), dict(st=0x1002), dict(rows=-1),
+               dict(rows=2 ** 31 - 1), dict(k=0), dict(k=-16), dict(k=200), dict(n=0), dict(E=0), dict(E=1025),
+               dict(off=None), dict(n=2 ** 30)):
+        assert gemm(**kw) and glu(**kw), kw
+    assert gemm(t=2) and gemm(n=260) and glu(n=192) and glu(hs=None) and glu(hs=0x1002)
+    moe.moe_expert_gemm_fp8(None, None, 0, 256, None, None, 256, 2, A, None, 0, None, stream=0)
