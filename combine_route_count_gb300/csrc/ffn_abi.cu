@@ -115,6 +115,20 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
   });
 }
 
+bool decode_config_ok(const moe_config* c, int32_t inter) {
+  return c && moe_validate_config(c) == MOE_OK && c->num_tokens <= MOE_DECODE_MAX_TOKENS &&
+         c->hidden % MOE_FP8_BLOCK == 0 && inter > 0 && inter % MOE_FP8_BLOCK == 0 && inter <= INT_MAX / 2;
+}
+
+size_t decode_codes_bytes(const moe_config* c, int32_t inter) {
+  return (static_cast<size_t>(c->num_tokens) * c->top_k * inter + 255) / 256 * 256;
+}
+
+size_t decode_workspace(const moe_config* c, int32_t inter) {
+  const size_t scales = static_cast<size_t>(c->num_tokens) * c->top_k * (inter / MOE_FP8_BLOCK) * sizeof(float);
+  return decode_codes_bytes(c, inter) + (scales + 255) / 256 * 256;
+}
+
 }  // namespace
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -169,4 +183,49 @@ MOE_API int moe_expert_glu_fp8(const void* a, const float* a_scales, int64_t row
   if (inter % MOE_FP8_BLOCK != 0) return MOE_EINVAL;
   return expert_product(true, a, a_scales, rows, hidden, w13, w13_scales, inter, num_experts, expert_offsets, hq,
                         h_scales, false, status, stream);
+}
+
+MOE_API int moe_decode_workspace_bytes(const moe_config* cfg, int32_t inter, size_t* bytes) {
+  if (!bytes || !decode_config_ok(cfg, inter)) return MOE_EINVAL;
+  *bytes = decode_workspace(cfg, inter);
+  return MOE_OK;
+}
+
+MOE_API int moe_decode_layer_fp8(const moe_config* cfg, int32_t inter, const void* xq, const float* x_scales,
+                                 const int32_t* topk_idx, const float* topk_w, const void* w13,
+                                 const float* w13_scales, const void* w2, const float* w2_scales, void* out,
+                                 int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("moe_decode_layer_fp8");
+  if (!decode_config_ok(cfg, inter)) return MOE_EINVAL;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if (!xq || !x_scales || !topk_idx || !topk_w || !w13 || !w13_scales || !w2 || !w2_scales || !out || !status ||
+      !workspace)
+    return MOE_EINVAL;
+  if (!aligned(xq, 16) || !aligned(x_scales, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(w13, 16) ||
+      !aligned(w13_scales, 4) || !aligned(w2, 16) || !aligned(w2_scales, 4) || !aligned(out, 16) ||
+      !aligned(status, 4) || !aligned(workspace, 256) || workspace_bytes < decode_workspace(cfg, inter))
+    return MOE_EINVAL;
+  return guarded([&] {
+    const int sms = sm_count();
+    if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    moe::DecodeParams p = {};
+    p.xq = static_cast<const uint8_t*>(xq);
+    p.x_scales = x_scales;
+    p.topk_idx = topk_idx;
+    p.topk_w = topk_w;
+    p.w13 = static_cast<const uint8_t*>(w13);
+    p.w13_scales = w13_scales;
+    p.w2 = static_cast<const uint8_t*>(w2);
+    p.w2_scales = w2_scales;
+    p.hq = static_cast<uint8_t*>(workspace);
+    p.h_scales = reinterpret_cast<float*>(p.hq + decode_codes_bytes(cfg, inter));
+    p.out = static_cast<uint8_t*>(out);
+    p.status = status;
+    p.T = cfg->num_tokens;
+    p.H = cfg->hidden;
+    p.K = cfg->top_k;
+    p.E = cfg->num_experts;
+    p.I = inter;
+    return launched(moe::launch_decode_layer(p, sms, static_cast<cudaStream_t>(stream)));
+  });
 }

@@ -16,6 +16,22 @@ namespace moe {
 // scale is taken, so that 1 / scale stays finite.
 constexpr float kTinyAmax = 0x1p-100f;
 
+// Loads that stay where they are written, behind the grid's dependency wait:
+// for data that the kernel before this one may have written.
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // ---- add_rms_norm_fp8: residual addition, RMS norm, quantisation -----------
 struct AddNormParams {
   const uint8_t* x;         // bf16 [T, H]
@@ -49,5 +65,23 @@ struct ExpertGemmParams {
 // Columns of out that one tile covers.
 int expert_gemm_n_tile(bool glu);
 cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool glu, bool f32, int sms, cudaStream_t stream);
+
+// ---- decode_layer: a whole expert layer for a few tokens ----------------------
+struct DecodeParams {
+  const uint8_t* xq;        // E4M3 [T, H]
+  const float* x_scales;    // [T, H/128]
+  const int32_t* topk_idx;  // [T, K]
+  const float* topk_w;      // [T, K]
+  const uint8_t* w13;       // E4M3 [E, 2I, H]
+  const float* w13_scales;  // [E, 2I/128, H/128]
+  const uint8_t* w2;        // E4M3 [E, H, I]
+  const float* w2_scales;   // [E, H/128, I/128]
+  uint8_t* hq;              // workspace: E4M3 [T*K, I], rows ordered by (expert, token)
+  float* h_scales;          // workspace: [T*K, I/128]
+  uint8_t* out;             // bf16 [T, H]
+  int32_t* status;
+  int32_t T, H, K, E, I;
+};
+cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream);
 
 }  // namespace moe

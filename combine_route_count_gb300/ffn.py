@@ -2,10 +2,12 @@
 
 Each function checks its tensors (type, shape, contiguity, device), then makes
 one call into libmoe.so on the given stream (torch's current stream if None).
-Outputs are the caller's tensors, as everywhere in this package; nothing is
-allocated and nothing waits for the GPU.  E4M3 codes may be given as
+Outputs are the caller's tensors, as everywhere in this package; the functions
+allocate nothing and nothing waits for the GPU.  E4M3 codes may be given as
 ``torch.float8_e4m3fn`` or as their ``torch.uint8`` bytes.  A wrong argument
 raises ``moe.MoEError`` with ``MOE_EINVAL`` before anything is enqueued.
+
+``DecodeLayer`` keeps one layer's weights and the workspace of its calls.
 """
 from __future__ import annotations
 
@@ -131,3 +133,51 @@ def expert_glu_fp8(a: torch.Tensor, a_scales: torch.Tensor, w13: torch.Tensor, w
     ph = _arg("hq", hq, _FP8, (rows, I), dev)
     pg = _arg("h_scales", h_scales, _F32, (rows, I // BLOCK), dev)
     moe.moe_expert_glu_fp8(pa, ps, rows, H, pw, pv, I, E, po, ph, pg, pt, stream)
+
+
+class DecodeLayer:
+    """A whole expert layer for a few tokens, for one layer's weights.
+
+    Keeps references to the weights (w13 E4M3 [E, 2*I, H], gate rows then up
+    rows; w2 E4M3 [E, H, I]; their scales float32 [E, 2*I/128, H/128] and
+    [E, H/128, I/128]) and owns the workspace for up to max_tokens tokens of
+    top_k experts.  One call may be in flight at a time: calls on several
+    streams need a layer object each."""
+
+    def __init__(self, max_tokens: int, top_k: int, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
+                 w2_scales: torch.Tensor):
+        self.device = _device("w13", w13, 3)
+        if not isinstance(w2, torch.Tensor) or w2.dim() != 3:
+            raise _wrong("w2 must be a tensor of 3 dimensions")
+        self.E, self.H, self.I = w2.shape
+        self.max_tokens, self.K = max_tokens, top_k
+        self._weights = (w13, w13_scales, w2, w2_scales)  # kept alive; their addresses are passed on
+        sizes = ("w13", w13, _FP8, (self.E, 2 * self.I, self.H)), \
+                ("w13_scales", w13_scales, _F32, (self.E, _blocks(2 * self.I), _blocks(self.H))), \
+                ("w2", w2, _FP8, (self.E, self.H, self.I)), \
+                ("w2_scales", w2_scales, _F32, (self.E, _blocks(self.H), _blocks(self.I)))
+        self._pointers = tuple(_arg(*s, self.device) for s in sizes)
+        nbytes = moe.moe_decode_workspace_bytes(moe.make_config(max_tokens, self.H, top_k, self.E, 1), self.I)
+        self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def forward(self, xq: torch.Tensor, x_scales: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                out: torch.Tensor, stream: Any = None) -> None:
+        """out[t] = sum_k topk_w[t,k] * expert(topk_idx[t,k])(x[t]); out bf16 [T, H], T <= max_tokens."""
+        dev = _device("xq", xq, 2)
+        T, H, K = xq.shape[0], self.H, self.K
+        if T > self.max_tokens or dev != self.device:
+            raise _wrong(f"xq has {T} tokens on {dev}, must have at most {self.max_tokens} on {self.device}")
+        px = _arg("xq", xq, _FP8, (T, H), dev)
+        ps = _arg("x_scales", x_scales, _F32, (T, H // BLOCK), dev)
+        pi = _arg("topk_idx", topk_idx, (torch.int32,), (T, K), dev)
+        pw = _arg("topk_w", topk_w, _F32, (T, K), dev)
+        po = _arg("out", out, _BF16, (T, H), dev)
+        moe.moe_decode_layer_fp8(moe.make_config(T, H, K, self.E, 1), self.I, px, ps, pi, pw, *self._pointers, po,
+                                 self.status, self.workspace, self.workspace.numel(), stream)
+
+    def get_error(self, stream: Any = None) -> int:
+        """Waits for the stream; the device status of the last call (MOE_OK or MOE_EROUTE)."""
+        s = torch.cuda.current_stream() if stream is None else stream
+        s.synchronize()
+        return int(self.status.item())

@@ -48,7 +48,8 @@ EXPORTS = ("moe_validate_config", "moe_workspace_bytes", "moe_recv_bound_rows", 
            "moe_dispatch_send_staged", "moe_kernel_times", "moe_dispatch_send_quantized",
            "moe_dense_capacity", "moe_dispatch_send_dense", "moe_combine_recv_dense",
            # include/moe_ffn.h
-           "moe_add_rms_norm_fp8", "moe_expert_gemm_fp8", "moe_expert_glu_fp8")
+           "moe_add_rms_norm_fp8", "moe_expert_gemm_fp8", "moe_expert_glu_fp8",
+           "moe_decode_workspace_bytes", "moe_decode_layer_fp8")
 
 
 class moe_config(ctypes.Structure):
@@ -107,6 +108,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_get_error": ([P, P], I),
         "moe_strerror": ([I], ctypes.c_char_p),
         "moe_add_rms_norm_fp8": ([P, P, P, I, I64, ctypes.c_int32, ctypes.c_float, P, P, P, P, P], I),
+        "moe_decode_workspace_bytes": ([C, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)], I),
+        "moe_decode_layer_fp8": ([C, ctypes.c_int32, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P], I),
         "moe_expert_gemm_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, I, P, P], I),
         "moe_expert_glu_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P], I),
     }
@@ -297,6 +300,7 @@ def moe_dispatch_send_noalloc(cfg: moe_config, x: Any, topk_idx: Any, expert_x: 
 
 MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
 MOE_NORM_MAX_HIDDEN = 65536
+MOE_DECODE_MAX_TOKENS = 64
 
 
 def moe_add_rms_norm_fp8(x: Any, residual: Any, weight: Any, weight_type: int, num_tokens: int, hidden: int,
@@ -319,6 +323,22 @@ def moe_expert_glu_fp8(a: Any, a_scales: Any, rows: int, hidden: int, w13: Any, 
     _check(load_library().moe_expert_glu_fp8(_ptr(a), _ptr(a_scales), rows, hidden, _ptr(w13), _ptr(w13_scales), inter,
                                              num_experts, _ptr(expert_offsets), _ptr(hq), _ptr(h_scales),
                                              _ptr(status), _stream(stream)), "moe_expert_glu_fp8")
+
+
+def moe_decode_workspace_bytes(cfg: moe_config, inter: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_decode_workspace_bytes(ctypes.byref(cfg), inter, ctypes.byref(n)),
+           "moe_decode_workspace_bytes")
+    return int(n.value)
+
+
+def moe_decode_layer_fp8(cfg: moe_config, inter: int, xq: Any, x_scales: Any, topk_idx: Any, topk_w: Any, w13: Any,
+                         w13_scales: Any, w2: Any, w2_scales: Any, out: Any, status: Any, workspace: Any,
+                         workspace_bytes: int, stream: Any = None) -> None:
+    _check(load_library().moe_decode_layer_fp8(ctypes.byref(cfg), inter, _ptr(xq), _ptr(x_scales), _ptr(topk_idx),
+                                               _ptr(topk_w), _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales),
+                                               _ptr(out), _ptr(status), _ptr(workspace), workspace_bytes,
+                                               _stream(stream)), "moe_decode_layer_fp8")
 
 
 # ---- convenience: one context with a torch-allocated workspace ---------------

@@ -10,6 +10,8 @@
  *   moe_add_rms_norm_fp8  x + residual -> RMS norm -> codes and scales
  *   moe_expert_glu_fp8    expert rows -> SiLU(gate) * up -> codes and scales
  *   moe_expert_gemm_fp8   expert rows -> one product, bf16 or float32 rows
+ *   moe_decode_layer_fp8  a few tokens through dispatch, both products and
+ *                         combine at once
  *
  * Quantisation of a block with largest magnitude amax, in float32:
  *   scale = max(amax, 2^-100) / 448 (1 for an all-zero block), inv = 1 / scale,
@@ -105,6 +107,44 @@ int moe_expert_gemm_fp8(const void* a, const float* a_scales, int64_t rows, int3
 int moe_expert_glu_fp8(const void* a, const float* a_scales, int64_t rows, int32_t hidden, const void* w13,
                        const float* w13_scales, int32_t inter, int32_t num_experts, const int32_t* expert_offsets,
                        void* hq, float* h_scales, int32_t* status, void* stream);
+
+/* Largest number of tokens of moe_decode_layer_fp8. */
+#define MOE_DECODE_MAX_TOKENS 64
+
+/* Device workspace (bytes, a multiple of 256) of moe_decode_layer_fp8: the
+ * quantised h of every (token, choice).  Its contents need no initialisation.
+ * MOE_EINVAL for a configuration the call does not take. */
+int moe_decode_workspace_bytes(const moe_config* cfg, int32_t inter, size_t* bytes);
+
+/* A whole expert layer for a few tokens, in two kernels and without a grouped
+ * copy of the rows:
+ *   h[t,k] = SiLU(gate) * up of token t by expert e = topk_idx[t,k], quantised
+ *            (as moe_expert_glu_fp8);
+ *   out[t] = bf16( sum_k topk_w[t,k] * (w2[e] . h[t,k]) ), products and sum in
+ *            float32, rounded once.
+ * The same layer through moe_dispatch_send_quantized, moe_expert_glu_fp8,
+ * moe_expert_gemm_fp8 and moe_combine_recv differs in that expert_y is rounded
+ * to bf16 there.  The chosen experts' weights are read once.
+ *   cfg          num_tokens <= MOE_DECODE_MAX_TOKENS, hidden % 128 == 0, else as
+ *                for moe_ctx_create (num_ranks plays no part beyond its checks)
+ *   inter        inner size of an expert, a multiple of 128
+ *   xq, x_scales device E4M3 [T, hidden] and float32 [T, hidden / 128], as
+ *                moe_add_rms_norm_fp8 writes them
+ *   topk_idx     device int32 [T, K];  topk_w  device float32 [T, K]
+ *   w13          device E4M3 [E, 2 * inter, hidden]: gate rows, then up rows
+ *   w13_scales   device float32 [E, 2 * inter / 128, hidden / 128]
+ *   w2           device E4M3 [E, hidden, inter]
+ *   w2_scales    device float32 [E, hidden / 128, inter / 128]
+ *   out          device bf16 [T, hidden]
+ *   status       device int32 [1], written: MOE_OK, or MOE_EROUTE if an index is
+ *                out of range or repeated within a token (out is then untouched)
+ *   workspace    device, at least moe_decode_workspace_bytes, 256-byte aligned;
+ *                calls that may overlap need one each
+ * xq, w13, w2 and out are 16-byte aligned.  num_tokens == 0 does nothing. */
+int moe_decode_layer_fp8(const moe_config* cfg, int32_t inter, const void* xq, const float* x_scales,
+                         const int32_t* topk_idx, const float* topk_w, const void* w13, const float* w13_scales,
+                         const void* w2, const float* w2_scales, void* out, int32_t* status, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

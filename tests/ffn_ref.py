@@ -100,3 +100,41 @@ def glu(P, S, rel):
     silu = gate * torch.sigmoid(gate)
     h = silu * up
     return h, 1.1 * sg * (up.abs() + su) + silu.abs() * su + 8 * 2.0 ** -23 * h.abs()
+
+
+def decode_layer(x, sx, idx, weights, w13, s13, w2, s2):
+    """The whole layer in float64 (tensors on one device), and a bound on a float32 kernel's error.
+
+    h is quantised by the rule, so its codes may fall to either side of a
+    rounding boundary that h is within its own error of: the bound takes the
+    codes of h - err and h + err (rounding is monotone)."""
+    import torch
+    T, K = idx.shape
+    H, I = w2.shape[1:]
+    out = torch.zeros(T, H, dtype=torch.float64, device=x.device)
+    bound = torch.zeros_like(out)
+    for e in sorted(set(idx.flatten().tolist())):
+        t, k = (idx == e).nonzero(as_tuple=True)
+        rel = product_error(sx.shape[1])
+        P, S = product(x[t], sx[t], w13[e:e + 1], s13[e:e + 1])
+        h, err = glu(P, S, rel)
+        h, err = f64(h), f64(err)
+        q, scale = quantise(h)
+        shape = (len(h), -1, BLOCK)
+        top_err = err.reshape(shape).max(-1)
+        wide = np.repeat(scale, BLOCK, 1)
+        srel = np.repeat(top_err / (scale * 448.0) + 2.0 ** -22, BLOCK, 1)
+        lo = e4m3((h - err) / wide - np.abs(h) / wide * srel)
+        hi = e4m3((h + err) / wide + np.abs(h) / wide * srel)
+        value = q * wide
+        dev = np.maximum(np.abs(hi * wide - value), np.abs(value - lo * wide)) + srel * np.abs(value) * 2
+        n = torch.arange(H, device=x.device) // BLOCK
+        c = torch.arange(I, device=x.device) // BLOCK
+        w = w2[e].float().double() * s2[e].double()[n][:, c]
+        value, dev = torch.from_numpy(value).to(x.device), torch.from_numpy(dev).to(x.device)
+        r = weights.double()[t, k][:, None]
+        out[t] += r * (value @ w.t())
+        bound[t] += r.abs() * ((dev + product_error(s2.shape[2]) * value.abs()) @ w.abs().t())
+    bound += (K + 8) * 2.0 ** -23 * bound + (K + 8 * K) * 2.0 ** -23 * out.abs()
+    _, ex = torch.frexp(out.abs() + bound)
+    return out, bound + torch.exp2(ex.double() - 9)

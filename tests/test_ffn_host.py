@@ -60,3 +60,22 @@ def test_product_checks(moe):
         assert gemm(**kw) and glu(**kw), kw
     assert gemm(t=2) and gemm(n=260) and glu(n=192) and glu(hs=None) and glu(hs=0x1002)
     moe.moe_expert_gemm_fp8(None, None, 0, 256, None, None, 256, 2, A, None, 0, None, stream=0)
+
+
+def test_decode_layer_checks(moe):
+    A, bad = 0x1000, 0x1008
+
+    def call(T=4, H=256, K=2, E=8, N=1, I=128, x=A, sx=A, idx=A, w=A, a=A, sa=A, b=A, sb=A, out=A, st=A, ws=A, n=1 << 20):
+        return refused(moe, moe.moe_decode_layer_fp8, moe.make_config(T, H, K, E, N), I, x, sx, idx, w, a, sa, b, sb,
+                       out, st, ws, n)
+
+    for kw in (dict(T=65), dict(T=-1), dict(H=200), dict(H=0), dict(K=0), dict(K=9), dict(K=17, E=32), dict(E=1032),
+               dict(N=3), dict(I=0), dict(I=64), dict(I=-128), dict(x=None), dict(sx=None), dict(idx=None),
+               dict(w=None), dict(a=None), dict(sa=None), dict(b=None), dict(sb=None), dict(out=None), dict(st=None),
+               dict(ws=None), dict(x=bad), dict(a=bad), dict(b=bad), dict(out=bad), dict(ws=0x1010), dict(n=1024),
+               dict(idx=0x1002), dict(w=0x1002), dict(sx=0x1002), dict(st=0x1002)):
+        assert call(**kw), kw
+    assert moe.moe_decode_workspace_bytes(moe.make_config(4, 256, 2, 8, 1), 128) == 8 * 128 + 256
+    with pytest.raises(moe.MoEError):
+        moe.moe_decode_workspace_bytes(moe.make_config(65, 256, 2, 8, 1), 128)
+    moe.moe_decode_layer_fp8(moe.make_config(0, 256, 2, 8, 1), 128, *[None] * 11, 0, stream=0)
