@@ -6,8 +6,8 @@
 //   q = E4M3(v / scale_b), per block b of 128 elements.
 //
 // All arithmetic is float32; the row's sum of squares is taken from the
-// float32 s, and v is quantised without passing through bf16 (y and
-// residual_out are separate roundings of v and s).
+// float32 s, and the codes come from the float32 s * weight without passing
+// through bf16 (y and residual_out are separate roundings of v and s).
 //
 // Bound by memory: with a residual and y, 2+2 bytes in and 2+2+1 out per
 // element, a few operations each.  A row has to be known before its first
@@ -118,9 +118,11 @@ __device__ __forceinline__ void finish_chunk(const AddNormParams& p, int64_t t, 
       widen(Chunk{__ldg(w), __ldg(w + 1)}, v);
     }
 #pragma unroll
-    for (int j = 0; j < kElems; ++j) v[j] *= s[j] * rms;
-    if (p.y) store_bf16(p.y + at * 2, v);
+    for (int j = 0; j < kElems; ++j) v[j] *= s[j];
   }
+  // v here is s * weight, still without rms: a block's codes do not depend on
+  // its common factor, and every rounding left out is fewer codes that fall to
+  // the wrong side.
   float amax = 0.0f;
 #pragma unroll
   for (int j = 0; j < kElems; ++j) amax = fmaxf(amax, fabsf(v[j]));
@@ -128,8 +130,9 @@ __device__ __forceinline__ void finish_chunk(const AddNormParams& p, int64_t t, 
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-  const float scale = amax > 0.0f ? __fdiv_rn(fmaxf(amax, kTinyAmax), 448.0f) : 1.0f;
-  const float inv = __fdiv_rn(1.0f, scale);
+  const float top = amax * rms;
+  const float scale = amax > 0.0f ? __fdiv_rn(fmaxf(top, kTinyAmax), 448.0f) : 1.0f;
+  const float inv = top >= kTinyAmax ? __fdiv_rn(448.0f, amax) : __fdiv_rn(rms, scale);
   if (act) {
     uint4 q;
     uint32_t* o = &q.x;
@@ -140,6 +143,11 @@ __device__ __forceinline__ void finish_chunk(const AddNormParams& p, int64_t t, 
              (fp8q::e4m3x2(__fmul_rn(e[2], inv), __fmul_rn(e[3], inv)) << 16);
     }
     ptx::st_v4(p.xq + at, q);
+    if (p.y) {
+#pragma unroll
+      for (int j = 0; j < kElems; ++j) v[j] *= rms;
+      store_bf16(p.y + at * 2, v);
+    }
     if ((c & 7) == 0) p.x_scales[t * (p.H / MOE_FP8_BLOCK) + (c >> 3)] = scale;
   }
 }
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(1024) add_norm_fp8_kernel(AddNormParams p, int
     // Two buffers in turn: a warp that is a round ahead cannot overwrite sums
     // still being read, because a barrier lies between.
     sum = row_sum(sum, s_sum[n & 1]);
-    finish_chunk<kResidual, kWeightF32>(p, t, c, c < chunks && t < p.T, s, rsqrtf(fmaf(sum, inv_h, p.eps)));
+    finish_chunk<kResidual, kWeightF32>(p, t, c, c < chunks && t < p.T, s, __frsqrt_rn(fmaf(sum, inv_h, p.eps)));
   }
 }
 
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(1024) add_norm_fp8_long_kernel(AddNormParams p
       sum = square_sum(s, sum);
     }
     sum = row_sum(sum, s_sum[n & 1]);
-    const float rms = rsqrtf(fmaf(sum, inv_h, p.eps));
+    const float rms = __frsqrt_rn(fmaf(sum, inv_h, p.eps));
     for (int c = threadIdx.x; c < chunks_up; c += blockDim.x) {
       if (c < chunks) load(c);
       finish_chunk<kResidual, kWeightF32>(p, t, c, c < chunks, s, rms);

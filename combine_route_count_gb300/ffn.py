@@ -25,32 +25,48 @@ _F32 = (torch.float32,)
 _FLOAT = (torch.bfloat16, torch.float32)
 
 
+# The calls are often launch-bound, so their checks are kept to a few attribute
+# reads per tensor: the raw stream and device queries below are what
+# torch.cuda.current_stream() and current_device() return, without the objects.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _wrong(what: str) -> "moe.MoEError":
     return moe.MoEError(moe.MOE_EINVAL, what)
 
 
-def _arg(name: str, t: Any, dtypes: tuple, shape: tuple, device: Any) -> int:
+def _arg(name: str, t: torch.Tensor, dtypes: tuple, shape: tuple, device: int) -> int:
     """The tensor's address; raises unless it is what the call takes."""
-    if not isinstance(t, torch.Tensor):
-        raise _wrong(f"{name} must be a tensor")
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        raise _wrong(f"{name} must be a tensor") from None
     if t.dtype not in dtypes:
         raise _wrong(f"{name} has type {t.dtype}, must be {' or '.join(map(str, dtypes))}")
     if t.shape != shape:
         raise _wrong(f"{name} has shape {tuple(t.shape)}, must be {tuple(shape)}")
     if not t.is_contiguous():
         raise _wrong(f"{name} must be contiguous")
-    if t.device != device:
-        raise _wrong(f"{name} is on {t.device}, must be on {device}")
-    return t.data_ptr()
+    raise _wrong(f"{name} is on {t.device}, must be on cuda:{device}")
 
 
-def _device(name: str, t: Any, ndim: int) -> Any:
+def _device(name: str, t: Any, ndim: int) -> int:
     """The device the call runs on: the first tensor's, which must be current."""
     if not isinstance(t, torch.Tensor) or t.dim() != ndim:
         raise _wrong(f"{name} must be a tensor of {ndim} dimensions")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _current_device():
         raise _wrong(f"{name} must be on the current CUDA device")
-    return t.device
+    return t.get_device()
+
+
+def _stream(stream: Any, device: int) -> int:
+    return _raw_stream(device) if stream is None else moe._stream(stream)
+
+
+def _lib() -> Any:
+    return moe._lib or moe.load_library()
 
 
 def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, xq: torch.Tensor, x_scales: torch.Tensor, *,
@@ -78,8 +94,10 @@ def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, xq: torch.Tensor, x_
         po = _arg("residual_out", residual_out, _BF16, (T, H), dev)
     if y is not None:
         py = _arg("y", y, _BF16, (T, H), dev)
-    moe.moe_add_rms_norm_fp8(px, pr, pw, moe.MOE_TYPE_F32 if weight.dtype == torch.float32 else moe.MOE_TYPE_BF16,
-                             T, H, eps, po, py, pq, ps, stream)
+    rc = _lib().moe_add_rms_norm_fp8(px, pr, pw, weight.dtype == torch.float32, T, H, eps, po, py, pq, ps,
+                                     _stream(stream, dev))
+    if rc:
+        raise moe.MoEError(rc, "moe_add_rms_norm_fp8")
 
 
 def _blocks(n: int) -> int:
@@ -115,8 +133,10 @@ def expert_gemm_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
     K % 16 == 0, N % 8 == 0."""
     dev, rows, K, N, E, pa, ps, pw, pv, po, pt = _product_args(a, a_scales, w, w_scales, expert_offsets, status)
     pout = _arg("out", out, _FLOAT, (rows, N), dev)
-    moe.moe_expert_gemm_fp8(pa, ps, rows, K, pw, pv, N, E, po, pout,
-                            moe.MOE_TYPE_F32 if out.dtype == torch.float32 else moe.MOE_TYPE_BF16, pt, stream)
+    rc = _lib().moe_expert_gemm_fp8(pa, ps, rows, K, pw, pv, N, E, po, pout, out.dtype == torch.float32, pt,
+                                    _stream(stream, dev))
+    if rc:
+        raise moe.MoEError(rc, "moe_expert_gemm_fp8")
 
 
 def expert_glu_fp8(a: torch.Tensor, a_scales: torch.Tensor, w13: torch.Tensor, w13_scales: torch.Tensor,
@@ -132,7 +152,9 @@ def expert_glu_fp8(a: torch.Tensor, a_scales: torch.Tensor, w13: torch.Tensor, w
     I = N // 2
     ph = _arg("hq", hq, _FP8, (rows, I), dev)
     pg = _arg("h_scales", h_scales, _F32, (rows, I // BLOCK), dev)
-    moe.moe_expert_glu_fp8(pa, ps, rows, H, pw, pv, I, E, po, ph, pg, pt, stream)
+    rc = _lib().moe_expert_glu_fp8(pa, ps, rows, H, pw, pv, I, E, po, ph, pg, pt, _stream(stream, dev))
+    if rc:
+        raise moe.MoEError(rc, "moe_expert_glu_fp8")
 
 
 class DecodeLayer:
@@ -146,7 +168,8 @@ class DecodeLayer:
 
     def __init__(self, max_tokens: int, top_k: int, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
                  w2_scales: torch.Tensor):
-        self.device = _device("w13", w13, 3)
+        dev = _device("w13", w13, 3)
+        self.device = w13.device
         if not isinstance(w2, torch.Tensor) or w2.dim() != 3:
             raise _wrong("w2 must be a tensor of 3 dimensions")
         self.E, self.H, self.I = w2.shape
@@ -156,25 +179,30 @@ class DecodeLayer:
                 ("w13_scales", w13_scales, _F32, (self.E, _blocks(2 * self.I), _blocks(self.H))), \
                 ("w2", w2, _FP8, (self.E, self.H, self.I)), \
                 ("w2_scales", w2_scales, _F32, (self.E, _blocks(self.H), _blocks(self.I)))
-        self._pointers = tuple(_arg(*s, self.device) for s in sizes)
-        nbytes = moe.moe_decode_workspace_bytes(moe.make_config(max_tokens, self.H, top_k, self.E, 1), self.I)
+        self._pointers = tuple(_arg(*s, dev) for s in sizes)
+        self._config = moe.make_config(max_tokens, self.H, top_k, self.E, 1)
+        nbytes = moe.moe_decode_workspace_bytes(self._config, self.I)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._own = (self.status.data_ptr(), self.workspace.data_ptr(), self.workspace.numel())
 
     def forward(self, xq: torch.Tensor, x_scales: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                 out: torch.Tensor, stream: Any = None) -> None:
         """out[t] = sum_k topk_w[t,k] * expert(topk_idx[t,k])(x[t]); out bf16 [T, H], T <= max_tokens."""
         dev = _device("xq", xq, 2)
         T, H, K = xq.shape[0], self.H, self.K
-        if T > self.max_tokens or dev != self.device:
-            raise _wrong(f"xq has {T} tokens on {dev}, must have at most {self.max_tokens} on {self.device}")
+        if T > self.max_tokens or dev != self.device.index:
+            raise _wrong(f"xq has {T} tokens on cuda:{dev}, must have at most {self.max_tokens} on {self.device}")
         px = _arg("xq", xq, _FP8, (T, H), dev)
         ps = _arg("x_scales", x_scales, _F32, (T, H // BLOCK), dev)
         pi = _arg("topk_idx", topk_idx, (torch.int32,), (T, K), dev)
         pw = _arg("topk_w", topk_w, _F32, (T, K), dev)
         po = _arg("out", out, _BF16, (T, H), dev)
-        moe.moe_decode_layer_fp8(moe.make_config(T, H, K, self.E, 1), self.I, px, ps, pi, pw, *self._pointers, po,
-                                 self.status, self.workspace, self.workspace.numel(), stream)
+        self._config.num_tokens = T
+        rc = _lib().moe_decode_layer_fp8(self._config, self.I, px, ps, pi, pw, *self._pointers, po, *self._own,
+                                         _stream(stream, dev))
+        if rc:
+            raise moe.MoEError(rc, "moe_decode_layer_fp8")
 
     def get_error(self, stream: Any = None) -> int:
         """Waits for the stream; the device status of the last call (MOE_OK or MOE_EROUTE)."""

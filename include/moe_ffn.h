@@ -18,8 +18,9 @@
  *   q = E4M3(v * inv), round to nearest even, saturating.
  * For blocks that hold a bf16 value of at least 2^-100 this is the rule of
  * moe_dispatch_send_fp8; below, the floor keeps 1 / scale finite.  A row that
- * holds an infinity or a NaN, or whose squares leave the float32 range, has no
- * defined outputs; other rows are not touched by it.
+ * holds an infinity or a NaN, or whose squares (in moe_add_rms_norm_fp8 also
+ * s * weight) leave the float32 range, has no defined outputs; other rows are
+ * not touched by it.
  *
  * Conventions as in moe.h: device pointers owned by the caller, no device
  * allocation, no host synchronisation, `stream` is a cudaStream_t, argument
