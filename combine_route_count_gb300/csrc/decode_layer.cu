@@ -1,32 +1,43 @@
-// A whole expert layer for a few tokens (T <= 64) in two kernels, weights and
-// activations block-scaled E4M3:
+// Products of few rows with many weights, on the 5th-generation tensor core:
 //
 //   decode_glu   h[t,k] = SiLU(W1[e] x[t]) * (W3[e] x[t]),  e = topk_idx[t,k],
 //                quantised by blocks of 128 like every payload here
-//   decode_down  out[t] = bf16( sum_k topk_w[t,k] * W2[e] h[t,k] )
+//   few_rows     decode: out[t] = bf16( sum_k topk_w[t,k] * W2[e] h[t,k] )
+//                dense:  out[i] = W a[i], one weight matrix, up to 64 rows
 //
-// Bound by memory: the chosen experts' weights are read once (3 * I * H bytes
-// each) for a handful of tokens, so what counts is to keep many weight bytes
-// in flight all the time and to start early.  The weights go straight from
-// global memory into the fragments of mma.sync (16 weight rows x 8 tokens,
-// K = 32): a lane's 16-byte loads hold the K elements of its row in an order
-// that is not the fragment's, but the token operand is loaded with the same
-// order, and a sum does not depend on it.  Shared memory, tensor memory and
-// their barriers would only add to the way; the arithmetic (16 x 8 tile of
-// which one or two token columns are real) stays far below the load time.
+// decode_glu and the decode form of few_rows are a whole expert layer for up
+// to 64 tokens in two kernels (moe_decode_layer_fp8); the dense form is
+// moe_expert_gemm_fp8's for a handful of rows.
 //
-// Each 128 of K is summed by four matrix instructions from zero and then added
-// with its two scales to float32 accumulators.
+// Bound by memory: the weights are read once for a few rows, so what counts is
+// to keep many weight bytes in flight on every SM and to start early.  Weight
+// tiles of 128 rows x 128 of K arrive by tiled TMA in a ring of stages, with
+// the token rows' block beside them, and are the 128-row operand of tcgen05.mma;
+// the tokens are its 16, 32 or 64 columns (kN).  A thread of the four epilogue
+// warps owns one weight row and a column per token; each K block's product is
+// scaled and added to its float32 registers as in expert_gemm.cu.  An earlier
+// form loaded the weights straight into mma.sync fragments: its register
+// stages kept too little in flight (one token, 8 of 256 experts, H 7168, inner
+// 2048: 95 us, 45 % of DRAM busy).
+//
+// decode_glu multiplies every token with every expert that has any row (the
+// columns of tokens that did not choose it are dropped), so x needs no
+// gathering; few_rows reads the rows of h, which decode_glu writes ordered by
+// (expert, token).
+//
+// Spread over the SMs: decode_glu's unit is 128 columns of one expert's h; few
+// units are split along K over a cluster.  few_rows gives 128 columns of out to
+// a cluster, which shares that tile's (expert, K block) items; partial sums are
+// exchanged through distributed shared memory and added in rank order.  Sums
+// have a fixed order: same inputs, same bits.
 //
 // Routing: every CTA sorts the T*K (token, expert) pairs itself (a bit per
 // token in a mask per expert; a pair's place among its expert's rows is the
-// number of lower bits set), about 2 us less than a kernel of its own.
-// Malformed routing is seen by every CTA alike: nothing is written but the
-// status.
+// number of lower bits set).  Malformed routing is seen by every CTA alike:
+// nothing is written but the status.
 //
-// decode_down is launched while decode_glu runs and brings in its first
-// weights before it waits for h.  Sums have a fixed order: same inputs, same
-// bits.
+// few_rows is launched while decode_glu runs and brings in its first weights
+// before it waits for h.  Waits are bounded (2 s) and report MOE_ETIMEDOUT.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -34,61 +45,106 @@
 #include "ffn_kernels.cuh"
 #include "fp8_quant.cuh"
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxPairs = MOE_DECODE_MAX_TOKENS * MOE_MAX_TOP_K;
 constexpr int kBlock = MOE_FP8_BLOCK;
+constexpr int kTileBytes = 128 * kBlock;  // 128 weight rows x 128 of K
+constexpr int kTmaWarp = 4, kMmaWarp = 5, kThreads = 192;
+constexpr int kMaxStages = 8;
 
-// The layer's routing, built by every CTA.  Rows are the pairs ordered by
-// (expert, token); expert number a is the a-th that has any.
+// ---- clusters ------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of CTA `rank`'s shared memory, at the place that `p` has in this CTA's.
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// ---- routing -------------------------------------------------------------------
+// Rows are the pairs ordered by (expert, token); expert number a is the a-th
+// that has any.
 struct Routing {
-  uint32_t mask[MOE_MAX_EXPERTS][2];  // tokens of each expert
-  int16_t active[kMaxPairs];          // the experts that have rows, ascending
-  int16_t first[kMaxPairs + 1];       // their first rows
-  int16_t row_of[MOE_MAX_EXPERTS];    // first row of each expert
-  uint8_t token[kMaxPairs];           // of each row
-  float weight[kMaxPairs];            // topk_w of each row
+  int32_t* active;   // the experts that have rows, ascending
+  int32_t* first;    // their first rows, then the number of rows
+  uint64_t* tokens;  // the tokens of expert number a, one bit each
+  int32_t* token;    // of each row
+  float* weight;     // topk_w of each row
+  // scratch, free after build_routing
+  uint32_t* mask;    // [E][2]
+  int32_t* row_of;   // [E]
+};
+struct RoutingShared {
   int32_t warp_active[32], warp_rows[32];
   int32_t n_active, bad;
 };
 
-__device__ __forceinline__ void build_routing(Routing& r, const DecodeParams& p) {
+__host__ __device__ inline int max_active(int pairs, int E) { return pairs < E ? pairs : E; }
+__host__ __device__ inline int routing_bytes(int pairs, int E) {
+  const int a = max_active(pairs, E);
+  return (a * 8 + a * 4 + (a + 1) * 4 + pairs * 8 + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, int pairs, int E) {
+  const int a = max_active(pairs, E);
+  Routing r;
+  r.tokens = reinterpret_cast<uint64_t*>(smem);
+  r.active = reinterpret_cast<int32_t*>(r.tokens + a);
+  r.first = r.active + a;
+  r.token = r.first + a + 1;
+  r.weight = reinterpret_cast<float*>(r.token + pairs);
+  r.mask = reinterpret_cast<uint32_t*>(scratch);
+  r.row_of = reinterpret_cast<int32_t*>(r.mask + 2 * E);
+  return r;
+}
+
+// Called by the whole CTA; ends with a barrier.
+__device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s, const DecodeParams& p) {
   const int pairs = p.T * p.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) r.bad = 0;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) r.mask[e][0] = r.mask[e][1] = 0;
+  if (threadIdx.x == 0) s.bad = 0;
+  for (int e = threadIdx.x; e < 2 * p.E; e += kThreads) r.mask[e] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += kThreads) {
     const int e = p.topk_idx[i], t = i / p.K;
     if (e < 0 || e >= p.E) {
-      r.bad = 1;
+      s.bad = 1;
     } else {
       const uint32_t bit = 1u << (t & 31);
-      if (atomicOr(&r.mask[e][t >> 5], bit) & bit) r.bad = 1;  // repeated within the token
+      if (atomicOr(&r.mask[2 * e + (t >> 5)], bit) & bit) s.bad = 1;  // repeated within the token
     }
   }
   __syncthreads();
-  if (r.bad) return;  // the same for the whole CTA
+  if (s.bad) return;  // the same for the whole CTA
   const int chunks = (p.E + 31) / 32;
-  for (int c = warp; c < chunks; c += kWarps) {
+  for (int c = warp; c < chunks; c += kThreads / 32) {
     const int e = c * 32 + lane;
-    const int n = e < p.E ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0;
+    const int n = e < p.E ? __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1]) : 0;
     const int rows = __reduce_add_sync(0xffffffffu, n);
     const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
     if (lane == 0) {
-      r.warp_active[c] = __popc(some);
-      r.warp_rows[c] = rows;
+      s.warp_active[c] = __popc(some);
+      s.warp_rows[c] = rows;
     }
   }
   __syncthreads();
-  for (int c = warp; c < chunks; c += kWarps) {
+  for (int c = warp; c < chunks; c += kThreads / 32) {
     const int e = c * 32 + lane;
-    const int n = e < p.E ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0;
-    const int before = lane < c ? r.warp_active[lane] : 0, before_rows = lane < c ? r.warp_rows[lane] : 0;
-    const int base = __reduce_add_sync(0xffffffffu, before);
-    const int base_row = __reduce_add_sync(0xffffffffu, before_rows);
+    const uint32_t low = e < p.E ? r.mask[2 * e] : 0, high = e < p.E ? r.mask[2 * e + 1] : 0;
+    const int n = __popc(low) + __popc(high);
+    const int base = __reduce_add_sync(0xffffffffu, lane < c ? s.warp_active[lane] : 0);
+    const int base_row = __reduce_add_sync(0xffffffffu, lane < c ? s.warp_rows[lane] : 0);
     const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
     int sum = n;
 #pragma unroll
@@ -98,323 +154,543 @@ __device__ __forceinline__ void build_routing(Routing& r, const DecodeParams& p)
     }
     if (n > 0) {
       const int a = base + __popc(some & ((1u << lane) - 1));
-      r.active[a] = static_cast<int16_t>(e);
-      r.first[a] = r.row_of[e] = static_cast<int16_t>(base_row + sum - n);
+      r.active[a] = e;
+      r.first[a] = r.row_of[e] = base_row + sum - n;
+      r.tokens[a] = static_cast<uint64_t>(high) << 32 | low;
     }
     if (c == chunks - 1 && lane == 0) {
-      const int n_active = base + __popc(some);
-      r.n_active = n_active;
-      r.first[n_active] = static_cast<int16_t>(pairs);
+      s.n_active = base + __popc(some);
+      r.first[s.n_active] = pairs;
     }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += kThreads) {
     const int e = p.topk_idx[i], t = i / p.K;
-    const int low = t < 32 ? __popc(r.mask[e][0] & ((1u << t) - 1))
-                           : __popc(r.mask[e][0]) + __popc(r.mask[e][1] & ((1u << (t - 32)) - 1));
-    const int row = r.row_of[e] + low;
-    r.token[row] = static_cast<uint8_t>(t);
+    const uint64_t mask = static_cast<uint64_t>(r.mask[2 * e + 1]) << 32 | r.mask[2 * e];
+    const int row = r.row_of[e] + __popcll(mask & ((1ull << t) - 1));
+    r.token[row] = t;
     r.weight[row] = p.topk_w[i];
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ uint4 ldg_v4(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-
-// Two 16-byte pieces of one row's 128 bytes of K: bytes [16 t, +16) and [64 + 16 t, +16).
-struct Piece {
-  uint4 a, b;
+// ---- what the kernels share ---------------------------------------------------
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t amax_ready[2];
+  uint64_t drained;
+  uint32_t tmem;
+  int gave_up;
 };
-__device__ __forceinline__ uint32_t word(const Piece& f, int i) {
-  const uint32_t w[8] = {f.a.x, f.a.y, f.a.z, f.a.w, f.b.x, f.b.y, f.b.z, f.b.w};
-  return w[i];
-}
-__device__ __forceinline__ Piece load_weights(const uint8_t* p) {
-  return Piece{ptx::ld_stream_v4(p), ptx::ld_stream_v4(p + 64)};
+
+__device__ __forceinline__ void init_barriers(Barriers& b, int stages) {
+  for (int i = 0; i < stages; ++i) {
+    ptx::mbar_init(&b.full[i], 1);
+    ptx::mbar_init(&b.empty[i], 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    ptx::mbar_init(&b.acc_full[i], 1);
+    ptx::mbar_init(&b.acc_empty[i], 4);
+    ptx::mbar_init(&b.amax_ready[i], 4);
+  }
+  ptx::mbar_init(&b.drained, 1);
+  ptx::mbar_fence_init();
+  b.gave_up = 0;
 }
 
-// d[0..3] = (rows g and g + 8) x (tokens 2t, 2t + 1), summed over 128 of K.
-__device__ __forceinline__ void mma_128(float* d, const Piece& lo, const Piece& hi, const Piece& x) {
-  d[0] = d[1] = d[2] = d[3] = 0.0f;
+// The scratch that build_routing wrote lies where TMA will write next.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// Waits (bounded) for the loads of iterations [it - stages, it) that may still be in flight.
+__device__ __forceinline__ void drain_loads(Barriers& b, uint32_t it, uint32_t stages) {
+  const unsigned long long start = tc::now_ns();
+  for (uint32_t j = it > stages ? it - stages : 0; j < it; ++j)
+    while (!ptx::mbar_try_wait(&b.full[j % stages], (j / stages) & 1) && tc::now_ns() - start < tc::kWaitLimitNs) {
+    }
+}
+
+// The matrix warp's part: kTiles products of 128 rows x kN columns for each of n K blocks.
+template <int kN, int kTiles>
+__device__ __forceinline__ void run_mma(Barriers& b, const uint8_t* ring, int stage_bytes, uint32_t stages, uint32_t n,
+                                        uint32_t& it) {
+  constexpr uint32_t kInstr = tc::instr_desc_e4m3(128, kN);
+  for (uint32_t end = it + n; it < end; ++it) {
+    const uint32_t st = it % stages, buf = it & 1;
+    if (it >= 2 && !tc::wait(&b.acc_empty[buf], (it / 2 - 1) & 1, &b.gave_up)) return;
+    if (!tc::wait(&b.full[st], (it / stages) & 1, &b.gave_up)) return;
+    tc::fence_after();
+    const uint64_t w = tc::smem_desc(ring + st * stage_bytes);
+    const uint64_t x = tc::smem_desc(ring + st * stage_bytes + kTiles * kTileBytes);
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(word(lo, 2 * s)), "r"(word(hi, 2 * s)), "r"(word(lo, 2 * s + 1)), "r"(word(hi, 2 * s + 1)),
-          "r"(word(x, 2 * s)), "r"(word(x, 2 * s + 1)));
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int k = 0; k < kBlock / 32; ++k)
+        tc::mma_e4m3(b.tmem + (buf * kTiles + m) * kN, w + m * (kTileBytes >> 4) + 2 * k, x + 2 * k, kInstr, k > 0);
+    tc::commit(&b.empty[st]);
+    tc::commit(&b.acc_full[buf]);
+  }
+}
+
+__device__ __forceinline__ void finish_mma(Barriers& b) {  // nothing in flight when the tensor memory is freed
+  tc::commit(&b.drained);
+  tc::wait(&b.drained, 0, &b.gave_up);
+}
+
+__host__ __device__ constexpr uint32_t tmem_columns(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+
+// acc[c] += product[c] * scale[c] * f for the kN columns of one tensor-memory
+// tile; scale in shared memory.
+template <int kN>
+__device__ __forceinline__ void add_scaled(uint32_t addr, const float* scale, float f, unsigned long long* acc) {
+  const unsigned long long ff = tc::pack2(f, f);
+#pragma unroll
+  for (int c = 0; c < kN; c += 16) {
+    uint32_t v[16];
+    tc::tmem_load_16(addr + c, v);
+    tc::wait_loads();
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(scale + c + j);
+      unsigned long long* a = acc + (c + j) / 2;
+      a[0] = tc::fma2(tc::pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                      tc::mul2(tc::pack2(s.x, s.y), ff), a[0]);
+      a[1] = tc::fma2(tc::pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])),
+                      tc::mul2(tc::pack2(s.z, s.w), ff), a[1]);
+    }
+  }
 }
 
 // ---- first kernel -----------------------------------------------------------
-// Unit: (expert with rows, block of 128 columns of h) = 128 gate and 128 up
-// rows of w13; a warp has 16 of each, as two 16-row operands of 8 gate rows
-// (fragment rows 0-7) and their 8 up rows (8-15), so that a lane ends up with
-// both halves of the same h.  kTiles token tiles of 8 cover T.
-template <int kTiles, int kDepth>
-__global__ void __launch_bounds__(kThreads, kTiles <= 2 ? 2 : 1) decode_glu_kernel(DecodeParams p) {
-  __shared__ Routing r;
-  __shared__ float s_amax[kWarps][kTiles * 8];
-  ptx::wait_prerequisites();
-  // From here on everything earlier in the stream is done, which
-  // decode_down's early reads of topk_idx, topk_w and the weights rely on.
-  ptx::launch_dependents();
-  build_routing(r, p);
-  if (r.bad) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int jb = p.I / kBlock, kb_n = p.H / kBlock;
-  const int units = r.n_active * jb;
-
-  Piece buf[kDepth][2][2];  // [stage][operand][gate, up]
-  const uint8_t* wp;        // this lane's gate row of operand 0
-  const int64_t up_off = static_cast<int64_t>(p.I) * p.H, m_off = static_cast<int64_t>(8) * p.H;
-  auto point_at = [&](int u) {
-    const int a = u / jb, j = u - a * jb;
-    wp = p.w13 + (static_cast<int64_t>(r.active[a]) * 2 * p.I + j * kBlock + warp * 16 + g) * p.H + q * 16;
-  };
-  auto fetch = [&](Piece (*f)[2], int kb) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const uint8_t* at = wp + m * m_off + kb * kBlock;
-      f[m][0] = load_weights(at);
-      f[m][1] = load_weights(at + up_off);
-    }
-  };
-  int u = blockIdx.x;
-  if (u < units) {
-    point_at(u);
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-      if (d < kb_n) fetch(buf[d], d);
+// Unit: (expert number a, block j of 128 columns of h).  kN columns: token t is
+// column t.
+template <int kN>
+__global__ void __launch_bounds__(kThreads, 1) decode_glu_kernel(const __grid_constant__ DecodeParams p,
+                                                                 uint32_t stages, uint32_t ranks) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ Barriers b;
+  __shared__ RoutingShared rs;
+  __shared__ __align__(16) float s_scale[4][2][kN];
+  __shared__ float s_amax[2][4][kN];
+  constexpr int kStageBytes = 2 * kTileBytes + kN * kBlock;
+  constexpr uint32_t kColumns = tmem_columns(4 * kN);
+  uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Routing r = routing_at(ring + stages * kStageBytes, ring, p.T * p.K, p.E);
+  if (threadIdx.x == 0) init_barriers(b, stages);
+  if (warp == kMmaWarp) tc::tmem_alloc(&b.tmem, kColumns);
+  if (threadIdx.x == kTmaWarp * 32) {
+    tc::tma_prefetch_map(&p.w13_map);
+    tc::tma_prefetch_map(&p.x_map);
   }
-  for (; u < units; u += gridDim.x) {
-    const int a = u / jb, j = u - a * jb, e = r.active[a];
-    const int row0 = r.first[a], n = r.first[a + 1] - row0;
-    const float* sg = p.w13_scales + (static_cast<int64_t>(e) * 2 * jb + j) * kb_n;
-    const float* su = sg + static_cast<int64_t>(jb) * kb_n;
-    // Token rows of this lane: column g of each tile as operand, columns 2q
-    // and 2q + 1 as results.  Columns past the expert's rows repeat row 0.
-    const uint8_t* x[kTiles];
-    const float* sx[kTiles][2];
+  tc::fence_before();
+  __syncthreads();
+  ptx::wait_prerequisites();
+  // From here on everything earlier in the stream is done, which few_rows'
+  // early reads of topk_idx, topk_w and the weights rely on.  This CTA has its
+  // tensor memory: CTAs of few_rows, which wait for this grid while they hold
+  // theirs, cannot keep it from it.
+  ptx::launch_dependents();
+  build_routing(r, rs, p);
+  tc::fence_after();
+  const int jb = p.I / kBlock, kb_all = p.H / kBlock;
+  const int units = rs.bad ? 0 : rs.n_active * jb;
+  const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+  const int kb0 = static_cast<int>(rank * kb_all / ranks), kb_n = static_cast<int>((rank + 1) * kb_all / ranks) - kb0;
+  const int step = static_cast<int>(gridDim.x / ranks), u0 = static_cast<int>(blockIdx.x / ranks);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = rs.bad ? MOE_EROUTE : MOE_OK;
+
+  // A cluster of several CTAs has one unit, whose sums meet below.
+  unsigned long long gate[kN / 2], up[kN / 2];
+  bool ok = true;
+  int round = 0;
+  auto finish = [&](int u) -> bool {  // epilogue warps: h from the sums, quantised
+    const int a = u / jb, j = u - a * jb;
+    const uint64_t tokens = r.tokens[a];
+    float (*amax)[kN] = s_amax[round & 1];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int c = i * 8 + g, c0 = i * 8 + 2 * q;
-      x[i] = p.xq + static_cast<int64_t>(r.token[row0 + (c < n ? c : 0)]) * p.H + q * 16;
-      sx[i][0] = p.x_scales + static_cast<int64_t>(r.token[row0 + (c0 < n ? c0 : 0)]) * kb_n;
-      sx[i][1] = p.x_scales + static_cast<int64_t>(r.token[row0 + (c0 + 1 < n ? c0 + 1 : 0)]) * kb_n;
+    for (int t = 0; t < kN; ++t) {
+      float g = t & 1 ? tc::hi2(gate[t / 2]) : tc::lo2(gate[t / 2]);
+      const float v = t & 1 ? tc::hi2(up[t / 2]) : tc::lo2(up[t / 2]);
+      if (tokens >> t & 1) {
+        g = g / (1.0f + expf(-g)) * v;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(g)));
+        if (lane == 0) amax[warp][t] = __uint_as_float(top);
+      }
+      gate[t / 2] = t & 1 ? tc::pack2(tc::lo2(gate[t / 2]), g) : tc::pack2(g, tc::hi2(gate[t / 2]));
     }
-    float acc[kTiles][2][4];
+    // All four warps' largest values.  The two copies alternate, so a warp one
+    // unit ahead does not overwrite.
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&b.amax_ready[round & 1]);
+    const bool all = tc::wait(&b.amax_ready[round & 1], (round >> 1) & 1, &b.gave_up);
+    if (!__all_sync(0xffffffffu, all)) return false;
+    int row = r.first[a];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][m][k] = 0.0f;
-    for (int kb0 = 0; kb0 < kb_n; kb0 += kDepth) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int kb = kb0 + d;
-        if (kb < kb_n) {
-          const float fg = __ldg(sg + kb), fu = __ldg(su + kb);
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
-            if (i * 8 < n) {
-              const Piece xf = {ldg_v4(x[i] + kb * kBlock), ldg_v4(x[i] + kb * kBlock + 64)};
-              const float s0 = __ldg(sx[i][0] + kb), s1 = __ldg(sx[i][1] + kb);
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                float v[4];
-                mma_128(v, buf[d][m][0], buf[d][m][1], xf);
-                acc[i][m][0] = fmaf(v[0], s0 * fg, acc[i][m][0]);
-                acc[i][m][1] = fmaf(v[1], s1 * fg, acc[i][m][1]);
-                acc[i][m][2] = fmaf(v[2], s0 * fu, acc[i][m][2]);
-                acc[i][m][3] = fmaf(v[3], s1 * fu, acc[i][m][3]);
-              }
-            }
+    for (int t = 0; t < kN; ++t) {
+      if (tokens >> t & 1) {
+        const float top = fmaxf(fmaxf(amax[0][t], amax[1][t]), fmaxf(amax[2][t], amax[3][t]));
+        const float scale = top > 0.0f ? __fdiv_rn(fmaxf(top, kTinyAmax), 448.0f) : 1.0f;
+        const float h = t & 1 ? tc::hi2(gate[t / 2]) : tc::lo2(gate[t / 2]);
+        p.hq[static_cast<int64_t>(row) * p.I + j * kBlock + threadIdx.x] =
+            static_cast<uint8_t>(fp8q::e4m3x2(__fmul_rn(h, __fdiv_rn(1.0f, scale)), 0.0f));
+        if (threadIdx.x == 0) p.h_scales[static_cast<int64_t>(row) * jb + j] = scale;
+        ++row;
+      }
+    }
+    ++round;
+    return true;
+  };
+
+  if (warp == kTmaWarp) {
+    if (lane == 0 && u0 < units) {
+      fence_async_proxy();
+      uint32_t it = 0;
+      for (int u = u0; ok && u < units; u += step) {
+        const int a = u / jb, j = u - a * jb;
+        const int w0 = r.active[a] * 2 * p.I + j * kBlock;
+        for (int kb = 0; kb < kb_n; ++kb, ++it) {
+          const uint32_t st = it % stages;
+          if (it >= stages && !tc::wait(&b.empty[st], (it / stages - 1) & 1, &b.gave_up)) {
+            ok = false;
+            break;
           }
-          if (kb + kDepth < kb_n) fetch(buf[d], kb + kDepth);
+          uint8_t* to = ring + st * kStageBytes;
+          const int k = (kb0 + kb) * kBlock;
+          ptx::mbar_arrive_expect_tx(&b.full[st], kStageBytes);
+          tc::tma_load_2d(to, &p.w13_map, k, w0, &b.full[st]);
+          tc::tma_load_2d(to + kTileBytes, &p.w13_map, k, w0 + p.I, &b.full[st]);
+          tc::tma_load_2d(to + 2 * kTileBytes, &p.x_map, k, 0, &b.full[st]);
         }
       }
+      if (!ok) drain_loads(b, it, stages);
     }
-    if (u + gridDim.x < units) {  // the next unit's weights are on their way during the epilogue
-      point_at(u + gridDim.x);
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d)
-        if (d < kb_n) fetch(buf[d], d);
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int u = u0; u < units && !b.gave_up; u += step) run_mma<kN, 2>(b, ring, kStageBytes, stages, kb_n, it);
+      finish_mma(b);
     }
+  } else {
+    const uint32_t lanes = b.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    uint32_t it = 0;
+    for (int u = u0; ok && u < units; u += step) {
+      const int a = u / jb, j = u - a * jb;
+      const float* sg = p.w13_scales + (static_cast<int64_t>(r.active[a]) * 2 * jb + j) * kb_all + kb0;
+      const float* su = sg + static_cast<int64_t>(jb) * kb_all;
+      const float* sx = p.x_scales + kb0;
+      // The tokens' scales of the next K block are read a block ahead.
+      float next[(kN + 31) / 32], next_g, next_u;
+      auto read = [&](int kb) {
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      if (i * 8 < n) {
-        float top0 = 0.0f, top1 = 0.0f;
+        for (int i = 0; i < (kN + 31) / 32; ++i)
+          next[i] = lane + 32 * i < p.T ? sx[static_cast<int64_t>(lane + 32 * i) * kb_all + kb] : 0.0f;
+        next_g = sg[kb];
+        next_u = su[kb];
+      };
+      read(0);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float* v = acc[i][m];
-          v[0] = v[0] / (1.0f + expf(-v[0])) * v[2];
-          v[1] = v[1] / (1.0f + expf(-v[1])) * v[3];
-          top0 = fmaxf(top0, fabsf(v[0]));
-          top1 = fmaxf(top1, fabsf(v[1]));
+      for (int c = 0; c < kN / 2; ++c) gate[c] = up[c] = 0;
+      for (int kb = 0; kb < kb_n; ++kb, ++it) {
+        const uint32_t buf = it & 1;
+        float* scale = s_scale[warp][buf];
+#pragma unroll
+        for (int i = 0; i < (kN + 31) / 32; ++i)
+          if (lane + 32 * i < kN) scale[lane + 32 * i] = next[i];
+        const float fg = next_g, fu = next_u;
+        if (kb + 1 < kb_n) read(kb + 1);
+        ok = tc::wait(&b.acc_full[buf], (it / 2) & 1, &b.gave_up);
+        if (!__all_sync(0xffffffffu, ok)) {  // also orders the scales' stores before their loads
+          ok = false;
+          break;
         }
+        __syncwarp();
+        tc::fence_after();
+        add_scaled<kN>(lanes + buf * 2 * kN, scale, fg, gate);
+        add_scaled<kN>(lanes + (buf * 2 + 1) * kN, scale, fu, up);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
+      }
+      if (ok && ranks == 1) ok = finish(u);
+    }
+  }
+  if (ranks > 1) {
+    // The ring is free: every load has been consumed.  [gate, up][column][row]
+    float* part = reinterpret_cast<float*>(ring);
+    __syncthreads();
+    const bool mine = warp < 4 && ok && u0 < units;
+    if (mine) {
 #pragma unroll
-        for (int s = 4; s < 32; s <<= 1) {
-          top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, s));
-          top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, s));
-        }
-        if (g == 0) {
-          s_amax[warp][i * 8 + 2 * q] = top0;
-          s_amax[warp][i * 8 + 2 * q + 1] = top1;
+      for (int c = 0; c < kN; ++c) {
+        part[c * 128 + threadIdx.x] = c & 1 ? tc::hi2(gate[c / 2]) : tc::lo2(gate[c / 2]);
+        part[(kN + c) * 128 + threadIdx.x] = c & 1 ? tc::hi2(up[c / 2]) : tc::lo2(up[c / 2]);
+      }
+    }
+    cluster_sync();
+    if (mine && rank == 0) {
+      for (uint32_t q = 1; q < ranks; ++q) {
+#pragma unroll
+        for (int c = 0; c < kN; c += 2) {
+          const float* at = part + c * 128 + threadIdx.x;
+          gate[c / 2] = tc::add2(gate[c / 2], tc::pack2(ld_cluster(at, q), ld_cluster(at + 128, q)));
+          up[c / 2] = tc::add2(up[c / 2], tc::pack2(ld_cluster(at + kN * 128, q), ld_cluster(at + (kN + 1) * 128, q)));
         }
       }
+      finish(u0);
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = i * 8 + 2 * q + h;
-        if (c < n) {
-          float amax = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_amax[w][c]);
-          const float scale = amax > 0.0f ? __fdiv_rn(fmaxf(amax, kTinyAmax), 448.0f) : 1.0f;
-          const float inv = __fdiv_rn(1.0f, scale);
-          uint8_t* dst = p.hq + static_cast<int64_t>(row0 + c) * p.I + j * kBlock + warp * 16 + g;
-          const uint32_t two = fp8q::e4m3x2(__fmul_rn(acc[i][0][h], inv), __fmul_rn(acc[i][1][h], inv));
-          dst[0] = static_cast<uint8_t>(two);
-          dst[8] = static_cast<uint8_t>(two >> 8);
-          if (warp == 0 && g == 0) p.h_scales[static_cast<int64_t>(row0 + c) * jb + j] = scale;
-        }
-      }
-    }
-    __syncthreads();  // s_amax is read before the next unit writes it
+    cluster_sync();  // no CTA leaves while its shared memory is being read
   }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (threadIdx.x == 0 && b.gave_up) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
+  if (warp == kMmaWarp) tc::tmem_free(b.tmem, kColumns);
 }
 
 // ---- second kernel ------------------------------------------------------------
-// A CTA owns 16 columns of out, for every token and expert; its warps share
-// the (expert, K block) items evenly, each a contiguous range.  A warp adds
-// what an expert gives to its own copy of out's columns in shared memory,
-// token by token (an expert has a token at most once: no two lanes meet); the
-// copies are added in warp order at the end.
-template <int kTiles, int kDepth>
-__global__ void __launch_bounds__(kThreads, 2) decode_down_kernel(DecodeParams p) {
-  extern __shared__ float s_out[];  // [kWarps][T][16]
-  __shared__ Routing r;
-  build_routing(r, p);  // topk_idx and topk_w: see the first kernel's launch_dependents
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int kb_n = p.I / kBlock, n0 = blockIdx.x * 16;
-  if (r.bad) {
-    ptx::wait_prerequisites();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_EROUTE;
-    return;
+// A cluster owns 128 columns of out.  Its CTAs share the (expert, K block)
+// items, each a contiguous range; what an expert gives to token t is added to
+// the CTA's s_out[t][column] when the CTA's part of that expert is complete
+// (dense: one expert, row i is token i with weight 1).
+template <int kN, bool kDense>
+__global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(const __grid_constant__ DecodeParams p, uint32_t stages,
+                                                            uint32_t ranks) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ Barriers b;
+  __shared__ RoutingShared rs;
+  __shared__ __align__(16) float s_scale[4][2][kN];
+  constexpr int kStageBytes = kTileBytes + kN * kBlock;
+  constexpr uint32_t kColumns = tmem_columns(2 * kN);
+  uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
+  float* s_out = reinterpret_cast<float*>(ring + stages * kStageBytes);  // [T][128]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Routing r = {};
+  if (threadIdx.x == 0) init_barriers(b, stages);
+  if (warp == kMmaWarp) tc::tmem_alloc(&b.tmem, kColumns);
+  if (threadIdx.x == kTmaWarp * 32) {
+    tc::tma_prefetch_map(&p.w2_map);
+    tc::tma_prefetch_map(&p.h_map);
   }
-  const int items = r.n_active * kb_n;
-  const int end = static_cast<int>(static_cast<int64_t>(items) * (warp + 1) / kWarps);
-  int it = static_cast<int>(static_cast<int64_t>(items) * warp / kWarps);
-  // Where the next item to fetch lies.
-  int fa = it / kb_n, fk = it - fa * kb_n, fetched = it;
-  Piece buf[kDepth][2];
-  auto fetch = [&](Piece* f) {
-    const uint8_t* w =
-        p.w2 + (static_cast<int64_t>(r.active[fa]) * p.H + n0 + g) * p.I + fk * kBlock + q * 16;
-    f[0] = load_weights(w);
-    f[1] = load_weights(w + static_cast<int64_t>(8) * p.I);
-    ++fetched;
-    if (++fk == kb_n) fk = 0, ++fa;
-  };
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d)
-    if (fetched < end) fetch(buf[d]);
-  float* mine = s_out + warp * p.T * 16;
-  for (int i = lane; i < p.T * 16; i += 32) mine[i] = 0.0f;
-  __syncwarp();
-  ptx::wait_prerequisites();  // hq and h_scales
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
+  tc::fence_before();
+  if (kDense) {
+    if (threadIdx.x == 0) rs.bad = 0, rs.n_active = 1;
+    __syncthreads();
+  } else {
+    r = routing_at(reinterpret_cast<uint8_t*>(s_out + p.T * 128), ring, p.T * p.K, p.E);
+    build_routing(r, rs, p);  // topk_idx and topk_w: see the first kernel's launch_dependents
+  }
+  tc::fence_after();
+  const int tile = static_cast<int>(blockIdx.x / ranks);
+  const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+  const int kb_n = p.h_blocks;
+  const int items = rs.bad ? 0 : rs.n_active * kb_n;
+  const int it0 = static_cast<int>(static_cast<int64_t>(items) * rank / ranks);
+  const int n = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / ranks) - it0;
+  bool ok = true;
 
-  int a = it / kb_n, kb = it - a * kb_n;
-  float acc[kTiles][4];
-#pragma unroll
-  for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-  while (it < end) {
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      if (it < end) {
-        const int row0 = r.first[a], n = r.first[a + 1] - row0;
-        const float fw = __ldg(p.w2_scales + (static_cast<int64_t>(r.active[a]) * (p.H / kBlock) + n0 / kBlock) * kb_n +
-                               kb);
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          if (i * 8 < n) {
-            const int c = i * 8 + g, c0 = i * 8 + 2 * q;
-            const uint8_t* h = p.hq + static_cast<int64_t>(row0 + (c < n ? c : 0)) * p.I + kb * kBlock + q * 16;
-            const Piece hf = {ld_v4(h), ld_v4(h + 64)};
-            const float s0 = ld_f32(p.h_scales + static_cast<int64_t>(row0 + (c0 < n ? c0 : 0)) * kb_n + kb);
-            const float s1 = ld_f32(p.h_scales + static_cast<int64_t>(row0 + (c0 + 1 < n ? c0 + 1 : 0)) * kb_n + kb);
-            float v[4];
-            mma_128(v, buf[d][0], buf[d][1], hf);
-            acc[i][0] = fmaf(v[0], s0 * fw, acc[i][0]);
-            acc[i][1] = fmaf(v[1], s1 * fw, acc[i][1]);
-            acc[i][2] = fmaf(v[2], s0 * fw, acc[i][2]);
-            acc[i][3] = fmaf(v[3], s1 * fw, acc[i][3]);
-          }
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      fence_async_proxy();
+      auto load_w = [&](int i) {
+        const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
+        ptx::mbar_arrive_expect_tx(&b.full[st], kStageBytes);
+        tc::tma_load_2d(ring + st * kStageBytes, &p.w2_map, kb * kBlock, (kDense ? 0 : r.active[a]) * p.H + tile * 128,
+                        &b.full[st]);
+      };
+      auto load_h = [&](int i) {
+        const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
+        tc::tma_load_2d(ring + st * kStageBytes + kTileBytes, &p.h_map, kb * kBlock, kDense ? 0 : r.first[a],
+                        &b.full[st]);
+      };
+      const int early = min(n, static_cast<int>(stages));
+      if (kDense) ptx::wait_prerequisites();
+      for (int i = 0; i < early; ++i) load_w(i);
+      if (!kDense) ptx::wait_prerequisites();  // h
+      for (int i = 0; i < early; ++i) load_h(i);
+      int i = early;
+      for (; i < n; ++i) {
+        if (!tc::wait(&b.empty[i % stages], (i / stages - 1) & 1, &b.gave_up)) {
+          ok = false;
+          break;
         }
-        if (fetched < end) fetch(buf[d]);
-        ++it;
-        if (++kb == kb_n || it == end) {  // this warp's part of the expert is complete
+        load_w(i);
+        load_h(i);
+      }
+      if (!ok) drain_loads(b, i, stages);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      run_mma<kN, 1>(b, ring, kStageBytes, stages, n, it);
+      finish_mma(b);
+    }
+  } else {
+    float* mine = s_out + threadIdx.x;
+    for (int t = 0; t < p.T; ++t) mine[t * 128] = 0.0f;
+    ptx::wait_prerequisites();  // h_scales
+    const uint32_t lanes = b.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const float* sw = p.w2_scales + static_cast<int64_t>(tile) * kb_n;
+    const int64_t sw_expert = static_cast<int64_t>(p.out_blocks) * kb_n;
+    unsigned long long acc[kN / 2];
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
+    for (int c = 0; c < kN / 2; ++c) acc[c] = 0;
+    int a = it0 / kb_n, kb = it0 - a * kb_n;
+    float next[(kN + 31) / 32], next_w = 0.0f;
+    auto read = [&](int a, int kb) {  // the scales of the next item, an item ahead
+      const int row0 = kDense ? 0 : r.first[a], rows = kDense ? p.T : r.first[a + 1] - row0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = i * 8 + 2 * q + h;
-              if (c < n) {
-                const float w = r.weight[row0 + c];
-                float* o = mine + r.token[row0 + c] * 16 + g;
-                o[0] = fmaf(w, acc[i][h], o[0]);
-                o[8] = fmaf(w, acc[i][2 + h], o[8]);
-              }
+      for (int i = 0; i < (kN + 31) / 32; ++i)
+        next[i] = lane + 32 * i < rows ? ld_f32(p.h_scales + static_cast<int64_t>(row0 + lane + 32 * i) * kb_n + kb)
+                                       : 0.0f;
+      next_w = ld_f32(sw + (kDense ? 0 : r.active[a]) * sw_expert + kb);
+    };
+    if (n > 0) read(a, kb);
+    for (int i = 0; i < n; ++i) {
+      const uint32_t buf = i & 1;
+      float* scale = s_scale[warp][buf];
+#pragma unroll
+      for (int c = 0; c < (kN + 31) / 32; ++c)
+        if (lane + 32 * c < kN) scale[lane + 32 * c] = next[c];
+      const float f = next_w;
+      const bool last = kb + 1 == kb_n;
+      const int a_now = a;
+      a = last ? a + 1 : a;
+      kb = last ? 0 : kb + 1;
+      if (i + 1 < n) read(a, kb);
+      ok = tc::wait(&b.acc_full[buf], (i / 2) & 1, &b.gave_up);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      tc::fence_after();
+      add_scaled<kN>(lanes + buf * kN, scale, f, acc);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
+      if (last || i + 1 == n) {
+        const int row0 = kDense ? 0 : r.first[a_now], rows = kDense ? p.T : r.first[a_now + 1] - row0;
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          if (c < rows) {
+            const float v = c & 1 ? tc::hi2(acc[c / 2]) : tc::lo2(acc[c / 2]);
+            if (kDense) {
+              mine[c * 128] = v;
+            } else {
+              float* o = mine + r.token[row0 + c] * 128;
+              *o = fmaf(r.weight[row0 + c], v, *o);
             }
-            acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
           }
-          if (kb == kb_n) kb = 0, ++a;
-          __syncwarp();
         }
+#pragma unroll
+        for (int c = 0; c < kN / 2; ++c) acc[c] = 0;
       }
     }
   }
+  // Token t's sum is formed by rank t % ranks, in rank order.
   __syncthreads();
-  for (int i = threadIdx.x; i < p.T * 16; i += kThreads) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_out[w * p.T * 16 + i];
-    reinterpret_cast<__nv_bfloat16*>(p.out)[static_cast<int64_t>(i >> 4) * p.H + n0 + (i & 15)] =
-        __float2bfloat16_rn(sum);
+  if (ranks > 1) cluster_sync();
+  const int column = tile * 128 + static_cast<int>(threadIdx.x);
+  if (warp < 4 && !rs.bad && !b.gave_up && column < p.H) {
+    for (int t = rank; t < p.T; t += ranks) {
+      const float* at = s_out + t * 128 + threadIdx.x;
+      float sum = 0.0f;
+      for (uint32_t q = 0; q < ranks; ++q) sum += q == rank ? *at : ld_cluster(at, q);
+      const int64_t to = static_cast<int64_t>(t) * p.H + column;
+      if (p.out_f32) reinterpret_cast<float*>(p.out)[to] = sum;
+      else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(sum);
+    }
   }
+  __syncthreads();
+  if (ranks > 1) cluster_sync();  // no CTA leaves while its shared memory is being read
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (threadIdx.x == 0 && b.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
+  if (warp == kMmaWarp) tc::tmem_free(b.tmem, kColumns);
 }
 
-template <int kTiles, int kDepthGlu, int kDepthDown>
-cudaError_t launch(const DecodeParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), const DecodeParams& p, uint32_t stages,
+                           uint32_t ranks, unsigned groups, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(groups * ranks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, stages, ranks);
+}
+
+template <int kN>
+cudaError_t launch_glu(const DecodeParams& p, int sms, cudaStream_t stream) {
+  constexpr uint32_t kStages = 4;
   const int pairs = p.T * p.K;
-  auto* glu = decode_glu_kernel<kTiles, kDepthGlu>;
-  const int resident = resident_ctas_per_sm(reinterpret_cast<const void*>(glu), kThreads, 0);
+  size_t ring = static_cast<size_t>(kStages) * (2 * kTileBytes + kN * kBlock);
+  const size_t smem = 1024 + ring + routing_bytes(pairs, p.E);
+  auto* kernel = decode_glu_kernel<kN>;
+  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
+  if (err != cudaSuccess) return err;
+  int64_t units = static_cast<int64_t>(max_active(pairs, p.E)) * (p.I / kBlock);
+  uint32_t ranks = 1;  // too few units for the SMs: split them along K
+  while (ranks < 8 && units * ranks * 2 <= sms && static_cast<int>(ranks) * 2 <= p.H / kBlock) ranks *= 2;
+  if (ranks == 1 && units > sms) units = sms;
+  return launch_cluster(kernel, p, kStages, ranks, static_cast<unsigned>(units), smem, stream);
+}
+
+template <int kN, bool kDense>
+cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
+  constexpr uint32_t kStages = 3;
+  const int pairs = p.T * p.K;
+  const size_t ring = static_cast<size_t>(kStages) * (kTileBytes + kN * kBlock);
+  const size_t smem = 1024 + ring + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E));
+  auto* kernel = few_rows_kernel<kN, kDense>;
+  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
+  if (err != cudaSuccess) return err;
+  const int resident = resident_ctas_per_sm(reinterpret_cast<const void*>(kernel), kThreads, smem);
   if (resident < 1) return cudaErrorInvalidConfiguration;
-  int64_t units = static_cast<int64_t>(pairs < p.E ? pairs : p.E) * (p.I / kBlock);
-  const int64_t most = static_cast<int64_t>(sms) * resident;
-  if (units > most) units = most;
-  cudaError_t err = launch_kernel(glu, dim3(static_cast<unsigned>(units)), dim3(kThreads), 0, stream, true, p);
-  if (err != cudaSuccess) return err;
-  auto* down = decode_down_kernel<kTiles, kDepthDown>;
-  const size_t smem = static_cast<size_t>(kWarps) * p.T * 16 * sizeof(float);
-  err = set_kernel_limits(reinterpret_cast<const void*>(down), smem);
-  if (err != cudaSuccess) return err;
-  return launch_kernel(down, dim3(p.H / 16), dim3(kThreads), smem, stream, true, p);
+  const int tiles = (p.H + 127) / 128;
+  const int64_t items = static_cast<int64_t>(kDense ? 1 : max_active(pairs, p.E)) * p.h_blocks;
+  uint32_t ranks = 1;
+  while (ranks < 8 && static_cast<int64_t>(tiles) * ranks * 2 <= static_cast<int64_t>(sms) * resident &&
+         ranks * 2 <= items)
+    ranks *= 2;
+  return launch_cluster(kernel, p, kStages, ranks, static_cast<unsigned>(tiles), smem, stream);
 }
 
 }  // namespace
 
+int few_rows_columns(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream) {
-  if (p.T <= 8) return launch<1, 2, 3>(p, sms, stream);
-  if (p.T <= 16) return launch<2, 2, 3>(p, sms, stream);
-  if (p.T <= 32) return launch<4, 2, 3>(p, sms, stream);
-  return launch<8, 2, 3>(p, sms, stream);
+  cudaError_t err;
+  switch (few_rows_columns(p.T)) {
+    case 16:
+      err = launch_glu<16>(p, sms, stream);
+      return err != cudaSuccess ? err : launch_few<16, false>(p, sms, stream);
+    case 32:
+      err = launch_glu<32>(p, sms, stream);
+      return err != cudaSuccess ? err : launch_few<32, false>(p, sms, stream);
+    default:
+      err = launch_glu<64>(p, sms, stream);
+      return err != cudaSuccess ? err : launch_few<64, false>(p, sms, stream);
+  }
+}
+
+cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream) {
+  switch (few_rows_columns(p.T)) {
+    case 16: return launch_few<16, true>(p, sms, stream);
+    case 32: return launch_few<32, true>(p, sms, stream);
+    default: return launch_few<64, true>(p, sms, stream);
+  }
 }
 
 }  // namespace moe

@@ -55,10 +55,10 @@ int launched(cudaError_t err) {
   return MOE_ECUDA;
 }
 
-// E4M3 matrix [rows, cols] as a tensor map of 128 x 128 boxes, 128-byte
+// E4M3 matrix [rows, cols] as a tensor map of box_rows x 128 boxes, 128-byte
 // swizzle, zeros outside.  The encoder is the driver's, found through the
 // runtime (no link against libcuda).
-bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
+bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows = 128) {
   using Encode = decltype(&cuTensorMapEncodeTiled);
   static std::atomic<Encode> known{nullptr};
   Encode encode = known.load(std::memory_order_acquire);
@@ -74,7 +74,7 @@ bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) 
   }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-  const cuuint32_t box[2] = {128, 128}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -96,6 +96,24 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
   return guarded([&] {
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    if (!glu && !offsets && rows <= moe::kFewRows) {
+      moe::DecodeParams p = {};
+      const int columns = moe::few_rows_columns(static_cast<int>(rows));
+      if (!encode_map(&p.w2_map, w, N, K) || !encode_map(&p.h_map, a, rows, K, columns))
+        return static_cast<int>(MOE_ECUDA);
+      p.w2_scales = w_scales;
+      p.h_scales = const_cast<float*>(a_scales);  // read only by launch_few_rows
+      p.out = out;
+      p.status = status;
+      p.T = static_cast<int32_t>(rows);
+      p.H = N;
+      p.K = p.E = 1;
+      p.I = K;
+      p.h_blocks = (K + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
+      p.out_blocks = (N + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
+      p.out_f32 = f32;
+      return launched(moe::launch_few_rows(p, sms, static_cast<cudaStream_t>(stream)));
+    }
     moe::ExpertGemmParams p = {};
     if (!encode_map(&p.a, a, rows, K) || !encode_map(&p.w, w, w_rows * E, K)) return static_cast<int>(MOE_ECUDA);
     p.a_scales = a_scales;
@@ -117,7 +135,9 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
 
 bool decode_config_ok(const moe_config* c, int32_t inter) {
   return c && moe_validate_config(c) == MOE_OK && c->num_tokens <= MOE_DECODE_MAX_TOKENS &&
-         c->hidden % MOE_FP8_BLOCK == 0 && inter > 0 && inter % MOE_FP8_BLOCK == 0 && inter <= INT_MAX / 2;
+         c->hidden % MOE_FP8_BLOCK == 0 && inter > 0 && inter % MOE_FP8_BLOCK == 0 &&
+         static_cast<int64_t>(inter) * 2 * c->num_experts <= INT_MAX &&
+         static_cast<int64_t>(c->hidden) * c->num_experts <= INT_MAX;
 }
 
 size_t decode_codes_bytes(const moe_config* c, int32_t inter) {
@@ -209,23 +229,28 @@ MOE_API int moe_decode_layer_fp8(const moe_config* cfg, int32_t inter, const voi
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
     moe::DecodeParams p = {};
-    p.xq = static_cast<const uint8_t*>(xq);
+    const int columns = moe::few_rows_columns(cfg->num_tokens);
+    if (!encode_map(&p.w13_map, w13, static_cast<int64_t>(cfg->num_experts) * 2 * inter, cfg->hidden) ||
+        !encode_map(&p.x_map, xq, cfg->num_tokens, cfg->hidden, columns) ||
+        !encode_map(&p.w2_map, w2, static_cast<int64_t>(cfg->num_experts) * cfg->hidden, inter) ||
+        !encode_map(&p.h_map, workspace, static_cast<int64_t>(cfg->num_tokens) * cfg->top_k, inter, columns))
+      return static_cast<int>(MOE_ECUDA);
     p.x_scales = x_scales;
     p.topk_idx = topk_idx;
     p.topk_w = topk_w;
-    p.w13 = static_cast<const uint8_t*>(w13);
     p.w13_scales = w13_scales;
-    p.w2 = static_cast<const uint8_t*>(w2);
     p.w2_scales = w2_scales;
     p.hq = static_cast<uint8_t*>(workspace);
     p.h_scales = reinterpret_cast<float*>(p.hq + decode_codes_bytes(cfg, inter));
-    p.out = static_cast<uint8_t*>(out);
+    p.out = out;
     p.status = status;
     p.T = cfg->num_tokens;
     p.H = cfg->hidden;
     p.K = cfg->top_k;
     p.E = cfg->num_experts;
     p.I = inter;
+    p.h_blocks = inter / MOE_FP8_BLOCK;
+    p.out_blocks = cfg->hidden / MOE_FP8_BLOCK;
     return launched(moe::launch_decode_layer(p, sms, static_cast<cudaStream_t>(stream)));
   });
 }

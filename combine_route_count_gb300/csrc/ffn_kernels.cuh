@@ -66,22 +66,31 @@ struct ExpertGemmParams {
 int expert_gemm_n_tile(bool glu);
 cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool glu, bool f32, int sms, cudaStream_t stream);
 
-// ---- decode_layer: a whole expert layer for a few tokens ----------------------
+// ---- decode_layer: products of few rows with many weights ----------------------
+constexpr int kFewRows = MOE_DECODE_MAX_TOKENS;  // most rows of either kernel
 struct DecodeParams {
-  const uint8_t* xq;        // E4M3 [T, H]
+  CUtensorMap w13_map;      // E4M3 [E * 2I, H], boxes of 128 rows (all boxes 128 wide)
+  CUtensorMap x_map;        // E4M3 [T, H], boxes of few_rows_columns(T) rows
+  CUtensorMap w2_map;       // E4M3 [E * H, I], boxes of 128 rows
+  CUtensorMap h_map;        // E4M3 [T*K, I], boxes of few_rows_columns(T) rows
   const float* x_scales;    // [T, H/128]
   const int32_t* topk_idx;  // [T, K]
   const float* topk_w;      // [T, K]
-  const uint8_t* w13;       // E4M3 [E, 2I, H]
   const float* w13_scales;  // [E, 2I/128, H/128]
-  const uint8_t* w2;        // E4M3 [E, H, I]
-  const float* w2_scales;   // [E, H/128, I/128]
+  const float* w2_scales;   // [E, out_blocks, h_blocks]
   uint8_t* hq;              // workspace: E4M3 [T*K, I], rows ordered by (expert, token)
-  float* h_scales;          // workspace: [T*K, I/128]
-  uint8_t* out;             // bf16 [T, H]
-  int32_t* status;
+  float* h_scales;          // workspace: [T*K, h_blocks]
+  void* out;                // [T, H], bf16 or float32
+  int32_t* status;          // may be null in launch_few_rows
   int32_t T, H, K, E, I;
+  int32_t h_blocks, out_blocks;  // ceil(I/128), ceil(H/128)
+  bool out_f32;
 };
+// Token columns of the matrix tiles for this many rows.
+int few_rows_columns(int rows);
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream);
+// One dense product of T <= kFewRows rows: out [T, H] = h [T, I] . w2 [H, I]^T,
+// from w2_map, h_map and the scales (K = E = 1).
+cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -109,7 +109,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                : "memory");
 }
 
-// Two float32 fused multiply-adds in one instruction.
+// Two float32 operations in one instruction.
 __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
   return static_cast<unsigned long long>(__float_as_uint(lo)) |
          (static_cast<unsigned long long>(__float_as_uint(hi)) << 32);
@@ -117,6 +117,16 @@ __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
 __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
   unsigned long long d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float lo2(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }

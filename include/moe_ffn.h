@@ -128,7 +128,8 @@ int moe_decode_workspace_bytes(const moe_config* cfg, int32_t inter, size_t* byt
  * to bf16 there.  The chosen experts' weights are read once.
  *   cfg          num_tokens <= MOE_DECODE_MAX_TOKENS, hidden % 128 == 0, else as
  *                for moe_ctx_create (num_ranks plays no part beyond its checks)
- *   inter        inner size of an expert, a multiple of 128
+ *   inter        inner size of an expert, a multiple of 128; E * 2 * inter and
+ *                E * hidden < 2^31
  *   xq, x_scales device E4M3 [T, hidden] and float32 [T, hidden / 128], as
  *                moe_add_rms_norm_fp8 writes them
  *   topk_idx     device int32 [T, K];  topk_w  device float32 [T, K]
@@ -137,8 +138,9 @@ int moe_decode_workspace_bytes(const moe_config* cfg, int32_t inter, size_t* byt
  *   w2           device E4M3 [E, hidden, inter]
  *   w2_scales    device float32 [E, hidden / 128, inter / 128]
  *   out          device bf16 [T, hidden]
- *   status       device int32 [1], written: MOE_OK, or MOE_EROUTE if an index is
- *                out of range or repeated within a token (out is then untouched)
+ *   status       device int32 [1], written: MOE_OK, MOE_EROUTE if an index is
+ *                out of range or repeated within a token (out is then untouched),
+ *                or MOE_ETIMEDOUT if a bounded wait gave up (out is incomplete)
  *   workspace    device, at least moe_decode_workspace_bytes, 256-byte aligned;
  *                calls that may overlap need one each
  * xq, w13, w2 and out are 16-byte aligned.  num_tokens == 0 does nothing. */
