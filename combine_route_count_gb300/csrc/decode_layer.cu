@@ -13,16 +13,15 @@
 // to keep many weight bytes in flight on every SM and to start early.  Weight
 // tiles of 128 rows x 128 of K arrive by tiled TMA in a ring of stages, with
 // the token rows' block beside them, and are the 128-row operand of tcgen05.mma;
-// the tokens are its 16, 32 or 64 columns (kN).  A thread of the four epilogue
-// warps owns one weight row and a column per token; each K block's product is
-// scaled and added to its float32 registers as in expert_gemm.cu.  An earlier
-// form loaded the weights straight into mma.sync fragments: its register
+// an expert's rows are its 16, 32, 48 or 64 columns.  A thread of the epilogue
+// warps owns one weight row and a column per token row; each K block's product
+// is scaled and added to its float32 registers as in expert_gemm.cu.  An
+// earlier form loaded the weights straight into mma.sync fragments: its register
 // stages kept too little in flight (one token, 8 of 256 experts, H 7168, inner
 // 2048: 95 us, 45 % of DRAM busy).
 //
-// decode_glu multiplies every token with every expert that has any row (the
-// columns of tokens that did not choose it are dropped), so x needs no
-// gathering; few_rows reads the rows of h, which decode_glu writes ordered by
+// decode_glu gathers the x rows of an expert's tokens (TMA gather of four rows
+// at a time); few_rows reads rows of h, which decode_glu writes ordered by
 // (expert, token).
 //
 // Spread over the SMs: decode_glu's unit is 128 columns of one expert's h; few
@@ -42,6 +41,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "ffn_kernels.cuh"
 #include "fp8_quant.cuh"
 #include "ptx.cuh"
@@ -52,8 +53,12 @@ namespace {
 
 constexpr int kBlock = MOE_FP8_BLOCK;
 constexpr int kTileBytes = 128 * kBlock;  // 128 weight rows x 128 of K
-constexpr int kTmaWarp = 4, kMmaWarp = 5, kThreads = 192;
+constexpr int kChunk = kFewChunk;         // token rows are handled 16 at a time
 constexpr int kMaxStages = 8;
+// Threads: the epilogue warps (two groups of four in decode_glu, one in
+// few_rows), one TMA warp, one matrix warp.
+constexpr int kGluEpilogue = 256, kGluThreads = kGluEpilogue + 64;
+constexpr int kFewEpilogue = 128, kFewThreads = kFewEpilogue + 64;
 
 // ---- clusters ------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -79,7 +84,6 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
 struct Routing {
   int32_t* active;   // the experts that have rows, ascending
   int32_t* first;    // their first rows, then the number of rows
-  uint64_t* tokens;  // the tokens of expert number a, one bit each
   int32_t* token;    // of each row
   float* weight;     // topk_w of each row
   // scratch, free after build_routing
@@ -94,14 +98,13 @@ struct RoutingShared {
 __host__ __device__ inline int max_active(int pairs, int E) { return pairs < E ? pairs : E; }
 __host__ __device__ inline int routing_bytes(int pairs, int E) {
   const int a = max_active(pairs, E);
-  return (a * 8 + a * 4 + (a + 1) * 4 + pairs * 8 + 15) / 16 * 16;
+  return (a * 4 + (a + 1) * 4 + pairs * 8 + 15) / 16 * 16;
 }
 
 __device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, int pairs, int E) {
   const int a = max_active(pairs, E);
   Routing r;
-  r.tokens = reinterpret_cast<uint64_t*>(smem);
-  r.active = reinterpret_cast<int32_t*>(r.tokens + a);
+  r.active = reinterpret_cast<int32_t*>(smem);
   r.first = r.active + a;
   r.token = r.first + a + 1;
   r.weight = reinterpret_cast<float*>(r.token + pairs);
@@ -113,10 +116,11 @@ __device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, i
 // Called by the whole CTA; ends with a barrier.
 __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s, const DecodeParams& p) {
   const int pairs = p.T * p.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int threads = blockDim.x;
   if (threadIdx.x == 0) s.bad = 0;
-  for (int e = threadIdx.x; e < 2 * p.E; e += kThreads) r.mask[e] = 0;
+  for (int e = threadIdx.x; e < 2 * p.E; e += threads) r.mask[e] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < pairs; i += threads) {
     const int e = p.topk_idx[i], t = i / p.K;
     if (e < 0 || e >= p.E) {
       s.bad = 1;
@@ -128,7 +132,7 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
   __syncthreads();
   if (s.bad) return;  // the same for the whole CTA
   const int chunks = (p.E + 31) / 32;
-  for (int c = warp; c < chunks; c += kThreads / 32) {
+  for (int c = warp; c < chunks; c += threads / 32) {
     const int e = c * 32 + lane;
     const int n = e < p.E ? __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1]) : 0;
     const int rows = __reduce_add_sync(0xffffffffu, n);
@@ -139,7 +143,7 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
     }
   }
   __syncthreads();
-  for (int c = warp; c < chunks; c += kThreads / 32) {
+  for (int c = warp; c < chunks; c += threads / 32) {
     const int e = c * 32 + lane;
     const uint32_t low = e < p.E ? r.mask[2 * e] : 0, high = e < p.E ? r.mask[2 * e + 1] : 0;
     const int n = __popc(low) + __popc(high);
@@ -156,7 +160,6 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
       const int a = base + __popc(some & ((1u << lane) - 1));
       r.active[a] = e;
       r.first[a] = r.row_of[e] = base_row + sum - n;
-      r.tokens[a] = static_cast<uint64_t>(high) << 32 | low;
     }
     if (c == chunks - 1 && lane == 0) {
       s.n_active = base + __popc(some);
@@ -164,7 +167,7 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < pairs; i += threads) {
     const int e = p.topk_idx[i], t = i / p.K;
     const uint64_t mask = static_cast<uint64_t>(r.mask[2 * e + 1]) << 32 | r.mask[2 * e];
     const int row = r.row_of[e] + __popcll(mask & ((1ull << t) - 1));
@@ -178,7 +181,6 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
 struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
-  uint64_t amax_ready[2];
   uint64_t drained;
   uint32_t tmem;
   int gave_up;
@@ -192,10 +194,8 @@ __device__ __forceinline__ void init_barriers(Barriers& b, int stages) {
   for (int i = 0; i < 2; ++i) {
     ptx::mbar_init(&b.acc_full[i], 1);
     ptx::mbar_init(&b.acc_empty[i], 4);
-    ptx::mbar_init(&b.amax_ready[i], 4);
   }
   ptx::mbar_init(&b.drained, 1);
-  ptx::mbar_fence_init();
   b.gave_up = 0;
 }
 
@@ -210,26 +210,28 @@ __device__ __forceinline__ void drain_loads(Barriers& b, uint32_t it, uint32_t s
     }
 }
 
-// The matrix warp's part: kTiles products of 128 rows x kN columns for each of n K blocks.
+__device__ __forceinline__ int chunks_of(int rows) { return (rows + kChunk - 1) / kChunk; }
+
+// One iteration of the matrix warp: kTiles products of 128 weight rows with
+// 16 * chunks token rows.  Tensor-memory tiles are kN columns apart.
 template <int kN, int kTiles>
-__device__ __forceinline__ void run_mma(Barriers& b, const uint8_t* ring, int stage_bytes, uint32_t stages, uint32_t n,
-                                        uint32_t& it) {
-  constexpr uint32_t kInstr = tc::instr_desc_e4m3(128, kN);
-  for (uint32_t end = it + n; it < end; ++it) {
-    const uint32_t st = it % stages, buf = it & 1;
-    if (it >= 2 && !tc::wait(&b.acc_empty[buf], (it / 2 - 1) & 1, &b.gave_up)) return;
-    if (!tc::wait(&b.full[st], (it / stages) & 1, &b.gave_up)) return;
-    tc::fence_after();
-    const uint64_t w = tc::smem_desc(ring + st * stage_bytes);
-    const uint64_t x = tc::smem_desc(ring + st * stage_bytes + kTiles * kTileBytes);
+__device__ __forceinline__ bool mma_block(Barriers& b, const uint8_t* ring, int stage_bytes, uint32_t stages,
+                                          uint32_t it, int chunks) {
+  const uint32_t instr = tc::instr_desc_e4m3(128, chunks * kChunk);
+  const uint32_t st = it % stages, buf = it & 1;
+  if (it >= 2 && !tc::wait(&b.acc_empty[buf], (it / 2 - 1) & 1, &b.gave_up)) return false;
+  if (!tc::wait(&b.full[st], (it / stages) & 1, &b.gave_up)) return false;
+  tc::fence_after();
+  const uint64_t w = tc::smem_desc(ring + st * stage_bytes);
+  const uint64_t x = tc::smem_desc(ring + st * stage_bytes + kTiles * kTileBytes);
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+  for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-      for (int k = 0; k < kBlock / 32; ++k)
-        tc::mma_e4m3(b.tmem + (buf * kTiles + m) * kN, w + m * (kTileBytes >> 4) + 2 * k, x + 2 * k, kInstr, k > 0);
-    tc::commit(&b.empty[st]);
-    tc::commit(&b.acc_full[buf]);
-  }
+    for (int k = 0; k < kBlock / 32; ++k)
+      tc::mma_e4m3(b.tmem + (buf * kTiles + m) * kN, w + m * (kTileBytes >> 4) + 2 * k, x + 2 * k, instr, k > 0);
+  tc::commit(&b.empty[st]);
+  tc::commit(&b.acc_full[buf]);
+  return true;
 }
 
 __device__ __forceinline__ void finish_mma(Barriers& b) {  // nothing in flight when the tensor memory is freed
@@ -239,45 +241,49 @@ __device__ __forceinline__ void finish_mma(Barriers& b) {  // nothing in flight 
 
 __host__ __device__ constexpr uint32_t tmem_columns(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
 
-// acc[c] += product[c] * scale[c] * f for the kN columns of one tensor-memory
-// tile; scale in shared memory.
-template <int kN>
-__device__ __forceinline__ void add_scaled(uint32_t addr, const float* scale, float f, unsigned long long* acc) {
-  const unsigned long long ff = tc::pack2(f, f);
+// acc[c] += v[c] * scale[c] * f for 16 columns; scale in shared memory.
+__device__ __forceinline__ void add_scaled(const uint32_t* v, const float* scale, unsigned long long ff,
+                                           unsigned long long* acc) {
 #pragma unroll
-  for (int c = 0; c < kN; c += 16) {
-    uint32_t v[16];
-    tc::tmem_load_16(addr + c, v);
-    tc::wait_loads();
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-      const float4 s = *reinterpret_cast<const float4*>(scale + c + j);
-      unsigned long long* a = acc + (c + j) / 2;
-      a[0] = tc::fma2(tc::pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                      tc::mul2(tc::pack2(s.x, s.y), ff), a[0]);
-      a[1] = tc::fma2(tc::pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])),
-                      tc::mul2(tc::pack2(s.z, s.w), ff), a[1]);
-    }
+  for (int j = 0; j < kChunk; j += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(scale + j);
+    acc[j / 2] = tc::fma2(tc::pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                          tc::mul2(tc::pack2(s.x, s.y), ff), acc[j / 2]);
+    acc[j / 2 + 1] = tc::fma2(tc::pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])),
+                              tc::mul2(tc::pack2(s.z, s.w), ff), acc[j / 2 + 1]);
   }
 }
 
 // ---- first kernel -----------------------------------------------------------
-// Unit: (expert number a, block j of 128 columns of h).  kN columns: token t is
-// column t.
+// Unit: (expert number a, block j of 128 columns of h).  The two epilogue
+// groups take the K blocks in turn, one tensor-memory buffer each; their sums
+// meet in shared memory, s_part[gate, up][token row][column], where the
+// token rows are then finished, each group every second one.
 template <int kN>
-__global__ void __launch_bounds__(kThreads, 1) decode_glu_kernel(const __grid_constant__ DecodeParams p,
-                                                                 uint32_t stages, uint32_t ranks) {
+__global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid_constant__ DecodeParams p,
+                                                                    uint32_t stages, uint32_t ranks) {
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers b;
+  __shared__ uint64_t part_ready[2], part_free, amax_ready[2];
   __shared__ RoutingShared rs;
-  __shared__ __align__(16) float s_scale[4][2][kN];
-  __shared__ float s_amax[2][4][kN];
+  __shared__ __align__(16) float s_scale[8][kN];
+  __shared__ float s_amax[kN][4];
   constexpr int kStageBytes = 2 * kTileBytes + kN * kBlock;
   constexpr uint32_t kColumns = tmem_columns(4 * kN);
+  constexpr int kTmaWarp = kGluEpilogue / 32, kMmaWarp = kTmaWarp + 1;
   uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
+  float* s_part = reinterpret_cast<float*>(ring + stages * kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Routing r = routing_at(ring + stages * kStageBytes, ring, p.T * p.K, p.E);
-  if (threadIdx.x == 0) init_barriers(b, stages);
+  const Routing r = routing_at(reinterpret_cast<uint8_t*>(s_part + 2 * kN * 128), ring, p.T * p.K, p.E);
+  if (threadIdx.x == 0) {
+    init_barriers(b, stages);
+    ptx::mbar_init(&part_ready[0], 4);
+    ptx::mbar_init(&part_ready[1], 4);
+    ptx::mbar_init(&part_free, 8);
+    ptx::mbar_init(&amax_ready[0], 4);
+    ptx::mbar_init(&amax_ready[1], 4);
+    ptx::mbar_fence_init();
+  }
   if (warp == kMmaWarp) tc::tmem_alloc(&b.tmem, kColumns);
   if (threadIdx.x == kTmaWarp * 32) {
     tc::tma_prefetch_map(&p.w13_map);
@@ -299,46 +305,36 @@ __global__ void __launch_bounds__(kThreads, 1) decode_glu_kernel(const __grid_co
   const int kb0 = static_cast<int>(rank * kb_all / ranks), kb_n = static_cast<int>((rank + 1) * kb_all / ranks) - kb0;
   const int step = static_cast<int>(gridDim.x / ranks), u0 = static_cast<int>(blockIdx.x / ranks);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = rs.bad ? MOE_EROUTE : MOE_OK;
-
-  // A cluster of several CTAs has one unit, whose sums meet below.
-  unsigned long long gate[kN / 2], up[kN / 2];
   bool ok = true;
-  int round = 0;
-  auto finish = [&](int u) -> bool {  // epilogue warps: h from the sums, quantised
-    const int a = u / jb, j = u - a * jb;
-    const uint64_t tokens = r.tokens[a];
-    float (*amax)[kN] = s_amax[round & 1];
-#pragma unroll
-    for (int t = 0; t < kN; ++t) {
-      float g = t & 1 ? tc::hi2(gate[t / 2]) : tc::lo2(gate[t / 2]);
-      const float v = t & 1 ? tc::hi2(up[t / 2]) : tc::lo2(up[t / 2]);
-      if (tokens >> t & 1) {
-        g = g / (1.0f + expf(-g)) * v;
-        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(g)));
-        if (lane == 0) amax[warp][t] = __uint_as_float(top);
+
+  // Epilogue: h of the unit's token rows from the sums in s_part (of all
+  // ranks' CTAs), quantised.  Group w takes rows w, w + 2, ...
+  auto finish = [&](int u, int round) -> bool {
+    const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
+    const int group = warp >> 2, column = threadIdx.x & 127;
+    for (int c = group; c < n; c += 2) {
+      float* at = s_part + c * 128 + column;
+      float g = at[0], v = at[kN * 128];
+      for (uint32_t q = 1; q < ranks; ++q) {
+        g += ld_cluster(at, q);
+        v += ld_cluster(at + kN * 128, q);
       }
-      gate[t / 2] = t & 1 ? tc::pack2(tc::lo2(gate[t / 2]), g) : tc::pack2(g, tc::hi2(gate[t / 2]));
+      g = g / (1.0f + expf(-g)) * v;
+      *at = g;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(g)));
+      if (lane == 0) s_amax[c][warp & 3] = __uint_as_float(top);
     }
-    // All four warps' largest values.  The two copies alternate, so a warp one
-    // unit ahead does not overwrite.
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&b.amax_ready[round & 1]);
-    const bool all = tc::wait(&b.amax_ready[round & 1], (round >> 1) & 1, &b.gave_up);
+    if (lane == 0) tc::mbar_arrive(&amax_ready[group]);
+    const bool all = tc::wait(&amax_ready[group], round & 1, &b.gave_up);
     if (!__all_sync(0xffffffffu, all)) return false;
-    int row = r.first[a];
-#pragma unroll
-    for (int t = 0; t < kN; ++t) {
-      if (tokens >> t & 1) {
-        const float top = fmaxf(fmaxf(amax[0][t], amax[1][t]), fmaxf(amax[2][t], amax[3][t]));
-        const float scale = top > 0.0f ? __fdiv_rn(fmaxf(top, kTinyAmax), 448.0f) : 1.0f;
-        const float h = t & 1 ? tc::hi2(gate[t / 2]) : tc::lo2(gate[t / 2]);
-        p.hq[static_cast<int64_t>(row) * p.I + j * kBlock + threadIdx.x] =
-            static_cast<uint8_t>(fp8q::e4m3x2(__fmul_rn(h, __fdiv_rn(1.0f, scale)), 0.0f));
-        if (threadIdx.x == 0) p.h_scales[static_cast<int64_t>(row) * jb + j] = scale;
-        ++row;
-      }
+    for (int c = group; c < n; c += 2) {
+      const float top = fmaxf(fmaxf(s_amax[c][0], s_amax[c][1]), fmaxf(s_amax[c][2], s_amax[c][3]));
+      const float scale = top > 0.0f ? __fdiv_rn(fmaxf(top, kTinyAmax), 448.0f) : 1.0f;
+      const float h = __fmul_rn(s_part[c * 128 + column], __fdiv_rn(1.0f, scale));
+      p.hq[static_cast<int64_t>(row0 + c) * p.I + j * kBlock + column] = static_cast<uint8_t>(fp8q::e4m3x2(h, 0.0f));
+      if (column == 0) p.h_scales[static_cast<int64_t>(row0 + c) * jb + j] = scale;
     }
-    ++round;
     return true;
   };
 
@@ -349,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_glu_kernel(const __grid_co
       for (int u = u0; ok && u < units; u += step) {
         const int a = u / jb, j = u - a * jb;
         const int w0 = r.active[a] * 2 * p.I + j * kBlock;
+        const int row0 = r.first[a], n = r.first[a + 1] - row0, rows = chunks_of(n) * kChunk;
         for (int kb = 0; kb < kb_n; ++kb, ++it) {
           const uint32_t st = it % stages;
           if (it >= stages && !tc::wait(&b.empty[st], (it / stages - 1) & 1, &b.gave_up)) {
@@ -357,10 +354,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_glu_kernel(const __grid_co
           }
           uint8_t* to = ring + st * kStageBytes;
           const int k = (kb0 + kb) * kBlock;
-          ptx::mbar_arrive_expect_tx(&b.full[st], kStageBytes);
+          ptx::mbar_arrive_expect_tx(&b.full[st], 2 * kTileBytes + rows * kBlock);
           tc::tma_load_2d(to, &p.w13_map, k, w0, &b.full[st]);
           tc::tma_load_2d(to + kTileBytes, &p.w13_map, k, w0 + p.I, &b.full[st]);
-          tc::tma_load_2d(to + 2 * kTileBytes, &p.x_map, k, 0, &b.full[st]);
+          // Rows past the expert's last repeat it; their columns are dropped.
+          for (int c = 0; c < rows; c += 4)
+            tc::tma_gather4(to + 2 * kTileBytes + c * kBlock, &p.x_map, k, r.token[row0 + min(c, n - 1)],
+                            r.token[row0 + min(c + 1, n - 1)], r.token[row0 + min(c + 2, n - 1)],
+                            r.token[row0 + min(c + 3, n - 1)], &b.full[st]);
         }
       }
       if (!ok) drain_loads(b, it, stages);
@@ -368,77 +369,109 @@ __global__ void __launch_bounds__(kThreads, 1) decode_glu_kernel(const __grid_co
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       uint32_t it = 0;
-      for (int u = u0; u < units && !b.gave_up; u += step) run_mma<kN, 2>(b, ring, kStageBytes, stages, kb_n, it);
+      for (int u = u0; ok && u < units; u += step) {
+        const int a = u / jb, chunks = chunks_of(r.first[a + 1] - r.first[a]);
+        for (int kb = 0; ok && kb < kb_n; ++kb, ++it)
+          ok = mma_block<kN, 2>(b, ring, kStageBytes, stages, it, chunks);
+      }
       finish_mma(b);
     }
   } else {
-    const uint32_t lanes = b.tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    uint32_t it = 0;
-    for (int u = u0; ok && u < units; u += step) {
-      const int a = u / jb, j = u - a * jb;
+    const int group = warp >> 2, column = threadIdx.x & 127;
+    const uint32_t lanes = b.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * 2 * kN;
+    float* scale = s_scale[warp];
+    uint32_t it = 0;  // of the whole CTA; this group takes those with it % 2 == group
+    int round = 0;
+    for (int u = u0; ok && u < units; u += step, ++round) {
+      const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
       const float* sg = p.w13_scales + (static_cast<int64_t>(r.active[a]) * 2 * jb + j) * kb_all + kb0;
       const float* su = sg + static_cast<int64_t>(jb) * kb_all;
-      const float* sx = p.x_scales + kb0;
-      // The tokens' scales of the next K block are read a block ahead.
+      const float* sx[(kN + 31) / 32];
+#pragma unroll
+      for (int i = 0; i < (kN + 31) / 32; ++i)
+        sx[i] = p.x_scales + static_cast<int64_t>(r.token[row0 + min(lane + 32 * i, n - 1)]) * kb_all + kb0;
+      // The scales of this group's next K block are read a turn ahead.
       float next[(kN + 31) / 32], next_g, next_u;
       auto read = [&](int kb) {
 #pragma unroll
         for (int i = 0; i < (kN + 31) / 32; ++i)
-          next[i] = lane + 32 * i < p.T ? sx[static_cast<int64_t>(lane + 32 * i) * kb_all + kb] : 0.0f;
+          if (32 * i < n) next[i] = sx[i][kb];
         next_g = sg[kb];
         next_u = su[kb];
       };
-      read(0);
+      unsigned long long gate[kN / 2], up[kN / 2];
 #pragma unroll
       for (int c = 0; c < kN / 2; ++c) gate[c] = up[c] = 0;
-      for (int kb = 0; kb < kb_n; ++kb, ++it) {
-        const uint32_t buf = it & 1;
-        float* scale = s_scale[warp][buf];
+      int kb = (it & 1) == static_cast<uint32_t>(group) ? 0 : 1;
+      if (kb < kb_n) read(kb);
+      for (; kb < kb_n; kb += 2) {
+        const uint32_t at = it + kb;
+        __syncwarp();  // the last turn's scales have been read
 #pragma unroll
         for (int i = 0; i < (kN + 31) / 32; ++i)
-          if (lane + 32 * i < kN) scale[lane + 32 * i] = next[i];
-        const float fg = next_g, fu = next_u;
-        if (kb + 1 < kb_n) read(kb + 1);
-        ok = tc::wait(&b.acc_full[buf], (it / 2) & 1, &b.gave_up);
-        if (!__all_sync(0xffffffffu, ok)) {  // also orders the scales' stores before their loads
+          if (32 * i < n && lane + 32 * i < kN) scale[lane + 32 * i] = next[i];
+        const unsigned long long fg = tc::pack2(next_g, next_g), fu = tc::pack2(next_u, next_u);
+        if (kb + 2 < kb_n) read(kb + 2);
+        ok = tc::wait(&b.acc_full[group], (at / 2) & 1, &b.gave_up);
+        if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         __syncwarp();
         tc::fence_after();
-        add_scaled<kN>(lanes + buf * 2 * kN, scale, fg, gate);
-        add_scaled<kN>(lanes + (buf * 2 + 1) * kN, scale, fu, up);
+#pragma unroll
+        for (int c = 0; c < kN; c += kChunk) {
+          if (c < n) {
+            uint32_t vg[kChunk], vu[kChunk];
+            tc::tmem_load_16(lanes + c, vg);
+            tc::tmem_load_16(lanes + kN + c, vu);
+            tc::wait_loads();
+            add_scaled(vg, scale + c, fg, gate + c / 2);
+            add_scaled(vu, scale + c, fu, up + c / 2);
+          }
+        }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
+        if (lane == 0) tc::mbar_arrive(&b.acc_empty[group]);
       }
-      if (ok && ranks == 1) ok = finish(u);
-    }
-  }
-  if (ranks > 1) {
-    // The ring is free: every load has been consumed.  [gate, up][column][row]
-    float* part = reinterpret_cast<float*>(ring);
-    __syncthreads();
-    const bool mine = warp < 4 && ok && u0 < units;
-    if (mine) {
+      it += kb_n;
+      if (!ok) break;
+      // The second group's sums, then both: s_part is written in full by each
+      // group, the second time on top of the first.
+      if (round > 0) ok = tc::wait(&part_free, (round - 1) & 1, &b.gave_up);
+      if (group == 0 && ok) ok = tc::wait(&part_ready[1], round & 1, &b.gave_up);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
 #pragma unroll
       for (int c = 0; c < kN; ++c) {
-        part[c * 128 + threadIdx.x] = c & 1 ? tc::hi2(gate[c / 2]) : tc::lo2(gate[c / 2]);
-        part[(kN + c) * 128 + threadIdx.x] = c & 1 ? tc::hi2(up[c / 2]) : tc::lo2(up[c / 2]);
-      }
-    }
-    cluster_sync();
-    if (mine && rank == 0) {
-      for (uint32_t q = 1; q < ranks; ++q) {
-#pragma unroll
-        for (int c = 0; c < kN; c += 2) {
-          const float* at = part + c * 128 + threadIdx.x;
-          gate[c / 2] = tc::add2(gate[c / 2], tc::pack2(ld_cluster(at, q), ld_cluster(at + 128, q)));
-          up[c / 2] = tc::add2(up[c / 2], tc::pack2(ld_cluster(at + kN * 128, q), ld_cluster(at + (kN + 1) * 128, q)));
+        if (c / kChunk * kChunk < n) {
+          float g = c & 1 ? tc::hi2(gate[c / 2]) : tc::lo2(gate[c / 2]);
+          float v = c & 1 ? tc::hi2(up[c / 2]) : tc::lo2(up[c / 2]);
+          float* to = s_part + c * 128 + column;
+          if (group == 0) {
+            g += to[0];
+            v += to[kN * 128];
+          }
+          to[0] = g;
+          to[kN * 128] = v;
         }
       }
-      finish(u0);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&part_ready[group]);
+      if (ranks == 1) {
+        ok = tc::wait(&part_ready[0], round & 1, &b.gave_up);
+        ok = __all_sync(0xffffffffu, ok) && finish(u, round);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&part_free);
+      }
     }
+  }
+  if (ranks > 1) {  // one unit a cluster: its sums meet in rank 0
+    __syncthreads();
+    cluster_sync();
+    if (warp < kTmaWarp && rank == 0 && ok && u0 < units) finish(u0, 0);
     __syncthreads();
     cluster_sync();  // no CTA leaves while its shared memory is being read
   }
@@ -455,19 +488,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_glu_kernel(const __grid_co
 // the CTA's s_out[t][column] when the CTA's part of that expert is complete
 // (dense: one expert, row i is token i with weight 1).
 template <int kN, bool kDense>
-__global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(const __grid_constant__ DecodeParams p, uint32_t stages,
-                                                            uint32_t ranks) {
+__global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
+    few_rows_kernel(const __grid_constant__ DecodeParams p, uint32_t stages, uint32_t ranks) {
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers b;
   __shared__ RoutingShared rs;
   __shared__ __align__(16) float s_scale[4][2][kN];
   constexpr int kStageBytes = kTileBytes + kN * kBlock;
   constexpr uint32_t kColumns = tmem_columns(2 * kN);
+  constexpr int kTmaWarp = kFewEpilogue / 32, kMmaWarp = kTmaWarp + 1;
   uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
   float* s_out = reinterpret_cast<float*>(ring + stages * kStageBytes);  // [T][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Routing r = {};
-  if (threadIdx.x == 0) init_barriers(b, stages);
+  if (threadIdx.x == 0) {
+    init_barriers(b, stages);
+    ptx::mbar_fence_init();
+  }
   if (warp == kMmaWarp) tc::tmem_alloc(&b.tmem, kColumns);
   if (threadIdx.x == kTmaWarp * 32) {
     tc::tma_prefetch_map(&p.w2_map);
@@ -488,6 +525,8 @@ __global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(co
   const int items = rs.bad ? 0 : rs.n_active * kb_n;
   const int it0 = static_cast<int>(static_cast<int64_t>(items) * rank / ranks);
   const int n = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / ranks) - it0;
+  auto row0_of = [&](int a) { return kDense ? 0 : r.first[a]; };
+  auto rows_of = [&](int a) { return kDense ? p.T : r.first[a + 1] - r.first[a]; };
   bool ok = true;
 
   if (warp == kTmaWarp) {
@@ -495,14 +534,15 @@ __global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(co
       fence_async_proxy();
       auto load_w = [&](int i) {
         const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
-        ptx::mbar_arrive_expect_tx(&b.full[st], kStageBytes);
+        ptx::mbar_arrive_expect_tx(&b.full[st], kTileBytes + chunks_of(rows_of(a)) * kChunk * kBlock);
         tc::tma_load_2d(ring + st * kStageBytes, &p.w2_map, kb * kBlock, (kDense ? 0 : r.active[a]) * p.H + tile * 128,
                         &b.full[st]);
       };
       auto load_h = [&](int i) {
         const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
-        tc::tma_load_2d(ring + st * kStageBytes + kTileBytes, &p.h_map, kb * kBlock, kDense ? 0 : r.first[a],
-                        &b.full[st]);
+        for (int c = 0; c < rows_of(a); c += kChunk)
+          tc::tma_load_2d(ring + st * kStageBytes + kTileBytes + c * kBlock, &p.h_map, kb * kBlock, row0_of(a) + c,
+                          &b.full[st]);
       };
       const int early = min(n, static_cast<int>(stages));
       if (kDense) ptx::wait_prerequisites();
@@ -522,8 +562,11 @@ __global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(co
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
-      uint32_t it = 0;
-      run_mma<kN, 1>(b, ring, kStageBytes, stages, n, it);
+      int a = it0 / kb_n, kb = it0 - a * kb_n;
+      for (int i = 0; ok && i < n; ++i) {
+        ok = mma_block<kN, 1>(b, ring, kStageBytes, stages, i, chunks_of(rows_of(a)));
+        if (++kb == kb_n) kb = 0, ++a;
+      }
       finish_mma(b);
     }
   } else {
@@ -539,23 +582,23 @@ __global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(co
     int a = it0 / kb_n, kb = it0 - a * kb_n;
     float next[(kN + 31) / 32], next_w = 0.0f;
     auto read = [&](int a, int kb) {  // the scales of the next item, an item ahead
-      const int row0 = kDense ? 0 : r.first[a], rows = kDense ? p.T : r.first[a + 1] - row0;
+      const int row0 = row0_of(a), rows = rows_of(a);
 #pragma unroll
       for (int i = 0; i < (kN + 31) / 32; ++i)
-        next[i] = lane + 32 * i < rows ? ld_f32(p.h_scales + static_cast<int64_t>(row0 + lane + 32 * i) * kb_n + kb)
-                                       : 0.0f;
+        if (32 * i < rows)
+          next[i] = ld_f32(p.h_scales + static_cast<int64_t>(row0 + min(lane + 32 * i, rows - 1)) * kb_n + kb);
       next_w = ld_f32(sw + (kDense ? 0 : r.active[a]) * sw_expert + kb);
     };
     if (n > 0) read(a, kb);
     for (int i = 0; i < n; ++i) {
       const uint32_t buf = i & 1;
+      const int row0 = row0_of(a), rows = rows_of(a);
       float* scale = s_scale[warp][buf];
 #pragma unroll
       for (int c = 0; c < (kN + 31) / 32; ++c)
-        if (lane + 32 * c < kN) scale[lane + 32 * c] = next[c];
-      const float f = next_w;
+        if (32 * c < rows && lane + 32 * c < kN) scale[lane + 32 * c] = next[c];
+      const unsigned long long f = tc::pack2(next_w, next_w);
       const bool last = kb + 1 == kb_n;
-      const int a_now = a;
       a = last ? a + 1 : a;
       kb = last ? 0 : kb + 1;
       if (i + 1 < n) read(a, kb);
@@ -566,21 +609,30 @@ __global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(co
       }
       __syncwarp();
       tc::fence_after();
-      add_scaled<kN>(lanes + buf * kN, scale, f, acc);
+#pragma unroll
+      for (int c = 0; c < kN; c += kChunk) {
+        if (c < rows) {
+          uint32_t v[kChunk];
+          tc::tmem_load_16(lanes + buf * kN + c, v);
+          tc::wait_loads();
+          add_scaled(v, scale + c, f, acc + c / 2);
+        }
+      }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
       if (last || i + 1 == n) {
-        const int row0 = kDense ? 0 : r.first[a_now], rows = kDense ? p.T : r.first[a_now + 1] - row0;
 #pragma unroll
         for (int c = 0; c < kN; ++c) {
-          if (c < rows) {
+          if (c / kChunk * kChunk < rows) {
             const float v = c & 1 ? tc::hi2(acc[c / 2]) : tc::lo2(acc[c / 2]);
-            if (kDense) {
-              mine[c * 128] = v;
-            } else {
-              float* o = mine + r.token[row0 + c] * 128;
-              *o = fmaf(r.weight[row0 + c], v, *o);
+            if (c < rows) {
+              if (kDense) {
+                mine[c * 128] = v;
+              } else {
+                float* o = mine + r.token[row0 + c] * 128;
+                *o = fmaf(r.weight[row0 + c], v, *o);
+              }
             }
           }
         }
@@ -593,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(co
   __syncthreads();
   if (ranks > 1) cluster_sync();
   const int column = tile * 128 + static_cast<int>(threadIdx.x);
-  if (warp < 4 && !rs.bad && !b.gave_up && column < p.H) {
+  if (threadIdx.x < 128 && !rs.bad && !b.gave_up && column < p.H) {
     for (int t = rank; t < p.T; t += ranks) {
       const float* at = s_out + t * 128 + threadIdx.x;
       float sum = 0.0f;
@@ -612,11 +664,11 @@ __global__ void __launch_bounds__(kThreads, kN <= 32 ? 3 : 2) few_rows_kernel(co
   if (warp == kMmaWarp) tc::tmem_free(b.tmem, kColumns);
 }
 
-cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), const DecodeParams& p, uint32_t stages,
-                           uint32_t ranks, unsigned groups, size_t smem, cudaStream_t stream) {
+cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), const DecodeParams& p, int threads,
+                           uint32_t stages, uint32_t ranks, unsigned groups, size_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(groups * ranks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -632,10 +684,10 @@ cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), con
 
 template <int kN>
 cudaError_t launch_glu(const DecodeParams& p, int sms, cudaStream_t stream) {
-  constexpr uint32_t kStages = 4;
+  constexpr uint32_t kStages = kN == 16 ? 5 : kN == 32 ? 4 : 3;
   const int pairs = p.T * p.K;
-  size_t ring = static_cast<size_t>(kStages) * (2 * kTileBytes + kN * kBlock);
-  const size_t smem = 1024 + ring + routing_bytes(pairs, p.E);
+  const size_t smem = 1024 + static_cast<size_t>(kStages) * (2 * kTileBytes + kN * kBlock) + 2 * kN * 128 * 4 +
+                      routing_bytes(pairs, p.E);
   auto* kernel = decode_glu_kernel<kN>;
   cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
   if (err != cudaSuccess) return err;
@@ -643,7 +695,7 @@ cudaError_t launch_glu(const DecodeParams& p, int sms, cudaStream_t stream) {
   uint32_t ranks = 1;  // too few units for the SMs: split them along K
   while (ranks < 8 && units * ranks * 2 <= sms && static_cast<int>(ranks) * 2 <= p.H / kBlock) ranks *= 2;
   if (ranks == 1 && units > sms) units = sms;
-  return launch_cluster(kernel, p, kStages, ranks, static_cast<unsigned>(units), smem, stream);
+  return launch_cluster(kernel, p, kGluThreads, kStages, ranks, static_cast<unsigned>(units), smem, stream);
 }
 
 template <int kN, bool kDense>
@@ -655,24 +707,23 @@ cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
   auto* kernel = few_rows_kernel<kN, kDense>;
   cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
   if (err != cudaSuccess) return err;
-  const int resident = resident_ctas_per_sm(reinterpret_cast<const void*>(kernel), kThreads, smem);
-  if (resident < 1) return cudaErrorInvalidConfiguration;
+  // CTAs that fit on an SM: by shared memory (2 KiB of it static), and by the launch bounds.
+  const int64_t resident = std::min(smem_ctas_per_sm(smem + 2048), kN <= 32 ? 3 : 2);
   const int tiles = (p.H + 127) / 128;
   const int64_t items = static_cast<int64_t>(kDense ? 1 : max_active(pairs, p.E)) * p.h_blocks;
   uint32_t ranks = 1;
-  while (ranks < 8 && static_cast<int64_t>(tiles) * ranks * 2 <= static_cast<int64_t>(sms) * resident &&
-         ranks * 2 <= items)
-    ranks *= 2;
-  return launch_cluster(kernel, p, kStages, ranks, static_cast<unsigned>(tiles), smem, stream);
+  while (ranks < 8 && tiles * static_cast<int64_t>(ranks) * 2 <= sms * resident && ranks * 2 <= items) ranks *= 2;
+  return launch_cluster(kernel, p, kFewThreads, kStages, ranks, static_cast<unsigned>(tiles), smem, stream);
 }
+
+// Most token columns a kernel variant holds, for this many tokens.
+int columns_for(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 }  // namespace
 
-int few_rows_columns(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream) {
   cudaError_t err;
-  switch (few_rows_columns(p.T)) {
+  switch (columns_for(p.T)) {
     case 16:
       err = launch_glu<16>(p, sms, stream);
       return err != cudaSuccess ? err : launch_few<16, false>(p, sms, stream);
@@ -686,7 +737,7 @@ cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t str
 }
 
 cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream) {
-  switch (few_rows_columns(p.T)) {
+  switch (columns_for(p.T)) {
     case 16: return launch_few<16, true>(p, sms, stream);
     case 32: return launch_few<32, true>(p, sms, stream);
     default: return launch_few<64, true>(p, sms, stream);

@@ -98,8 +98,7 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
     if (!glu && !offsets && rows <= moe::kFewRows) {
       moe::DecodeParams p = {};
-      const int columns = moe::few_rows_columns(static_cast<int>(rows));
-      if (!encode_map(&p.w2_map, w, N, K) || !encode_map(&p.h_map, a, rows, K, columns))
+      if (!encode_map(&p.w2_map, w, N, K) || !encode_map(&p.h_map, a, rows, K, moe::kFewChunk))
         return static_cast<int>(MOE_ECUDA);
       p.w2_scales = w_scales;
       p.h_scales = const_cast<float*>(a_scales);  // read only by launch_few_rows
@@ -229,11 +228,11 @@ MOE_API int moe_decode_layer_fp8(const moe_config* cfg, int32_t inter, const voi
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
     moe::DecodeParams p = {};
-    const int columns = moe::few_rows_columns(cfg->num_tokens);
     if (!encode_map(&p.w13_map, w13, static_cast<int64_t>(cfg->num_experts) * 2 * inter, cfg->hidden) ||
-        !encode_map(&p.x_map, xq, cfg->num_tokens, cfg->hidden, columns) ||
+        !encode_map(&p.x_map, xq, cfg->num_tokens, cfg->hidden, 1) ||
         !encode_map(&p.w2_map, w2, static_cast<int64_t>(cfg->num_experts) * cfg->hidden, inter) ||
-        !encode_map(&p.h_map, workspace, static_cast<int64_t>(cfg->num_tokens) * cfg->top_k, inter, columns))
+        !encode_map(&p.h_map, workspace, static_cast<int64_t>(cfg->num_tokens) * cfg->top_k, inter,
+                    moe::kFewChunk))
       return static_cast<int>(MOE_ECUDA);
     p.x_scales = x_scales;
     p.topk_idx = topk_idx;

@@ -68,11 +68,12 @@ cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool glu, bool f32, in
 
 // ---- decode_layer: products of few rows with many weights ----------------------
 constexpr int kFewRows = MOE_DECODE_MAX_TOKENS;  // most rows of either kernel
+constexpr int kFewChunk = 16;
 struct DecodeParams {
   CUtensorMap w13_map;      // E4M3 [E * 2I, H], boxes of 128 rows (all boxes 128 wide)
-  CUtensorMap x_map;        // E4M3 [T, H], boxes of few_rows_columns(T) rows
+  CUtensorMap x_map;        // E4M3 [T, H], boxes of one row (gathered)
   CUtensorMap w2_map;       // E4M3 [E * H, I], boxes of 128 rows
-  CUtensorMap h_map;        // E4M3 [T*K, I], boxes of few_rows_columns(T) rows
+  CUtensorMap h_map;        // E4M3 [T*K, I], boxes of kFewChunk rows
   const float* x_scales;    // [T, H/128]
   const int32_t* topk_idx;  // [T, K]
   const float* topk_w;      // [T, K]
@@ -86,8 +87,6 @@ struct DecodeParams {
   int32_t h_blocks, out_blocks;  // ceil(I/128), ceil(H/128)
   bool out_f32;
 };
-// Token columns of the matrix tiles for this many rows.
-int few_rows_columns(int rows);
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream);
 // One dense product of T <= kFewRows rows: out [T, H] = h [T, I] . w2 [H, I]^T,
 // from w2_map, h_map and the scales (K = E = 1).
