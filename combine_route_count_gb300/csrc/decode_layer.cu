@@ -54,11 +54,10 @@ namespace {
 constexpr int kBlock = MOE_FP8_BLOCK;
 constexpr int kTileBytes = 128 * kBlock;  // 128 weight rows x 128 of K
 constexpr int kChunk = kFewChunk;         // token rows are handled 16 at a time
-constexpr int kMaxStages = 8;
-// Threads: the epilogue warps (two groups of four in decode_glu, one in
-// few_rows), one TMA warp, one matrix warp.
-constexpr int kGluEpilogue = 256, kGluThreads = kGluEpilogue + 64;
-constexpr int kFewEpilogue = 128, kFewThreads = kFewEpilogue + 64;
+constexpr int kMaxStages = 12;
+constexpr int kMaxRanks = 4;              // CTAs of a cluster in few_rows
+constexpr int kTmaWarp = 4, kMmaWarp = 5;  // warps 0-3: epilogue
+constexpr int kThreads = 192;
 
 // ---- clusters ------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -93,6 +92,7 @@ struct Routing {
 struct RoutingShared {
   int32_t warp_active[32], warp_rows[32];
   int32_t n_active, bad;
+  int32_t most_rows;  // of one expert
 };
 
 __host__ __device__ inline int max_active(int pairs, int E) { return pairs < E ? pairs : E; }
@@ -100,6 +100,9 @@ __host__ __device__ inline int routing_bytes(int pairs, int E) {
   const int a = max_active(pairs, E);
   return (a * 4 + (a + 1) * 4 + pairs * 8 + 15) / 16 * 16;
 }
+
+// What build_routing needs besides lies at the start of the ring, before any load.
+static_assert(MOE_MAX_EXPERTS * 12 <= kTileBytes && 32 * 8 <= kTileBytes, "scratch fits in one stage");
 
 __device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, int pairs, int E) {
   const int a = max_active(pairs, E);
@@ -113,40 +116,107 @@ __device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, i
   return r;
 }
 
-// Called by the whole CTA; ends with a barrier.
+// Called by the whole CTA; ends with a barrier.  For at most 32 pairs: every
+// pair counts the pairs before it, which spares the per-expert masks and their
+// scan (8 pairs of 256 experts: 1.6 instead of 2.1 us from the launch's wait;
+// with 128 pairs the counting takes 6.8 us).
+__device__ __forceinline__ void build_routing_small(const Routing& r, RoutingShared& s, const DecodeParams& p) {
+  const int pairs = p.T * p.K, i = threadIdx.x;
+  int32_t* expert = reinterpret_cast<int32_t*>(r.mask);  // [pairs]
+  int32_t* heads = expert + pairs;                       // [pairs] whether the pair is its expert's first
+  int e = 0;
+  float w = 0.0f;
+  if (i < pairs) {
+    e = p.topk_idx[i];
+    w = p.topk_w[i];
+    expert[i] = e;
+  }
+  if (i == 0) s.bad = 0, s.most_rows = 1;
+  __syncthreads();
+  int row = 0;
+  bool head = i < pairs;
+  if (i < pairs) {
+    const int t0 = i / p.K * p.K;  // the token's first pair
+    int before_me = 0;
+    if (e < 0 || e >= p.E) s.bad = 1;
+    for (int j = 0; j < pairs; ++j) {
+      const int other = expert[j];
+      const bool before = other == e && j < i;
+      row += other < e || before;
+      before_me += before;
+      head = head && !before;
+      if (before && j >= t0) s.bad = 1;  // repeated within the token
+    }
+    heads[i] = head;
+    if (before_me > 0) atomicMax(&s.most_rows, before_me + 1);
+  }
+  __syncthreads();
+  if (s.bad) return;  // the same for the whole CTA
+  if (i < pairs) {
+    r.token[row] = i / p.K;
+    r.weight[row] = w;
+    int a = 0;
+    for (int j = 0; j < pairs; ++j) a += heads[j] && expert[j] < e;
+    if (head) {
+      r.active[a] = e;
+      r.first[a] = row;
+    }
+    if (row == pairs - 1) {  // of the last expert
+      s.n_active = a + 1;
+      r.first[a + 1] = pairs;
+    }
+  }
+  __syncthreads();
+}
+
 __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s, const DecodeParams& p) {
   const int pairs = p.T * p.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int threads = blockDim.x;
-  if (threadIdx.x == 0) s.bad = 0;
-  for (int e = threadIdx.x; e < 2 * p.E; e += threads) r.mask[e] = 0;
+  if (pairs <= 32) {
+    build_routing_small(r, s, p);
+    return;
+  }
+  constexpr int kMost = (kFewRows * MOE_MAX_TOP_K + kThreads - 1) / kThreads;
+  int expert[kMost];
+  float weight[kMost];
+#pragma unroll
+  for (int m = 0; m < kMost; ++m) {
+    const int i = threadIdx.x + m * kThreads;
+    expert[m] = i < pairs ? p.topk_idx[i] : 0;
+    weight[m] = i < pairs ? p.topk_w[i] : 0.0f;
+  }
+  if (threadIdx.x == 0) s.bad = 0, s.most_rows = 1;
+  for (int e = threadIdx.x; e < 2 * p.E; e += kThreads) r.mask[e] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += threads) {
-    const int e = p.topk_idx[i], t = i / p.K;
-    if (e < 0 || e >= p.E) {
-      s.bad = 1;
-    } else {
-      const uint32_t bit = 1u << (t & 31);
-      if (atomicOr(&r.mask[2 * e + (t >> 5)], bit) & bit) s.bad = 1;  // repeated within the token
+#pragma unroll
+  for (int m = 0; m < kMost; ++m) {
+    const int i = threadIdx.x + m * kThreads, e = expert[m], t = i / p.K;
+    if (i < pairs) {
+      if (e < 0 || e >= p.E) {
+        s.bad = 1;
+      } else {
+        const uint32_t bit = 1u << (t & 31);
+        if (atomicOr(&r.mask[2 * e + (t >> 5)], bit) & bit) s.bad = 1;  // repeated within the token
+      }
     }
   }
   __syncthreads();
   if (s.bad) return;  // the same for the whole CTA
   const int chunks = (p.E + 31) / 32;
-  for (int c = warp; c < chunks; c += threads / 32) {
+  for (int c = warp; c < chunks; c += kThreads / 32) {
     const int e = c * 32 + lane;
     const int n = e < p.E ? __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1]) : 0;
-    const int rows = __reduce_add_sync(0xffffffffu, n);
+    const int rows = __reduce_add_sync(0xffffffffu, n), most = __reduce_max_sync(0xffffffffu, n);
     const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
     if (lane == 0) {
+      atomicMax(&s.most_rows, most);
       s.warp_active[c] = __popc(some);
       s.warp_rows[c] = rows;
     }
   }
   __syncthreads();
-  for (int c = warp; c < chunks; c += threads / 32) {
+  for (int c = warp; c < chunks; c += kThreads / 32) {
     const int e = c * 32 + lane;
-    const uint32_t low = e < p.E ? r.mask[2 * e] : 0, high = e < p.E ? r.mask[2 * e + 1] : 0;
-    const int n = __popc(low) + __popc(high);
+    const int n = e < p.E ? __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1]) : 0;
     const int base = __reduce_add_sync(0xffffffffu, lane < c ? s.warp_active[lane] : 0);
     const int base_row = __reduce_add_sync(0xffffffffu, lane < c ? s.warp_rows[lane] : 0);
     const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
@@ -167,12 +237,15 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += threads) {
-    const int e = p.topk_idx[i], t = i / p.K;
-    const uint64_t mask = static_cast<uint64_t>(r.mask[2 * e + 1]) << 32 | r.mask[2 * e];
-    const int row = r.row_of[e] + __popcll(mask & ((1ull << t) - 1));
-    r.token[row] = t;
-    r.weight[row] = p.topk_w[i];
+#pragma unroll
+  for (int m = 0; m < kMost; ++m) {
+    const int i = threadIdx.x + m * kThreads, e = expert[m], t = i / p.K;
+    if (i < pairs) {
+      const uint64_t mask = static_cast<uint64_t>(r.mask[2 * e + 1]) << 32 | r.mask[2 * e];
+      const int row = r.row_of[e] + __popcll(mask & ((1ull << t) - 1));
+      r.token[row] = t;
+      r.weight[row] = weight[m];
+    }
   }
   __syncthreads();
 }
@@ -186,8 +259,8 @@ struct Barriers {
   int gave_up;
 };
 
-__device__ __forceinline__ void init_barriers(Barriers& b, int stages) {
-  for (int i = 0; i < stages; ++i) {
+__device__ __forceinline__ void init_barriers(Barriers& b) {
+  for (int i = 0; i < kMaxStages; ++i) {
     ptx::mbar_init(&b.full[i], 1);
     ptx::mbar_init(&b.empty[i], 1);
   }
@@ -212,26 +285,12 @@ __device__ __forceinline__ void drain_loads(Barriers& b, uint32_t it, uint32_t s
 
 __device__ __forceinline__ int chunks_of(int rows) { return (rows + kChunk - 1) / kChunk; }
 
-// One iteration of the matrix warp: kTiles products of 128 weight rows with
-// 16 * chunks token rows.  Tensor-memory tiles are kN columns apart.
-template <int kN, int kTiles>
-__device__ __forceinline__ bool mma_block(Barriers& b, const uint8_t* ring, int stage_bytes, uint32_t stages,
-                                          uint32_t it, int chunks) {
+// One thread issues 128 weight rows x 16 * chunks token rows over 128 of K.
+__device__ __forceinline__ void mma_tile(uint32_t tmem, const uint8_t* w, const uint8_t* x, int chunks) {
   const uint32_t instr = tc::instr_desc_e4m3(128, chunks * kChunk);
-  const uint32_t st = it % stages, buf = it & 1;
-  if (it >= 2 && !tc::wait(&b.acc_empty[buf], (it / 2 - 1) & 1, &b.gave_up)) return false;
-  if (!tc::wait(&b.full[st], (it / stages) & 1, &b.gave_up)) return false;
-  tc::fence_after();
-  const uint64_t w = tc::smem_desc(ring + st * stage_bytes);
-  const uint64_t x = tc::smem_desc(ring + st * stage_bytes + kTiles * kTileBytes);
+  const uint64_t wd = tc::smem_desc(w), xd = tc::smem_desc(x);
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int k = 0; k < kBlock / 32; ++k)
-      tc::mma_e4m3(b.tmem + (buf * kTiles + m) * kN, w + m * (kTileBytes >> 4) + 2 * k, x + 2 * k, instr, k > 0);
-  tc::commit(&b.empty[st]);
-  tc::commit(&b.acc_full[buf]);
-  return true;
+  for (int k = 0; k < kBlock / 32; ++k) tc::mma_e4m3(tmem, wd + 2 * k, xd + 2 * k, instr, k > 0);
 }
 
 __device__ __forceinline__ void finish_mma(Barriers& b) {  // nothing in flight when the tensor memory is freed
@@ -255,31 +314,25 @@ __device__ __forceinline__ void add_scaled(const uint32_t* v, const float* scale
 }
 
 // ---- first kernel -----------------------------------------------------------
-// Unit: (expert number a, block j of 128 columns of h).  The two epilogue
-// groups take the K blocks in turn, one tensor-memory buffer each; their sums
-// meet in shared memory, s_part[gate, up][token row][column], where the
-// token rows are then finished, each group every second one.
+// Unit: (expert number a, block j of 128 columns of h).  A thread of the
+// epilogue owns column j * 128 + threadIdx.x of h.  Two CTAs share an SM: where
+// units do not fill the last round, the ones left have the memory to
+// themselves, and one CTA's routing and epilogues pass while the other streams.
 template <int kN>
-__global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid_constant__ DecodeParams p,
-                                                                    uint32_t stages, uint32_t ranks) {
+__global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_constant__ DecodeParams p,
+                                                                 uint32_t ring_bytes, uint32_t ranks) {
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers b;
-  __shared__ uint64_t part_ready[2], part_free, amax_ready[2];
+  __shared__ uint64_t amax_ready[2];
   __shared__ RoutingShared rs;
-  __shared__ __align__(16) float s_scale[8][kN];
-  __shared__ float s_amax[kN][4];
-  constexpr int kStageBytes = 2 * kTileBytes + kN * kBlock;
+  __shared__ __align__(16) float s_scale[4][2][kN];
+  __shared__ __align__(16) float s_amax[2][kN][4];
   constexpr uint32_t kColumns = tmem_columns(4 * kN);
-  constexpr int kTmaWarp = kGluEpilogue / 32, kMmaWarp = kTmaWarp + 1;
   uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
-  float* s_part = reinterpret_cast<float*>(ring + stages * kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Routing r = routing_at(reinterpret_cast<uint8_t*>(s_part + 2 * kN * 128), ring, p.T * p.K, p.E);
+  const Routing r = routing_at(ring + ring_bytes, ring, p.T * p.K, p.E);
   if (threadIdx.x == 0) {
-    init_barriers(b, stages);
-    ptx::mbar_init(&part_ready[0], 4);
-    ptx::mbar_init(&part_ready[1], 4);
-    ptx::mbar_init(&part_free, 8);
+    init_barriers(b);
     ptx::mbar_init(&amax_ready[0], 4);
     ptx::mbar_init(&amax_ready[1], 4);
     ptx::mbar_fence_init();
@@ -299,6 +352,9 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
   ptx::launch_dependents();
   build_routing(r, rs, p);
   tc::fence_after();
+  // Stages as large as the fullest expert needs.
+  const uint32_t stage_bytes = 2 * kTileBytes + chunks_of(rs.most_rows) * kChunk * kBlock;
+  const uint32_t stages = min(ring_bytes / stage_bytes, static_cast<uint32_t>(kMaxStages));
   const int jb = p.I / kBlock, kb_all = p.H / kBlock;
   const int units = rs.bad ? 0 : rs.n_active * jb;
   const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
@@ -307,33 +363,62 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = rs.bad ? MOE_EROUTE : MOE_OK;
   bool ok = true;
 
-  // Epilogue: h of the unit's token rows from the sums in s_part (of all
-  // ranks' CTAs), quantised.  Group w takes rows w, w + 2, ...
+  unsigned long long gate[kN / 2], up[kN / 2];
+  // Epilogue warps: h of the unit's token rows from the sums, quantised.
   auto finish = [&](int u, int round) -> bool {
     const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
-    const int group = warp >> 2, column = threadIdx.x & 127;
-    for (int c = group; c < n; c += 2) {
-      float* at = s_part + c * 128 + column;
-      float g = at[0], v = at[kN * 128];
-      for (uint32_t q = 1; q < ranks; ++q) {
-        g += ld_cluster(at, q);
-        v += ld_cluster(at + kN * 128, q);
+    float (*amax)[4] = s_amax[round & 1];  // in turn: a warp one unit ahead does not overwrite
+#pragma unroll
+    for (int c0 = 0; c0 < kN; c0 += kChunk) {
+      if (c0 < n) {
+        float h[kChunk];
+        uint32_t top[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          const int c = c0 + i;
+          const float g = c & 1 ? tc::hi2(gate[c / 2]) : tc::lo2(gate[c / 2]);
+          const float v = c & 1 ? tc::hi2(up[c / 2]) : tc::lo2(up[c / 2]);
+          // Of a denominator beyond 2^126 the quotient becomes 0; it is below 2^-119 there.
+          h[i] = __fdividef(g, 1.0f + expf(-g)) * v;
+          top[i] = __float_as_uint(fabsf(h[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          if (lane == 0) amax[c0 + i][warp] = __uint_as_float(top[i]);
+          if (i & 1) gate[(c0 + i) / 2] = tc::pack2(h[i - 1], h[i]);
+        }
       }
-      g = g / (1.0f + expf(-g)) * v;
-      *at = g;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(g)));
-      if (lane == 0) s_amax[c][warp & 3] = __uint_as_float(top);
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&amax_ready[group]);
-    const bool all = tc::wait(&amax_ready[group], round & 1, &b.gave_up);
+    if (lane == 0) tc::mbar_arrive(&amax_ready[round & 1]);
+    const bool all = tc::wait(&amax_ready[round & 1], (round >> 1) & 1, &b.gave_up);
     if (!__all_sync(0xffffffffu, all)) return false;
-    for (int c = group; c < n; c += 2) {
-      const float top = fmaxf(fmaxf(s_amax[c][0], s_amax[c][1]), fmaxf(s_amax[c][2], s_amax[c][3]));
-      const float scale = top > 0.0f ? __fdiv_rn(fmaxf(top, kTinyAmax), 448.0f) : 1.0f;
-      const float h = __fmul_rn(s_part[c * 128 + column], __fdiv_rn(1.0f, scale));
-      p.hq[static_cast<int64_t>(row0 + c) * p.I + j * kBlock + column] = static_cast<uint8_t>(fp8q::e4m3x2(h, 0.0f));
-      if (column == 0) p.h_scales[static_cast<int64_t>(row0 + c) * jb + j] = scale;
+    uint8_t* dst = p.hq + static_cast<int64_t>(row0) * p.I + j * kBlock + threadIdx.x;
+    // A lane computes the scale of its column of tokens; all use it.
+#pragma unroll
+    for (int c0 = 0; c0 < kN; c0 += 32) {
+      if (c0 < n) {
+        const float4 m = *reinterpret_cast<const float4*>(amax[c0 + (lane & (kN < 32 ? kN - 1 : 31))]);
+        const float top = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
+        const float scale = top > 0.0f ? __fdiv_rn(fmaxf(top, kTinyAmax), 448.0f) : 1.0f;
+        const float inv = __fdiv_rn(1.0f, scale);
+        if (warp == 0 && c0 + lane < n) p.h_scales[static_cast<int64_t>(row0 + c0 + lane) * jb + j] = scale;
+#pragma unroll
+        for (int i0 = 0; i0 < 32 && c0 + i0 < kN; i0 += kChunk) {
+          if (c0 + i0 < n) {
+#pragma unroll
+            for (int i = i0; i < i0 + kChunk; ++i) {
+              const int c = c0 + i;
+              const float h = c & 1 ? tc::hi2(gate[c / 2]) : tc::lo2(gate[c / 2]);
+              const float f = __shfl_sync(0xffffffffu, inv, i);
+              const uint8_t q = static_cast<uint8_t>(fp8q::e4m3x2(__fmul_rn(h, f), 0.0f));
+              if (c < n) dst[static_cast<int64_t>(c) * p.I] = q;
+            }
+          }
+        }
+      }
     }
     return true;
   };
@@ -352,7 +437,7 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
             ok = false;
             break;
           }
-          uint8_t* to = ring + st * kStageBytes;
+          uint8_t* to = ring + st * stage_bytes;
           const int k = (kb0 + kb) * kBlock;
           ptx::mbar_arrive_expect_tx(&b.full[st], 2 * kTileBytes + rows * kBlock);
           tc::tma_load_2d(to, &p.w13_map, k, w0, &b.full[st]);
@@ -371,16 +456,24 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
       uint32_t it = 0;
       for (int u = u0; ok && u < units; u += step) {
         const int a = u / jb, chunks = chunks_of(r.first[a + 1] - r.first[a]);
-        for (int kb = 0; ok && kb < kb_n; ++kb, ++it)
-          ok = mma_block<kN, 2>(b, ring, kStageBytes, stages, it, chunks);
+        for (int kb = 0; kb < kb_n; ++kb, ++it) {
+          const uint32_t st = it % stages, buf = it & 1;
+          ok = (it < 2 || tc::wait(&b.acc_empty[buf], (it / 2 - 1) & 1, &b.gave_up)) &&
+               tc::wait(&b.full[st], (it / stages) & 1, &b.gave_up);
+          if (!ok) break;
+          tc::fence_after();
+          const uint8_t* at = ring + st * stage_bytes;
+          mma_tile(b.tmem + buf * 2 * kN, at, at + 2 * kTileBytes, chunks);
+          mma_tile(b.tmem + (buf * 2 + 1) * kN, at + kTileBytes, at + 2 * kTileBytes, chunks);
+          tc::commit(&b.empty[st]);
+          tc::commit(&b.acc_full[buf]);
+        }
       }
       finish_mma(b);
     }
   } else {
-    const int group = warp >> 2, column = threadIdx.x & 127;
-    const uint32_t lanes = b.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * 2 * kN;
-    float* scale = s_scale[warp];
-    uint32_t it = 0;  // of the whole CTA; this group takes those with it % 2 == group
+    const uint32_t lanes = b.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    uint32_t it = 0;
     int round = 0;
     for (int u = u0; ok && u < units; u += step, ++round) {
       const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
@@ -390,7 +483,7 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < (kN + 31) / 32; ++i)
         sx[i] = p.x_scales + static_cast<int64_t>(r.token[row0 + min(lane + 32 * i, n - 1)]) * kb_all + kb0;
-      // The scales of this group's next K block are read a turn ahead.
+      // The scales of the next K block are read a block ahead.
       float next[(kN + 31) / 32], next_g, next_u;
       auto read = [&](int kb) {
 #pragma unroll
@@ -399,20 +492,18 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
         next_g = sg[kb];
         next_u = su[kb];
       };
-      unsigned long long gate[kN / 2], up[kN / 2];
+      read(0);
 #pragma unroll
       for (int c = 0; c < kN / 2; ++c) gate[c] = up[c] = 0;
-      int kb = (it & 1) == static_cast<uint32_t>(group) ? 0 : 1;
-      if (kb < kb_n) read(kb);
-      for (; kb < kb_n; kb += 2) {
-        const uint32_t at = it + kb;
-        __syncwarp();  // the last turn's scales have been read
+      for (int kb = 0; kb < kb_n; ++kb, ++it) {
+        const uint32_t buf = it & 1;
+        float* scale = s_scale[warp][buf];
 #pragma unroll
         for (int i = 0; i < (kN + 31) / 32; ++i)
           if (32 * i < n && lane + 32 * i < kN) scale[lane + 32 * i] = next[i];
         const unsigned long long fg = tc::pack2(next_g, next_g), fu = tc::pack2(next_u, next_u);
-        if (kb + 2 < kb_n) read(kb + 2);
-        ok = tc::wait(&b.acc_full[group], (at / 2) & 1, &b.gave_up);
+        if (kb + 1 < kb_n) read(kb + 1);
+        ok = tc::wait(&b.acc_full[buf], (it / 2) & 1, &b.gave_up);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -422,56 +513,64 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < kN; c += kChunk) {
           if (c < n) {
-            uint32_t vg[kChunk], vu[kChunk];
-            tc::tmem_load_16(lanes + c, vg);
-            tc::tmem_load_16(lanes + kN + c, vu);
+            uint32_t v[kChunk];
+            tc::tmem_load_16(lanes + buf * 2 * kN + c, v);
             tc::wait_loads();
-            add_scaled(vg, scale + c, fg, gate + c / 2);
-            add_scaled(vu, scale + c, fu, up + c / 2);
+            add_scaled(v, scale + c, fg, gate + c / 2);
+            tc::tmem_load_16(lanes + (buf * 2 + 1) * kN + c, v);
+            tc::wait_loads();
+            add_scaled(v, scale + c, fu, up + c / 2);
           }
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&b.acc_empty[group]);
+        if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
       }
-      it += kb_n;
-      if (!ok) break;
-      // The second group's sums, then both: s_part is written in full by each
-      // group, the second time on top of the first.
-      if (round > 0) ok = tc::wait(&part_free, (round - 1) & 1, &b.gave_up);
-      if (group == 0 && ok) ok = tc::wait(&part_ready[1], round & 1, &b.gave_up);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-#pragma unroll
-      for (int c = 0; c < kN; ++c) {
-        if (c / kChunk * kChunk < n) {
-          float g = c & 1 ? tc::hi2(gate[c / 2]) : tc::lo2(gate[c / 2]);
-          float v = c & 1 ? tc::hi2(up[c / 2]) : tc::lo2(up[c / 2]);
-          float* to = s_part + c * 128 + column;
-          if (group == 0) {
-            g += to[0];
-            v += to[kN * 128];
-          }
-          to[0] = g;
-          to[kN * 128] = v;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&part_ready[group]);
-      if (ranks == 1) {
-        ok = tc::wait(&part_ready[0], round & 1, &b.gave_up);
-        ok = __all_sync(0xffffffffu, ok) && finish(u, round);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&part_free);
-      }
+      if (ok && ranks == 1) ok = finish(u, round);
     }
   }
-  if (ranks > 1) {  // one unit a cluster: its sums meet in rank 0
+  if (ranks > 1) {
+    // One unit a cluster: its sums meet in rank 0, through the ring, which is
+    // free now: every load has been consumed.  [gate, up][token row][column]
+    float* part = reinterpret_cast<float*>(ring);
+    const bool mine = warp < kTmaWarp && ok && u0 < units;
+    const int n = u0 < units ? r.first[u0 / jb + 1] - r.first[u0 / jb] : 0;
+    __syncthreads();
+    if (mine) {
+#pragma unroll
+      for (int c = 0; c < kN; c += 8) {
+        if (c < n) {
+#pragma unroll
+          for (int i = c; i < c + 8; ++i) {
+            part[i * 128 + threadIdx.x] = i & 1 ? tc::hi2(gate[i / 2]) : tc::lo2(gate[i / 2]);
+            part[(kN + i) * 128 + threadIdx.x] = i & 1 ? tc::hi2(up[i / 2]) : tc::lo2(up[i / 2]);
+          }
+        }
+      }
+    }
     __syncthreads();
     cluster_sync();
-    if (warp < kTmaWarp && rank == 0 && ok && u0 < units) finish(u0, 0);
+    if (mine && rank == 0) {
+      for (uint32_t q = 1; q < ranks; ++q) {
+#pragma unroll
+        for (int c = 0; c < kN; c += 8) {
+          if (c < n) {
+            float v[16];  // all on their way before the first is needed
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[i] = ld_cluster(part + (c + i) * 128 + threadIdx.x, q);
+              v[8 + i] = ld_cluster(part + (kN + c + i) * 128 + threadIdx.x, q);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              gate[(c + i) / 2] = tc::add2(gate[(c + i) / 2], tc::pack2(v[i], v[i + 1]));
+              up[(c + i) / 2] = tc::add2(up[(c + i) / 2], tc::pack2(v[8 + i], v[9 + i]));
+            }
+          }
+        }
+      }
+      finish(u0, 0);
+    }
     __syncthreads();
     cluster_sync();  // no CTA leaves while its shared memory is being read
   }
@@ -486,23 +585,23 @@ __global__ void __launch_bounds__(kGluThreads, 1) decode_glu_kernel(const __grid
 // A cluster owns 128 columns of out.  Its CTAs share the (expert, K block)
 // items, each a contiguous range; what an expert gives to token t is added to
 // the CTA's s_out[t][column] when the CTA's part of that expert is complete
-// (dense: one expert, row i is token i with weight 1).
+// (dense: one expert, row i is token i with weight 1).  The ring has a stage an
+// item; the matrix warp and the epilogue take two items of an expert at a time,
+// which halves what a turn costs the epilogue beside its sums.
 template <int kN, bool kDense>
-__global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
-    few_rows_kernel(const __grid_constant__ DecodeParams p, uint32_t stages, uint32_t ranks) {
+__global__ void __launch_bounds__(kThreads, 2)
+    few_rows_kernel(const __grid_constant__ DecodeParams p, uint32_t ring_bytes, uint32_t ranks) {
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers b;
   __shared__ RoutingShared rs;
-  __shared__ __align__(16) float s_scale[4][2][kN];
-  constexpr int kStageBytes = kTileBytes + kN * kBlock;
-  constexpr uint32_t kColumns = tmem_columns(2 * kN);
-  constexpr int kTmaWarp = kFewEpilogue / 32, kMmaWarp = kTmaWarp + 1;
+  __shared__ __align__(16) float s_scale[4][2][2][kN];  // [warp][buffer][item]
+  constexpr uint32_t kColumns = tmem_columns(4 * kN);
   uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
-  float* s_out = reinterpret_cast<float*>(ring + stages * kStageBytes);  // [T][128]
+  float* s_out = reinterpret_cast<float*>(ring + ring_bytes);  // [T][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Routing r = {};
   if (threadIdx.x == 0) {
-    init_barriers(b, stages);
+    init_barriers(b);
     ptx::mbar_fence_init();
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&b.tmem, kColumns);
@@ -512,13 +611,15 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
   }
   tc::fence_before();
   if (kDense) {
-    if (threadIdx.x == 0) rs.bad = 0, rs.n_active = 1;
+    if (threadIdx.x == 0) rs.bad = 0, rs.n_active = 1, rs.most_rows = p.T;
     __syncthreads();
   } else {
     r = routing_at(reinterpret_cast<uint8_t*>(s_out + p.T * 128), ring, p.T * p.K, p.E);
     build_routing(r, rs, p);  // topk_idx and topk_w: see the first kernel's launch_dependents
   }
   tc::fence_after();
+  const uint32_t stage_bytes = kTileBytes + chunks_of(rs.most_rows) * kChunk * kBlock;
+  const uint32_t stages = min(ring_bytes / stage_bytes, static_cast<uint32_t>(kMaxStages));
   const int tile = static_cast<int>(blockIdx.x / ranks);
   const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
   const int kb_n = p.h_blocks;
@@ -535,13 +636,13 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
       auto load_w = [&](int i) {
         const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
         ptx::mbar_arrive_expect_tx(&b.full[st], kTileBytes + chunks_of(rows_of(a)) * kChunk * kBlock);
-        tc::tma_load_2d(ring + st * kStageBytes, &p.w2_map, kb * kBlock, (kDense ? 0 : r.active[a]) * p.H + tile * 128,
+        tc::tma_load_2d(ring + st * stage_bytes, &p.w2_map, kb * kBlock, (kDense ? 0 : r.active[a]) * p.H + tile * 128,
                         &b.full[st]);
       };
       auto load_h = [&](int i) {
         const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
         for (int c = 0; c < rows_of(a); c += kChunk)
-          tc::tma_load_2d(ring + st * kStageBytes + kTileBytes + c * kBlock, &p.h_map, kb * kBlock, row0_of(a) + c,
+          tc::tma_load_2d(ring + st * stage_bytes + kTileBytes + c * kBlock, &p.h_map, kb * kBlock, row0_of(a) + c,
                           &b.full[st]);
       };
       const int early = min(n, static_cast<int>(stages));
@@ -563,9 +664,23 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       int a = it0 / kb_n, kb = it0 - a * kb_n;
-      for (int i = 0; ok && i < n; ++i) {
-        ok = mma_block<kN, 1>(b, ring, kStageBytes, stages, i, chunks_of(rows_of(a)));
-        if (++kb == kb_n) kb = 0, ++a;
+      for (int i = 0, turn = 0; i < n; ++turn) {
+        const uint32_t buf = turn & 1;
+        const int two = i + 1 < n && kb + 1 < kb_n ? 2 : 1, chunks = chunks_of(rows_of(a));
+        ok = turn < 2 || tc::wait(&b.acc_empty[buf], (turn / 2 - 1) & 1, &b.gave_up);
+        for (int m = 0; ok && m < two; ++m, ++i) {
+          const uint32_t st = i % stages;
+          ok = tc::wait(&b.full[st], (i / stages) & 1, &b.gave_up);
+          if (!ok) break;
+          tc::fence_after();
+          const uint8_t* at = ring + st * stage_bytes;
+          mma_tile(b.tmem + (buf * 2 + m) * kN, at, at + kTileBytes, chunks);
+          tc::commit(&b.empty[st]);
+        }
+        if (!ok) break;
+        tc::commit(&b.acc_full[buf]);
+        kb += two;
+        if (kb == kb_n) kb = 0, ++a;
       }
       finish_mma(b);
     }
@@ -580,29 +695,40 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
 #pragma unroll
     for (int c = 0; c < kN / 2; ++c) acc[c] = 0;
     int a = it0 / kb_n, kb = it0 - a * kb_n;
-    float next[(kN + 31) / 32], next_w = 0.0f;
-    auto read = [&](int a, int kb) {  // the scales of the next item, an item ahead
+    float next[2][(kN + 31) / 32], next_w[2];
+    auto read = [&](int a, int kb, int two) {  // the scales of the next turn, a turn ahead
       const int row0 = row0_of(a), rows = rows_of(a);
 #pragma unroll
-      for (int i = 0; i < (kN + 31) / 32; ++i)
-        if (32 * i < rows)
-          next[i] = ld_f32(p.h_scales + static_cast<int64_t>(row0 + min(lane + 32 * i, rows - 1)) * kb_n + kb);
-      next_w = ld_f32(sw + (kDense ? 0 : r.active[a]) * sw_expert + kb);
+      for (int m = 0; m < 2; ++m) {
+        if (m < two) {
+#pragma unroll
+          for (int i = 0; i < (kN + 31) / 32; ++i)
+            if (32 * i < rows)
+              next[m][i] = ld_f32(p.h_scales + static_cast<int64_t>(row0 + min(lane + 32 * i, rows - 1)) * kb_n + kb + m);
+          next_w[m] = ld_f32(sw + (kDense ? 0 : r.active[a]) * sw_expert + kb + m);
+        }
+      }
     };
-    if (n > 0) read(a, kb);
-    for (int i = 0; i < n; ++i) {
-      const uint32_t buf = i & 1;
-      const int row0 = row0_of(a), rows = rows_of(a);
-      float* scale = s_scale[warp][buf];
+    int two = n > 1 && kb + 1 < kb_n ? 2 : 1;
+    if (n > 0) read(a, kb, two);
+    for (int i = 0, turn = 0; i < n; ++turn) {
+      const uint32_t buf = turn & 1;
+      const int row0 = row0_of(a), rows = rows_of(a), two_now = two;
+      unsigned long long f[2];
 #pragma unroll
-      for (int c = 0; c < (kN + 31) / 32; ++c)
-        if (32 * c < rows && lane + 32 * c < kN) scale[lane + 32 * c] = next[c];
-      const unsigned long long f = tc::pack2(next_w, next_w);
-      const bool last = kb + 1 == kb_n;
-      a = last ? a + 1 : a;
-      kb = last ? 0 : kb + 1;
-      if (i + 1 < n) read(a, kb);
-      ok = tc::wait(&b.acc_full[buf], (i / 2) & 1, &b.gave_up);
+      for (int m = 0; m < 2; ++m) {
+        f[m] = tc::pack2(next_w[m], next_w[m]);
+#pragma unroll
+        for (int c = 0; c < (kN + 31) / 32; ++c)
+          if (32 * c < rows && lane + 32 * c < kN) s_scale[warp][buf][m][lane + 32 * c] = next[m][c];
+      }
+      i += two_now;
+      kb += two_now;
+      const bool last = kb == kb_n;
+      if (last) kb = 0, ++a;
+      two = i + 1 < n && kb + 1 < kb_n ? 2 : 1;
+      if (i < n) read(a, kb, two);
+      ok = tc::wait(&b.acc_full[buf], (turn / 2) & 1, &b.gave_up);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -612,26 +738,40 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
 #pragma unroll
       for (int c = 0; c < kN; c += kChunk) {
         if (c < rows) {
-          uint32_t v[kChunk];
-          tc::tmem_load_16(lanes + buf * kN + c, v);
+          uint32_t v[2][kChunk];
+          tc::tmem_load_16(lanes + buf * 2 * kN + c, v[0]);
+          if (two_now == 2) tc::tmem_load_16(lanes + (buf * 2 + 1) * kN + c, v[1]);
           tc::wait_loads();
-          add_scaled(v, scale + c, f, acc + c / 2);
+          add_scaled(v[0], s_scale[warp][buf][0] + c, f[0], acc + c / 2);
+          if (two_now == 2) add_scaled(v[1], s_scale[warp][buf][1] + c, f[1], acc + c / 2);
         }
       }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
-      if (last || i + 1 == n) {
+      if (last || i == n) {
 #pragma unroll
-        for (int c = 0; c < kN; ++c) {
-          if (c / kChunk * kChunk < rows) {
-            const float v = c & 1 ? tc::hi2(acc[c / 2]) : tc::lo2(acc[c / 2]);
-            if (c < rows) {
-              if (kDense) {
-                mine[c * 128] = v;
-              } else {
-                float* o = mine + r.token[row0 + c] * 128;
-                *o = fmaf(r.weight[row0 + c], v, *o);
+        for (int c0 = 0; c0 < kN; c0 += 8) {
+          if (c0 < rows) {
+            float* at[8];
+            float old[8], weight[8];
+            if (!kDense) {  // the token rows of an expert are different tokens
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int row = row0 + min(c0 + i, rows - 1);
+                at[i] = mine + r.token[row] * 128;
+                weight[i] = r.weight[row];
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) old[i] = *at[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = c0 + i;
+              const float v = c & 1 ? tc::hi2(acc[c / 2]) : tc::lo2(acc[c / 2]);
+              if (c < rows) {
+                if (kDense) mine[c * 128] = v;
+                else *at[i] = fmaf(weight[i], v, old[i]);
               }
             }
           }
@@ -645,14 +785,31 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
   __syncthreads();
   if (ranks > 1) cluster_sync();
   const int column = tile * 128 + static_cast<int>(threadIdx.x);
+  constexpr int kBatch = kN / 8;
   if (threadIdx.x < 128 && !rs.bad && !b.gave_up && column < p.H) {
-    for (int t = rank; t < p.T; t += ranks) {
-      const float* at = s_out + t * 128 + threadIdx.x;
-      float sum = 0.0f;
-      for (uint32_t q = 0; q < ranks; ++q) sum += q == rank ? *at : ld_cluster(at, q);
-      const int64_t to = static_cast<int64_t>(t) * p.H + column;
-      if (p.out_f32) reinterpret_cast<float*>(p.out)[to] = sum;
-      else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(sum);
+    for (int t0 = rank; t0 < p.T; t0 += kBatch * ranks) {
+      float v[kBatch][kMaxRanks];  // all on their way before the first is needed
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m) {
+        const int t = min(t0 + m * static_cast<int>(ranks), p.T - 1);
+        const float* at = s_out + t * 128 + threadIdx.x;
+#pragma unroll
+        for (int q = 0; q < kMaxRanks; ++q)
+          if (q < static_cast<int>(ranks)) v[m][q] = q == static_cast<int>(rank) ? *at : ld_cluster(at, q);
+      }
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m) {
+        const int t = t0 + m * static_cast<int>(ranks);
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kMaxRanks; ++q)
+          if (q < static_cast<int>(ranks)) sum += v[m][q];
+        const int64_t to = static_cast<int64_t>(t) * p.H + column;
+        if (t < p.T) {
+          if (p.out_f32) reinterpret_cast<float*>(p.out)[to] = sum;
+          else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(sum);
+        }
+      }
     }
   }
   __syncthreads();
@@ -664,12 +821,14 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 32 ? 3 : 2)
   if (warp == kMmaWarp) tc::tmem_free(b.tmem, kColumns);
 }
 
-cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), const DecodeParams& p, int threads,
-                           uint32_t stages, uint32_t ranks, unsigned groups, size_t smem, cudaStream_t stream) {
+cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), const DecodeParams& p, size_t rest,
+                           size_t ring, uint32_t ranks, unsigned groups, cudaStream_t stream) {
+  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), rest + ring);
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(groups * ranks);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = rest + ring;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -679,41 +838,47 @@ cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), con
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ranks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, stages, ranks);
+  return cudaLaunchKernelEx(&cfg, kernel, p, static_cast<uint32_t>(ring), ranks);
 }
+
+// Dynamic shared memory of one of two CTAs on an SM, and of a CTA that has one
+// to itself: without the static part (up to 5 KiB) and the driver's 1 KiB.
+constexpr size_t kHalfSm = 228 * 1024 / 2 - 6 * 1024, kWholeSm = 228 * 1024 - 6 * 1024;
+#ifdef SWEEP
+}
+#include <cstdlib>
+namespace {
+size_t env(const char* n, size_t d) { const char* v = std::getenv(n); return v ? std::atoi(v) : d; }
+#else
+size_t env(const char*, size_t d) { return d; }
+#endif
 
 template <int kN>
 cudaError_t launch_glu(const DecodeParams& p, int sms, cudaStream_t stream) {
-  constexpr uint32_t kStages = kN == 16 ? 5 : kN == 32 ? 4 : 3;
   const int pairs = p.T * p.K;
-  const size_t smem = 1024 + static_cast<size_t>(kStages) * (2 * kTileBytes + kN * kBlock) + 2 * kN * 128 * 4 +
-                      routing_bytes(pairs, p.E);
-  auto* kernel = decode_glu_kernel<kN>;
-  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
-  if (err != cudaSuccess) return err;
+  const size_t rest = 1024 + routing_bytes(pairs, p.E);
   int64_t units = static_cast<int64_t>(max_active(pairs, p.E)) * (p.I / kBlock);
-  uint32_t ranks = 1;  // too few units for the SMs: split them along K
-  while (ranks < 8 && units * ranks * 2 <= sms && static_cast<int>(ranks) * 2 <= p.H / kBlock) ranks *= 2;
-  if (ranks == 1 && units > sms) units = sms;
-  return launch_cluster(kernel, p, kGluThreads, kStages, ranks, static_cast<unsigned>(units), smem, stream);
+  // Too few units for the SMs: split them along K, eight blocks or more each.
+  uint32_t ranks = 1;
+  while (ranks < 8 && units * ranks * 2 <= sms && static_cast<int>(ranks) * 16 <= p.H / kBlock) ranks *= 2;
+  if (ranks == 1 && units > 2 * sms) units = 2 * sms;
+  return launch_cluster(decode_glu_kernel<kN>, p, rest, env("GLU", kHalfSm) - rest, ranks, static_cast<unsigned>(units), stream);
 }
 
 template <int kN, bool kDense>
 cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
-  constexpr uint32_t kStages = 3;
   const int pairs = p.T * p.K;
-  const size_t ring = static_cast<size_t>(kStages) * (kTileBytes + kN * kBlock);
-  const size_t smem = 1024 + ring + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E));
-  auto* kernel = few_rows_kernel<kN, kDense>;
-  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
-  if (err != cudaSuccess) return err;
-  // CTAs that fit on an SM: by shared memory (2 KiB of it static), and by the launch bounds.
-  const int64_t resident = std::min(smem_ctas_per_sm(smem + 2048), kN <= 32 ? 3 : 2);
-  const int tiles = (p.H + 127) / 128;
+  const size_t rest = 1024 + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E));
+  const int64_t tiles = (p.H + 127) / 128;
   const int64_t items = static_cast<int64_t>(kDense ? 1 : max_active(pairs, p.E)) * p.h_blocks;
+  // Up to 16 rows two CTAs share an SM, else their sums leave too little for the rings.
+  const int per_sm = kN == 16 ? 2 : 1;
   uint32_t ranks = 1;
-  while (ranks < 8 && tiles * static_cast<int64_t>(ranks) * 2 <= sms * resident && ranks * 2 <= items) ranks *= 2;
-  return launch_cluster(kernel, p, kFewThreads, kStages, ranks, static_cast<unsigned>(tiles), smem, stream);
+  while (ranks < kMaxRanks && tiles * ranks * 2 <= per_sm * sms && ranks * 2 * 4 <= items) ranks *= 2;
+  size_t ring = (tiles * ranks > sms ? kHalfSm : kWholeSm) - rest;
+  ring = env("FEW", ring);
+  const size_t most = (items + ranks - 1) / ranks * (kTileBytes + kN * kBlock);  // a stage for each item
+  return launch_cluster(few_rows_kernel<kN, kDense>, p, rest, std::min(ring, most), ranks, static_cast<unsigned>(tiles), stream);
 }
 
 // Most token columns a kernel variant holds, for this many tokens.
