@@ -42,6 +42,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "ffn_kernels.cuh"
 #include "fp8_quant.cuh"
@@ -78,10 +81,13 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
 }
 
 // ---- routing -------------------------------------------------------------------
-// Rows are the pairs ordered by (expert, token); expert number a is the a-th
-// that has any.
+// Rows are the pairs ordered by (expert, token).  An expert with more rows than
+// a tile has columns (kN) appears several times in the list of those at work,
+// with up to kN of its rows each: its weights are then read again, mostly from
+// L2.  (A variant with 64 columns for 64 tokens needed registers for all of
+// them whatever an expert had, and was slower on the usual experts.)
 struct Routing {
-  int32_t* active;   // the experts that have rows, ascending
+  int32_t* active;   // the experts at work, ascending
   int32_t* first;    // their first rows, then the number of rows
   int32_t* token;    // of each row
   float* weight;     // topk_w of each row
@@ -95,17 +101,17 @@ struct RoutingShared {
   int32_t most_rows;  // of one expert
 };
 
-__host__ __device__ inline int max_active(int pairs, int E) { return pairs < E ? pairs : E; }
-__host__ __device__ inline int routing_bytes(int pairs, int E) {
-  const int a = max_active(pairs, E);
+__host__ __device__ inline int max_active(int pairs, int E, int kN) { return (pairs < E ? pairs : E) + pairs / kN; }
+__host__ __device__ inline int routing_bytes(int pairs, int E, int kN) {
+  const int a = max_active(pairs, E, kN);
   return (a * 4 + (a + 1) * 4 + pairs * 8 + 15) / 16 * 16;
 }
 
 // What build_routing needs besides lies at the start of the ring, before any load.
 static_assert(MOE_MAX_EXPERTS * 12 <= kTileBytes && 32 * 8 <= kTileBytes, "scratch fits in one stage");
 
-__device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, int pairs, int E) {
-  const int a = max_active(pairs, E);
+__device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, int pairs, int E, int kN) {
+  const int a = max_active(pairs, E, kN);
   Routing r;
   r.active = reinterpret_cast<int32_t*>(smem);
   r.first = r.active + a;
@@ -120,10 +126,10 @@ __device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, i
 // pair counts the pairs before it, which spares the per-expert masks and their
 // scan (8 pairs of 256 experts: 1.6 instead of 2.1 us from the launch's wait;
 // with 128 pairs the counting takes 6.8 us).
-__device__ __forceinline__ void build_routing_small(const Routing& r, RoutingShared& s, const DecodeParams& p) {
+__device__ __forceinline__ void build_routing_small(const Routing& r, RoutingShared& s, const DecodeParams& p, int kN) {
   const int pairs = p.T * p.K, i = threadIdx.x;
   int32_t* expert = reinterpret_cast<int32_t*>(r.mask);  // [pairs]
-  int32_t* heads = expert + pairs;                       // [pairs] whether the pair is its expert's first
+  int32_t* heads = expert + pairs;                       // [pairs] whether the pair begins a list entry
   int e = 0;
   float w = 0.0f;
   if (i < pairs) {
@@ -134,7 +140,7 @@ __device__ __forceinline__ void build_routing_small(const Routing& r, RoutingSha
   if (i == 0) s.bad = 0, s.most_rows = 1;
   __syncthreads();
   int row = 0;
-  bool head = i < pairs;
+  bool head = false;  // the first of its expert's rows in a list entry
   if (i < pairs) {
     const int t0 = i / p.K * p.K;  // the token's first pair
     int before_me = 0;
@@ -144,11 +150,11 @@ __device__ __forceinline__ void build_routing_small(const Routing& r, RoutingSha
       const bool before = other == e && j < i;
       row += other < e || before;
       before_me += before;
-      head = head && !before;
       if (before && j >= t0) s.bad = 1;  // repeated within the token
     }
+    head = before_me % kN == 0;
     heads[i] = head;
-    if (before_me > 0) atomicMax(&s.most_rows, before_me + 1);
+    atomicMax(&s.most_rows, min(before_me + 1, kN));
   }
   __syncthreads();
   if (s.bad) return;  // the same for the whole CTA
@@ -156,23 +162,23 @@ __device__ __forceinline__ void build_routing_small(const Routing& r, RoutingSha
     r.token[row] = i / p.K;
     r.weight[row] = w;
     int a = 0;
-    for (int j = 0; j < pairs; ++j) a += heads[j] && expert[j] < e;
+    for (int j = 0; j < pairs; ++j) a += heads[j] && (expert[j] < e || (expert[j] == e && j < i));
     if (head) {
       r.active[a] = e;
       r.first[a] = row;
     }
-    if (row == pairs - 1) {  // of the last expert
-      s.n_active = a + 1;
-      r.first[a + 1] = pairs;
+    if (row == pairs - 1) {  // of the last entry
+      s.n_active = head ? a + 1 : a;
+      r.first[s.n_active] = pairs;
     }
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s, const DecodeParams& p) {
+__device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s, const DecodeParams& p, int kN) {
   const int pairs = p.T * p.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (pairs <= 32) {
-    build_routing_small(r, s, p);
+    build_routing_small(r, s, p, kN);
     return;
   }
   constexpr int kMost = (kFewRows * MOE_MAX_TOP_K + kThreads - 1) / kThreads;
@@ -206,10 +212,10 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
     const int e = c * 32 + lane;
     const int n = e < p.E ? __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1]) : 0;
     const int rows = __reduce_add_sync(0xffffffffu, n), most = __reduce_max_sync(0xffffffffu, n);
-    const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+    const int entries = __reduce_add_sync(0xffffffffu, (n + kN - 1) / kN);
     if (lane == 0) {
-      atomicMax(&s.most_rows, most);
-      s.warp_active[c] = __popc(some);
+      atomicMax(&s.most_rows, min(most, kN));
+      s.warp_active[c] = entries;
       s.warp_rows[c] = rows;
     }
   }
@@ -219,20 +225,23 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
     const int n = e < p.E ? __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1]) : 0;
     const int base = __reduce_add_sync(0xffffffffu, lane < c ? s.warp_active[lane] : 0);
     const int base_row = __reduce_add_sync(0xffffffffu, lane < c ? s.warp_rows[lane] : 0);
-    const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
-    int sum = n;
+    const int entries = (n + kN - 1) / kN;
+    int sum = n << 16 | entries;  // both running sums at once: at most 1024 rows
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, sum, d);
       if (lane >= d) sum += up;
     }
     if (n > 0) {
-      const int a = base + __popc(some & ((1u << lane) - 1));
-      r.active[a] = e;
-      r.first[a] = r.row_of[e] = base_row + sum - n;
+      const int a = base + (sum & 0xffff) - entries, row = base_row + (sum >> 16) - n;
+      r.row_of[e] = row;
+      for (int k = 0; k < entries; ++k) {
+        r.active[a + k] = e;
+        r.first[a + k] = row + k * kN;
+      }
     }
-    if (c == chunks - 1 && lane == 0) {
-      s.n_active = base + __popc(some);
+    if (c == chunks - 1 && lane == 31) {
+      s.n_active = base + (sum & 0xffff);
       r.first[s.n_active] = pairs;
     }
   }
@@ -271,6 +280,16 @@ __device__ __forceinline__ void init_barriers(Barriers& b) {
   ptx::mbar_init(&b.drained, 1);
   b.gave_up = 0;
 }
+
+// A place in the ring and how often it has been passed, counted without
+// divisions: one thread issues all loads, another all matrix instructions, and
+// each has to keep up with the memory.
+struct Place {
+  uint32_t st = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++st == stages) st = 0, phase ^= 1;
+  }
+};
 
 // The scratch that build_routing wrote lies where TMA will write next.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -315,9 +334,10 @@ __device__ __forceinline__ void add_scaled(const uint32_t* v, const float* scale
 
 // ---- first kernel -----------------------------------------------------------
 // Unit: (expert number a, block j of 128 columns of h).  A thread of the
-// epilogue owns column j * 128 + threadIdx.x of h.  Two CTAs share an SM: where
-// units do not fill the last round, the ones left have the memory to
-// themselves, and one CTA's routing and epilogues pass while the other streams.
+// epilogue owns column j * 128 + threadIdx.x of h.  Two CTAs share an SM: one
+// CTA's routing and epilogues pass while the other streams.  The units that
+// are left when every CTA has had the same number are split along K over
+// groups of 2, 4 or 8 CTAs of a cluster, as far as the CTAs go.
 template <int kN>
 __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_constant__ DecodeParams p,
                                                                  uint32_t ring_bytes, uint32_t ranks) {
@@ -330,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   constexpr uint32_t kColumns = tmem_columns(4 * kN);
   uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Routing r = routing_at(ring + ring_bytes, ring, p.T * p.K, p.E);
+  const Routing r = routing_at(ring + ring_bytes, ring, p.T * p.K, p.E, kN);
   if (threadIdx.x == 0) {
     init_barriers(b);
     ptx::mbar_init(&amax_ready[0], 4);
@@ -350,20 +370,38 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   // tensor memory: CTAs of few_rows, which wait for this grid while they hold
   // theirs, cannot keep it from it.
   ptx::launch_dependents();
-  build_routing(r, rs, p);
+  build_routing(r, rs, p, kN);
   tc::fence_after();
   // Stages as large as the fullest expert needs.
   const uint32_t stage_bytes = 2 * kTileBytes + chunks_of(rs.most_rows) * kChunk * kBlock;
   const uint32_t stages = min(ring_bytes / stage_bytes, static_cast<uint32_t>(kMaxStages));
   const int jb = p.I / kBlock, kb_all = p.H / kBlock;
   const int units = rs.bad ? 0 : rs.n_active * jb;
-  const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
-  const int kb0 = static_cast<int>(rank * kb_all / ranks), kb_n = static_cast<int>((rank + 1) * kb_all / ranks) - kb0;
-  const int step = static_cast<int>(gridDim.x / ranks), u0 = static_cast<int>(blockIdx.x / ranks);
+  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  int split = 1;  // CTAs that share one of the last units
+  const int whole = units / grid * grid, left = units - whole;
+  while (split < static_cast<int>(ranks) && left * split * 2 <= grid) split *= 2;
+  // This CTA's units: cta, cta + grid, ... below `whole` (or all, without a
+  // split), all of K; then its share of unit `shared`.
+  const int end = split > 1 ? whole : units, part = cta % split;
+  const int shared = split > 1 && whole + cta / split < units ? whole + cta / split : -1;
+  struct Span {
+    int u, kb0, kb_n;
+  };
+  auto first_span = [&]() {
+    if (cta < end) return Span{cta, 0, kb_all};
+    return Span{shared, part * kb_all / split, (part + 1) * kb_all / split - part * kb_all / split};
+  };
+  auto next_span = [&](Span v) {  // u < 0: no more
+    if (v.u == shared) return Span{-1, 0, 0};
+    if (v.u + grid < end) return Span{v.u + grid, 0, kb_all};
+    return Span{shared, part * kb_all / split, (part + 1) * kb_all / split - part * kb_all / split};
+  };
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = rs.bad ? MOE_EROUTE : MOE_OK;
   bool ok = true;
 
   unsigned long long gate[kN / 2], up[kN / 2];
+  int round = 0;  // units this CTA has finished
   // Epilogue warps: h of the unit's token rows from the sums, quantised.
   auto finish = [&](int u, int round) -> bool {
     const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
@@ -424,29 +462,35 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   };
 
   if (warp == kTmaWarp) {
-    if (lane == 0 && u0 < units) {
+    if (lane == 0) {
       fence_async_proxy();
       uint32_t it = 0;
-      for (int u = u0; ok && u < units; u += step) {
-        const int a = u / jb, j = u - a * jb;
-        const int w0 = r.active[a] * 2 * p.I + j * kBlock;
+      Place at;
+      for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
+        const int a = v.u / jb, j = v.u - a * jb;
+        const int w0 = r.active[a] * 2 * p.I + j * kBlock, w1 = w0 + p.I;
         const int row0 = r.first[a], n = r.first[a + 1] - row0, rows = chunks_of(n) * kChunk;
-        for (int kb = 0; kb < kb_n; ++kb, ++it) {
-          const uint32_t st = it % stages;
-          if (it >= stages && !tc::wait(&b.empty[st], (it / stages - 1) & 1, &b.gave_up)) {
+        int token[kN];  // rows past the expert's last repeat it; their columns are dropped
+#pragma unroll
+        for (int c = 0; c < kN; ++c) token[c] = r.token[row0 + min(c, n - 1)];
+        const uint32_t bytes = 2 * kTileBytes + rows * kBlock;
+        const int k_end = (v.kb0 + v.kb_n) * kBlock;
+        for (int k = v.kb0 * kBlock; k < k_end; k += kBlock, ++it) {
+          if (it >= stages && !tc::wait(&b.empty[at.st], at.phase ^ 1, &b.gave_up)) {
             ok = false;
             break;
           }
-          uint8_t* to = ring + st * stage_bytes;
-          const int k = (kb0 + kb) * kBlock;
-          ptx::mbar_arrive_expect_tx(&b.full[st], 2 * kTileBytes + rows * kBlock);
-          tc::tma_load_2d(to, &p.w13_map, k, w0, &b.full[st]);
-          tc::tma_load_2d(to + kTileBytes, &p.w13_map, k, w0 + p.I, &b.full[st]);
-          // Rows past the expert's last repeat it; their columns are dropped.
-          for (int c = 0; c < rows; c += 4)
-            tc::tma_gather4(to + 2 * kTileBytes + c * kBlock, &p.x_map, k, r.token[row0 + min(c, n - 1)],
-                            r.token[row0 + min(c + 1, n - 1)], r.token[row0 + min(c + 2, n - 1)],
-                            r.token[row0 + min(c + 3, n - 1)], &b.full[st]);
+          uint8_t* to = ring + at.st * stage_bytes;
+          uint64_t* full = &b.full[at.st];
+          ptx::mbar_arrive_expect_tx(full, bytes);
+          tc::tma_load_2d(to, &p.w13_map, k, w0, full);
+          tc::tma_load_2d(to + kTileBytes, &p.w13_map, k, w1, full);
+#pragma unroll
+          for (int c = 0; c < kN; c += 4)
+            if (c < rows)
+              tc::tma_gather4(to + 2 * kTileBytes + c * kBlock, &p.x_map, k, token[c], token[c + 1], token[c + 2],
+                              token[c + 3], full);
+          at.next(stages);
         }
       }
       if (!ok) drain_loads(b, it, stages);
@@ -454,19 +498,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       uint32_t it = 0;
-      for (int u = u0; ok && u < units; u += step) {
-        const int a = u / jb, chunks = chunks_of(r.first[a + 1] - r.first[a]);
-        for (int kb = 0; kb < kb_n; ++kb, ++it) {
-          const uint32_t st = it % stages, buf = it & 1;
+      Place at;
+      for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
+        const int a = v.u / jb, chunks = chunks_of(r.first[a + 1] - r.first[a]);
+        for (int kb = 0; kb < v.kb_n; ++kb, ++it) {
+          const uint32_t buf = it & 1;
           ok = (it < 2 || tc::wait(&b.acc_empty[buf], (it / 2 - 1) & 1, &b.gave_up)) &&
-               tc::wait(&b.full[st], (it / stages) & 1, &b.gave_up);
+               tc::wait(&b.full[at.st], at.phase, &b.gave_up);
           if (!ok) break;
           tc::fence_after();
-          const uint8_t* at = ring + st * stage_bytes;
-          mma_tile(b.tmem + buf * 2 * kN, at, at + 2 * kTileBytes, chunks);
-          mma_tile(b.tmem + (buf * 2 + 1) * kN, at + kTileBytes, at + 2 * kTileBytes, chunks);
-          tc::commit(&b.empty[st]);
+          const uint8_t* w = ring + at.st * stage_bytes;
+          mma_tile(b.tmem + buf * 2 * kN, w, w + 2 * kTileBytes, chunks);
+          mma_tile(b.tmem + (buf * 2 + 1) * kN, w + kTileBytes, w + 2 * kTileBytes, chunks);
+          tc::commit(&b.empty[at.st]);
           tc::commit(&b.acc_full[buf]);
+          at.next(stages);
         }
       }
       finish_mma(b);
@@ -474,35 +520,42 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   } else {
     const uint32_t lanes = b.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     uint32_t it = 0;
-    int round = 0;
-    for (int u = u0; ok && u < units; u += step, ++round) {
-      const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
-      const float* sg = p.w13_scales + (static_cast<int64_t>(r.active[a]) * 2 * jb + j) * kb_all + kb0;
+    for (Span v = first_span(); ok && v.u >= 0; v = next_span(v), ++round) {
+      const int a = v.u / jb, j = v.u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
+      const float* sg = p.w13_scales + (static_cast<int64_t>(r.active[a]) * 2 * jb + j) * kb_all + v.kb0;
       const float* su = sg + static_cast<int64_t>(jb) * kb_all;
       const float* sx[(kN + 31) / 32];
 #pragma unroll
       for (int i = 0; i < (kN + 31) / 32; ++i)
-        sx[i] = p.x_scales + static_cast<int64_t>(r.token[row0 + min(lane + 32 * i, n - 1)]) * kb_all + kb0;
-      // The scales of the next K block are read a block ahead.
-      float next[(kN + 31) / 32], next_g, next_u;
+        sx[i] = p.x_scales + static_cast<int64_t>(r.token[row0 + min(lane + 32 * i, n - 1)]) * kb_all + v.kb0;
+      // The token rows' scales of the next K block are read a block ahead, the
+      // weights' of 32 blocks at a time (one a lane), 32 blocks ahead.
+      float next[(kN + 31) / 32], lane_g, lane_u, ahead_g = 0.0f, ahead_u = 0.0f;
       auto read = [&](int kb) {
 #pragma unroll
         for (int i = 0; i < (kN + 31) / 32; ++i)
           if (32 * i < n) next[i] = sx[i][kb];
-        next_g = sg[kb];
-        next_u = su[kb];
       };
+      auto read_weights = [&](int kb) {
+        if (kb + lane < v.kb_n) ahead_g = sg[kb + lane], ahead_u = su[kb + lane];
+      };
+      read_weights(0);
       read(0);
 #pragma unroll
       for (int c = 0; c < kN / 2; ++c) gate[c] = up[c] = 0;
-      for (int kb = 0; kb < kb_n; ++kb, ++it) {
+      for (int kb = 0; kb < v.kb_n; ++kb, ++it) {
         const uint32_t buf = it & 1;
         float* scale = s_scale[warp][buf];
+        if ((kb & 31) == 0) {
+          lane_g = ahead_g, lane_u = ahead_u;
+          read_weights(kb + 32);
+        }
 #pragma unroll
         for (int i = 0; i < (kN + 31) / 32; ++i)
           if (32 * i < n && lane + 32 * i < kN) scale[lane + 32 * i] = next[i];
-        const unsigned long long fg = tc::pack2(next_g, next_g), fu = tc::pack2(next_u, next_u);
-        if (kb + 1 < kb_n) read(kb + 1);
+        const float g = __shfl_sync(0xffffffffu, lane_g, kb & 31), u = __shfl_sync(0xffffffffu, lane_u, kb & 31);
+        const unsigned long long fg = tc::pack2(g, g), fu = tc::pack2(u, u);
+        if (kb + 1 < v.kb_n) read(kb + 1);
         ok = tc::wait(&b.acc_full[buf], (it / 2) & 1, &b.gave_up);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -513,28 +566,30 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
 #pragma unroll
         for (int c = 0; c < kN; c += kChunk) {
           if (c < n) {
-            uint32_t v[kChunk];
-            tc::tmem_load_16(lanes + buf * 2 * kN + c, v);
+            uint32_t d[kChunk];
+            tc::tmem_load_16(lanes + buf * 2 * kN + c, d);
             tc::wait_loads();
-            add_scaled(v, scale + c, fg, gate + c / 2);
-            tc::tmem_load_16(lanes + (buf * 2 + 1) * kN + c, v);
+            add_scaled(d, scale + c, fg, gate + c / 2);
+            tc::tmem_load_16(lanes + (buf * 2 + 1) * kN + c, d);
             tc::wait_loads();
-            add_scaled(v, scale + c, fu, up + c / 2);
+            add_scaled(d, scale + c, fu, up + c / 2);
           }
         }
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
       }
-      if (ok && ranks == 1) ok = finish(u, round);
+      if (v.u == shared) break;  // its sums are not complete
+      if (ok) ok = finish(v.u, round);
     }
   }
   if (ranks > 1) {
-    // One unit a cluster: its sums meet in rank 0, through the ring, which is
-    // free now: every load has been consumed.  [gate, up][token row][column]
-    float* part = reinterpret_cast<float*>(ring);
-    const bool mine = warp < kTmaWarp && ok && u0 < units;
-    const int n = u0 < units ? r.first[u0 / jb + 1] - r.first[u0 / jb] : 0;
+    // The shared unit's sums meet in the first CTA of its group, through the
+    // ring, which is free now: every load has been consumed.
+    // [gate, up][token row][column]
+    float* sums = reinterpret_cast<float*>(ring);
+    const bool mine = warp < kTmaWarp && ok && shared >= 0;
+    const int n = shared >= 0 ? r.first[shared / jb + 1] - r.first[shared / jb] : 0;
     __syncthreads();
     if (mine) {
 #pragma unroll
@@ -542,24 +597,25 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
         if (c < n) {
 #pragma unroll
           for (int i = c; i < c + 8; ++i) {
-            part[i * 128 + threadIdx.x] = i & 1 ? tc::hi2(gate[i / 2]) : tc::lo2(gate[i / 2]);
-            part[(kN + i) * 128 + threadIdx.x] = i & 1 ? tc::hi2(up[i / 2]) : tc::lo2(up[i / 2]);
+            sums[i * 128 + threadIdx.x] = i & 1 ? tc::hi2(gate[i / 2]) : tc::lo2(gate[i / 2]);
+            sums[(kN + i) * 128 + threadIdx.x] = i & 1 ? tc::hi2(up[i / 2]) : tc::lo2(up[i / 2]);
           }
         }
       }
     }
     __syncthreads();
     cluster_sync();
-    if (mine && rank == 0) {
-      for (uint32_t q = 1; q < ranks; ++q) {
+    if (mine && part == 0) {
+      const uint32_t rank = cluster_rank();
+      for (uint32_t q = rank + 1; q < rank + split; ++q) {
 #pragma unroll
         for (int c = 0; c < kN; c += 8) {
           if (c < n) {
             float v[16];  // all on their way before the first is needed
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              v[i] = ld_cluster(part + (c + i) * 128 + threadIdx.x, q);
-              v[8 + i] = ld_cluster(part + (kN + c + i) * 128 + threadIdx.x, q);
+              v[i] = ld_cluster(sums + (c + i) * 128 + threadIdx.x, q);
+              v[8 + i] = ld_cluster(sums + (kN + c + i) * 128 + threadIdx.x, q);
             }
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
@@ -569,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
           }
         }
       }
-      finish(u0, 0);
+      finish(shared, round);
     }
     __syncthreads();
     cluster_sync();  // no CTA leaves while its shared memory is being read
@@ -614,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x == 0) rs.bad = 0, rs.n_active = 1, rs.most_rows = p.T;
     __syncthreads();
   } else {
-    r = routing_at(reinterpret_cast<uint8_t*>(s_out + p.T * 128), ring, p.T * p.K, p.E);
-    build_routing(r, rs, p);  // topk_idx and topk_w: see the first kernel's launch_dependents
+    r = routing_at(reinterpret_cast<uint8_t*>(s_out + p.T * 128), ring, p.T * p.K, p.E, kN);
+    build_routing(r, rs, p, kN);  // topk_idx and topk_w: see the first kernel's launch_dependents
   }
   tc::fence_after();
   const uint32_t stage_bytes = kTileBytes + chunks_of(rs.most_rows) * kChunk * kBlock;
@@ -633,49 +689,71 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kTmaWarp) {
     if (lane == 0) {
       fence_async_proxy();
-      auto load_w = [&](int i) {
-        const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
-        ptx::mbar_arrive_expect_tx(&b.full[st], kTileBytes + chunks_of(rows_of(a)) * kChunk * kBlock);
-        tc::tma_load_2d(ring + st * stage_bytes, &p.w2_map, kb * kBlock, (kDense ? 0 : r.active[a]) * p.H + tile * 128,
-                        &b.full[st]);
+      // Weights and rows of an item go to one stage; the first stages get
+      // their weights before h is ready, so the two walk separately.
+      struct Walk {
+        Place at;
+        int a, kb, row, rows;
       };
-      auto load_h = [&](int i) {
-        const int a = (it0 + i) / kb_n, kb = it0 + i - a * kb_n, st = i % stages;
-        for (int c = 0; c < rows_of(a); c += kChunk)
-          tc::tma_load_2d(ring + st * stage_bytes + kTileBytes + c * kBlock, &p.h_map, kb * kBlock, row0_of(a) + c,
-                          &b.full[st]);
+      auto enter = [&](Walk& v) {
+        v.row = kDense ? tile * 128 : r.active[v.a] * p.H + tile * 128;
+        v.rows = rows_of(v.a);
+      };
+      auto step = [&](Walk& v) {
+        v.at.next(stages);
+        if (++v.kb == kb_n) {
+          v.kb = 0;
+          if (++v.a < rs.n_active) enter(v);
+        }
+      };
+      Walk w = {{}, it0 / kb_n, it0 % kb_n, 0, 0};
+      if (n > 0) enter(w);
+      Walk h = w;
+      auto load_w = [&]() {
+        uint64_t* full = &b.full[w.at.st];
+        ptx::mbar_arrive_expect_tx(full, kTileBytes + chunks_of(w.rows) * kChunk * kBlock);
+        tc::tma_load_2d(ring + w.at.st * stage_bytes, &p.w2_map, w.kb * kBlock, w.row, full);
+        step(w);
+      };
+      auto load_h = [&]() {
+        const int row0 = row0_of(h.a);
+        for (int c = 0; c < h.rows; c += kChunk)
+          tc::tma_load_2d(ring + h.at.st * stage_bytes + kTileBytes + c * kBlock, &p.h_map, h.kb * kBlock, row0 + c,
+                          &b.full[h.at.st]);
+        step(h);
       };
       const int early = min(n, static_cast<int>(stages));
       if (kDense) ptx::wait_prerequisites();
-      for (int i = 0; i < early; ++i) load_w(i);
+      for (int i = 0; i < early; ++i) load_w();
       if (!kDense) ptx::wait_prerequisites();  // h
-      for (int i = 0; i < early; ++i) load_h(i);
+      for (int i = 0; i < early; ++i) load_h();
       int i = early;
       for (; i < n; ++i) {
-        if (!tc::wait(&b.empty[i % stages], (i / stages - 1) & 1, &b.gave_up)) {
+        if (!tc::wait(&b.empty[w.at.st], w.at.phase ^ 1, &b.gave_up)) {
           ok = false;
           break;
         }
-        load_w(i);
-        load_h(i);
+        load_w();
+        load_h();
       }
       if (!ok) drain_loads(b, i, stages);
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       int a = it0 / kb_n, kb = it0 - a * kb_n;
+      Place at;
       for (int i = 0, turn = 0; i < n; ++turn) {
         const uint32_t buf = turn & 1;
         const int two = i + 1 < n && kb + 1 < kb_n ? 2 : 1, chunks = chunks_of(rows_of(a));
         ok = turn < 2 || tc::wait(&b.acc_empty[buf], (turn / 2 - 1) & 1, &b.gave_up);
         for (int m = 0; ok && m < two; ++m, ++i) {
-          const uint32_t st = i % stages;
-          ok = tc::wait(&b.full[st], (i / stages) & 1, &b.gave_up);
+          ok = tc::wait(&b.full[at.st], at.phase, &b.gave_up);
           if (!ok) break;
           tc::fence_after();
-          const uint8_t* at = ring + st * stage_bytes;
-          mma_tile(b.tmem + (buf * 2 + m) * kN, at, at + kTileBytes, chunks);
-          tc::commit(&b.empty[st]);
+          const uint8_t* w = ring + at.st * stage_bytes;
+          mma_tile(b.tmem + (buf * 2 + m) * kN, w, w + kTileBytes, chunks);
+          tc::commit(&b.empty[at.st]);
+          at.next(stages);
         }
         if (!ok) break;
         tc::commit(&b.acc_full[buf]);
@@ -696,24 +774,35 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int c = 0; c < kN / 2; ++c) acc[c] = 0;
     int a = it0 / kb_n, kb = it0 - a * kb_n;
     float next[2][(kN + 31) / 32], next_w[2];
-    auto read = [&](int a, int kb, int two) {  // the scales of the next turn, a turn ahead
-      const int row0 = row0_of(a), rows = rows_of(a);
+    const float *hs[(kN + 31) / 32], *ws;
+    int next_rows;
+    auto enter = [&](int a) {  // the expert of the next turn's scales
+      const int row0 = row0_of(a);
+      next_rows = rows_of(a);
+#pragma unroll
+      for (int i = 0; i < (kN + 31) / 32; ++i)
+        hs[i] = p.h_scales + static_cast<int64_t>(row0 + min(lane + 32 * i, next_rows - 1)) * kb_n;
+      ws = sw + (kDense ? 0 : r.active[a]) * sw_expert;
+    };
+    auto read = [&](int kb, int two) {  // the scales of the next turn, a turn ahead
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (m < two) {
 #pragma unroll
           for (int i = 0; i < (kN + 31) / 32; ++i)
-            if (32 * i < rows)
-              next[m][i] = ld_f32(p.h_scales + static_cast<int64_t>(row0 + min(lane + 32 * i, rows - 1)) * kb_n + kb + m);
-          next_w[m] = ld_f32(sw + (kDense ? 0 : r.active[a]) * sw_expert + kb + m);
+            if (32 * i < next_rows) next[m][i] = ld_f32(hs[i] + kb + m);
+          next_w[m] = ld_f32(ws + kb + m);
         }
       }
     };
     int two = n > 1 && kb + 1 < kb_n ? 2 : 1;
-    if (n > 0) read(a, kb, two);
+    if (n > 0) {
+      enter(a);
+      read(kb, two);
+    }
     for (int i = 0, turn = 0; i < n; ++turn) {
       const uint32_t buf = turn & 1;
-      const int row0 = row0_of(a), rows = rows_of(a), two_now = two;
+      const int row0 = row0_of(a), rows = next_rows, two_now = two;
       unsigned long long f[2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -727,7 +816,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool last = kb == kb_n;
       if (last) kb = 0, ++a;
       two = i + 1 < n && kb + 1 < kb_n ? 2 : 1;
-      if (i < n) read(a, kb, two);
+      if (i < n) {
+        if (last) enter(a);
+        read(kb, two);
+      }
       ok = tc::wait(&b.acc_full[buf], (turn / 2) & 1, &b.gave_up);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -841,72 +933,129 @@ cudaError_t launch_cluster(void (*kernel)(DecodeParams, uint32_t, uint32_t), con
   return cudaLaunchKernelEx(&cfg, kernel, p, static_cast<uint32_t>(ring), ranks);
 }
 
-// Dynamic shared memory of one of two CTAs on an SM, and of a CTA that has one
-// to itself: without the static part (up to 5 KiB) and the driver's 1 KiB.
-constexpr size_t kHalfSm = 228 * 1024 / 2 - 6 * 1024, kWholeSm = 228 * 1024 - 6 * 1024;
+// Dynamic shared memory that a kernel's CTA may have when `per_sm` of them share
+// an SM; cached per device and kernel.
+size_t smem_budget(const void* kernel, int per_sm) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, size_t> known;  // static shared memory
+  size_t fixed = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = known.find({dev, kernel});
+    if (it == known.end()) {
+      cudaFuncAttributes attr;
+      if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return 0;
+      // Both kernels want the SM's whole shared memory, so that they can meet on one SM.
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return 0;
+      it = known.emplace(std::make_pair(dev, kernel), attr.sharedSizeBytes).first;
+    }
+    fixed = it->second;
+  }
+  constexpr size_t kSm = 228 * 1024, kReserved = 1024;  // of each CTA, the driver's
+  return kSm / per_sm - kReserved - fixed;
+}
+
+// Clusters of four CTAs of decode_glu, two CTAs an SM, that are resident at one
+// time: a cluster's CTAs share a GPC, so not every SM can be used.  Asked for
+// CTAs that have an SM each and doubled (the query does not count on a second
+// CTA).  Cached per device and kernel.
+int resident_clusters(void (*kernel)(DecodeParams, uint32_t, uint32_t), size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, int> known;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = known.find({dev, reinterpret_cast<const void*>(kernel)});
+  if (it != known.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 4;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[{dev, reinterpret_cast<const void*>(kernel)}] = 2 * n;
+  return 2 * n;
+}
+
 #ifdef SWEEP
 }
 #include <cstdlib>
 namespace {
 size_t env(const char* n, size_t d) { const char* v = std::getenv(n); return v ? std::atoi(v) : d; }
-#else
-size_t env(const char*, size_t d) { return d; }
 #endif
-
 template <int kN>
 cudaError_t launch_glu(const DecodeParams& p, int sms, cudaStream_t stream) {
+  auto* kernel = decode_glu_kernel<kN>;
   const int pairs = p.T * p.K;
-  const size_t rest = 1024 + routing_bytes(pairs, p.E);
-  int64_t units = static_cast<int64_t>(max_active(pairs, p.E)) * (p.I / kBlock);
-  // Too few units for the SMs: split them along K, eight blocks or more each.
+  const size_t rest = 1024 + routing_bytes(pairs, p.E, kN);
+  const size_t budget = smem_budget(reinterpret_cast<const void*>(kernel), 2);
+  if (budget < rest + 2 * kTileBytes + kN * kBlock) return cudaErrorInvalidConfiguration;
+  const cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), budget);
+  if (err != cudaSuccess) return err;
+  const int64_t units = static_cast<int64_t>(max_active(pairs, p.E, kN)) * (p.I / kBlock);
+  const int kb_n = p.H / kBlock;
   uint32_t ranks = 1;
-  while (ranks < 8 && units * ranks * 2 <= sms && static_cast<int>(ranks) * 16 <= p.H / kBlock) ranks *= 2;
-  if (ranks == 1 && units > 2 * sms) units = 2 * sms;
-  return launch_cluster(decode_glu_kernel<kN>, p, rest, env("GLU", kHalfSm) - rest, ranks, static_cast<unsigned>(units), stream);
+  int64_t groups = units;
+  if (units > 2 * sms) {
+    // Several rounds: clusters of four, so that the last one can be split.
+    const int clusters = kb_n >= 16 ? std::min(resident_clusters(kernel, budget), 2 * sms / 4) : 0;
+    ranks = clusters * 4 >= sms ? 4 : 1;
+    groups = ranks > 1 ? clusters : 2 * sms;
+  } else {
+    // Too few units for the SMs: split them along K, eight blocks or more each.
+    while (ranks < 8 && units * ranks * 2 <= sms && static_cast<int>(ranks) * 16 <= kb_n) ranks *= 2;
+  }
+  return launch_cluster(kernel, p, rest, budget - rest, ranks, static_cast<unsigned>(groups), stream);
 }
 
 template <int kN, bool kDense>
 cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
+  auto* kernel = few_rows_kernel<kN, kDense>;
   const int pairs = p.T * p.K;
-  const size_t rest = 1024 + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E));
+  const size_t rest = 1024 + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E, kN));
   const int64_t tiles = (p.H + 127) / 128;
-  const int64_t items = static_cast<int64_t>(kDense ? 1 : max_active(pairs, p.E)) * p.h_blocks;
-  // Up to 16 rows two CTAs share an SM, else their sums leave too little for the rings.
-  const int per_sm = kN == 16 ? 2 : 1;
+  const int64_t items = static_cast<int64_t>(kDense ? 1 : max_active(pairs, p.E, kN)) * p.h_blocks;
+  // Up to 16 tokens two CTAs share an SM, else their sums leave too little for the rings.
+  const int per_sm = p.T <= 16 ? 2 : 1;
   uint32_t ranks = 1;
   while (ranks < kMaxRanks && tiles * ranks * 2 <= per_sm * sms && ranks * 2 * 4 <= items) ranks *= 2;
-  size_t ring = (tiles * ranks > sms ? kHalfSm : kWholeSm) - rest;
-  ring = env("FEW", ring);
-  const size_t most = (items + ranks - 1) / ranks * (kTileBytes + kN * kBlock);  // a stage for each item
-  return launch_cluster(few_rows_kernel<kN, kDense>, p, rest, std::min(ring, most), ranks, static_cast<unsigned>(tiles), stream);
+  const size_t stage = kTileBytes + kN * kBlock;
+  const size_t budget = smem_budget(reinterpret_cast<const void*>(kernel), tiles * ranks > sms ? per_sm : 1);
+  if (budget < rest + stage) return cudaErrorInvalidConfiguration;
+  const size_t most = (items + ranks - 1) / ranks * stage;  // a stage for each item
+  const size_t ring = std::min(std::min(budget, static_cast<size_t>(227 * 1024 - 8 * 1024)) - rest, most);
+  return launch_cluster(kernel, p, rest, ring, ranks, static_cast<unsigned>(tiles), stream);
 }
-
-// Most token columns a kernel variant holds, for this many tokens.
-int columns_for(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 }  // namespace
 
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream) {
-  cudaError_t err;
-  switch (columns_for(p.T)) {
-    case 16:
-      err = launch_glu<16>(p, sms, stream);
-      return err != cudaSuccess ? err : launch_few<16, false>(p, sms, stream);
-    case 32:
-      err = launch_glu<32>(p, sms, stream);
-      return err != cudaSuccess ? err : launch_few<32, false>(p, sms, stream);
-    default:
-      err = launch_glu<64>(p, sms, stream);
-      return err != cudaSuccess ? err : launch_few<64, false>(p, sms, stream);
-  }
+#ifdef SWEEP
+  const bool narrow = env("NARROW", p.T <= 16 || p.T * p.K <= 6 * p.E);
+#else
+  const bool narrow = p.T <= 16 || p.T * p.K <= 6 * p.E;
+#endif
+  cudaError_t err = narrow ? launch_glu<16>(p, sms, stream) : launch_glu<32>(p, sms, stream);
+  if (err != cudaSuccess) return err;
+  return narrow ? launch_few<16, false>(p, sms, stream) : launch_few<32, false>(p, sms, stream);
 }
 
 cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream) {
-  switch (columns_for(p.T)) {
-    case 16: return launch_few<16, true>(p, sms, stream);
-    case 32: return launch_few<32, true>(p, sms, stream);
-    default: return launch_few<64, true>(p, sms, stream);
-  }
+  if (p.T <= 16) return launch_few<16, true>(p, sms, stream);
+  return p.T <= 32 ? launch_few<32, true>(p, sms, stream) : launch_few<64, true>(p, sms, stream);
 }
 
 }  // namespace moe
