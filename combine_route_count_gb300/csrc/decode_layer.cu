@@ -62,21 +62,10 @@ constexpr int kMaxRanks = 4;              // CTAs of a cluster in few_rows
 constexpr int kTmaWarp = 4, kMmaWarp = 5;  // warps 0-3: epilogue
 constexpr int kThreads = 192;
 
-// ---- clusters ------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // A float of CTA `rank`'s shared memory, at the place that `p` has in this CTA's.
 __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-  uint32_t at;
   float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::at_rank(p, rank)) : "memory");
   return v;
 }
 
@@ -604,9 +593,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
       }
     }
     __syncthreads();
-    cluster_sync();
+    tc::cluster_sync();
     if (mine && part == 0) {
-      const uint32_t rank = cluster_rank();
+      const uint32_t rank = tc::cluster_rank();
       for (uint32_t q = rank + 1; q < rank + split; ++q) {
 #pragma unroll
         for (int c = 0; c < kN; c += 8) {
@@ -628,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
       finish(shared, round);
     }
     __syncthreads();
-    cluster_sync();  // no CTA leaves while its shared memory is being read
+    tc::cluster_sync();  // no CTA leaves while its shared memory is being read
   }
   tc::fence_before();
   __syncthreads();
@@ -677,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t stage_bytes = kTileBytes + chunks_of(rs.most_rows) * kChunk * kBlock;
   const uint32_t stages = min(ring_bytes / stage_bytes, static_cast<uint32_t>(kMaxStages));
   const int tile = static_cast<int>(blockIdx.x / ranks);
-  const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+  const uint32_t rank = ranks > 1 ? tc::cluster_rank() : 0;
   const int kb_n = p.h_blocks;
   const int items = rs.bad ? 0 : rs.n_active * kb_n;
   const int it0 = static_cast<int>(static_cast<int64_t>(items) * rank / ranks);
@@ -875,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   // Token t's sum is formed by rank t % ranks, in rank order.
   __syncthreads();
-  if (ranks > 1) cluster_sync();
+  if (ranks > 1) tc::cluster_sync();
   const int column = tile * 128 + static_cast<int>(threadIdx.x);
   constexpr int kBatch = kN / 8;
   if (threadIdx.x < 128 && !rs.bad && !b.gave_up && column < p.H) {
@@ -905,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncthreads();
-  if (ranks > 1) cluster_sync();  // no CTA leaves while its shared memory is being read
+  if (ranks > 1) tc::cluster_sync();  // no CTA leaves while its shared memory is being read
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -1015,8 +1004,9 @@ cudaError_t launch_glu(const DecodeParams& p, int sms, cudaStream_t stream) {
     ranks = clusters * 4 >= sms ? 4 : 1;
     groups = ranks > 1 ? clusters : 2 * sms;
   } else {
-    // Too few units for the SMs: split them along K, eight blocks or more each.
-    while (ranks < 8 && units * ranks * 2 <= sms && static_cast<int>(ranks) * 16 <= kb_n) ranks *= 2;
+    // Too few units for two CTAs an SM: split them along K, eight blocks or
+    // more each (one token, 128 units: 66.9 us unsplit, 65.1 us in twos).
+    while (ranks < 8 && units * ranks <= sms && static_cast<int>(ranks) * 16 <= kb_n) ranks *= 2;
   }
   return launch_cluster(kernel, p, rest, budget - rest, ranks, static_cast<unsigned>(groups), stream);
 }

@@ -11,20 +11,25 @@
 //
 // The scales differ from block to block of K, so a block's product cannot be
 // left to accumulate in tensor memory: each block of K = 128 (four matrix
-// instructions) goes to one of two tensor-memory buffers of 256 columns, and
-// the epilogue warps add it, scaled, to float32 accumulators in registers
-// while the tensor core fills the other buffer.
+// instructions) goes to a tensor-memory buffer of its own, and the epilogue
+// warps add it, scaled, to float32 accumulators in registers while the tensor
+// core fills other buffers.
 //
-// One CTA per SM, tile 128 rows x 256 columns (glu: 128 gate + 128 up
-// columns, 128 columns of h), 10 warps: 8 epilogue warps (two per quarter of
-// the tensor-memory lanes; a thread owns one row and half of the columns, 128
-// accumulators, two per fma.rn.f32x2), one TMA warp, one matrix warp.
-// Operands arrive by tiled TMA into kStages stages of 48 KiB with the 128-byte
-// swizzle that the matrix instruction reads.  At 256 columns the operands'
-// shared-memory reads (48 KiB per 512 cycles of matrix work) stay below the
-// shared-memory rate and the 2 x 256 columns use the whole tensor memory.
-// Rows past the end of an expert and columns past N are computed and not
-// stored: rows and columns do not mix.
+// One CTA per SM, tile 128 rows x 256 columns (glu: 128 gate + 128 up columns,
+// 128 columns of h), 12 warps: two epilogue groups of four, each with half of
+// the columns (glu: 64 gate columns and their up columns), one TMA warp, one
+// matrix warp, two that only fill their group.  A thread of the epilogue owns
+// one row and 128 columns, added two at a time.  Operands arrive by tiled TMA
+// into kStages stages of 48 KiB with the 128-byte swizzle that the matrix
+// instruction reads.  Rows past the end of an expert and columns past N are
+// computed and not stored: rows and columns do not mix.
+//
+// What bounds large products is the way of a buffer: from the last matrix
+// instruction over a barrier to the epilogue, out of tensor memory, and over a
+// barrier back takes 700 to 1000 cycles, 128 x 256 x 128 of matrix work 512.
+// With two buffers of 256 columns a K block took 1190 cycles.  So each half of
+// the columns has its own two buffers of 128 (a half's matrix work: 297
+// cycles), and four are on their way at a time.
 //
 // Tiles are dealt out statically (tile b, b+G, ...), rows fastest, so that the
 // CTAs at work at one time share weight columns in L2.  Waits are bounded (2 s)
@@ -47,13 +52,16 @@ constexpr int kABytes = kTileM * kBlockK, kBBytes = kTileN * kBlockK;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpilogueWarps = 8;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers a thread: 168 at launch (65536 / 384), of which the last group gives
+// up what the epilogue's two take: 256 * 216 + 128 * 72 = 384 * 168.
+constexpr int kRegsEpilogue = 216, kRegsRest = 72;
 constexpr uint32_t kTmemColumns = 512;
 constexpr int kCols = 128;  // accumulators of one epilogue thread
 
 struct Shared {
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[2][2], acc_empty[2][2];  // [half of the columns][buffer]
   uint64_t amax_ready[2];
   uint64_t drained;
   uint32_t tmem;
@@ -101,19 +109,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
   g.lo = reinterpret_cast<int32_t*>(stages + kStages * kStageBytes);
   g.hi = g.lo + p.E;
   g.start = g.hi + p.E;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
-      ptx::mbar_init(&s.empty[i], 1);
+      ptx::mbar_init(&s.empty[i], 2);  // both matrix warps
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&s.acc_full[i], 1);
-      ptx::mbar_init(&s.acc_empty[i], kEpilogueWarps);
+      for (int h = 0; h < 2; ++h) {
+        ptx::mbar_init(&s.acc_full[h][i], 1);
+        ptx::mbar_init(&s.acc_empty[h][i], kEpilogueWarps / 2);
+      }
       ptx::mbar_init(&s.amax_ready[i], kEpilogueWarps);
     }
-    ptx::mbar_init(&s.drained, 1);
+    ptx::mbar_init(&s.drained, 2);
     ptx::mbar_fence_init();
     s.gave_up = 0;
   }
@@ -154,28 +164,40 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
   __syncthreads();
   tc::fence_after();
   const int64_t tiles = static_cast<int64_t>(g.start[p.E]) * p.n_tiles;
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = s.tmem, tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
   const int kblocks = p.kblocks;
 
-  if (warp == kTmaWarp) {
-    if (lane == 0) {
+  if (warp >= kEpilogueWarps) {
+    tc::fewer_registers<kRegsRest>();
+    if (warp == kTmaWarp) {
       uint32_t it = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile tile = find_tile(g, p.E, p.n_tiles, t);
         const int w0 = tile.e * p.w_rows + tile.n * (kGlu ? kTileN / 2 : kTileN);
-        const int w1 = kGlu ? w0 + p.N : w0 + kTileN / 2;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int st = it % kStages;
-          if (it >= kStages && !tc::wait(&s.empty[st], (it / kStages - 1) & 1, &s.gave_up)) {
-            ok = false;
-            break;
-          }
+          ok = it < kStages || tc::wait(&s.empty[st], (it / kStages - 1) & 1, &s.gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           uint8_t* a = stages + st * kStageBytes;
-          ptx::mbar_arrive_expect_tx(&s.full[st], kStageBytes);
-          tc::tma_load_2d(a, &p.a, kb * kBlockK, tile.row0, &s.full[st]);
-          tc::tma_load_2d(a + kABytes, &p.w, kb * kBlockK, w0, &s.full[st]);
-          tc::tma_load_2d(a + kABytes + kBBytes / 2, &p.w, kb * kBlockK, w1, &s.full[st]);
+          if (tc::elect()) {
+            ptx::mbar_arrive_expect_tx(&s.full[st], kStageBytes);
+            tc::tma_load_2d(a, &p.a, kb * kBlockK, tile.row0, &s.full[st]);
+            // The first half of the columns, then the second; glu (boxes of 64
+            // rows): 64 gate rows and their up rows each.
+            uint8_t* b = a + kABytes;
+            if (kGlu) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                tc::tma_load_2d(b + q * (kBBytes / 4), &p.w, kb * kBlockK, w0 + (q & 1) * p.N + (q >> 1) * 64,
+                                &s.full[st]);
+            } else {
+              tc::tma_load_2d(b, &p.w, kb * kBlockK, w0, &s.full[st]);
+              tc::tma_load_2d(b + kBBytes / 2, &p.w, kb * kBlockK, w0 + kTileN / 2, &s.full[st]);
+            }
+          }
+          __syncwarp();
         }
       }
       if (!ok) {  // loads still in flight write to this CTA's shared memory: wait (bounded) for them
@@ -187,42 +209,45 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
           }
       }
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t kInstr = tc::instr_desc_e4m3(kTileM, kTileN);
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      constexpr uint32_t kInstr = tc::instr_desc_e4m3(kTileM, kTileN / 2);
+      const int h = warp - kMmaWarp;
       uint32_t it = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int st = it % kStages, buf = it & 1;
-          if (it >= 2 && !tc::wait(&s.acc_empty[buf], (it / 2 - 1) & 1, &s.gave_up)) {
-            ok = false;
-            break;
-          }
-          if (!tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up)) {
-            ok = false;
-            break;
-          }
+          ok = (it < 2 || tc::wait(&s.acc_empty[h][buf], (it / 2 - 1) & 1, &s.gave_up)) &&
+               tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc::fence_after();
           const uint64_t a = tc::smem_desc(stages + st * kStageBytes);
-          const uint64_t b = tc::smem_desc(stages + st * kStageBytes + kABytes);
+          const uint64_t b = tc::smem_desc(stages + st * kStageBytes + kABytes + h * (kBBytes / 2));
+          if (tc::elect()) {
 #pragma unroll
-          for (int k = 0; k < kBlockK / 32; ++k)
-            tc::mma_e4m3(tmem + buf * kTileN, a + 2 * k, b + 2 * k, kInstr, k > 0);
-          tc::commit(&s.empty[st]);
-          tc::commit(&s.acc_full[buf]);
+            for (int k = 0; k < kBlockK / 32; ++k)
+              tc::mma_e4m3(tmem_u + h * kTileN + buf * kCols, a + 2 * k, b + 2 * k, kInstr, k > 0);
+            tc::commit(&s.acc_full[h][buf]);
+            tc::commit(&s.empty[st]);
+          }
+          __syncwarp();
         }
       }
       // Nothing may be in flight when the tensor memory is freed.
-      tc::commit(&s.drained);
+      if (tc::elect()) tc::commit(&s.drained);
+      __syncwarp();
       tc::wait(&s.drained, 0, &s.gave_up);
     }
   } else {
+    tc::more_registers<kRegsEpilogue>();
     const int half = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint32_t it = 0;
     int parity = 0, round = 0;
     bool ok = true;
+    // Rows that begin on 32-byte boundaries are stored by whole sectors.
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.N) * (kF32 ? 4 : 2)) & 31) == 0;
     for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++round) {
       const Tile tile = find_tile(g, p.E, p.n_tiles, t);
       const bool act = r < tile.rows;
@@ -240,39 +265,47 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
       unsigned long long acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
+      // A warp none of whose rows exist only passes the buffers on.
+      const bool some = (warp & 3) * 32 < tile.rows;
+      float next_a = sa[0], next_0 = sw0[0], next_1 = kGlu ? sw1[0] : 0.0f;  // scales, a block ahead
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
-        const float a = sa[kb];
-        const float f0 = a * sw0[kb], f1 = kGlu ? a * sw1[kb] : f0;
+        const float f0 = next_a * next_0, f1 = kGlu ? next_a * next_1 : f0;
         const unsigned long long scale0 = tc::pack2(f0, f0), scale1 = tc::pack2(f1, f1);
+        if (kb + 1 < kblocks) {
+          next_a = sa[kb + 1];
+          next_0 = sw0[kb + 1];
+          if (kGlu) next_1 = sw1[kb + 1];
+        }
         const int buf = it & 1;
-        ok = tc::wait(&s.acc_full[buf], (it / 2) & 1, &s.gave_up);
+        ok = tc::wait(&s.acc_full[half][buf], (it / 2) & 1, &s.gave_up);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc::fence_after();
-        // glu: 64 gate columns, then the 64 up columns of the same h.
-        const uint32_t c0 = lanes + buf * kTileN + half * (kGlu ? kCols / 2 : kCols);
-        const uint32_t c1 = c0 + (kGlu ? kTileN / 2 : kCols / 2);
-        uint32_t v[2][16];
-        tc::tmem_load_16(c0, v[0]);
+        if (some) {
+          const uint32_t from = lanes + half * kTileN + buf * kCols;
+          uint32_t v[2][32];
+          tc::tmem_load_32(from, v[0]);
 #pragma unroll
-        for (int c = 0; c < kCols / 16; ++c) {
-          tc::wait_loads();
-          if (c + 1 < kCols / 16)
-            tc::tmem_load_16((c + 1) * 16 < kCols / 2 ? c0 + (c + 1) * 16 : c1 + (c + 1) * 16 - kCols / 2,
-                             v[(c + 1) & 1]);
-          else {
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+          for (int c = 0; c < 4; ++c) {
+            tc::wait_loads();
+            if (c < 3) {
+              tc::tmem_load_32(from + (c + 1) * 32, v[(c + 1) & 1]);
+            } else {
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&s.acc_empty[half][buf]);
+            }
+            const uint32_t* d = v[c & 1];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[c * 16 + j] = tc::fma2(tc::pack2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])),
+                                         c < 2 ? scale0 : scale1, acc[c * 16 + j]);
           }
-          const unsigned long long scale = c * 16 < kCols / 2 ? scale0 : scale1;
-          const uint32_t* d = v[c & 1];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[c * 8 + j] = tc::fma2(tc::pack2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), scale,
-                                      acc[c * 8 + j]);
+        } else {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.acc_empty[half][buf]);
         }
       }
       if (!ok) break;
@@ -319,18 +352,25 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
       } else if (act) {
         const int n0 = tile.n * kTileN + half * kCols;
         uint8_t* dst = static_cast<uint8_t*>(p.out) + (row * p.N + n0) * (kF32 ? 4 : 2);
+        constexpr int kStep = kF32 ? 8 : 16;  // columns of 32 bytes, a whole sector
 #pragma unroll
-        for (int c = 0; c < kCols; c += 8) {
-          if (n0 + c < p.N) {  // N is a multiple of 8
-            const unsigned long long* v = acc + c / 2;
-            if (kF32) {
-              ptx::st_v4(dst + c * 4, make_uint4(v[0], v[0] >> 32, v[1], v[1] >> 32));
-              ptx::st_v4(dst + c * 4 + 16, make_uint4(v[2], v[2] >> 32, v[3], v[3] >> 32));
-            } else {
-              ptx::st_v4(dst + c * 2,
-                         make_uint4(bf16x2(tc::lo2(v[0]), tc::hi2(v[0])), bf16x2(tc::lo2(v[1]), tc::hi2(v[1])),
-                                    bf16x2(tc::lo2(v[2]), tc::hi2(v[2])), bf16x2(tc::lo2(v[3]), tc::hi2(v[3]))));
-            }
+        for (int c = 0; c < kCols; c += kStep) {
+          const unsigned long long* v = acc + c / 2;
+          uint4 q[2];
+          if (kF32) {
+            q[0] = make_uint4(v[0], v[0] >> 32, v[1], v[1] >> 32);
+            q[1] = make_uint4(v[2], v[2] >> 32, v[3], v[3] >> 32);
+          } else {
+            uint32_t* o = &q[0].x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = bf16x2(tc::lo2(v[j]), tc::hi2(v[j]));
+          }
+          uint8_t* to = dst + c * (kF32 ? 4 : 2);
+          if (wide && n0 + c + kStep <= p.N) {
+            tc::st_v8(to, q[0], q[1]);
+          } else {  // N is a multiple of 8
+            if (n0 + c < p.N) ptx::st_v4(to, q[0]);
+            if (n0 + c + kStep / 2 < p.N) ptx::st_v4(to + 16, q[1]);
           }
         }
       }

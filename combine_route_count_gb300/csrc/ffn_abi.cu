@@ -114,7 +114,7 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
       return launched(moe::launch_few_rows(p, sms, static_cast<cudaStream_t>(stream)));
     }
     moe::ExpertGemmParams p = {};
-    if (!encode_map(&p.a, a, rows, K) || !encode_map(&p.w, w, w_rows * E, K)) return static_cast<int>(MOE_ECUDA);
+    if (!encode_map(&p.a, a, rows, K) || !encode_map(&p.w, w, w_rows * E, K, glu ? 64 : 128)) return static_cast<int>(MOE_ECUDA);
     p.a_scales = a_scales;
     p.w_scales = w_scales;
     p.offsets = offsets;

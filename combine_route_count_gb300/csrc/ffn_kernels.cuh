@@ -50,7 +50,7 @@ cudaError_t launch_add_norm_fp8(const AddNormParams& p, bool weight_f32, int sms
 // ---- expert_gemm: grouped block-scaled E4M3 products ------------------------
 struct ExpertGemmParams {
   CUtensorMap a;            // E4M3 [rows, K], boxes of 128 x 128
-  CUtensorMap w;            // E4M3 [E * w_rows, K], boxes of 128 x 128
+  CUtensorMap w;            // E4M3 [E * w_rows, K], boxes of 128 x 128, glu: 64 rows
   const float* a_scales;    // [rows, kblocks]
   const float* w_scales;    // [E, w_blocks, kblocks]
   const int32_t* offsets;   // [E+1] first row of each expert, or null: all rows are expert 0's
