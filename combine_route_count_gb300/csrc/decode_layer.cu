@@ -58,6 +58,8 @@ constexpr int kBlock = MOE_FP8_BLOCK;
 constexpr int kTileBytes = 128 * kBlock;  // 128 weight rows x 128 of K
 constexpr int kChunk = kFewChunk;         // token rows are handled 16 at a time
 constexpr int kMaxStages = 12;
+constexpr int kMaxBufs = 4;               // tensor-memory buffers, each for one turn
+__host__ __device__ constexpr int bufs(int columns) { return columns == 16 ? 4 : 2; }
 constexpr int kMaxRanks = 4;              // CTAs of a cluster in few_rows
 constexpr int kTmaWarp = 4, kMmaWarp = 5;  // warps 0-3: epilogue
 constexpr int kThreads = 192;
@@ -251,7 +253,7 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
 // ---- what the kernels share ---------------------------------------------------
 struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[kMaxBufs], acc_empty[kMaxBufs];
   uint64_t drained;
   uint32_t tmem;
   int gave_up;
@@ -262,7 +264,7 @@ __device__ __forceinline__ void init_barriers(Barriers& b) {
     ptx::mbar_init(&b.full[i], 1);
     ptx::mbar_init(&b.empty[i], 1);
   }
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kMaxBufs; ++i) {
     ptx::mbar_init(&b.acc_full[i], 1);
     ptx::mbar_init(&b.acc_empty[i], 4);
   }
@@ -302,7 +304,8 @@ __device__ __forceinline__ void mma_tile(uint32_t tmem, const uint8_t* w, const 
 }
 
 __device__ __forceinline__ void finish_mma(Barriers& b) {  // nothing in flight when the tensor memory is freed
-  tc::commit(&b.drained);
+  if (tc::elect()) tc::commit(&b.drained);
+  __syncwarp();
   tc::wait(&b.drained, 0, &b.gave_up);
 }
 
@@ -336,9 +339,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   __shared__ RoutingShared rs;
   __shared__ __align__(16) float s_scale[4][2][kN];
   __shared__ __align__(16) float s_amax[2][kN][4];
-  constexpr uint32_t kColumns = tmem_columns(4 * kN);
+  constexpr uint32_t kBufs = bufs(kN), kColumns = tmem_columns(kBufs * 2 * kN);
   uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Routing r = routing_at(ring + ring_bytes, ring, p.T * p.K, p.E, kN);
   if (threadIdx.x == 0) {
     init_barriers(b);
@@ -451,24 +454,23 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   };
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {
-      fence_async_proxy();
-      uint32_t it = 0;
-      Place at;
-      for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
-        const int a = v.u / jb, j = v.u - a * jb;
-        const int w0 = r.active[a] * 2 * p.I + j * kBlock, w1 = w0 + p.I;
-        const int row0 = r.first[a], n = r.first[a + 1] - row0, rows = chunks_of(n) * kChunk;
-        int token[kN];  // rows past the expert's last repeat it; their columns are dropped
+    fence_async_proxy();
+    uint32_t it = 0;
+    Place at;
+    for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
+      const int a = v.u / jb, j = v.u - a * jb;
+      const int w0 = r.active[a] * 2 * p.I + j * kBlock, w1 = w0 + p.I;
+      const int row0 = r.first[a], n = r.first[a + 1] - row0, rows = chunks_of(n) * kChunk;
+      int token[kN];  // rows past the expert's last repeat it; their columns are dropped
 #pragma unroll
-        for (int c = 0; c < kN; ++c) token[c] = r.token[row0 + min(c, n - 1)];
-        const uint32_t bytes = 2 * kTileBytes + rows * kBlock;
-        const int k_end = (v.kb0 + v.kb_n) * kBlock;
-        for (int k = v.kb0 * kBlock; k < k_end; k += kBlock, ++it) {
-          if (it >= stages && !tc::wait(&b.empty[at.st], at.phase ^ 1, &b.gave_up)) {
-            ok = false;
-            break;
-          }
+      for (int c = 0; c < kN; ++c) token[c] = r.token[row0 + min(c, n - 1)];
+      const uint32_t bytes = 2 * kTileBytes + rows * kBlock;
+      const int k_end = (v.kb0 + v.kb_n) * kBlock;
+      for (int k = v.kb0 * kBlock; k < k_end; k += kBlock, ++it) {
+        ok = it < stages || tc::wait(&b.empty[at.st], at.phase ^ 1, &b.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (tc::elect()) {
           uint8_t* to = ring + at.st * stage_bytes;
           uint64_t* full = &b.full[at.st];
           ptx::mbar_arrive_expect_tx(full, bytes);
@@ -479,33 +481,37 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
             if (c < rows)
               tc::tma_gather4(to + 2 * kTileBytes + c * kBlock, &p.x_map, k, token[c], token[c + 1], token[c + 2],
                               token[c + 3], full);
-          at.next(stages);
         }
+        __syncwarp();
+        at.next(stages);
       }
-      if (!ok) drain_loads(b, it, stages);
     }
+    if (!ok) drain_loads(b, it, stages);
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      Place at;
-      for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
-        const int a = v.u / jb, chunks = chunks_of(r.first[a + 1] - r.first[a]);
-        for (int kb = 0; kb < v.kb_n; ++kb, ++it) {
-          const uint32_t buf = it & 1;
-          ok = (it < 2 || tc::wait(&b.acc_empty[buf], (it / 2 - 1) & 1, &b.gave_up)) &&
-               tc::wait(&b.full[at.st], at.phase, &b.gave_up);
-          if (!ok) break;
-          tc::fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
+    uint32_t it = 0;
+    Place at;
+    for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
+      const int a = v.u / jb, chunks = chunks_of(r.first[a + 1] - r.first[a]);
+      for (int kb = 0; kb < v.kb_n; ++kb, ++it) {
+        const uint32_t buf = it % kBufs;
+        ok = (it < kBufs || tc::wait(&b.acc_empty[buf], (it / kBufs - 1) & 1, &b.gave_up)) &&
+             tc::wait(&b.full[at.st], at.phase, &b.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after();
+        if (tc::elect()) {
           const uint8_t* w = ring + at.st * stage_bytes;
-          mma_tile(b.tmem + buf * 2 * kN, w, w + 2 * kTileBytes, chunks);
-          mma_tile(b.tmem + (buf * 2 + 1) * kN, w + kTileBytes, w + 2 * kTileBytes, chunks);
-          tc::commit(&b.empty[at.st]);
+          mma_tile(tmem + buf * 2 * kN, w, w + 2 * kTileBytes, chunks);
+          mma_tile(tmem + (buf * 2 + 1) * kN, w + kTileBytes, w + 2 * kTileBytes, chunks);
           tc::commit(&b.acc_full[buf]);
-          at.next(stages);
+          tc::commit(&b.empty[at.st]);
         }
+        __syncwarp();
+        at.next(stages);
       }
-      finish_mma(b);
     }
+    finish_mma(b);
   } else {
     const uint32_t lanes = b.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     uint32_t it = 0;
@@ -533,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
 #pragma unroll
       for (int c = 0; c < kN / 2; ++c) gate[c] = up[c] = 0;
       for (int kb = 0; kb < v.kb_n; ++kb, ++it) {
-        const uint32_t buf = it & 1;
-        float* scale = s_scale[warp][buf];
+        const uint32_t buf = it % kBufs;
+        float* scale = s_scale[warp][it & 1];
         if ((kb & 31) == 0) {
           lane_g = ahead_g, lane_u = ahead_u;
           read_weights(kb + 32);
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
         const float g = __shfl_sync(0xffffffffu, lane_g, kb & 31), u = __shfl_sync(0xffffffffu, lane_u, kb & 31);
         const unsigned long long fg = tc::pack2(g, g), fu = tc::pack2(u, u);
         if (kb + 1 < v.kb_n) read(kb + 1);
-        ok = tc::wait(&b.acc_full[buf], (it / 2) & 1, &b.gave_up);
+        ok = tc::wait(&b.acc_full[buf], (it / kBufs) & 1, &b.gave_up);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -640,10 +646,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ Barriers b;
   __shared__ RoutingShared rs;
   __shared__ __align__(16) float s_scale[4][2][2][kN];  // [warp][buffer][item]
-  constexpr uint32_t kColumns = tmem_columns(4 * kN);
+  constexpr uint32_t kBufs = bufs(kN), kColumns = tmem_columns(kBufs * 2 * kN);
   uint8_t* ring = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
   float* s_out = reinterpret_cast<float*>(ring + ring_bytes);  // [T][128]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Routing r = {};
   if (threadIdx.x == 0) {
     init_barriers(b);
@@ -676,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   bool ok = true;
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {
+    {
       fence_async_proxy();
       // Weights and rows of an item go to one stage; the first stages get
       // their weights before h is ready, so the two walk separately.
@@ -699,16 +705,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (n > 0) enter(w);
       Walk h = w;
       auto load_w = [&]() {
-        uint64_t* full = &b.full[w.at.st];
-        ptx::mbar_arrive_expect_tx(full, kTileBytes + chunks_of(w.rows) * kChunk * kBlock);
-        tc::tma_load_2d(ring + w.at.st * stage_bytes, &p.w2_map, w.kb * kBlock, w.row, full);
+        if (tc::elect()) {
+          uint64_t* full = &b.full[w.at.st];
+          ptx::mbar_arrive_expect_tx(full, kTileBytes + chunks_of(w.rows) * kChunk * kBlock);
+          tc::tma_load_2d(ring + w.at.st * stage_bytes, &p.w2_map, w.kb * kBlock, w.row, full);
+        }
+        __syncwarp();
         step(w);
       };
       auto load_h = [&]() {
-        const int row0 = row0_of(h.a);
-        for (int c = 0; c < h.rows; c += kChunk)
-          tc::tma_load_2d(ring + h.at.st * stage_bytes + kTileBytes + c * kBlock, &p.h_map, h.kb * kBlock, row0 + c,
-                          &b.full[h.at.st]);
+        if (tc::elect()) {
+          const int row0 = row0_of(h.a);
+          for (int c = 0; c < h.rows; c += kChunk)
+            tc::tma_load_2d(ring + h.at.st * stage_bytes + kTileBytes + c * kBlock, &p.h_map, h.kb * kBlock, row0 + c,
+                            &b.full[h.at.st]);
+        }
+        __syncwarp();
         step(h);
       };
       const int early = min(n, static_cast<int>(stages));
@@ -718,39 +730,41 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < early; ++i) load_h();
       int i = early;
       for (; i < n; ++i) {
-        if (!tc::wait(&b.empty[w.at.st], w.at.phase ^ 1, &b.gave_up)) {
-          ok = false;
-          break;
-        }
+        ok = tc::wait(&b.empty[w.at.st], w.at.phase ^ 1, &b.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         load_w();
         load_h();
       }
       if (!ok) drain_loads(b, i, stages);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      int a = it0 / kb_n, kb = it0 - a * kb_n;
-      Place at;
-      for (int i = 0, turn = 0; i < n; ++turn) {
-        const uint32_t buf = turn & 1;
-        const int two = i + 1 < n && kb + 1 < kb_n ? 2 : 1, chunks = chunks_of(rows_of(a));
-        ok = turn < 2 || tc::wait(&b.acc_empty[buf], (turn / 2 - 1) & 1, &b.gave_up);
-        for (int m = 0; ok && m < two; ++m, ++i) {
-          ok = tc::wait(&b.full[at.st], at.phase, &b.gave_up);
-          if (!ok) break;
-          tc::fence_after();
-          const uint8_t* w = ring + at.st * stage_bytes;
-          mma_tile(b.tmem + (buf * 2 + m) * kN, w, w + kTileBytes, chunks);
-          tc::commit(&b.empty[at.st]);
-          at.next(stages);
-        }
+    const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
+    int a = it0 / kb_n, kb = it0 - a * kb_n;
+    Place at;
+    for (uint32_t i = 0, turn = 0; i < static_cast<uint32_t>(n); ++turn) {
+      const uint32_t buf = turn % kBufs;
+      const int two = i + 1 < static_cast<uint32_t>(n) && kb + 1 < kb_n ? 2 : 1, chunks = chunks_of(rows_of(a));
+      ok = turn < kBufs || tc::wait(&b.acc_empty[buf], (turn / kBufs - 1) & 1, &b.gave_up);
+      for (int m = 0; m < two; ++m, ++i) {
+        ok = ok && tc::wait(&b.full[at.st], at.phase, &b.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tc::commit(&b.acc_full[buf]);
-        kb += two;
-        if (kb == kb_n) kb = 0, ++a;
+        tc::fence_after();
+        if (tc::elect()) {
+          const uint8_t* w = ring + at.st * stage_bytes;
+          mma_tile(tmem + (buf * 2 + m) * kN, w, w + kTileBytes, chunks);
+          tc::commit(&b.empty[at.st]);
+          if (m + 1 == two) tc::commit(&b.acc_full[buf]);
+        }
+        __syncwarp();
+        at.next(stages);
       }
-      finish_mma(b);
+      if (!ok) break;
+      kb += two;
+      if (kb == kb_n) kb = 0, ++a;
     }
+    finish_mma(b);
   } else {
     float* mine = s_out + threadIdx.x;
     for (int t = 0; t < p.T; ++t) mine[t * 128] = 0.0f;
@@ -789,8 +803,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       enter(a);
       read(kb, two);
     }
-    for (int i = 0, turn = 0; i < n; ++turn) {
-      const uint32_t buf = turn & 1;
+    for (uint32_t i = 0, turn = 0; static_cast<int>(i) < n; ++turn) {
+      const uint32_t buf = turn % kBufs;
       const int row0 = row0_of(a), rows = next_rows, two_now = two;
       unsigned long long f[2];
 #pragma unroll
@@ -798,18 +812,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         f[m] = tc::pack2(next_w[m], next_w[m]);
 #pragma unroll
         for (int c = 0; c < (kN + 31) / 32; ++c)
-          if (32 * c < rows && lane + 32 * c < kN) s_scale[warp][buf][m][lane + 32 * c] = next[m][c];
+          if (32 * c < rows && lane + 32 * c < kN) s_scale[warp][turn & 1][m][lane + 32 * c] = next[m][c];
       }
       i += two_now;
       kb += two_now;
       const bool last = kb == kb_n;
       if (last) kb = 0, ++a;
-      two = i + 1 < n && kb + 1 < kb_n ? 2 : 1;
-      if (i < n) {
+      two = static_cast<int>(i) + 1 < n && kb + 1 < kb_n ? 2 : 1;
+      if (static_cast<int>(i) < n) {
         if (last) enter(a);
         read(kb, two);
       }
-      ok = tc::wait(&b.acc_full[buf], (turn / 2) & 1, &b.gave_up);
+      ok = tc::wait(&b.acc_full[buf], (turn / kBufs) & 1, &b.gave_up);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -823,14 +837,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           tc::tmem_load_16(lanes + buf * 2 * kN + c, v[0]);
           if (two_now == 2) tc::tmem_load_16(lanes + (buf * 2 + 1) * kN + c, v[1]);
           tc::wait_loads();
-          add_scaled(v[0], s_scale[warp][buf][0] + c, f[0], acc + c / 2);
-          if (two_now == 2) add_scaled(v[1], s_scale[warp][buf][1] + c, f[1], acc + c / 2);
+          add_scaled(v[0], s_scale[warp][turn & 1][0] + c, f[0], acc + c / 2);
+          if (two_now == 2) add_scaled(v[1], s_scale[warp][turn & 1][1] + c, f[1], acc + c / 2);
         }
       }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&b.acc_empty[buf]);
-      if (last || i == n) {
+      if (last || static_cast<int>(i) == n) {
 #pragma unroll
         for (int c0 = 0; c0 < kN; c0 += 8) {
           if (c0 < rows) {
