@@ -1,13 +1,16 @@
 // Products of few rows with many weights, on the 5th-generation tensor core:
 //
-//   decode_glu   h[t,k] = SiLU(W1[e] x[t]) * (W3[e] x[t]),  e = topk_idx[t,k],
+//   row_groups   decode: h[t,k] = SiLU(W1[e] x[t]) * (W3[e] x[t]),  e = topk_idx[t,k],
 //                quantised by blocks of 128 like every payload here
+//                glu, gemm: the products of expert_gemm.cu for grouped rows,
+//                where an expert has a few
 //   few_rows     decode: out[t] = bf16( sum_k topk_w[t,k] * W2[e] h[t,k] )
 //                dense:  out[i] = W a[i], one weight matrix, up to 64 rows
 //
-// decode_glu and the decode form of few_rows are a whole expert layer for up
-// to 64 tokens in two kernels (moe_decode_layer_fp8); the dense form is
-// moe_expert_gemm_fp8's for a handful of rows.
+// The decode forms are a whole expert layer for up to 64 tokens in two kernels
+// (moe_decode_layer_fp8).  The others serve moe_expert_glu_fp8 and
+// moe_expert_gemm_fp8: the dense form for up to 64 rows of one matrix, the
+// grouped ones for up to four rows an expert on average.
 //
 // Bound by memory: the weights are read once for a few rows, so what counts is
 // to keep many weight bytes in flight on every SM and to start early.  Weight
@@ -20,11 +23,11 @@
 // stages kept too little in flight (one token, 8 of 256 experts, H 7168, inner
 // 2048: 95 us, 45 % of DRAM busy).
 //
-// decode_glu gathers the x rows of an expert's tokens (TMA gather of four rows
-// at a time); few_rows reads rows of h, which decode_glu writes ordered by
+// row_groups gathers the x rows of an expert's tokens (TMA gather of four rows
+// at a time); few_rows reads rows of h, which row_groups writes ordered by
 // (expert, token).
 //
-// Spread over the SMs: decode_glu's unit is 128 columns of one expert's h; few
+// Spread over the SMs: row_groups' unit is 128 columns of one expert's h; few
 // units are split along K over a cluster.  few_rows gives 128 columns of out to
 // a cluster, which shares that tile's (expert, K block) items; partial sums are
 // exchanged through distributed shared memory and added in rank order.  Sums
@@ -35,7 +38,7 @@
 // number of lower bits set).  Malformed routing is seen by every CTA alike:
 // nothing is written but the status.
 //
-// few_rows is launched while decode_glu runs and brings in its first weights
+// few_rows is launched while row_groups runs and brings in its first weights
 // before it waits for h.  Waits are bounded (2 s) and report MOE_ETIMEDOUT.
 
 #include <cuda_bf16.h>
@@ -79,7 +82,8 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
 // them whatever an expert had, and was slower on the usual experts.)
 struct Routing {
   int32_t* active;   // the experts at work, ascending
-  int32_t* first;    // their first rows, then the number of rows
+  int32_t* first;    // their first rows
+  int32_t* count;    // how many rows, 1 .. kN
   int32_t* token;    // of each row
   float* weight;     // topk_w of each row
   // scratch, free after build_routing
@@ -93,9 +97,9 @@ struct RoutingShared {
 };
 
 __host__ __device__ inline int max_active(int pairs, int E, int kN) { return (pairs < E ? pairs : E) + pairs / kN; }
-__host__ __device__ inline int routing_bytes(int pairs, int E, int kN) {
+__host__ __device__ inline int routing_bytes(int pairs, int E, int kN, bool by_token) {
   const int a = max_active(pairs, E, kN);
-  return (a * 4 + (a + 1) * 4 + pairs * 8 + 15) / 16 * 16;
+  return (a * 12 + (by_token ? pairs * 8 : 0) + 15) / 16 * 16;
 }
 
 // What build_routing needs besides lies at the start of the ring, before any load.
@@ -106,7 +110,8 @@ __device__ __forceinline__ Routing routing_at(uint8_t* smem, uint8_t* scratch, i
   Routing r;
   r.active = reinterpret_cast<int32_t*>(smem);
   r.first = r.active + a;
-  r.token = r.first + a + 1;
+  r.count = r.first + a;
+  r.token = r.count + a;
   r.weight = reinterpret_cast<float*>(r.token + pairs);
   r.mask = reinterpret_cast<uint32_t*>(scratch);
   r.row_of = reinterpret_cast<int32_t*>(r.mask + 2 * E);
@@ -155,13 +160,13 @@ __device__ __forceinline__ void build_routing_small(const Routing& r, RoutingSha
     int a = 0;
     for (int j = 0; j < pairs; ++j) a += heads[j] && (expert[j] < e || (expert[j] == e && j < i));
     if (head) {
+      int rest = 0;  // of the expert's pairs, from this one on
+      for (int j = i; j < pairs; ++j) rest += expert[j] == e;
       r.active[a] = e;
       r.first[a] = row;
+      r.count[a] = min(rest, kN);
     }
-    if (row == pairs - 1) {  // of the last entry
-      s.n_active = head ? a + 1 : a;
-      r.first[s.n_active] = pairs;
-    }
+    if (row == pairs - 1) s.n_active = head ? a + 1 : a;  // of the last entry
   }
   __syncthreads();
 }
@@ -229,12 +234,10 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
       for (int k = 0; k < entries; ++k) {
         r.active[a + k] = e;
         r.first[a + k] = row + k * kN;
+        r.count[a + k] = min(n - k * kN, kN);
       }
     }
-    if (c == chunks - 1 && lane == 31) {
-      s.n_active = base + (sum & 0xffff);
-      r.first[s.n_active] = pairs;
-    }
+    if (c == chunks - 1 && lane == 31) s.n_active = base + (sum & 0xffff);
   }
   __syncthreads();
 #pragma unroll
@@ -246,6 +249,54 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
       r.token[row] = t;
       r.weight[row] = weight[m];
     }
+  }
+  __syncthreads();
+}
+
+// The same list for rows that come grouped: expert e's are [offsets[e], offsets[e+1]).
+__device__ __forceinline__ void build_groups(const Routing& r, RoutingShared& s, const DecodeParams& p, int kN) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = (p.E + 31) / 32;
+  if (threadIdx.x == 0) s.bad = 0, s.most_rows = 1;
+  // Clamped: a damaged table cannot lead outside the buffers.
+  auto rows_of = [&](int e, int& lo) {
+    lo = 0;
+    if (e >= p.E) return 0;
+    lo = min(max(p.offsets[e], 0), p.T);
+    return min(max(p.offsets[e + 1], lo), p.T) - lo;
+  };
+  __syncthreads();
+  for (int c = warp; c < chunks; c += kThreads / 32) {
+    int lo;
+    const int n = rows_of(c * 32 + lane, lo);
+    const int entries = __reduce_add_sync(0xffffffffu, (n + kN - 1) / kN), most = __reduce_max_sync(0xffffffffu, n);
+    if (lane == 0) {
+      atomicMax(&s.most_rows, min(most, kN));
+      s.warp_active[c] = entries;
+    }
+  }
+  __syncthreads();
+  // Offsets out of order may give rows to several experts: no more entries
+  // than the list has room for.
+  const int room = max_active(p.T, p.E, kN);
+  for (int c = warp; c < chunks; c += kThreads / 32) {
+    int lo;
+    const int e = c * 32 + lane, n = rows_of(e, lo), entries = (n + kN - 1) / kN;
+    const int base = __reduce_add_sync(0xffffffffu, lane < c ? s.warp_active[lane] : 0);
+    int sum = entries;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += up;
+    }
+    for (int k = 0; k < entries; ++k) {
+      const int a = base + sum - entries + k;
+      if (a < room) {
+        r.active[a] = e;
+        r.first[a] = lo + k * kN;
+        r.count[a] = min(n - k * kN, kN);
+      }
+    }
+    if (c == chunks - 1 && lane == 31) s.n_active = min(base + sum, room);
   }
   __syncthreads();
 }
@@ -309,6 +360,11 @@ __device__ __forceinline__ void finish_mma(Barriers& b) {  // nothing in flight 
   tc::wait(&b.drained, 0, &b.gave_up);
 }
 
+__device__ __forceinline__ void store_out(const DecodeParams& p, int64_t to, float v) {
+  if (p.out_f32) reinterpret_cast<float*>(p.out)[to] = v;
+  else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(v);
+}
+
 __host__ __device__ constexpr uint32_t tmem_columns(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
 
 // acc[c] += v[c] * scale[c] * f for 16 columns; scale in shared memory.
@@ -330,8 +386,10 @@ __device__ __forceinline__ void add_scaled(const uint32_t* v, const float* scale
 // CTA's routing and epilogues pass while the other streams.  The units that
 // are left when every CTA has had the same number are split along K over
 // groups of 2, 4 or 8 CTAs of a cluster, as far as the CTAs go.
-template <int kN>
-__global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_constant__ DecodeParams p,
+// (gemm: 256 columns of the product, two a thread.)
+enum Form { kDecode, kGlu, kGemm };
+template <int kN, Form kForm>
+__global__ void __launch_bounds__(kThreads, 2) row_groups_kernel(const __grid_constant__ DecodeParams p,
                                                                  uint32_t ring_bytes, uint32_t ranks) {
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers b;
@@ -361,13 +419,17 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   // early reads of topk_idx, topk_w and the weights rely on.  This CTA has its
   // tensor memory: CTAs of few_rows, which wait for this grid while they hold
   // theirs, cannot keep it from it.
-  ptx::launch_dependents();
-  build_routing(r, rs, p, kN);
+  if (kForm == kDecode) {
+    ptx::launch_dependents();
+    build_routing(r, rs, p, kN);
+  } else {
+    build_groups(r, rs, p, kN);
+  }
   tc::fence_after();
   // Stages as large as the fullest expert needs.
   const uint32_t stage_bytes = 2 * kTileBytes + chunks_of(rs.most_rows) * kChunk * kBlock;
   const uint32_t stages = min(ring_bytes / stage_bytes, static_cast<uint32_t>(kMaxStages));
-  const int jb = p.I / kBlock, kb_all = p.H / kBlock;
+  const int jb = kForm == kGemm ? (p.I + 255) / 256 : p.I / kBlock, kb_all = (p.H + kBlock - 1) / kBlock;
   const int units = rs.bad ? 0 : rs.n_active * jb;
   const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
   int split = 1;  // CTAs that share one of the last units
@@ -389,14 +451,33 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
     if (v.u + grid < end) return Span{v.u + grid, 0, kb_all};
     return Span{shared, part * kb_all / split, (part + 1) * kb_all / split - part * kb_all / split};
   };
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = rs.bad ? MOE_EROUTE : MOE_OK;
+  if (kForm == kDecode && blockIdx.x == 0 && threadIdx.x == 0) *p.status = rs.bad ? MOE_EROUTE : MOE_OK;
   bool ok = true;
 
   unsigned long long gate[kN / 2], up[kN / 2];
   int round = 0;  // units this CTA has finished
   // Epilogue warps: h of the unit's token rows from the sums, quantised.
   auto finish = [&](int u, int round) -> bool {
-    const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
+    const int a = u / jb, j = u - a * jb, row0 = r.first[a], n = r.count[a];
+    if (kForm == kGemm) {
+#pragma unroll
+      for (int c0 = 0; c0 < kN; c0 += kChunk) {
+        if (c0 < n) {
+#pragma unroll
+          for (int c = c0; c < c0 + kChunk; ++c) {
+            const float v0 = c & 1 ? tc::hi2(gate[c / 2]) : tc::lo2(gate[c / 2]);
+            const float v1 = c & 1 ? tc::hi2(up[c / 2]) : tc::lo2(up[c / 2]);
+            const int column = j * 256 + static_cast<int>(threadIdx.x);
+            const int64_t to = static_cast<int64_t>(row0 + c) * p.I + column;
+            if (c < n) {
+              if (column < p.I) store_out(p, to, v0);
+              if (column + 128 < p.I) store_out(p, to + 128, v1);
+            }
+          }
+        }
+      }
+      return true;
+    }
     float (*amax)[4] = s_amax[round & 1];  // in turn: a warp one unit ahead does not overwrite
 #pragma unroll
     for (int c0 = 0; c0 < kN; c0 += kChunk) {
@@ -459,11 +540,14 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
     Place at;
     for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
       const int a = v.u / jb, j = v.u - a * jb;
-      const int w0 = r.active[a] * 2 * p.I + j * kBlock, w1 = w0 + p.I;
-      const int row0 = r.first[a], n = r.first[a + 1] - row0, rows = chunks_of(n) * kChunk;
+      const int w0 = kForm == kGemm ? r.active[a] * p.I + j * 256 : r.active[a] * 2 * p.I + j * kBlock;
+      const int w1 = w0 + (kForm == kGemm ? 128 : p.I);
+      const int row0 = r.first[a], n = r.count[a], rows = chunks_of(n) * kChunk;
       int token[kN];  // rows past the expert's last repeat it; their columns are dropped
+      if (kForm == kDecode) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c) token[c] = r.token[row0 + min(c, n - 1)];
+        for (int c = 0; c < kN; ++c) token[c] = r.token[row0 + min(c, n - 1)];
+      }
       const uint32_t bytes = 2 * kTileBytes + rows * kBlock;
       const int k_end = (v.kb0 + v.kb_n) * kBlock;
       for (int k = v.kb0 * kBlock; k < k_end; k += kBlock, ++it) {
@@ -476,9 +560,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
           ptx::mbar_arrive_expect_tx(full, bytes);
           tc::tma_load_2d(to, &p.w13_map, k, w0, full);
           tc::tma_load_2d(to + kTileBytes, &p.w13_map, k, w1, full);
+          if (kForm != kDecode)
+            for (int c = 0; c < rows; c += kChunk)
+              tc::tma_load_2d(to + 2 * kTileBytes + c * kBlock, &p.x_map, k, row0 + c, full);
 #pragma unroll
           for (int c = 0; c < kN; c += 4)
-            if (c < rows)
+            if (kForm == kDecode && c < rows)
               tc::tma_gather4(to + 2 * kTileBytes + c * kBlock, &p.x_map, k, token[c], token[c + 1], token[c + 2],
                               token[c + 3], full);
         }
@@ -492,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
     uint32_t it = 0;
     Place at;
     for (Span v = first_span(); ok && v.u >= 0; v = next_span(v)) {
-      const int a = v.u / jb, chunks = chunks_of(r.first[a + 1] - r.first[a]);
+      const int a = v.u / jb, chunks = chunks_of(r.count[a]);
       for (int kb = 0; kb < v.kb_n; ++kb, ++it) {
         const uint32_t buf = it % kBufs;
         ok = (it < kBufs || tc::wait(&b.acc_empty[buf], (it / kBufs - 1) & 1, &b.gave_up)) &&
@@ -516,13 +603,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
     const uint32_t lanes = b.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     uint32_t it = 0;
     for (Span v = first_span(); ok && v.u >= 0; v = next_span(v), ++round) {
-      const int a = v.u / jb, j = v.u - a * jb, row0 = r.first[a], n = r.first[a + 1] - row0;
-      const float* sg = p.w13_scales + (static_cast<int64_t>(r.active[a]) * 2 * jb + j) * kb_all + v.kb0;
-      const float* su = sg + static_cast<int64_t>(jb) * kb_all;
+      const int a = v.u / jb, j = v.u - a * jb, row0 = r.first[a], n = r.count[a];
+      // Rows of blocks of the weights' scales that this thread's columns lie in.
+      const int blocks = (p.I + kBlock - 1) / kBlock, b0 = kForm == kGemm ? min(2 * j, blocks - 1) : j;
+      const int b1 = kForm == kGemm ? min(2 * j + 1, blocks - 1) : jb + j;
+      const float* sw = p.w13_scales +
+                        static_cast<int64_t>(r.active[a]) * (kForm == kGemm ? blocks : 2 * blocks) * kb_all + v.kb0;
+      const float *sg = sw + static_cast<int64_t>(b0) * kb_all, *su = sw + static_cast<int64_t>(b1) * kb_all;
       const float* sx[(kN + 31) / 32];
 #pragma unroll
-      for (int i = 0; i < (kN + 31) / 32; ++i)
-        sx[i] = p.x_scales + static_cast<int64_t>(r.token[row0 + min(lane + 32 * i, n - 1)]) * kb_all + v.kb0;
+      for (int i = 0; i < (kN + 31) / 32; ++i) {
+        const int row = row0 + min(lane + 32 * i, n - 1);
+        sx[i] = p.x_scales + static_cast<int64_t>(kForm == kDecode ? r.token[row] : row) * kb_all + v.kb0;
+      }
       // The token rows' scales of the next K block are read a block ahead, the
       // weights' of 32 blocks at a time (one a lane), 32 blocks ahead.
       float next[(kN + 31) / 32], lane_g, lane_u, ahead_g = 0.0f, ahead_u = 0.0f;
@@ -584,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
     // [gate, up][token row][column]
     float* sums = reinterpret_cast<float*>(ring);
     const bool mine = warp < kTmaWarp && ok && shared >= 0;
-    const int n = shared >= 0 ? r.first[shared / jb + 1] - r.first[shared / jb] : 0;
+    const int n = shared >= 0 ? r.count[shared / jb] : 0;
     __syncthreads();
     if (mine) {
 #pragma unroll
@@ -628,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_glu_kernel(const __grid_co
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (threadIdx.x == 0 && b.gave_up) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
+  if (threadIdx.x == 0 && b.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
   if (warp == kMmaWarp) tc::tmem_free(b.tmem, kColumns);
 }
 
@@ -678,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int it0 = static_cast<int>(static_cast<int64_t>(items) * rank / ranks);
   const int n = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / ranks) - it0;
   auto row0_of = [&](int a) { return kDense ? 0 : r.first[a]; };
-  auto rows_of = [&](int a) { return kDense ? p.T : r.first[a + 1] - r.first[a]; };
+  auto rows_of = [&](int a) { return kDense ? p.T : r.count[a]; };
   bool ok = true;
 
   if (warp == kTmaWarp) {
@@ -901,8 +994,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (q < static_cast<int>(ranks)) sum += v[m][q];
         const int64_t to = static_cast<int64_t>(t) * p.H + column;
         if (t < p.T) {
-          if (p.out_f32) reinterpret_cast<float*>(p.out)[to] = sum;
-          else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(sum);
+          store_out(p, to, sum);
         }
       }
     }
@@ -962,7 +1054,7 @@ size_t smem_budget(const void* kernel, int per_sm) {
   return kSm / per_sm - kReserved - fixed;
 }
 
-// Clusters of four CTAs of decode_glu, two CTAs an SM, that are resident at one
+// Clusters of four CTAs of row_groups, two CTAs an SM, that are resident at one
 // time: a cluster's CTAs share a GPC, so not every SM can be used.  Asked for
 // CTAs that have an SM each and doubled (the query does not count on a second
 // CTA).  Cached per device and kernel.
@@ -993,23 +1085,18 @@ int resident_clusters(void (*kernel)(DecodeParams, uint32_t, uint32_t), size_t s
   return 2 * n;
 }
 
-#ifdef SWEEP
-}
-#include <cstdlib>
-namespace {
-size_t env(const char* n, size_t d) { const char* v = std::getenv(n); return v ? std::atoi(v) : d; }
-#endif
-template <int kN>
-cudaError_t launch_glu(const DecodeParams& p, int sms, cudaStream_t stream) {
-  auto* kernel = decode_glu_kernel<kN>;
-  const int pairs = p.T * p.K;
-  const size_t rest = 1024 + routing_bytes(pairs, p.E, kN);
+template <int kN, Form kForm>
+cudaError_t launch_groups(const DecodeParams& p, int sms, cudaStream_t stream) {
+  auto* kernel = row_groups_kernel<kN, kForm>;
+  const int rows = p.T * p.K;
+  const size_t rest = 1024 + routing_bytes(rows, p.E, kN, kForm == kDecode);
   const size_t budget = smem_budget(reinterpret_cast<const void*>(kernel), 2);
   if (budget < rest + 2 * kTileBytes + kN * kBlock) return cudaErrorInvalidConfiguration;
   const cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), budget);
   if (err != cudaSuccess) return err;
-  const int64_t units = static_cast<int64_t>(max_active(pairs, p.E, kN)) * (p.I / kBlock);
-  const int kb_n = p.H / kBlock;
+  const int64_t units =
+      static_cast<int64_t>(max_active(rows, p.E, kN)) * (kForm == kGemm ? (p.I + 255) / 256 : p.I / kBlock);
+  const int kb_n = (p.H + kBlock - 1) / kBlock;
   uint32_t ranks = 1;
   int64_t groups = units;
   if (units > 2 * sms) {
@@ -1029,7 +1116,7 @@ template <int kN, bool kDense>
 cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
   auto* kernel = few_rows_kernel<kN, kDense>;
   const int pairs = p.T * p.K;
-  const size_t rest = 1024 + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E, kN));
+  const size_t rest = 1024 + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E, kN, true));
   const int64_t tiles = (p.H + 127) / 128;
   const int64_t items = static_cast<int64_t>(kDense ? 1 : max_active(pairs, p.E, kN)) * p.h_blocks;
   // Up to 16 tokens two CTAs share an SM, else their sums leave too little for the rings.
@@ -1047,12 +1134,8 @@ cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream) {
-#ifdef SWEEP
-  const bool narrow = env("NARROW", p.T <= 16 || p.T * p.K <= 6 * p.E);
-#else
   const bool narrow = p.T <= 16 || p.T * p.K <= 6 * p.E;
-#endif
-  cudaError_t err = narrow ? launch_glu<16>(p, sms, stream) : launch_glu<32>(p, sms, stream);
+  cudaError_t err = narrow ? launch_groups<16, kDecode>(p, sms, stream) : launch_groups<32, kDecode>(p, sms, stream);
   if (err != cudaSuccess) return err;
   return narrow ? launch_few<16, false>(p, sms, stream) : launch_few<32, false>(p, sms, stream);
 }
@@ -1060,6 +1143,10 @@ cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t str
 cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream) {
   if (p.T <= 16) return launch_few<16, true>(p, sms, stream);
   return p.T <= 32 ? launch_few<32, true>(p, sms, stream) : launch_few<64, true>(p, sms, stream);
+}
+
+cudaError_t launch_row_groups(const DecodeParams& p, bool glu, int sms, cudaStream_t stream) {
+  return glu ? launch_groups<16, kGlu>(p, sms, stream) : launch_groups<16, kGemm>(p, sms, stream);
 }
 
 }  // namespace moe

@@ -113,6 +113,27 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
       p.out_f32 = f32;
       return launched(moe::launch_few_rows(p, sms, static_cast<cudaStream_t>(stream)));
     }
+    // A few rows an expert: weight rows, not token rows, as the 128 rows of the
+    // matrix tiles.
+    if (offsets && rows <= static_cast<int64_t>(4) * E) {
+      moe::DecodeParams p = {};
+      if (!encode_map(&p.w13_map, w, w_rows * E, K) || !encode_map(&p.x_map, a, rows, K, moe::kFewChunk))
+        return static_cast<int>(MOE_ECUDA);
+      p.x_scales = a_scales;
+      p.w13_scales = w_scales;
+      p.offsets = offsets;
+      p.hq = static_cast<uint8_t*>(out);
+      p.h_scales = h_scales;
+      p.out = out;
+      p.status = status;
+      p.T = static_cast<int32_t>(rows);
+      p.H = K;
+      p.K = 1;
+      p.E = E;
+      p.I = N;
+      p.out_f32 = f32;
+      return launched(moe::launch_row_groups(p, glu, sms, static_cast<cudaStream_t>(stream)));
+    }
     moe::ExpertGemmParams p = {};
     if (!encode_map(&p.a, a, rows, K) || !encode_map(&p.w, w, w_rows * E, K, glu ? 64 : 128)) return static_cast<int>(MOE_ECUDA);
     p.a_scales = a_scales;

@@ -71,18 +71,19 @@ constexpr int kFewRows = MOE_DECODE_MAX_TOKENS;  // most rows of either kernel
 constexpr int kFewChunk = 16;
 struct DecodeParams {
   CUtensorMap w13_map;      // E4M3 [E * 2I, H], boxes of 128 rows (all boxes 128 wide)
-  CUtensorMap x_map;        // E4M3 [T, H], boxes of one row (gathered)
+  CUtensorMap x_map;        // E4M3 [T, H], boxes of one row (gathered) or of kFewChunk rows
   CUtensorMap w2_map;       // E4M3 [E * H, I], boxes of 128 rows
   CUtensorMap h_map;        // E4M3 [T*K, I], boxes of kFewChunk rows
   const float* x_scales;    // [T, H/128]
   const int32_t* topk_idx;  // [T, K]
   const float* topk_w;      // [T, K]
+  const int32_t* offsets;   // launch_row_groups: [E+1] first row of each expert
   const float* w13_scales;  // [E, 2I/128, H/128]
   const float* w2_scales;   // [E, out_blocks, h_blocks]
   uint8_t* hq;              // workspace: E4M3 [T*K, I], rows ordered by (expert, token)
   float* h_scales;          // workspace: [T*K, h_blocks]
   void* out;                // [T, H], bf16 or float32
-  int32_t* status;          // may be null in launch_few_rows
+  int32_t* status;          // may be null but in launch_decode_layer
   int32_t T, H, K, E, I;
   int32_t h_blocks, out_blocks;  // ceil(I/128), ceil(H/128)
   bool out_f32;
@@ -91,5 +92,9 @@ cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t str
 // One dense product of T <= kFewRows rows: out [T, H] = h [T, I] . w2 [H, I]^T,
 // from w2_map, h_map and the scales (K = E = 1).
 cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream);
+// Grouped products of T rows, a few for each of E experts (K = 1): out [T, I] =
+// x [T, H] . w13 [e, I, H]^T, or (glu) hq, h_scales from w13 [e, 2I, H]; x_map
+// with boxes of kFewChunk rows.
+cudaError_t launch_row_groups(const DecodeParams& p, bool glu, int sms, cudaStream_t stream);
 
 }  // namespace moe
