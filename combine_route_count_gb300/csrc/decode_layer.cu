@@ -5,18 +5,17 @@
 //                glu, gemm: the products of expert_gemm.cu for grouped rows,
 //                where an expert has a few
 //   few_rows     decode: out[t] = bf16( sum_k topk_w[t,k] * W2[e] h[t,k] )
-//                dense:  out[i] = W a[i], one weight matrix, up to 64 rows
+//                dense:  out[i] = W a[i], one weight matrix, up to 32 rows
 //
 // The decode forms are a whole expert layer for up to 64 tokens in two kernels
 // (moe_decode_layer_fp8).  The others serve moe_expert_glu_fp8 and
-// moe_expert_gemm_fp8: the dense form for up to 64 rows of one matrix, the
-// grouped ones for up to four rows an expert on average.
+// moe_expert_gemm_fp8 where experts have few rows or there are few tiles.
 //
 // Bound by memory: the weights are read once for a few rows, so what counts is
 // to keep many weight bytes in flight on every SM and to start early.  Weight
 // tiles of 128 rows x 128 of K arrive by tiled TMA in a ring of stages, with
 // the token rows' block beside them, and are the 128-row operand of tcgen05.mma;
-// an expert's rows are its 16, 32, 48 or 64 columns.  A thread of the epilogue
+// 16 or 32 rows of one expert are its columns.  A thread of the epilogue
 // warps owns one weight row and a column per token row; each K block's product
 // is scaled and added to its float32 registers as in expert_gemm.cu.  An
 // earlier form loaded the weights straight into mma.sync fragments: its register
@@ -177,7 +176,7 @@ __device__ __forceinline__ void build_routing(const Routing& r, RoutingShared& s
     build_routing_small(r, s, p, kN);
     return;
   }
-  constexpr int kMost = (kFewRows * MOE_MAX_TOP_K + kThreads - 1) / kThreads;
+  constexpr int kMost = (kFewTokens * MOE_MAX_TOP_K + kThreads - 1) / kThreads;
   int expert[kMost];
   float weight[kMost];
 #pragma unroll
@@ -261,6 +260,7 @@ __device__ __forceinline__ void build_groups(const Routing& r, RoutingShared& s,
   auto rows_of = [&](int e, int& lo) {
     lo = 0;
     if (e >= p.E) return 0;
+    if (!p.offsets) return p.T;  // one expert
     lo = min(max(p.offsets[e], 0), p.T);
     return min(max(p.offsets[e + 1], lo), p.T) - lo;
   };
@@ -1141,8 +1141,7 @@ cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t str
 }
 
 cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream) {
-  if (p.T <= 16) return launch_few<16, true>(p, sms, stream);
-  return p.T <= 32 ? launch_few<32, true>(p, sms, stream) : launch_few<64, true>(p, sms, stream);
+  return p.T <= 16 ? launch_few<16, true>(p, sms, stream) : launch_few<32, true>(p, sms, stream);
 }
 
 cudaError_t launch_row_groups(const DecodeParams& p, bool glu, int sms, cudaStream_t stream) {

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -80,6 +81,32 @@ bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Which kernel a product takes.  The tile kernel (expert_gemm.cu) gives 128
+// rows of one expert to a tile and all of K to one CTA, which is what many rows
+// want; with few rows its tiles are mostly empty, and with few tiles a long K is
+// walked by few SMs.  The few-row kernels (decode_layer.cu) put weight rows in
+// the tile's 128 and split K, and read the weights again for every 16 rows of
+// an expert.  Measured in us, tile kernel against row groups:
+//   glu   E 256, H 7168, inner 1024: 529 / 447 at 2 rows an expert, 638 / 647 at
+//         16; E 8, H = inner = 1024: 17.5 / 7.0 at 16, 18.3 / 8.9 at 64; E 8,
+//         H = inner = 4096 (256 tiles): 68 / 54 at 32, 68 / 72 at 64; E 1, H 7168,
+//         inner 2048: 33 / 17 at 64 rows, 28 / 20 at 128, 28 / 31 at 256
+//   gemm  E 256, N 7168, K 2048: 441 / 450 at 2; N 1024, K 7168: 232 / 229 at 2,
+//         280 / 284 at 8; E 32, N 512, K 4096: 16.6 / 9.9 at half a row, 18.1 /
+//         18.1 at 8; E 1, N 1024, K 8192: 28.7 / 14.9 at 128 rows
+// and, for one matrix, against the few-row product: N 7168, K 2048: 9.3 / 6.2 at
+// one row, 9.3 / 8.4 at 32, 9.5 / 11.6 at 64; N = K = 512: 4.8 / 5.2 at 16.
+enum class Product { kTiles, kRowGroups, kFewRows };
+
+Product choose_product(bool glu, bool grouped, int64_t rows, int32_t kblocks, int64_t n_tiles, int32_t E, int sms) {
+  if (!glu && !grouped && rows <= moe::kFewDenseRows && kblocks >= 8) return Product::kFewRows;
+  const int64_t tiles = (std::min<int64_t>(rows, E) + rows / 128) * n_tiles;
+  int64_t most = glu ? 16 : 8;  // rows an expert
+  if (tiles * 4 <= sms) most = 128;
+  else if (glu && tiles <= sms) most = 64;
+  return rows <= most * E && (glu || kblocks >= 24) ? Product::kRowGroups : Product::kTiles;
+}
+
 // What the two grouped products have in common; N: columns of the output.
 int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows, int32_t K, const void* w,
                    const float* w_scales, int32_t N, int32_t E, const int32_t* offsets, void* out, float* h_scales,
@@ -96,7 +123,10 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
   return guarded([&] {
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
-    if (!glu && !offsets && rows <= moe::kFewRows) {
+    const int32_t kblocks = (K + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
+    const int32_t n_tiles = (N + moe::expert_gemm_n_tile(glu) - 1) / moe::expert_gemm_n_tile(glu);
+    const Product product = choose_product(glu, offsets != nullptr, rows, kblocks, n_tiles, E, sms);
+    if (product == Product::kFewRows) {
       moe::DecodeParams p = {};
       if (!encode_map(&p.w2_map, w, N, K) || !encode_map(&p.h_map, a, rows, K, moe::kFewChunk))
         return static_cast<int>(MOE_ECUDA);
@@ -108,14 +138,12 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
       p.H = N;
       p.K = p.E = 1;
       p.I = K;
-      p.h_blocks = (K + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
+      p.h_blocks = kblocks;
       p.out_blocks = (N + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
       p.out_f32 = f32;
       return launched(moe::launch_few_rows(p, sms, static_cast<cudaStream_t>(stream)));
     }
-    // A few rows an expert: weight rows, not token rows, as the 128 rows of the
-    // matrix tiles.
-    if (offsets && rows <= static_cast<int64_t>(4) * E) {
+    if (product == Product::kRowGroups) {
       moe::DecodeParams p = {};
       if (!encode_map(&p.w13_map, w, w_rows * E, K) || !encode_map(&p.x_map, a, rows, K, moe::kFewChunk))
         return static_cast<int>(MOE_ECUDA);
@@ -143,9 +171,9 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
     p.h_scales = h_scales;
     p.status = status;
     p.rows = rows;
-    p.kblocks = (K + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
+    p.kblocks = kblocks;
     p.N = N;
-    p.n_tiles = (N + moe::expert_gemm_n_tile(glu) - 1) / moe::expert_gemm_n_tile(glu);
+    p.n_tiles = n_tiles;
     p.E = E;
     p.w_rows = static_cast<int32_t>(w_rows);
     p.w_blocks = static_cast<int32_t>((w_rows + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK);

@@ -67,7 +67,8 @@ int expert_gemm_n_tile(bool glu);
 cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool glu, bool f32, int sms, cudaStream_t stream);
 
 // ---- decode_layer: products of few rows with many weights ----------------------
-constexpr int kFewRows = MOE_DECODE_MAX_TOKENS;  // most rows of either kernel
+constexpr int kFewTokens = MOE_DECODE_MAX_TOKENS;  // of launch_decode_layer
+constexpr int kFewDenseRows = 32;                // of launch_few_rows
 constexpr int kFewChunk = 16;
 struct DecodeParams {
   CUtensorMap w13_map;      // E4M3 [E * 2I, H], boxes of 128 rows (all boxes 128 wide)
@@ -77,7 +78,7 @@ struct DecodeParams {
   const float* x_scales;    // [T, H/128]
   const int32_t* topk_idx;  // [T, K]
   const float* topk_w;      // [T, K]
-  const int32_t* offsets;   // launch_row_groups: [E+1] first row of each expert
+  const int32_t* offsets;   // launch_row_groups: [E+1] first row of each expert, or null (E = 1)
   const float* w13_scales;  // [E, 2I/128, H/128]
   const float* w2_scales;   // [E, out_blocks, h_blocks]
   uint8_t* hq;              // workspace: E4M3 [T*K, I], rows ordered by (expert, token)
@@ -89,10 +90,10 @@ struct DecodeParams {
   bool out_f32;
 };
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream);
-// One dense product of T <= kFewRows rows: out [T, H] = h [T, I] . w2 [H, I]^T,
+// One dense product of T <= kFewDenseRows rows: out [T, H] = h [T, I] . w2 [H, I]^T,
 // from w2_map, h_map and the scales (K = E = 1).
 cudaError_t launch_few_rows(const DecodeParams& p, int sms, cudaStream_t stream);
-// Grouped products of T rows, a few for each of E experts (K = 1): out [T, I] =
+// Products of T rows, grouped by E experts (K = 1): out [T, I] =
 // x [T, H] . w13 [e, I, H]^T, or (glu) hq, h_scales from w13 [e, 2I, H]; x_map
 // with boxes of kFewChunk rows.
 cudaError_t launch_row_groups(const DecodeParams& p, bool glu, int sms, cudaStream_t stream);

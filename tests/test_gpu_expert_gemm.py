@@ -158,6 +158,38 @@ def test_long_k(ffn):
     check_gemm(ffn, *inputs(3, 6, 1, 256, 65536), None, torch.float32)
 
 
+# K long enough that products of few rows are split along it, and kernels that
+# put weight rows into the matrix tile take over; with a last block of 16.
+@pytest.mark.parametrize("name", ["even", "ragged", "ones", "many", "one_hot"])
+@pytest.mark.parametrize("N", [8, 264, 640])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_grouped_long_k(ffn, name, N, dtype):
+    counts = COUNTS[name]
+    check_gemm(ffn, *inputs(N, sum(counts), len(counts), N, 25 * 128 + 16 if name == "many" else 40 * 128 + 16),
+               offsets_of(counts), dtype)
+
+
+@pytest.mark.parametrize("rows", [1, 16, 17, 32, 33, 64, 100, 128, 129])
+@pytest.mark.parametrize("N,K", [(1024, 6000), (136, 4096), (24, 26 * 128)])
+def test_dense_long_k(ffn, rows, N, K):
+    check_gemm(ffn, *inputs(rows, rows, 1, N, K), None, torch.float32)
+    check_gemm(ffn, *inputs(rows, rows, 1, N, K, integers=True), None, torch.float32, exact=K < 4096)
+
+
+@pytest.mark.parametrize("rows_each", [1, 2, 15, 16, 17, 40, 64, 65, 130])
+def test_glu_rows_per_expert(ffn, rows_each):
+    """Across the sizes at which another kernel takes over, with one expert far fuller than the others."""
+    counts = [rows_each] * 12
+    counts[3], counts[7] = 0, 3 * rows_each
+    check_glu(ffn, *inputs(rows_each, sum(counts), 12, 2 * 1024, 768), offsets_of(counts))
+    check_glu(ffn, *inputs(rows_each, sum(counts), 12, 2 * 256, 768), offsets_of(counts))
+
+
+def test_glu_many_experts(ffn):
+    counts = [(5 * i) % 7 for i in range(1024)]
+    check_glu(ffn, *inputs(1, sum(counts), 1024, 2 * 128, 256), offsets_of(counts))
+
+
 def test_rows_that_no_expert_owns_stay(ffn):
     for off in ([3, 5, 5, 9], [4, 4, 4, 4]):
         a, sa, w, sw = inputs(4, 12, 3, 128, 128, integers=True)
@@ -173,6 +205,7 @@ def test_damaged_offsets_stay_inside(ffn, off):
     a, sa, w, sw = inputs(5, 12, 3, 256, 256)
     t = torch.tensor(off, dtype=torch.int32, device="cuda")
     gemm(ffn, a, sa, w, sw, t, torch.bfloat16)
+    gemm(ffn, *inputs(5, 12, 3, 256, 4096), t, torch.bfloat16)
     glu(ffn, a, sa, w, sw, t)
 
 
