@@ -19,6 +19,9 @@ LIB = os.path.join(PKG, "libmoe.so")
 # its buffer before use (MOE_ECORRUPT); a separate library and object folder.
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libmoe_checked.so")
+# The CPython module of ffn.py: argument checks on torch tensors, calls into
+# libmoe.so next to it.  Built against the installed torch, with the host compiler.
+LIB_FFN = os.path.join(PKG, "_ffn.so")
 SOURCES = ["route_count.cu", "route_split.cu", "route_cluster.cu", "route_pack.cu", "route_pack_fp8.cu", "dispatch_pack.cu", "dispatch_fp8.cu", "dispatch_staged.cu", "dense_a2a.cu", "combine.cu", "combine_two_level.cu", "moe_abi.cu", "moe_noalloc.cu",
            "add_norm_fp8.cu", "expert_gemm.cu", "decode_layer.cu", "ffn_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -69,7 +72,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List
         objs = list(ex.map(compile_one, SOURCES))
     tmp = lib + f".tmp{os.getpid()}"
     libdir = _cuda_lib_dir(nv)
-    cmd = [nv] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + [
+    cmd = [nv] + ARCH + ["-shared", "-cudart", "shared", "-Xlinker", f"-soname={os.path.basename(lib)}", "-o", tmp] + objs + [
         "-Xlinker", f"-rpath,{libdir}", "-L", libdir]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -78,5 +81,32 @@ def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List
     return lib
 
 
+def build_ffn(force: bool = False) -> str:
+    """Compile csrc/ffn_py.cc into _ffn.so next to libmoe.so; returns its path."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "ffn_py.cc")
+    if not force and os.path.exists(LIB_FFN) and os.path.getmtime(LIB_FFN) >= _newest_input():
+        return LIB_FFN
+    build()
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = LIB_FFN + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
+    for inc in (INCLUDE, os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-I", inc]
+    lib = os.path.join(troot, "lib")
+    cmd += [LIB, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", os.path.join(cuda, "lib64"), "-lcudart",
+            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}", f"-Wl,-rpath,{os.path.join(cuda, 'lib64')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on ffn_py.cc:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, LIB_FFN)
+    return LIB_FFN
+
+
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
+    print(build_ffn(force=True))

@@ -22,6 +22,7 @@ def ffn():
         pytest.skip("no CUDA device")
     from combine_route_count_gb300 import build, ffn as f, moe
     build.build()
+    build.build_ffn()
     moe.load_library()
     return f
 
