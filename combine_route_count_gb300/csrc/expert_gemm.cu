@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         for (int j = 0; j < kCols / 2; ++j) {
           const float gate = j & 1 ? tc::hi2(acc[j / 2]) : tc::lo2(acc[j / 2]);
           const float up = j & 1 ? tc::hi2(acc[kCols / 4 + j / 2]) : tc::lo2(acc[kCols / 4 + j / 2]);
-          h[j] = gate / (1.0f + expf(-gate)) * up;
+          // Of a denominator beyond 2^126 the quotient becomes 0; it is below 2^-119 there.
+          h[j] = __fdividef(gate, 1.0f + expf(-gate)) * up;
           amax = fmaxf(amax, fabsf(h[j]));
         }
         // The other half of the row's 128 columns is another warp's.  The two
