@@ -101,6 +101,25 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Lane i of four holds units u[0..3] of row i; after it, unit i of rows 0..3.
+template <int kWords>
+__device__ __forceinline__ void transpose_4(uint32_t (&u)[4][kWords], int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & d) continue;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? u[j][i] : u[j + d][i], d);
+        u[j][i] = upper ? got : u[j][i];
+        u[j + d][i] = upper ? u[j + d][i] : got;
+      }
+    }
+  }
+}
+
 template <bool kGlu, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertGemmParams p) {
   extern __shared__ uint8_t s_raw[];
@@ -247,7 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     uint32_t it = 0;
     int parity = 0, round = 0;
     bool ok = true;
-    // Rows that begin on 32-byte boundaries are stored by whole sectors.
+    // Rows that begin on 32-byte boundaries are stored by whole sectors, four
+    // lanes side by side.  (A lane a row: 32 lines an instruction, and the
+    // experts' second products, 128 rows each, take 870 us instead of 765.)
     const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.N) * (kF32 ? 4 : 2)) & 31) == 0;
     for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++round) {
       const Tile tile = find_tile(g, p.E, p.n_tiles, t);
@@ -335,44 +356,49 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         amax = fmaxf(amax, s.amax[parity][half ^ 1][r]);
         const float scale = amax > 0.0f ? __fdiv_rn(fmaxf(amax, kTinyAmax), 448.0f) : 1.0f;
         const float inv = __fdiv_rn(1.0f, scale);
-        if (act) {
-          uint8_t* dst = static_cast<uint8_t*>(p.out) + row * p.N + tile.n * kBlockK + half * (kCols / 2);
+        // Four lanes store 64 bytes of a row together.
+        uint32_t u[4][4];
 #pragma unroll
-          for (int c = 0; c < kCols / 2; c += 16) {
-            uint4 q;
-            uint32_t* o = &q.x;
+        for (int c = 0; c < kCols / 2; c += 4)
+          u[c / 16][c / 4 & 3] = fp8q::e4m3x2(__fmul_rn(h[c], inv), __fmul_rn(h[c + 1], inv)) |
+                                 (fp8q::e4m3x2(__fmul_rn(h[c + 2], inv), __fmul_rn(h[c + 3], inv)) << 16);
+        transpose_4(u, lane);
+        const int r0 = r & ~3;
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(tile.row0 + r0) * p.N + tile.n * kBlockK +
+                       half * (kCols / 2) + (lane & 3) * 16;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float* e = h + c + 4 * j;
-              o[j] = fp8q::e4m3x2(__fmul_rn(e[0], inv), __fmul_rn(e[1], inv)) |
-                     (fp8q::e4m3x2(__fmul_rn(e[2], inv), __fmul_rn(e[3], inv)) << 16);
+        for (int k = 0; k < 4; ++k)
+          if (r0 + k < tile.rows)
+            ptx::st_v4(dst + static_cast<int64_t>(k) * p.N, make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]));
+        if (act && half == 0) p.h_scales[row * (p.N / kBlockK) + tile.n] = scale;
+      } else if (some) {
+        // Four lanes store 128 bytes of a row together, 32 each.
+        constexpr int kStep = kF32 ? 8 : 16;  // columns of 32 bytes
+        const int n0 = tile.n * kTileN + half * kCols + (lane & 3) * kStep, r0 = r & ~3;
+        const int64_t stride = static_cast<int64_t>(p.N) * (kF32 ? 4 : 2);
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + (tile.row0 + r0) * stride + static_cast<int64_t>(n0) * (kF32 ? 4 : 2);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 4 * kStep) {
+          uint32_t u[4][8];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (kF32) u[i / 8][i & 7] = static_cast<uint32_t>(acc[(c + i) / 2] >> (i & 1 ? 32 : 0));
+            else u[i / 8][i & 7] = bf16x2(tc::lo2(acc[c / 2 + i]), tc::hi2(acc[c / 2 + i]));
+          }
+          transpose_4(u, lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint8_t* to = dst + k * stride + c * (kF32 ? 4 : 2);
+            const uint4 q0 = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+            const uint4 q1 = make_uint4(u[k][4], u[k][5], u[k][6], u[k][7]);
+            if (r0 + k < tile.rows) {
+              if (wide && n0 + c + kStep <= p.N) {
+                tc::st_v8(to, q0, q1);
+              } else {  // N is a multiple of 8
+                if (n0 + c < p.N) ptx::st_v4(to, q0);
+                if (n0 + c + kStep / 2 < p.N) ptx::st_v4(to + 16, q1);
+              }
             }
-            ptx::st_v4(dst + c, q);
-          }
-          if (half == 0) p.h_scales[row * (p.N / kBlockK) + tile.n] = scale;
-        }
-      } else if (act) {
-        const int n0 = tile.n * kTileN + half * kCols;
-        uint8_t* dst = static_cast<uint8_t*>(p.out) + (row * p.N + n0) * (kF32 ? 4 : 2);
-        constexpr int kStep = kF32 ? 8 : 16;  // columns of 32 bytes, a whole sector
-#pragma unroll
-        for (int c = 0; c < kCols; c += kStep) {
-          const unsigned long long* v = acc + c / 2;
-          uint4 q[2];
-          if (kF32) {
-            q[0] = make_uint4(v[0], v[0] >> 32, v[1], v[1] >> 32);
-            q[1] = make_uint4(v[2], v[2] >> 32, v[3], v[3] >> 32);
-          } else {
-            uint32_t* o = &q[0].x;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = bf16x2(tc::lo2(v[j]), tc::hi2(v[j]));
-          }
-          uint8_t* to = dst + c * (kF32 ? 4 : 2);
-          if (wide && n0 + c + kStep <= p.N) {
-            tc::st_v8(to, q[0], q[1]);
-          } else {  // N is a multiple of 8
-            if (n0 + c < p.N) ptx::st_v4(to, q[0]);
-            if (n0 + c + kStep / 2 < p.N) ptx::st_v4(to + 16, q[1]);
           }
         }
       }
