@@ -86,24 +86,27 @@ bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, 
 // want; with few rows its tiles are mostly empty, and with few tiles a long K is
 // walked by few SMs.  The few-row kernels (decode_layer.cu) put weight rows in
 // the tile's 128 and split K, and read the weights again for every 16 rows of
-// an expert.  Measured in us, tile kernel against row groups:
-//   glu   E 256, H 7168, inner 1024: 529 / 447 at 2 rows an expert, 638 / 647 at
-//         16; E 8, H = inner = 1024: 17.5 / 7.0 at 16, 18.3 / 8.9 at 64; E 8,
-//         H = inner = 4096 (256 tiles): 68 / 54 at 32, 68 / 72 at 64; E 1, H 7168,
-//         inner 2048: 33 / 17 at 64 rows, 28 / 20 at 128, 28 / 31 at 256
-//   gemm  E 256, N 7168, K 2048: 441 / 450 at 2; N 1024, K 7168: 232 / 229 at 2,
-//         280 / 284 at 8; E 32, N 512, K 4096: 16.6 / 9.9 at half a row, 18.1 /
-//         18.1 at 8; E 1, N 1024, K 8192: 28.7 / 14.9 at 128 rows
-// and, for one matrix, against the few-row product: N 7168, K 2048: 9.3 / 6.2 at
-// one row, 9.3 / 8.4 at 32, 9.5 / 11.6 at 64; N = K = 512: 4.8 / 5.2 at 16.
+// an expert.  Measured in us, tile kernel / row groups:
+//   glu   E 256, H 7168, inner 1024: 465 / 460 at 2 rows an expert, 538 / 531 at
+//         8, 545 / 597 at 16; E 8, H = inner = 4096 (256 tiles): 47 / 47 at 8,
+//         47 / 53 at 32; E 8, H = inner = 1024 (64 tiles): 8.3 / 7.9 at 32, 8.2 /
+//         8.9 at 64; E 1, H 7168, inner 2048 (16 tiles): 25 / 17 at 64 rows,
+//         25 / 20 at 128, 26 / 31 at 256
+//   gemm  E 256, N 7168, K 2048: 466 / 467 at 2, 543 / 546 at 8; N 1024, K 7168:
+//         274 / 273 at 8, 278 / 285 at 16; E 32, N 512, K 4096: 16.8 / 9.8 at half
+//         a row, 18.7 / 17.9 at 8; E 1, N 1024, K 8192 (4 tiles): 25 / 13 at 64
+//         rows, 28 / 15 at 128; E 4, N 768, K 5120: 18.3 / 16.9 at 128 (24 tiles),
+//         18.4 / 22.4 at 256
+// and, for one matrix, tile kernel / few-row product: N 7168, K 2048: 10.1 / 6.1
+// at one row, 10.1 / 7.6 at 32; N 2048, K 128: 4.3 / 3.5 at 16.
 enum class Product { kTiles, kRowGroups, kFewRows };
 
 Product choose_product(bool glu, bool grouped, int64_t rows, int32_t kblocks, int64_t n_tiles, int32_t E, int sms) {
-  if (!glu && !grouped && rows <= moe::kFewDenseRows && kblocks >= 8) return Product::kFewRows;
+  if (!glu && !grouped && rows <= moe::kFewDenseRows) return Product::kFewRows;
   const int64_t tiles = (std::min<int64_t>(rows, E) + rows / 128) * n_tiles;
-  int64_t most = glu ? 16 : 8;  // rows an expert
+  int64_t most = 8;  // rows an expert
   if (tiles * 4 <= sms) most = 128;
-  else if (glu && tiles <= sms) most = 64;
+  else if (glu && tiles <= sms) most = 32;
   return rows <= most * E && (glu || kblocks >= 24) ? Product::kRowGroups : Product::kTiles;
 }
 
