@@ -99,6 +99,29 @@ def test_many_more_rows_than_ctas(ffn):
     check(ffn, ref.bf16(rng, 9001, 256), ref.bf16(rng, 256), ref.bf16(rng, 9001, 256))
 
 
+@pytest.mark.parametrize("H", [640, 20480])
+@pytest.mark.parametrize("residual", [True, False])
+def test_rows_on_16_byte_boundaries(ffn, H, residual):
+    """Rows that begin between 32-byte sectors take other loads and stores; the results are the same bits."""
+    T, rng = 37, np.random.default_rng(H)
+    x, r, w = ref.bf16(rng, T, H), ref.bf16(rng, T, H), ref.bf16(rng, H)
+    q0, s0, ro0, y0 = run(ffn, x, w, r if residual else None)
+
+    def shifted(t):  # a copy 16 bytes past a sector's beginning
+        buf = torch.empty(T * H + 16, dtype=torch.bfloat16, device="cuda")
+        v = buf[8:8 + T * H].view(T, H)
+        assert v.data_ptr() % 32 == 16
+        return v.copy_(t)
+
+    xd, rd = shifted(x), shifted(r) if residual else None
+    y, ro = shifted(torch.zeros_like(x)), shifted(torch.zeros_like(x)) if residual else None
+    q = torch.empty(T, H, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty(T, H // 128, device="cuda")
+    ffn.add_rms_norm_fp8(xd, w.cuda(), q, s, residual=rd, residual_out=ro, y=y)
+    assert np.array_equal(ref.f64(q.float()), q0) and np.array_equal(ref.f64(s), s0)
+    assert torch.equal(y, y0) and (not residual or torch.equal(ro, ro0))
+
+
 def test_offsets_past_32_bits(ffn):
     """More than 2^32 bytes of x and more than 2^31 codes: the last rows are right."""
     T, H = 131072 + 3, 16384
