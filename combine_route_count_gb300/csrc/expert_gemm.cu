@@ -29,8 +29,9 @@
 // barrier back takes 700 to 1000 cycles, 128 x 256 x 128 of matrix work 512.
 // With two buffers of 256 columns a K block took 1190 cycles.  So each half of
 // the columns has its own two buffers of 128, and four are on their way at a
-// time: 865 cycles.  8192 x 4096 x 7168: 164 us on zeros (2.93 PFLOP/s), 172 us
-// on random values, where the power limit lowers the clock.
+// time: 680 cycles a K block, and about 4000 a tile for its end.  8192 x 4096 x
+// 7168: 164 us on zeros (2.93 PFLOP/s), 172 us on random values, where the power
+// limit lowers the clock; leaving out half of the operand loads changed neither.
 //
 // Tiles are dealt out statically (tile b, b+G, ...), rows fastest, so that the
 // CTAs at work at one time share weight columns in L2.  Waits are bounded (2 s)
