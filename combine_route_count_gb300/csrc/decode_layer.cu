@@ -376,23 +376,16 @@ __device__ __forceinline__ void store_out(const DecodeParams& p, int64_t to, flo
   else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(v);
 }
 
-// Four columns of a row of out, those that exist.
+// Four columns of a row of out, whose rows are a multiple of 8 long.
 __device__ __forceinline__ void store_out_4(const DecodeParams& p, int t, int column, float4 v) {
   const int64_t to = static_cast<int64_t>(t) * p.H + column;
-  if (p.H % 4 == 0) {
-    if (p.out_f32) {
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + to) = v;
-    } else {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-      uint2 o = {*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)};
-      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + to) = o;
-    }
-    return;
+  if (p.out_f32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + to) = v;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    uint2 o = {*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)};
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + to) = o;
   }
-  const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (column + i < p.H) store_out(p, to + i, f[i]);
 }
 
 __host__ __device__ constexpr uint32_t tmem_columns(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
