@@ -158,7 +158,15 @@ __device__ __forceinline__ void finish_chunk(const AddNormParams& p, int64_t t, 
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
   const float top = amax * rms;
   const float scale = amax > 0.0f ? __fdiv_rn(fmaxf(top, kTinyAmax), 448.0f) : 1.0f;
-  const float inv = top >= kTinyAmax ? __fdiv_rn(448.0f, amax) : __fdiv_rn(rms, scale);
+  // Below the floor 448 / amax may be infinite, and so may rms / scale: such a
+  // block's values take rms first.
+  const bool tiny = fminf(amax, top) < kTinyAmax;
+  const float inv = __fdiv_rn(tiny ? 1.0f : 448.0f, tiny ? scale : amax);
+  if (__any_sync(0xffffffffu, tiny)) {
+#pragma unroll
+    for (int j = 0; j < kElems; ++j) v[j] *= tiny ? rms : 1.0f;
+    if (tiny) rms = 1.0f;
+  }
   if (act) {
     uint4 q;
     uint32_t* o = &q.x;
