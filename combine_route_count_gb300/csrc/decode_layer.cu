@@ -347,12 +347,13 @@ struct Place {
 // The scratch that build_routing wrote lies where TMA will write next.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// Waits (bounded) for the loads of iterations [it - stages, it) that may still be in flight.
-__device__ __forceinline__ void drain_loads(Barriers& b, uint32_t it, uint32_t stages) {
+// Waits (bounded) for the loads of iterations [it - stages, it), which may still
+// be in flight: they write to this CTA's shared memory, so it does not end or use
+// the ring otherwise before them, whichever warp gave up.
+__device__ __forceinline__ void drain_loads(Barriers& b, uint32_t it, uint32_t stages, uint32_t test_drop) {
   const unsigned long long start = tc::now_ns();
   for (uint32_t j = it > stages ? it - stages : 0; j < it; ++j)
-    while (!ptx::mbar_try_wait(&b.full[j % stages], (j / stages) & 1) && tc::now_ns() - start < tc::kWaitLimitNs) {
-    }
+    if (j != test_drop) tc::settle(&b.full[j % stages], (j / stages) & 1, start);
 }
 
 __device__ __forceinline__ int chunks_of(int rows) { return (rows + kChunk - 1) / kChunk; }
@@ -368,7 +369,7 @@ __device__ __forceinline__ void mma_tile(uint32_t tmem, const uint8_t* w, const 
 __device__ __forceinline__ void finish_mma(Barriers& b) {  // nothing in flight when the tensor memory is freed
   if (tc::elect()) tc::commit(&b.drained);
   __syncwarp();
-  tc::wait(&b.drained, 0, &b.gave_up);
+  tc::settle(&b.drained, 0, tc::now_ns());
 }
 
 __device__ __forceinline__ void store_out(const DecodeParams& p, int64_t to, float v) {
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 2) row_groups_kernel(const __grid_co
         ok = it < stages || tc::wait(&b.empty[at.st], at.phase ^ 1, &b.gave_up);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (tc::elect()) {
+        if (tc::elect() && it != p.test_drop) {
           uint8_t* to = ring + at.st * stage_bytes;
           uint64_t* full = &b.full[at.st];
           ptx::mbar_arrive_expect_tx(full, bytes);
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 2) row_groups_kernel(const __grid_co
         at.next(stages);
       }
     }
-    if (!ok) drain_loads(b, it, stages);
+    drain_loads(b, it, stages, p.test_drop);
   } else if (warp == kMmaWarp) {
     const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
     uint32_t it = 0;
@@ -805,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       struct Walk {
         Place at;
         int a, kb, row, rows;
+        uint32_t item;
       };
       auto enter = [&](Walk& v) {
         v.row = kDense ? tile * 128 : r.active[v.a] * p.H + tile * 128;
@@ -812,16 +814,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       };
       auto step = [&](Walk& v) {
         v.at.next(stages);
+        ++v.item;
         if (++v.kb == kb_n) {
           v.kb = 0;
           if (++v.a < rs.n_active) enter(v);
         }
       };
-      Walk w = {{}, it0 / kb_n, it0 % kb_n, 0, 0};
+      Walk w = {{}, it0 / kb_n, it0 % kb_n, 0, 0, 0};
       if (n > 0) enter(w);
       Walk h = w;
       auto load_w = [&]() {
-        if (tc::elect()) {
+        if (tc::elect() && w.item != p.test_drop) {
           uint64_t* full = &b.full[w.at.st];
           ptx::mbar_arrive_expect_tx(full, kTileBytes + chunks_of(w.rows) * kChunk * kBlock);
           tc::tma_load_2d(ring + w.at.st * stage_bytes, &p.w2_map, w.kb * kBlock, w.row, full);
@@ -830,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         step(w);
       };
       auto load_h = [&]() {
-        if (tc::elect()) {
+        if (tc::elect() && h.item != p.test_drop) {
           const int row0 = row0_of(h.a);
           for (int c = 0; c < h.rows; c += kChunk)
             tc::tma_load_2d(ring + h.at.st * stage_bytes + kTileBytes + c * kBlock, &p.h_map, h.kb * kBlock, row0 + c,
@@ -852,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         load_w();
         load_h();
       }
-      if (!ok) drain_loads(b, i, stages);
+      drain_loads(b, i, stages, p.test_drop);
     }
   } else if (warp == kMmaWarp) {
     const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* a = stages + st * kStageBytes;
-          if (tc::elect()) {
+          if (tc::elect() && it != p.test_drop) {
             ptx::mbar_arrive_expect_tx(&s.full[st], kStageBytes);
             tc::tma_load_2d(a, &p.a, kb * kBlockK, tile.row0, &s.full[st]);
             // The first half of the columns, then the second; glu (boxes of 64
@@ -221,14 +221,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
           __syncwarp();
         }
       }
-      if (!ok) {  // loads still in flight write to this CTA's shared memory: wait (bounded) for them
-        const uint32_t oldest = it > kStages ? it - kStages : 0;
-        const unsigned long long start = tc::now_ns();
-        for (uint32_t j = oldest; j < it; ++j)
-          while (!ptx::mbar_try_wait(&s.full[j % kStages], (j / kStages) & 1) &&
-                 tc::now_ns() - start < tc::kWaitLimitNs) {
-          }
-      }
+      // Loads in flight write to this CTA's shared memory: it does not end before
+      // them, whichever warp gave up.
+      const unsigned long long start = tc::now_ns();
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+        if (j != p.test_drop) tc::settle(&s.full[j % kStages], (j / kStages) & 1, start);
     }
     if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       constexpr uint32_t kInstr = tc::instr_desc_e4m3(kTileM, kTileN / 2);
@@ -258,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
       // Nothing may be in flight when the tensor memory is freed.
       if (tc::elect()) tc::commit(&s.drained);
       __syncwarp();
-      tc::wait(&s.drained, 0, &s.gave_up);
+      tc::settle(&s.drained, 0, tc::now_ns());
     }
   } else {
     tc::more_registers<kRegsEpilogue>();

@@ -41,6 +41,11 @@ int sm_count() {
   return n;
 }
 
+// moe_ffn_test_drop_load's.
+std::atomic<int32_t> g_test_drop{-1};
+
+uint32_t test_drop() { return static_cast<uint32_t>(g_test_drop.load(std::memory_order_relaxed)); }
+
 template <class F>
 int guarded(F&& f) {
   try {
@@ -144,6 +149,7 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
       p.h_blocks = kblocks;
       p.out_blocks = (N + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK;
       p.out_f32 = f32;
+      p.test_drop = test_drop();
       return launched(moe::launch_few_rows(p, sms, static_cast<cudaStream_t>(stream)));
     }
     if (product == Product::kRowGroups) {
@@ -163,6 +169,7 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
       p.E = E;
       p.I = N;
       p.out_f32 = f32;
+      p.test_drop = test_drop();
       return launched(moe::launch_row_groups(p, glu, sms, static_cast<cudaStream_t>(stream)));
     }
     moe::ExpertGemmParams p = {};
@@ -180,6 +187,7 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
     p.E = E;
     p.w_rows = static_cast<int32_t>(w_rows);
     p.w_blocks = static_cast<int32_t>((w_rows + MOE_FP8_BLOCK - 1) / MOE_FP8_BLOCK);
+    p.test_drop = test_drop();
     return launched(moe::launch_expert_gemm(p, glu, f32, sms, static_cast<cudaStream_t>(stream)));
   });
 }
@@ -302,6 +310,13 @@ MOE_API int moe_decode_layer_fp8(const moe_config* cfg, int32_t inter, const voi
     p.I = inter;
     p.h_blocks = inter / MOE_FP8_BLOCK;
     p.out_blocks = cfg->hidden / MOE_FP8_BLOCK;
+    p.test_drop = test_drop();
     return launched(moe::launch_decode_layer(p, sms, static_cast<cudaStream_t>(stream)));
   });
+}
+
+MOE_API int moe_ffn_test_drop_load(int32_t load) {
+  if (load < -1) return MOE_EINVAL;
+  g_test_drop.store(load, std::memory_order_relaxed);
+  return MOE_OK;
 }

@@ -61,6 +61,7 @@ struct ExpertGemmParams {
   int32_t kblocks, N, n_tiles, E;
   int32_t w_rows;           // weight rows of one expert: N, glu: 2N (gate rows, then up rows)
   int32_t w_blocks;         // ceil(w_rows / 128)
+  uint32_t test_drop;       // the number of a load that each CTA leaves out; UINT32_MAX: none
 };
 // Columns of out that one tile covers.
 int expert_gemm_n_tile(bool glu);
@@ -88,6 +89,7 @@ struct DecodeParams {
   int32_t T, H, K, E, I;
   int32_t h_blocks, out_blocks;  // ceil(I/128), ceil(H/128)
   bool out_f32;
+  uint32_t test_drop;       // as in ExpertGemmParams
 };
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream);
 // One dense product of T <= kFewDenseRows rows: out [T, H] = h [T, I] . w2 [H, I]^T,

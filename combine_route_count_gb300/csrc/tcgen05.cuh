@@ -38,6 +38,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
+// The same for what is still in flight when a CTA ends: it goes on waiting where
+// another thread has given up, until kWaitLimitNs after `start`.
+__device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity, unsigned long long start) {
+  while (!ptx::mbar_try_wait(bar, parity) && now_ns() - start < kWaitLimitNs) {
+  }
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
 }

@@ -49,7 +49,7 @@ EXPORTS = ("moe_validate_config", "moe_workspace_bytes", "moe_recv_bound_rows", 
            "moe_dense_capacity", "moe_dispatch_send_dense", "moe_combine_recv_dense",
            # include/moe_ffn.h
            "moe_add_rms_norm_fp8", "moe_expert_gemm_fp8", "moe_expert_glu_fp8",
-           "moe_decode_workspace_bytes", "moe_decode_layer_fp8")
+           "moe_decode_workspace_bytes", "moe_decode_layer_fp8", "moe_ffn_test_drop_load")
 
 
 class moe_config(ctypes.Structure):
@@ -110,6 +110,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_add_rms_norm_fp8": ([P, P, P, I, I64, ctypes.c_int32, ctypes.c_float, P, P, P, P, P], I),
         "moe_decode_workspace_bytes": ([C, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)], I),
         "moe_decode_layer_fp8": ([C, ctypes.c_int32, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P], I),
+        "moe_ffn_test_drop_load": ([ctypes.c_int32], I),
         "moe_expert_gemm_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, I, P, P], I),
         "moe_expert_glu_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P], I),
     }
@@ -339,6 +340,10 @@ def moe_decode_layer_fp8(cfg: moe_config, inter: int, xq: Any, x_scales: Any, to
                                                _ptr(topk_w), _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales),
                                                _ptr(out), _ptr(status), _ptr(workspace), workspace_bytes,
                                                _stream(stream)), "moe_decode_layer_fp8")
+
+
+def moe_ffn_test_drop_load(load: int) -> None:
+    _check(load_library().moe_ffn_test_drop_load(load), "moe_ffn_test_drop_load")
 
 
 # ---- convenience: one context with a torch-allocated workspace ---------------

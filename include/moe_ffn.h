@@ -149,6 +149,12 @@ int moe_decode_layer_fp8(const moe_config* cfg, int32_t inter, const void* xq, c
                          const void* w2, const float* w2_scales, void* out, int32_t* status, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* For tests of failure detection: in later calls of this process every CTA of a
+ * product kernel leaves out its operand load number `load` (from 0), as if the
+ * copy never arrived.  The wait for it runs out after its limit (2 s), and the
+ * call reports MOE_ETIMEDOUT.  -1 (the default): none.  MOE_EINVAL below -1. */
+int moe_ffn_test_drop_load(int32_t load);
+
 #ifdef __cplusplus
 }
 #endif
