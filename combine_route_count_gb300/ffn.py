@@ -99,8 +99,10 @@ class DecodeLayer:
     Keeps references to the weights (w13 E4M3 [E, 2*I, H], gate rows then up
     rows; w2 E4M3 [E, H, I]; their scales float32 [E, 2*I/128, H/128] and
     [E, H/128, I/128]) and owns the workspace for up to max_tokens tokens of
-    top_k experts.  One call may be in flight at a time: calls on several
-    streams need a layer object each."""
+    top_k experts.  Calls may be on any stream, also on another than the one
+    the layer was built on, but only one may be in flight at a time: calls that
+    may overlap need a layer object each.  Building a layer waits for the
+    current stream."""
 
     def __init__(self, max_tokens: int, top_k: int, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
                  w2_scales: torch.Tensor):
@@ -122,6 +124,10 @@ class DecodeLayer:
         nbytes = moe.moe_decode_workspace_bytes(moe.make_config(max_tokens, H, top_k, E, 1), I)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        if not torch.cuda.is_current_stream_capturing():
+            # What this stream still does with the new blocks (the zero; their
+            # users before) is over before a call on another stream writes them.
+            torch.cuda.current_stream().synchronize()
         self._plan = struct.pack("6i7Q", max_tokens, H, top_k, E, I, dev, *pointers, self.status.data_ptr(),
                                  self.workspace.data_ptr(), self.workspace.numel())
 

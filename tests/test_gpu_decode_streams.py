@@ -1,0 +1,50 @@
+"""DecodeLayer on streams other than the one it was built on, without a device synchronisation between."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+from test_gpu_decode_layer import ffn, run, tokens, weights  # noqa: E402,F401
+
+
+def occupy(ms):
+    """Work on the current stream that takes about this long."""
+    torch.cuda._sleep(int(ms * 2.0e6))
+
+
+def test_building_stream_is_busy(ffn):  # noqa: F811
+    """What the building stream has yet to do does not undo the status of a call on another stream."""
+    from combine_route_count_gb300 import moe
+    ws = weights(1, 8, 256, 128)
+    x, sx, idx, w = tokens(2, 6, 256, 2, 8)
+    run(ffn.DecodeLayer(6, 2, *ws), x, sx, idx, w)  # everything is loaded
+    idx[3, 1] = 8
+    out = torch.full((6, 256), -7.25, dtype=torch.bfloat16, device="cuda")
+    builder, caller = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(builder):
+        # The block that the status word will take is still being written.
+        before = torch.empty(1, dtype=torch.int32, device="cuda")
+        occupy(100)
+        before.zero_()
+        del before
+        layer = ffn.DecodeLayer(6, 2, *ws)
+    layer.forward(x, sx, idx, w, out, stream=caller)
+    caller.synchronize()
+    builder.synchronize()
+    assert layer.get_error(caller) == moe.MOE_EROUTE
+    assert (out == -7.25).all()
+
+
+def test_built_and_called_in_a_capture(ffn):  # noqa: F811
+    ws, tk = weights(9, 8, 256, 128), tokens(10, 6, 256, 2, 8)
+    want, out = run(ffn.DecodeLayer(6, 2, *ws), *tk), torch.zeros(6, 256, dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer = ffn.DecodeLayer(6, 2, *ws)
+        layer.forward(*tk, out)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and int(layer.status) == 0
