@@ -102,7 +102,8 @@ class DecodeLayer:
     top_k experts.  Calls may be on any stream, also on another than the one
     the layer was built on, but only one may be in flight at a time: calls that
     may overlap need a layer object each.  Building a layer waits for the
-    current stream."""
+    current stream.  A layer may be dropped while a call is in flight; one that
+    is part of a CUDA graph has to live as long as the graph."""
 
     def __init__(self, max_tokens: int, top_k: int, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
                  w2_scales: torch.Tensor):
@@ -124,6 +125,7 @@ class DecodeLayer:
         nbytes = moe.moe_decode_workspace_bytes(moe.make_config(max_tokens, H, top_k, E, 1), I)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._streams = {_raw_stream(dev)}
         if not torch.cuda.is_current_stream_capturing():
             # What this stream still does with the new blocks (the zero; their
             # users before) is over before a call on another stream writes them.
@@ -134,7 +136,17 @@ class DecodeLayer:
     def forward(self, xq: torch.Tensor, x_scales: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                 out: torch.Tensor, stream: Any = None) -> None:
         """out[t] = sum_k topk_w[t,k] * expert(topk_idx[t,k])(x[t]); out bf16 [T, H], T <= max_tokens."""
-        _module.decode_layer_fp8(self._plan, xq, x_scales, topk_idx, topk_w, out, _stream(stream, xq))
+        handle = _stream(stream, xq)
+        if handle not in self._streams:
+            self._use_on(handle)
+        _module.decode_layer_fp8(self._plan, xq, x_scales, topk_idx, topk_w, out, handle)
+
+    def _use_on(self, handle: int) -> None:
+        """Memory that is freed with the layer is not given to others before this stream is done with it."""
+        stream = torch.cuda.ExternalStream(handle, device=self.device)
+        for t in (self.workspace, self.status, *self._weights):
+            t.record_stream(stream)
+        self._streams.add(handle)
 
     def get_error(self, stream: Any = None) -> int:
         """Waits for the stream; the device status of the last call (MOE_OK, MOE_EROUTE or MOE_ETIMEDOUT)."""

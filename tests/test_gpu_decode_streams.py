@@ -1,4 +1,6 @@
 """DecodeLayer on streams other than the one it was built on, without a device synchronisation between."""
+import gc
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -35,6 +37,30 @@ def test_building_stream_is_busy(ffn):  # noqa: F811
     builder.synchronize()
     assert layer.get_error(caller) == moe.MOE_EROUTE
     assert (out == -7.25).all()
+
+
+@pytest.mark.parametrize("T", [1, 24])
+def test_layer_dropped_while_a_call_is_in_flight(ffn, T):  # noqa: F811
+    """The workspace of a dropped layer is not given to others while a call on a side stream uses it."""
+    ws, tk = weights(3, 16, 512, 384), tokens(4, T, 512, 4, 16)
+    layer = ffn.DecodeLayer(T, 4, *ws)
+    want, out = run(layer, *tk), torch.empty(T, 512, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    del layer
+    gc.collect()
+    torch.cuda.synchronize()
+    layer = ffn.DecodeLayer(T, 4, *ws)
+    nbytes, address = layer.workspace.numel(), layer.workspace.data_ptr()
+    with torch.cuda.stream(side):
+        occupy(50)
+    layer.forward(*tk, out, stream=side)
+    del layer
+    gc.collect()
+    others = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert not side.query()  # the call has not ended yet
+    assert all(t.data_ptr() != address for t in others)
+    side.synchronize()
+    assert torch.equal(out, want)
 
 
 def test_built_and_called_in_a_capture(ffn):  # noqa: F811
