@@ -149,7 +149,8 @@ class DecodeLayer:
         self._streams.add(handle)
 
     def get_error(self, stream: Any = None) -> int:
-        """Waits for the stream; the device status of the last call (MOE_OK, MOE_EROUTE or MOE_ETIMEDOUT)."""
-        s = torch.cuda.current_stream() if stream is None else stream
-        s.synchronize()
+        """Waits for the stream (given as to forward); the device status of the last call that had tokens.
+
+        MOE_OK, MOE_EROUTE or MOE_ETIMEDOUT; MOE_OK before the first such call."""
+        torch.cuda.ExternalStream(_stream(stream, self.status), device=self.device).synchronize()
         return int(self.status.item())

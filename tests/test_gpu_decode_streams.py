@@ -63,6 +63,35 @@ def test_layer_dropped_while_a_call_is_in_flight(ffn, T):  # noqa: F811
     assert torch.equal(out, want)
 
 
+def test_streams_as_forward_takes_them(ffn):  # noqa: F811
+    from combine_route_count_gb300 import moe
+    ws, tk = weights(5, 8, 256, 128), tokens(6, 6, 256, 2, 8)
+    layer = ffn.DecodeLayer(6, 2, *ws)
+    want, side = run(layer, *tk), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream, 0):
+        out = torch.zeros(6, 256, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        layer.forward(*tk, out, stream=stream)
+        assert layer.get_error(stream) == moe.MOE_OK
+        assert torch.equal(out, want)
+
+
+def test_status_is_of_the_last_call_with_tokens(ffn):  # noqa: F811
+    from combine_route_count_gb300 import moe
+    layer = ffn.DecodeLayer(6, 2, *weights(7, 8, 256, 128))
+    assert layer.get_error() == moe.MOE_OK
+    tk = tokens(8, 6, 256, 2, 8)
+    empty = [t[:0] for t in tk] + [torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")]
+    layer.forward(*empty)
+    assert layer.get_error() == moe.MOE_OK
+    tk[2][0, 0] = -1
+    layer.forward(*tk, torch.empty(6, 256, dtype=torch.bfloat16, device="cuda"))
+    assert layer.get_error() == moe.MOE_EROUTE
+    layer.forward(*empty)
+    assert layer.get_error() == moe.MOE_EROUTE
+
+
 def test_built_and_called_in_a_capture(ffn):  # noqa: F811
     ws, tk = weights(9, 8, 256, 128), tokens(10, 6, 256, 2, 8)
     want, out = run(ffn.DecodeLayer(6, 2, *ws), *tk), torch.zeros(6, 256, dtype=torch.bfloat16, device="cuda")
