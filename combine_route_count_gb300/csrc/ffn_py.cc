@@ -209,22 +209,36 @@ PyObject* expert_product(PyObject*, PyObject* const* v, Py_ssize_t n) {
               "moe_expert_gemm_fp8");
 }
 
-// What DecodeLayer keeps, packed by Python's struct ("6i7Q").
+// What DecodeLayer keeps, packed by Python's struct ("6i3Q").
 struct Plan {
   int32_t max_tokens, H, K, E, I, device;
-  uint64_t w13, w13_scales, w2, w2_scales, status, workspace, workspace_bytes;
+  uint64_t status, workspace, workspace_bytes;
 };
 
-// (plan, xq, x_scales, topk_idx, topk_w, out, stream)
+// Whether the tuple (w13, w13_scales, w2, w2_scales) is what DecodeLayer takes; the addresses.
+bool weights(PyObject* tuple, int64_t E, int64_t H, int64_t I, int device, void** at) {
+  if (!PyTuple_Check(tuple) || PyTuple_GET_SIZE(tuple) != 4) {
+    PyErr_SetString(PyExc_TypeError, "weights must be a tuple of four tensors");
+    return false;
+  }
+  const int64_t w13[3] = {E, 2 * I, H}, s13[3] = {E, blocks(2 * I), blocks(H)};
+  const int64_t w2[3] = {E, H, I}, s2[3] = {E, blocks(H), blocks(I)};
+  return arg("w13", PyTuple_GET_ITEM(tuple, 0), kFp8, 3, w13, device, at) &&
+         arg("w13_scales", PyTuple_GET_ITEM(tuple, 1), kF32, 3, s13, device, at + 1) &&
+         arg("w2", PyTuple_GET_ITEM(tuple, 2), kFp8, 3, w2, device, at + 2) &&
+         arg("w2_scales", PyTuple_GET_ITEM(tuple, 3), kF32, 3, s2, device, at + 3);
+}
+
+// (plan, weights, xq, x_scales, topk_idx, topk_w, out, stream)
 PyObject* decode_layer_fp8(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (!count_is(n, 7)) return nullptr;
+  if (!count_is(n, 8)) return nullptr;
   if (!PyBytes_Check(v[0]) || PyBytes_GET_SIZE(v[0]) != static_cast<Py_ssize_t>(sizeof(Plan))) {
     PyErr_SetString(PyExc_TypeError, "plan must be packed as the module expects");
     return nullptr;
   }
   Plan p;
   std::memcpy(&p, PyBytes_AS_STRING(v[0]), sizeof p);
-  const at::Tensor* x = tensor("xq", v[1]);
+  const at::Tensor* x = tensor("xq", v[2]);
   if (!x) return nullptr;
   if (x->dim() != 2) return fail(MOE_EINVAL, "xq must have 2 dimensions");
   const int dev = device_of("xq", *x);
@@ -233,36 +247,33 @@ PyObject* decode_layer_fp8(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (T > p.max_tokens || dev != p.device)
     return fail(MOE_EINVAL, "xq has %lld tokens on cuda:%d, must have at most %d on cuda:%d", static_cast<long long>(T),
                 dev, p.max_tokens, p.device);
-  void *px, *ps, *pi, *pw, *po, *stream;
-  if (!arg2("xq", v[1], kFp8, T, p.H, dev, &px) ||
-      !arg2("x_scales", v[2], kF32, T, p.H / MOE_FP8_BLOCK, dev, &ps) ||
-      !arg2("topk_idx", v[3], kI32, T, p.K, dev, &pi) || !arg2("topk_w", v[4], kF32, T, p.K, dev, &pw) ||
-      !arg2("out", v[5], kBf16, T, p.H, dev, &po) || !stream_of(v[6], &stream))
+  void *px, *ps, *pi, *pw, *po, *w[4], *stream;
+  if (!arg2("xq", v[2], kFp8, T, p.H, dev, &px) ||
+      !arg2("x_scales", v[3], kF32, T, p.H / MOE_FP8_BLOCK, dev, &ps) ||
+      !arg2("topk_idx", v[4], kI32, T, p.K, dev, &pi) || !arg2("topk_w", v[5], kF32, T, p.K, dev, &pw) ||
+      !arg2("out", v[6], kBf16, T, p.H, dev, &po) || !weights(v[1], p.E, p.H, p.I, dev, w) ||
+      !stream_of(v[7], &stream))
     return nullptr;
   const moe_config cfg = {static_cast<int32_t>(T), p.H, p.K, p.E, 1};
   auto at = [](uint64_t address) { return reinterpret_cast<void*>(address); };
   return done(moe_decode_layer_fp8(&cfg, p.I, px, static_cast<float*>(ps), static_cast<int32_t*>(pi),
-                                   static_cast<float*>(pw), at(p.w13), static_cast<float*>(at(p.w13_scales)), at(p.w2),
-                                   static_cast<float*>(at(p.w2_scales)), po, static_cast<int32_t*>(at(p.status)),
+                                   static_cast<float*>(pw), w[0], static_cast<float*>(w[1]), w[2],
+                                   static_cast<float*>(w[3]), po, static_cast<int32_t*>(at(p.status)),
                                    at(p.workspace), p.workspace_bytes, stream),
               "moe_decode_layer_fp8");
 }
 
-// (tensor, kind, shape..., device): the address of a weight that is what DecodeLayer takes.
-PyObject* check(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (!count_is(n, 7)) return nullptr;
-  const char* name = PyUnicode_AsUTF8(v[0]);
-  if (!name) return nullptr;
-  int64_t shape[3];
-  for (int i = 0; i < 3; ++i) {
-    shape[i] = PyLong_AsLongLong(v[3 + i]);
-    if (shape[i] == -1 && PyErr_Occurred()) return nullptr;
+// (weights, E, H, I, device): refuses weights that DecodeLayer does not take.
+PyObject* check_weights(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (!count_is(n, 5)) return nullptr;
+  int64_t size[4];
+  for (int i = 0; i < 4; ++i) {
+    size[i] = PyLong_AsLongLong(v[1 + i]);
+    if (size[i] == -1 && PyErr_Occurred()) return nullptr;
   }
-  const long device = PyLong_AsLong(v[6]);
-  if (device == -1 && PyErr_Occurred()) return nullptr;
-  void* address;
-  if (!arg(name, v[1], v[2] == Py_True ? kFp8 : kF32, 3, shape, static_cast<int>(device), &address)) return nullptr;
-  return PyLong_FromVoidPtr(address);
+  void* at[4];
+  if (!weights(v[0], size[0], size[1], size[2], static_cast<int>(size[3]), at)) return nullptr;
+  Py_RETURN_NONE;
 }
 
 PyObject* init(PyObject*, PyObject* error) {
@@ -294,7 +305,7 @@ PyMethodDef kMethods[] = {
     {"add_rms_norm_fp8", fast<add_rms_norm_fp8>(), METH_FASTCALL, nullptr},
     {"expert_product", fast<expert_product>(), METH_FASTCALL, nullptr},
     {"decode_layer_fp8", fast<decode_layer_fp8>(), METH_FASTCALL, nullptr},
-    {"check", fast<check>(), METH_FASTCALL, nullptr},
+    {"check_weights", fast<check_weights>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ffn", "Argument checks and calls of ffn.py.", -1, kMethods};

@@ -99,7 +99,9 @@ class DecodeLayer:
     Keeps references to the weights (w13 E4M3 [E, 2*I, H], gate rows then up
     rows; w2 E4M3 [E, H, I]; their scales float32 [E, 2*I/128, H/128] and
     [E, H/128, I/128]) and owns the workspace for up to max_tokens tokens of
-    top_k experts.  Calls may be on any stream, also on another than the one
+    top_k experts.  Every call reads the weights where the tensors then have
+    them: they may be overwritten, or given other storage of the same shape,
+    between calls.  Calls may be on any stream, also on another than the one
     the layer was built on, but only one may be in flight at a time: calls that
     may overlap need a layer object each.  Building a layer waits for the
     current stream.  A layer may be dropped while a call is in flight; one that
@@ -115,13 +117,9 @@ class DecodeLayer:
             raise wrong("w13 must be on the current CUDA device")
         self.E, self.H, self.I = w2.shape
         self.max_tokens, self.K, self.device = max_tokens, top_k, w13.device
-        E, H, I, dev, check = self.E, self.H, self.I, self.device.index, _native().check
-        self._weights = (w13, w13_scales, w2, w2_scales)  # kept alive; their addresses are passed on
-        up = lambda n: (n + BLOCK - 1) // BLOCK  # noqa: E731
-        pointers = (check("w13", w13, True, E, 2 * I, H, dev),
-                    check("w13_scales", w13_scales, False, E, up(2 * I), up(H), dev),
-                    check("w2", w2, True, E, H, I, dev),
-                    check("w2_scales", w2_scales, False, E, up(H), up(I), dev))
+        E, H, I, dev = self.E, self.H, self.I, self.device.index
+        self._weights = (w13, w13_scales, w2, w2_scales)
+        _native().check_weights(self._weights, E, H, I, dev)
         nbytes = moe.moe_decode_workspace_bytes(moe.make_config(max_tokens, H, top_k, E, 1), I)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -130,7 +128,7 @@ class DecodeLayer:
             # What this stream still does with the new blocks (the zero; their
             # users before) is over before a call on another stream writes them.
             torch.cuda.current_stream().synchronize()
-        self._plan = struct.pack("6i7Q", max_tokens, H, top_k, E, I, dev, *pointers, self.status.data_ptr(),
+        self._plan = struct.pack("6i3Q", max_tokens, H, top_k, E, I, dev, self.status.data_ptr(),
                                  self.workspace.data_ptr(), self.workspace.numel())
 
     def forward(self, xq: torch.Tensor, x_scales: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
@@ -139,7 +137,7 @@ class DecodeLayer:
         handle = _stream(stream, xq)
         if handle not in self._streams:
             self._use_on(handle)
-        _module.decode_layer_fp8(self._plan, xq, x_scales, topk_idx, topk_w, out, handle)
+        _module.decode_layer_fp8(self._plan, self._weights, xq, x_scales, topk_idx, topk_w, out, handle)
 
     def _use_on(self, handle: int) -> None:
         """Memory that is freed with the layer is not given to others before this stream is done with it."""
