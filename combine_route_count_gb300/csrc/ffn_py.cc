@@ -121,7 +121,14 @@ bool stream_of(PyObject* o, void** stream) {
   return *stream || !PyErr_Occurred();
 }
 
-PyObject* done(int rc, const char* what) {
+// A call into libmoe.so, without the interpreter lock: a launch waits while the
+// launch queue is full, and what empties it may need the lock (a host function
+// in the stream, another thread).
+template <class F>
+PyObject* call(const char* what, F&& f) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int rc = f();  // a C entry point: nothing is thrown
+  PyEval_RestoreThread(state);
   if (rc != MOE_OK) return fail(rc, "%s", what);
   Py_RETURN_NONE;
 }
@@ -162,9 +169,10 @@ PyObject* add_rms_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double eps = PyFloat_AsDouble(a[4]);
   if ((eps == -1.0 && PyErr_Occurred()) || !stream_of(a[8], &stream) || !fits("H", H)) return nullptr;
   const int type = THPVariable_Unpack(a[1]).scalar_type() == at::ScalarType::Float ? MOE_TYPE_F32 : MOE_TYPE_BF16;
-  return done(moe_add_rms_norm_fp8(px, pr, pw, type, T, static_cast<int32_t>(H), static_cast<float>(eps), po, py, pq,
-                                   static_cast<float*>(ps), stream),
-              "moe_add_rms_norm_fp8");
+  return call("moe_add_rms_norm_fp8", [&] {
+    return moe_add_rms_norm_fp8(px, pr, pw, type, T, static_cast<int32_t>(H), static_cast<float>(eps), po, py, pq,
+                                static_cast<float*>(ps), stream);
+  });
 }
 
 // (glu, a, a_scales, w, w_scales, out or hq, None or h_scales, expert_offsets, status, stream)
@@ -196,17 +204,19 @@ PyObject* expert_product(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (!arg2("hq", v[5], kFp8, rows, N / 2, dev, &po) ||
         !arg2("h_scales", v[6], kF32, rows, N / 2 / MOE_FP8_BLOCK, dev, &ph))
       return nullptr;
-    return done(moe_expert_glu_fp8(pa, static_cast<float*>(ps), rows, k, pw, static_cast<float*>(pv),
-                                   static_cast<int32_t>(N / 2), experts, static_cast<int32_t*>(pe), po,
-                                   static_cast<float*>(ph), static_cast<int32_t*>(pt), stream),
-                "moe_expert_glu_fp8");
+    return call("moe_expert_glu_fp8", [&] {
+      return moe_expert_glu_fp8(pa, static_cast<float*>(ps), rows, k, pw, static_cast<float*>(pv),
+                                static_cast<int32_t>(N / 2), experts, static_cast<int32_t*>(pe), po,
+                                static_cast<float*>(ph), static_cast<int32_t*>(pt), stream);
+    });
   }
   if (!arg2("out", v[5], kFloat, rows, N, dev, &po)) return nullptr;
   const int type = THPVariable_Unpack(v[5]).scalar_type() == at::ScalarType::Float ? MOE_TYPE_F32 : MOE_TYPE_BF16;
-  return done(moe_expert_gemm_fp8(pa, static_cast<float*>(ps), rows, k, pw, static_cast<float*>(pv),
-                                  static_cast<int32_t>(N), experts, static_cast<int32_t*>(pe), po, type,
-                                  static_cast<int32_t*>(pt), stream),
-              "moe_expert_gemm_fp8");
+  return call("moe_expert_gemm_fp8", [&] {
+    return moe_expert_gemm_fp8(pa, static_cast<float*>(ps), rows, k, pw, static_cast<float*>(pv),
+                               static_cast<int32_t>(N), experts, static_cast<int32_t*>(pe), po, type,
+                               static_cast<int32_t*>(pt), stream);
+  });
 }
 
 // What DecodeLayer keeps, packed by Python's struct ("6i3Q").
@@ -256,11 +266,12 @@ PyObject* decode_layer_fp8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     return nullptr;
   const moe_config cfg = {static_cast<int32_t>(T), p.H, p.K, p.E, 1};
   auto at = [](uint64_t address) { return reinterpret_cast<void*>(address); };
-  return done(moe_decode_layer_fp8(&cfg, p.I, px, static_cast<float*>(ps), static_cast<int32_t*>(pi),
-                                   static_cast<float*>(pw), w[0], static_cast<float*>(w[1]), w[2],
-                                   static_cast<float*>(w[3]), po, static_cast<int32_t*>(at(p.status)),
-                                   at(p.workspace), p.workspace_bytes, stream),
-              "moe_decode_layer_fp8");
+  return call("moe_decode_layer_fp8", [&] {
+    return moe_decode_layer_fp8(&cfg, p.I, px, static_cast<float*>(ps), static_cast<int32_t*>(pi),
+                                static_cast<float*>(pw), w[0], static_cast<float*>(w[1]), w[2],
+                                static_cast<float*>(w[3]), po, static_cast<int32_t*>(at(p.status)), at(p.workspace),
+                                p.workspace_bytes, stream);
+  });
 }
 
 // (weights, E, H, I, device): refuses weights that DecodeLayer does not take.
