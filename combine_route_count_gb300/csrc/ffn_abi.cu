@@ -122,7 +122,8 @@ int expert_product(bool glu, const void* a, const float* a_scales, int64_t rows,
   const int64_t w_rows = glu ? 2 * static_cast<int64_t>(N) : N;
   if (rows < 0 || rows > INT_MAX - 128 || K <= 0 || K % 16 != 0 || N <= 0 || E < 1 || E > MOE_MAX_EXPERTS)
     return MOE_EINVAL;
-  if (w_rows * E > INT_MAX || (!offsets && E != 1)) return MOE_EINVAL;
+  // A tile's end past the last column, and a block's past the last element, are int32 as well.
+  if (K > INT_MAX - 127 || w_rows * E > INT_MAX - 255 || (!offsets && E != 1)) return MOE_EINVAL;
   if (rows == 0) return MOE_OK;
   if (!a || !a_scales || !w || !w_scales || !out || (glu && !h_scales)) return MOE_EINVAL;
   if (!aligned(a, 16) || !aligned(a_scales, 4) || !aligned(w, 16) || !aligned(w_scales, 4) || !aligned(offsets, 4) ||

@@ -76,10 +76,10 @@ int moe_add_rms_norm_fp8(const void* x, const void* residual, const void* weight
  * accumulated in float32 and rounded once.  With expert_offsets of
  * moe_dispatch_recv this turns dispatched rows into the expert_y that
  * moe_combine_send takes.
- *   a               device E4M3 [rows, k], k % 16 == 0
+ *   a               device E4M3 [rows, k], k % 16 == 0, k <= 2^31 - 128
  *   a_scales        device float32 [rows, ceil(k / 128)]
  *   w               device E4M3 [num_experts, n, k], n % 8 == 0,
- *                   num_experts * n < 2^31
+ *                   num_experts * n <= 2^31 - 256
  *   w_scales        device float32 [num_experts, ceil(n / 128), ceil(k / 128)]
  *   expert_offsets  device int32 [num_experts + 1], non-decreasing; read on the
  *                   device, values outside [0, rows] are taken as the nearest
@@ -99,9 +99,10 @@ int moe_expert_gemm_fp8(const void* a, const float* a_scales, int64_t rows, int3
  *   moe_expert_gemm_fp8, left in float32;
  *   h = gate / (1 + exp(-gate)) * up;  (hq, h_scales) = h quantised,
  * which is what moe_expert_gemm_fp8 takes for the second product.
- *   a, a_scales     device E4M3 [rows, hidden] and its scales, hidden % 16 == 0
+ *   a, a_scales     device E4M3 [rows, hidden] and its scales, hidden % 16 == 0,
+ *                   hidden <= 2^31 - 128
  *   w13             device E4M3 [num_experts, 2 * inter, hidden]: gate rows,
- *                   then up rows; inter % 128 == 0
+ *                   then up rows; inter % 128 == 0, num_experts * 2 * inter <= 2^31 - 256
  *   w13_scales      device float32 [num_experts, 2 * inter / 128, ceil(hidden / 128)]
  *   hq, h_scales    device E4M3 [rows, inter], float32 [rows, inter / 128]
  * Everything else as for moe_expert_gemm_fp8. */
