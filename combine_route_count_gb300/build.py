@@ -22,6 +22,7 @@ LIB_CHECKED = os.path.join(PKG, "libmoe_checked.so")
 # The CPython module of ffn.py: argument checks on torch tensors, calls into
 # libmoe.so next to it.  Built against the installed torch, with the host compiler.
 LIB_FFN = os.path.join(PKG, "_ffn.so")
+STAMP_FFN = os.path.join(BUILD, "ffn.stamp")
 SOURCES = ["route_count.cu", "route_split.cu", "route_cluster.cu", "route_pack.cu", "route_pack_fp8.cu", "dispatch_pack.cu", "dispatch_fp8.cu", "dispatch_staged.cu", "dense_a2a.cu", "combine.cu", "combine_two_level.cu", "moe_abi.cu", "moe_noalloc.cu",
            "add_norm_fp8.cu", "expert_gemm.cu", "decode_layer.cu", "ffn_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,6 +42,14 @@ def _cuda_lib_dir(nv: str) -> str:
 def _newest_input() -> float:
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return max(os.path.getmtime(p) for p in paths)
+
+
+def _read(path: str) -> Optional[str]:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List[str]] = None,
@@ -87,10 +96,12 @@ def build_ffn(force: bool = False) -> str:
 
     import torch
     src = os.path.join(CSRC, "ffn_py.cc")
-    if not force and os.path.exists(LIB_FFN) and os.path.getmtime(LIB_FFN) >= _newest_input():
+    troot = os.path.dirname(torch.__file__)
+    # What the module was compiled against: another torch or Python needs another module.
+    against = f"torch {torch.__version__} in {troot}, {sysconfig.get_config_var('SOABI')}\n"
+    if not force and os.path.exists(LIB_FFN) and os.path.getmtime(LIB_FFN) >= _newest_input() and _read(STAMP_FFN) == against:
         return LIB_FFN
     build()
-    troot = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = LIB_FFN + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
@@ -104,6 +115,9 @@ def build_ffn(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on ffn_py.cc:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_FFN)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(STAMP_FFN, "w") as f:
+        f.write(against)
     return LIB_FFN
 
 
