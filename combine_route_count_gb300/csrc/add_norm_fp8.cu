@@ -17,7 +17,7 @@
 // codes leave as one 16-byte store per lane).  Threads of a row only meet
 // once, for the sum.  A CTA walks rows b, b+G, ... and loads the next row
 // before it waits for the current row's sum.  16384 x 7168 with a residual and y:
-// 170 to 173 us, 6.2 TB/s.
+// 171 to 174 us, 6.1 TB/s.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,12 +33,28 @@ namespace {
 constexpr int kElems = 16;  // elements of one chunk
 
 // A chunk of bf16 is 32 bytes, one sector, moved whole or as two halves.  Whole
-// needs 32-byte alignment.  Measured in us, halves / whole stores / whole loads
-// and stores: 777 x 4224 without a residual 5.15 / 4.98 / 4.81, 16384 x 7168
-// 102 / 97 / 95; with a residual 2048 x 7168 23.2 / 22.6 / 22.1, 8192 x 12288
-// 149 / 139 / 139, but 16384 x 7168 173 / 171 / 181: many long rows of two inputs
-// are loaded by halves.
+// needs 32-byte alignment.  Whole stores are never slower than halves by more
+// than noise; whole loads help until the two inputs of a residual are much
+// larger than L2.  Measured in us, halves / whole stores / whole loads and stores:
+//   no residual, y   8192 x 1024 9.1 / 9.0 / 8.8, 16384 x 7168 102 / 97 / 95,
+//                    16384 x 16384 271 / 233 / 220; without y -1 to 5 % from
+//                    left to right
+//   residual, y      9216 x 1024 15.6 / 15.9 / 15.1, 8192 x 2048 26.9 / 27.4 / 26.5;
+//                    from 2^25 elements on: 8192 x 4096 53.1 / 50.9 / 52.5, 8192 x
+//                    7168 88.8 / 87.2 / 92.1, 16384 x 7168 176 / 173 / 182, 8192 x
+//                    16384 195 / 194 / 203, but 4096 x 12288 77.5 / 71.7 / 70.9
+//   residual only    16384 x 1024 21.1 / 21.2 / 20.2, 8192 x 7168 65.7 / 65.3 / 64.1;
+//                    from 2^26 on, rows up to 8192: 16384 x 4096 77.7 / 76.3 / 79.8,
+//                    8192 x 8192 75.1 / 74.9 / 77.5, 16384 x 8192 147 / 148 / 158;
+//                    longer rows: 16384 x 12288 243 / 226 / 213
 enum Access { kHalves, kSectorStores, kSectors };
+
+// Which one rows on 32-byte boundaries take.
+Access choose_access(bool residual, bool y, int64_t T, int32_t H) {
+  const int64_t n = T * H;
+  const bool halves_in = residual && (y ? n >= 1 << 25 : n >= 1 << 26 && H <= 8192);
+  return halves_in ? kSectorStores : kSectors;
+}
 
 struct Chunk {
   uint4 a, b;
@@ -225,7 +241,10 @@ __global__ void __launch_bounds__(1024) add_norm_fp8_kernel(AddNormParams p, int
 }
 
 // Longer rows: 1024 threads walk the row twice, the second time from the
-// caches.  A thread reads its own columns again before it writes them.
+// caches.  A thread reads its own columns again before it writes them.  With y,
+// 4096 rows: of 32768 228 us (0.79 of the copy rate's floor) with a residual, 171
+// (0.59) without; of 65536 424 (0.85) and 295 (0.68); of 16512 156 (0.58) and 119
+// (0.43), where only 8 threads of 1024 have work in the second step of a walk.
 template <bool kResidual, bool kWeightF32, Access kAccess>
 __global__ void __launch_bounds__(1024) add_norm_fp8_long_kernel(AddNormParams p, int chunks) {
   __shared__ float s_sum[2][32];
@@ -271,9 +290,10 @@ cudaError_t launch(const AddNormParams& p, int sms, cudaStream_t stream) {
 
 template <Access kAccess>
 cudaError_t launch_access(const AddNormParams& p, bool weight_f32, int sms, cudaStream_t stream) {
-  if (p.residual)
+  if (kAccess == kSectorStores || p.residual)
     return weight_f32 ? launch<true, true, kAccess>(p, sms, stream) : launch<true, false, kAccess>(p, sms, stream);
-  return weight_f32 ? launch<false, true, kAccess>(p, sms, stream) : launch<false, false, kAccess>(p, sms, stream);
+  if constexpr (kAccess != kSectorStores)
+    return weight_f32 ? launch<false, true, kAccess>(p, sms, stream) : launch<false, false, kAccess>(p, sms, stream);
 }
 
 }  // namespace
@@ -282,8 +302,9 @@ cudaError_t launch_add_norm_fp8(const AddNormParams& p, bool weight_f32, int sms
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.residual) |
                        reinterpret_cast<uintptr_t>(p.residual_out) | reinterpret_cast<uintptr_t>(p.y);
   if (at % 32 != 0) return launch_access<kHalves>(p, weight_f32, sms, stream);
-  if (p.residual && p.T > 8192) return launch_access<kSectorStores>(p, weight_f32, sms, stream);
-  return launch_access<kSectors>(p, weight_f32, sms, stream);
+  return choose_access(p.residual, p.y, p.T, p.H) == kSectorStores
+             ? launch_access<kSectorStores>(p, weight_f32, sms, stream)
+             : launch_access<kSectors>(p, weight_f32, sms, stream);
 }
 
 }  // namespace moe
