@@ -102,6 +102,20 @@ bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, 
 //         a row, 18.7 / 17.9 at 8; E 1, N 1024, K 8192 (4 tiles): 25 / 13 at 64
 //         rows, 28 / 15 at 128; E 4, N 768, K 5120: 18.3 / 16.9 at 128 (24 tiles),
 //         18.4 / 22.4 at 256
+// The host knows the mean rows an expert, not their counts, and a skewed router
+// costs row groups more.  With many tiles, rows on all / a quarter / one (E 256: on
+// 256 / 64 / 8) of the experts:
+//   glu   E 64, H 2048, inner 1408: mean 2 62.4 / 59.4, 20.5 / 13.6, 11.4 / 10.7;
+//         4 62.6 / 59.7, 20.6 / 13.7, 11.6 / 12.6; 8 63.2 / 60.3, 20.5 / 21.9,
+//         11.6 / 18.2
+//         E 256, H 7168, inner 1024: mean 2 552 / 549, 154 / 145, 29.8 / 34.3; 8
+//         557 / 552, 155 / 154, 32.4 / 103
+//   gemm  E 64, N = K = 4096: mean 2 161 / 160, 46.5 / 45.8, 17.0 / 15.4; 4 162 /
+//         160, 47.6 / 47.8, 17.0 / 21.5; 8 163 / 163, 47.3 / 57.1, 17.4 / 36.0
+// So row groups take a mean of up to 4: beyond it they gain 5 % at most and may
+// lose a multiple.  With few tiles, where they take more, they keep their gain
+// however the rows lie (E 8, H = inner = 1024, mean 32: 8.3 / 7.3 on 8, 2 or 1
+// expert; gemm E 4, N 768, K 5120, mean 128: 18.2 / 16.9 on 4, 18.2 / 16.2 on 1).
 // and, for one matrix, tile kernel / few-row product: N 7168, K 2048: 10.1 / 6.1
 // at one row, 10.1 / 7.6 at 32; N 2048, K 128: 4.3 / 3.5 at 16.
 enum class Product { kTiles, kRowGroups, kFewRows };
@@ -109,7 +123,7 @@ enum class Product { kTiles, kRowGroups, kFewRows };
 Product choose_product(bool glu, bool grouped, int64_t rows, int32_t kblocks, int64_t n_tiles, int32_t E, int sms) {
   if (!glu && !grouped && rows <= moe::kFewDenseRows) return Product::kFewRows;
   const int64_t tiles = (std::min<int64_t>(rows, E) + rows / 128) * n_tiles;
-  int64_t most = 8;  // rows an expert
+  int64_t most = 4;  // rows an expert
   if (tiles * 4 <= sms) most = 128;
   else if (glu && tiles <= sms) most = 32;
   return rows <= most * E && (glu || kblocks >= 24) ? Product::kRowGroups : Product::kTiles;

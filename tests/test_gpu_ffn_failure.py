@@ -38,7 +38,7 @@ def timed_out(call, status):
 
 # The rows, experts and K that take the tile kernel, row groups (alone and as a
 # cluster) and the few-row kernel (alone and as a cluster).
-GEMM = [([300, 100], 512, 1024), ([5] * 16, 640, 40 * 128), ([3, 0, 9], 264, 40 * 128), ([7], 136, 128), ([20], 1024, 6000)]
+GEMM = [([300, 100], 512, 1024), ([4] * 16, 640, 40 * 128), ([3, 0, 9], 264, 40 * 128), ([7], 136, 128), ([20], 1024, 6000)]
 
 
 @pytest.mark.parametrize("counts,N,K", GEMM)
