@@ -1117,8 +1117,13 @@ cudaError_t launch_groups(const DecodeParams& p, int sms, cudaStream_t stream) {
   uint32_t ranks = 1;
   int64_t groups = units;
   if (units > 2 * sms) {
-    // Several rounds: clusters of four, so that the last one can be split.
-    const int clusters = kb_n >= 16 ? std::min(resident_clusters(kernel, budget), 2 * sms / 4) : 0;
+    // Several rounds: clusters of four, so that the last one can be split.  That
+    // costs 1 to 5 % where it finds nothing to split, and pays with a long K: 64
+    // tokens of 2, not split / split in us: H 1024, 320 units 46.9 / 54.2, 610
+    // 70.3 / 71.5; H 2048, 308 60.6 / 59.0, 320 61.6 / 67.2, 610 91.1 / 92.5; H 4096,
+    // 308 90.8 / 85.4, 320 92.0 / 91.6, 360 93.2 / 89.4, 610 117 / 118; H 7168, 308
+    // 152 / 140, 320 155 / 149, 610 209 / 210.
+    const int clusters = kb_n >= 32 ? std::min(resident_clusters(kernel, budget), 2 * sms / 4) : 0;
     ranks = clusters * 4 >= sms ? 4 : 1;
     groups = ranks > 1 ? clusters : 2 * sms;
   } else {
