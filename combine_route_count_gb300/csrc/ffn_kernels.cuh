@@ -16,16 +16,8 @@ namespace moe {
 // scale is taken, so that 1 / scale stays finite.
 constexpr float kTinyAmax = 0x1p-100f;
 
-// Loads that stay where they are written, behind the grid's dependency wait:
-// for data that the kernel before this one may have written.
-__device__ __forceinline__ uint4 ld_v4(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
+// A load that stays where it is written, behind the grid's dependency wait: for
+// data that the kernel before this one may have written.
 __device__ __forceinline__ float ld_f32(const float* p) {
   float v;
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
