@@ -1141,7 +1141,14 @@ cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
   const size_t rest = 1024 + static_cast<size_t>(p.T) * 512 + (kDense ? 0 : routing_bytes(pairs, p.E, kN, true));
   const int64_t tiles = (p.H + 127) / 128;
   const int64_t items = static_cast<int64_t>(kDense ? 1 : max_active(pairs, p.E, kN)) * p.h_blocks;
-  // Up to 16 tokens two CTAs share an SM, else their sums leave too little for the rings.
+  // Up to 16 tokens two CTAs share an SM, else their sums leave too little for the
+  // rings.  As many CTAs a tile as are resident at once, with four items each or
+  // more.  Measured in us, clusters of 1 / 2 / 4: a layer of 8 tokens, 2 of 8 experts,
+  // H 256, inner 512 16.9 / 13.6 / 11.7; 64 tokens, 6 of 64, H 4096, inner 1408 314 / 218 /
+  // 173; 32 tokens, 1 of 8, H 7168, inner 2048 81.9 / 67.6 / 76.3 (not resident with 4);
+  // 8 tokens, 1 of 8, H 16384, inner 512 36.7 / 36.8 / 41.5; dense, 16 rows: N 1024, K
+  // 8192 18.8 / 12.6 / 9.0, N 16384, K 4096 15.6 / 15.3 / 19.1, N 256, K 512 (4 items)
+  // 4.0 / 4.5 / 4.2, N 2048, K 128 (1 item) 3.3 / 4.4 / 4.4.
   const int per_sm = p.T <= 16 ? 2 : 1;
   uint32_t ranks = 1;
   while (ranks < kMaxRanks && tiles * ranks * 2 <= per_sm * sms && ranks * 2 * 4 <= items) ranks *= 2;
@@ -1156,7 +1163,17 @@ cudaError_t launch_few(const DecodeParams& p, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_decode_layer(const DecodeParams& p, int sms, cudaStream_t stream) {
-  const bool narrow = p.T <= 16 || p.T * p.K <= 6 * p.E;
+  // 16 columns need half of the registers and buffers a turn; an expert with more
+  // rows has several entries, and its weights are read again.  Measured in us,
+  // 32 / 16 columns, with T * K / E rows an expert on average, routed evenly:
+  //   6   2 of 8 experts, H 4096, inner 2048 48.4 / 43.2; 4 of 16, H 4096, inner 1408
+  //       53.2 / 53.4; 6 of 64, H 4096, inner 1408 173.8 / 172.5; 8 of 64, H 2048, inner
+  //       768 77.3 / 71.5
+  //   8   43.5 / 43.3, 53.4 / 53.4, -, 78.1 / 72.3
+  //   12  43.8 / 43.8, 55.4 / 55.8; 16: 44.5 / 47.4, 57.3 / 61.9
+  // and with all tokens on the same K experts: 6 28.5 / 29.8, 32.1 / 32.9, 47.4 / 49.5,
+  // 30.4 / 31.4; 12 31.5 / 32.7, 39.2 / 35.0.
+  const bool narrow = p.T <= 16 || p.T * p.K <= 8 * p.E;
   cudaError_t err = narrow ? launch_groups<16, kDecode>(p, sms, stream) : launch_groups<32, kDecode>(p, sms, stream);
   if (err != cudaSuccess) return err;
   return narrow ? launch_few<16, false>(p, sms, stream) : launch_few<32, false>(p, sms, stream);
