@@ -77,7 +77,8 @@ def expert_gemm_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
     without the first dimension for one expert); out bf16 or float32 [rows, N].
     expert_offsets int32 [E+1], e.g. ``dispatch_recv()["expert_offsets"]``;
     None for one expert with all rows.  K % 16 == 0, N % 8 == 0.  status int32
-    [1] is set to MOE_ETIMEDOUT if a wait inside the kernel gives up."""
+    [1], which the caller sets to MOE_OK, becomes MOE_ETIMEDOUT if a wait inside
+    the kernel gives up; without one, incomplete rows are not reported."""
     (_module or _native()).expert_product(False, a, a_scales, w, w_scales, out, None, expert_offsets, status,
                                           _stream(stream, a))
 
@@ -87,7 +88,7 @@ def expert_glu_fp8(a: torch.Tensor, a_scales: torch.Tensor, w13: torch.Tensor, w
                    status: Optional[torch.Tensor] = None, stream: Any = None) -> None:
     """h = SiLU(a . gate^T) * (a . up^T), quantised: the rows of the second product.
 
-    As expert_gemm_fp8, with w13 [E, 2*I, H] (gate rows, then up rows; I a
+    As expert_gemm_fp8 (status too), with w13 [E, 2*I, H] (gate rows, then up rows; I a
     multiple of 128); hq E4M3 [rows, I], h_scales float32 [rows, I/128]."""
     (_module or _native()).expert_product(True, a, a_scales, w13, w13_scales, hq, h_scales, expert_offsets, status,
                                           _stream(stream, a))

@@ -38,6 +38,7 @@ class ExpertLayer:
         self.norm = torch.ones(hidden, dtype=torch.bfloat16, device="cuda")
         self.router = torch.randn(experts, hidden, generator=g, device="cuda", dtype=torch.bfloat16)
         self.moe = moe.MoELayer(tokens, hidden, top_k, experts, 1)
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")  # of the products
         self.decode = ffn.DecodeLayer(few, top_k, self.w13, self.s13, self.w2, self.s2)
 
     def normalise(self, x, residual):
@@ -59,9 +60,9 @@ class ExpertLayer:
         self.moe.dispatch_send_quantized(q, scales, idx, ex, es)
         offsets = self.moe.dispatch_recv()["expert_offsets"]
         hq, hs = torch.empty(rows, self.I, dtype=FP8, device=dev), torch.empty(rows, self.I // 128, device=dev)
-        ffn.expert_glu_fp8(ex, es, self.w13, self.s13, hq, hs, expert_offsets=offsets)
+        ffn.expert_glu_fp8(ex, es, self.w13, self.s13, hq, hs, expert_offsets=offsets, status=self.status)
         y = torch.empty(rows, self.H, dtype=torch.bfloat16, device=dev)
-        ffn.expert_gemm_fp8(hq, hs, self.w2, self.s2, y, expert_offsets=offsets)
+        ffn.expert_gemm_fp8(hq, hs, self.w2, self.s2, y, expert_offsets=offsets, status=self.status)
         out = torch.empty(T, self.H, dtype=torch.bfloat16, device=dev)
         self.moe.combine_send(y)
         self.moe.combine_recv(weight, out)
@@ -83,7 +84,7 @@ def run(tokens, few, hidden, inter, experts, top_k, seed=0):
     idx, weight = layer.route(y)
     many = layer.forward_many(q, scales, idx, weight)
     part = layer.forward_few(q[:few], scales[:few], idx[:few], weight[:few])
-    for status in (layer.moe.get_error(), layer.decode.get_error()):
+    for status in (layer.moe.get_error(), int(layer.status), layer.decode.get_error()):
         if status != moe.MOE_OK:
             raise moe.MoEError(status, "expert layer")
     return many, part

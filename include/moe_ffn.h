@@ -17,10 +17,15 @@
  *   scale = max(amax, 2^-100) / 448 (1 for an all-zero block), inv = 1 / scale,
  *   q = E4M3(v * inv), round to nearest even, saturating.
  * For blocks that hold a bf16 value of at least 2^-100 this is the rule of
- * moe_dispatch_send_fp8; below, the floor keeps 1 / scale finite.  A row that
- * holds an infinity or a NaN, or whose squares (in moe_add_rms_norm_fp8 also
- * s * weight) leave the float32 range, has no defined outputs; other rows are
- * not touched by it.
+ * moe_dispatch_send_fp8; below, the floor keeps 1 / scale finite.  Here v is not
+ * a value in memory but the result of a computation, and each call takes v * inv
+ * with as few roundings as it can: moe_add_rms_norm_fp8 as (s * weight) * (448 /
+ * amax(s * weight)), without the block's common factor.  So a code whose v lies
+ * within float32 error of the middle between two codes may be either of them.
+ * A row that holds an infinity or a NaN has no defined outputs, nor has a row of
+ * moe_add_rms_norm_fp8 whose sum of squares overflows float32, whose mean(s^2) +
+ * eps is not a normal float32, or where the largest s * weight of a block is
+ * neither zero nor a normal float32; other rows are not touched by it.
  *
  * Conventions as in moe.h: device pointers owned by the caller, no device
  * allocation, no host synchronisation, `stream` is a cudaStream_t, argument
@@ -88,7 +93,8 @@ int moe_add_rms_norm_fp8(const void* x, const void* residual, const void* weight
  *   out             device bf16 or float32 (out_type MOE_TYPE_*) [rows, n]
  *   status          device int32 [1], or NULL; set to MOE_ETIMEDOUT from MOE_OK
  *                   if a bounded wait inside the kernel gives up (the outputs
- *                   are then incomplete), otherwise not touched
+ *                   are then incomplete), otherwise not touched.  The only
+ *                   sign of it: with NULL nothing tells
  * a, w and out are 16-byte aligned.  rows == 0 is allowed; rows < 2^31 - 128. */
 int moe_expert_gemm_fp8(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,
                         const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_offsets,
@@ -98,7 +104,9 @@ int moe_expert_gemm_fp8(const void* a, const float* a_scales, int64_t rows, int3
  *   gate = a . w13[e, 0..inter), up = a . w13[e, inter..2 inter), each as in
  *   moe_expert_gemm_fp8, left in float32;
  *   h = gate / (1 + exp(-gate)) * up;  (hq, h_scales) = h quantised,
- * which is what moe_expert_gemm_fp8 takes for the second product.
+ * which is what moe_expert_gemm_fp8 takes for the second product.  For gates
+ * below about -87.3, where 1 + exp(-gate) passes 2^126, h is 0 (its size is less
+ * than 2^-119 of up).
  *   a, a_scales     device E4M3 [rows, hidden] and its scales, hidden % 16 == 0,
  *                   hidden <= 2^31 - 128
  *   w13             device E4M3 [num_experts, 2 * inter, hidden]: gate rows,
