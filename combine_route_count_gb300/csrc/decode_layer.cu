@@ -20,9 +20,9 @@
 // is scaled and added to its float32 registers as in expert_gemm.cu.  An
 // earlier form loaded the weights straight into mma.sync fragments: its register
 // stages kept too little in flight (one token, 8 of 256 experts, H 7168, inner
-// 2048: 95 us, 45 % of DRAM busy).  Now: 63 us, 5.6 TB/s; 37 tokens, 6 of 64
-// experts, H 4096, inner 1408: 159 us, 6.8 TB/s; glu of 512 rows over 256 experts,
-// H 7168, inner 1024: 470 us, 6.9 TB/s.
+// 2048: 95 us, 45 % of DRAM busy).  Now: 62 to 63 us, 5.6 TB/s; 37 tokens, 6 of 64
+// experts, H 4096, inner 1408: 156 to 164 us, 6.7 TB/s; glu of 512 rows over 256
+// experts, H 7168, inner 1024: 466 to 485 us, 6.8 TB/s.
 //
 // row_groups gathers the x rows of an expert's tokens (TMA gather of four rows
 // at a time); few_rows reads rows of h, which row_groups writes ordered by

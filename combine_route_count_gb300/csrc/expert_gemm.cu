@@ -29,9 +29,14 @@
 // barrier back takes 700 to 1000 cycles, 128 x 256 x 128 of matrix work 512.
 // With two buffers of 256 columns a K block took 1190 cycles.  So each half of
 // the columns has its own two buffers of 128, and four are on their way at a
-// time: 680 cycles a K block, and about 4000 a tile for its end.  8192 x 4096 x
-// 7168: 164 us on zeros (2.93 PFLOP/s), 172 us on random values, where the power
-// limit lowers the clock; leaving out half of the operand loads changed neither.
+// time: on zeros, at 2070 MHz and in 8 whole rounds of tiles, 660 cycles a K block
+// up to K = 1024, 720 to 2048 and 740 to 780 beyond, and about 4700 a tile beside
+// them (its end, and its share of the launch).  8192 rows, N 7168, K 4096: 164 us
+// on zeros (2.93 PFLOP/s); on random values 179 us in bursts of 20 calls and 199
+// to 204 call after call, where the power limit holds the SMs at 1690 MHz: 164 us
+// at that clock are 201.  So at the full clock the buffers' way is the bound,
+// and in a long run the power.  Leaving out half of the operand loads changed
+// neither.
 //
 // Tiles are dealt out statically (tile b, b+G, ...), rows fastest, so that the
 // CTAs at work at one time share weight columns in L2.  Waits are bounded (2 s)

@@ -4,7 +4,7 @@
 // A feed-forward call on a few tokens takes a few microseconds on the GPU; the
 // same checks in Python (type, shape, contiguity, device and address of five to
 // seven tensors) took as long as the launch (one token's norm: 8.2 us a call
-// in Python, 3.1 us here).  Nothing is kept between calls.  A wrong argument
+// in Python, 3.2 us here).  Nothing is kept between calls.  A wrong argument
 // raises the error class given to init with MOE_EINVAL, before anything is
 // enqueued.
 
