@@ -61,3 +61,43 @@ def test_no_lock_in_a_launch(tmp_path):
     os.symlink(build.LIB_FFN, tmp_path / "_ffn.so")
     r = subprocess.run([sys.executable, "-c", CHILD, str(tmp_path)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "without the lock" in r.stdout, r.stdout + r.stderr
+
+
+def in_a_new_thread(f):
+    import threading
+    result = []
+
+    def work():
+        try:
+            result.append(f())
+        except Exception as e:  # noqa: BLE001
+            result.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not isinstance(result[0], Exception), result[0]
+
+
+def test_a_thread_whose_first_cuda_call_is_a_product():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from test_gpu_decode_layer import run, tokens, weights
+    from test_gpu_expert_gemm import inputs, offsets_of
+
+    from combine_route_count_gb300 import build, ffn
+    build.build_ffn()
+    # The few-row kernel, row groups and the tile kernel; then the layer.
+    for counts, N, K in (([7], 136, 128), ([2] * 12, 264, 40 * 128), ([300, 100], 512, 1024)):
+        args, off = inputs(1, sum(counts), len(counts), N, K), offsets_of(counts) if len(counts) > 1 else None
+        want, out = torch.empty(sum(counts), N, device="cuda"), torch.zeros(sum(counts), N, device="cuda")
+        ffn.expert_gemm_fp8(*args, want, expert_offsets=off)
+        torch.cuda.synchronize()
+        in_a_new_thread(lambda: ffn.expert_gemm_fp8(*args, out, expert_offsets=off, stream=0))
+        assert torch.equal(out, want)
+    tk = tokens(2, 6, 256, 2, 8)
+    layer = ffn.DecodeLayer(6, 2, *weights(1, 8, 256, 128))
+    want, out = run(layer, *tk), torch.zeros(6, 256, dtype=torch.bfloat16, device="cuda")
+    in_a_new_thread(lambda: layer.forward(*tk, out, stream=0))
+    assert torch.equal(out, want)
