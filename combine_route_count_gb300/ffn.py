@@ -18,6 +18,7 @@ from __future__ import annotations
 import importlib
 import os
 import struct
+import threading
 from typing import Any, Optional
 
 import torch
@@ -104,7 +105,8 @@ class DecodeLayer:
     them: they may be overwritten, or given other storage of the same shape,
     between calls.  Calls may be on any stream, also on another than the one
     the layer was built on, but only one may be in flight at a time: calls that
-    may overlap need a layer object each.  Building a layer waits for the
+    may overlap need a layer object each (calls of several threads on one stream
+    do not overlap).  Building a layer waits for the
     current stream.  A layer may be dropped while a call is in flight; one that
     is part of a CUDA graph has to live as long as the graph."""
 
@@ -125,6 +127,7 @@ class DecodeLayer:
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._streams = {_raw_stream(dev)}
+        self._lock = threading.Lock()  # a call is two launches, made without the interpreter lock
         if not torch.cuda.is_current_stream_capturing():
             # What this stream still does with the new blocks (the zero; their
             # users before) is over before a call on another stream writes them.
@@ -136,9 +139,10 @@ class DecodeLayer:
                 out: torch.Tensor, stream: Any = None) -> None:
         """out[t] = sum_k topk_w[t,k] * expert(topk_idx[t,k])(x[t]); out bf16 [T, H], T <= max_tokens."""
         handle = _stream(stream, xq)
-        if handle not in self._streams:
-            self._use_on(handle)
-        _module.decode_layer_fp8(self._plan, self._weights, xq, x_scales, topk_idx, topk_w, out, handle)
+        with self._lock:
+            if handle not in self._streams:
+                self._use_on(handle)
+            _module.decode_layer_fp8(self._plan, self._weights, xq, x_scales, topk_idx, topk_w, out, handle)
 
     def _use_on(self, handle: int) -> None:
         """Memory that is freed with the layer is not given to others before this stream is done with it."""

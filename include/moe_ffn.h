@@ -151,7 +151,9 @@ int moe_decode_workspace_bytes(const moe_config* cfg, int32_t inter, size_t* byt
  *                out of range or repeated within a token (out is then untouched),
  *                or MOE_ETIMEDOUT if a bounded wait gave up (out is incomplete)
  *   workspace    device, at least moe_decode_workspace_bytes, 256-byte aligned;
- *                calls that may overlap need one each
+ *                calls that may overlap need one each.  A call is two launches:
+ *                host threads that share a stream and a workspace may not be
+ *                inside this call at the same time
  * xq, w13, w2 and out are 16-byte aligned.  num_tokens == 0 does nothing. */
 int moe_decode_layer_fp8(const moe_config* cfg, int32_t inter, const void* xq, const float* x_scales,
                          const int32_t* topk_idx, const float* topk_w, const void* w13, const float* w13_scales,

@@ -101,3 +101,40 @@ def test_a_thread_whose_first_cuda_call_is_a_product():
     want, out = run(layer, *tk), torch.zeros(6, 256, dtype=torch.bfloat16, device="cuda")
     in_a_new_thread(lambda: layer.forward(*tk, out, stream=0))
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("threads", [2, 4])
+def test_one_layer_from_several_threads(threads):
+    """Calls of several threads on one stream come one after the other, both kernels of each together."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import threading
+
+    from test_gpu_decode_layer import run, tokens, weights
+
+    from combine_route_count_gb300 import build, ffn
+    build.build_ffn()
+    layer = ffn.DecodeLayer(16, 4, *weights(1, 16, 512, 384))
+    batches = [tokens(2 + i, 16 - i, 512, 4, 16) for i in range(threads)]
+    alone = [run(layer, *b) for b in batches]
+    outs = [torch.zeros(400, *a.shape, dtype=a.dtype, device="cuda") for a in alone]
+    torch.cuda.synchronize()
+    start, errors = threading.Barrier(threads), []
+
+    def work(i):
+        try:
+            start.wait()
+            for o in outs[i]:
+                layer.forward(*batches[i], o, stream=0)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    workers = [threading.Thread(target=work, args=(i,)) for i in range(threads)]
+    for w in workers:
+        w.start()
+    for w in workers:
+        w.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for a, o in zip(alone, outs):
+        assert (o == a).all(), f"{int((o != a).flatten(1).any(1).sum())} of {len(o)} calls"
