@@ -19,12 +19,13 @@ LIB = os.path.join(PKG, "libmoe.so")
 # its buffer before use (MOE_ECORRUPT); a separate library and object folder.
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libmoe_checked.so")
-# The CPython module of ffn.py: argument checks on torch tensors, calls into
+# The CPython module of ffn.py and train.py: argument checks on torch tensors, calls into
 # libmoe.so next to it.  Built against the installed torch, with the host compiler.
 LIB_FFN = os.path.join(PKG, "_ffn.so")
 STAMP_FFN = os.path.join(BUILD, "ffn.stamp")
 SOURCES = ["route_count.cu", "route_split.cu", "route_cluster.cu", "route_pack.cu", "route_pack_fp8.cu", "dispatch_pack.cu", "dispatch_fp8.cu", "dispatch_staged.cu", "dense_a2a.cu", "combine.cu", "combine_two_level.cu", "moe_abi.cu", "moe_noalloc.cu",
-           "add_norm_fp8.cu", "expert_gemm.cu", "decode_layer.cu", "ffn_abi.cu"]
+           "add_norm_fp8.cu", "expert_gemm.cu", "decode_layer.cu", "ffn_abi.cu",
+           "router.cu", "route_grad.cu", "expert_linear.cu", "train_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -95,7 +96,7 @@ def build_ffn(force: bool = False) -> str:
     import sysconfig
 
     import torch
-    src = os.path.join(CSRC, "ffn_py.cc")
+    src = [os.path.join(CSRC, "ffn_py.cc"), os.path.join(CSRC, "train_py.cc")]
     troot = os.path.dirname(torch.__file__)
     # What the module was compiled against: another torch or Python needs another module.
     against = f"torch {torch.__version__} in {troot}, {sysconfig.get_config_var('SOABI')}\n"
@@ -104,7 +105,7 @@ def build_ffn(force: bool = False) -> str:
     build()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = LIB_FFN + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", *src, "-o", tmp]
     for inc in (INCLUDE, os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
         cmd += ["-I", inc]
@@ -113,7 +114,7 @@ def build_ffn(force: bool = False) -> str:
             "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}", f"-Wl,-rpath,{os.path.join(cuda, 'lib64')}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on ffn_py.cc:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on _ffn.so:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_FFN)
     os.makedirs(BUILD, exist_ok=True)
     with open(STAMP_FFN, "w") as f:

@@ -1,0 +1,697 @@
+// The bf16 products of an expert layer and their gradients, on the 5th-generation
+// tensor core.  Three products of one shape, out = A x B summed over kc:
+//
+//              out [rows of a tile, columns]      summed over        A          B
+//   forward    [rows of expert e, N]              K                  a          w[e]
+//   input      [rows of expert e, K]              N                  dy         w[e], by its other axis
+//   weight     [N, K] of expert e                 rows of expert e   dy, a: both by their other axis
+//
+// "By its other axis": the axis that is summed over is not the contiguous one.  The
+// matrix instruction takes such operands as they lie (MN-major): TMA boxes of 64
+// columns x 64 summed rows, no transposition anywhere.
+//
+// One CTA per SM, tile 128 x 256, 64 of the summed axis a stage, 4 stages of 48
+// KiB by tiled TMA (128-byte swizzle).  12 warps: eight for the epilogue (two
+// groups of four, each with half of the columns), one for TMA, one for the matrix
+// instructions, two for the bias gradient.  A tile's sum stays in tensor memory:
+// two buffers of 256 columns, so that one tile's epilogue runs under the next
+// one's products.
+//
+// Rows past the end of an expert and columns past the last are computed and not
+// stored.  What is summed over must end exactly: past the end of K or N the tensor
+// maps give zeros (w is a map of three dimensions, so that they end with the
+// expert); rows past the end of an expert belong to the next one, and the matrix
+// warp overwrites them with zeros in the last stage.
+//
+// Tiles are dealt out statically (tile b, b+G, ...).  Waits are bounded (2 s) and
+// report MOE_ETIMEDOUT.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ffn_kernels.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+#include "train_kernels.cuh"
+
+namespace moe {
+namespace {
+
+enum Mode { kForward, kInput, kWeight };
+
+constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
+constexpr int kStages = 4;
+constexpr int kABytes = kTileM * kBlockK * 2, kBBytes = kTileN * kBlockK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kChunkBytes = 64 * kBlockK * 2;  // a box of 64 x 64
+constexpr int kEpilogueWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kBiasWarp = 10;
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemColumns = 512;
+constexpr int kUnit = 64;  // columns that an epilogue warp works on at a time
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drained;
+  uint32_t tmem;
+  int gave_up;
+};
+
+// Per expert: where its rows begin and end, and how many row tiles come before it.
+struct Groups {
+  int32_t *lo, *hi, *start;
+};
+
+struct Tile {
+  int e;
+  int row0, rows;  // first row of out and how many exist (weight: of the expert's matrix)
+  int n;           // column tile
+  int k0, kc;      // the summed axis: where it begins, how long it is
+};
+
+template <Mode kMode>
+__device__ __forceinline__ int64_t tile_count(const Groups& g, const LinearParams& p) {
+  if (kMode == kWeight) return static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles;
+  return static_cast<int64_t>(g.start[p.E]) * p.n_tiles;
+}
+
+template <Mode kMode>
+__device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p, int64_t t) {
+  Tile r;
+  if (kMode == kWeight) {
+    const int64_t per = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+    r.e = static_cast<int>(t / per);
+    const int64_t local = t - r.e * per;
+    const int m = static_cast<int>(local / p.n_tiles);
+    r.n = static_cast<int>(local - static_cast<int64_t>(m) * p.n_tiles);
+    r.row0 = m * kTileM;
+    r.rows = min(kTileM, p.M - r.row0);
+    r.k0 = g.lo[r.e];
+    r.kc = g.hi[r.e] - r.k0;
+    return r;
+  }
+  int lo = 0, hi = p.E;  // largest e with start[e] * n_tiles <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(g.start[mid]) * p.n_tiles <= t) lo = mid;
+    else hi = mid;
+  }
+  const int m_tiles = g.start[lo + 1] - g.start[lo];
+  const int64_t local = t - static_cast<int64_t>(g.start[lo]) * p.n_tiles;
+  r.e = lo;
+  r.n = static_cast<int>(local / m_tiles);
+  r.row0 = g.lo[lo] + static_cast<int>(local - static_cast<int64_t>(r.n) * m_tiles) * kTileM;
+  r.rows = min(kTileM, g.hi[lo] - r.row0);
+  r.k0 = 0;
+  r.kc = p.kc;
+  return r;
+}
+
+__device__ __forceinline__ int blocks_of(int kc) { return (kc + kBlockK - 1) / kBlockK; }
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// ---- rows in and out of the epilogue ------------------------------------------
+// A lane holds 128 bytes of its own row; four lanes move 128 bytes of one row
+// together, 32 each, for their four rows in turn.
+
+// Lane i of four holds units u[0..3] of row i; after it, unit i of rows 0..3.  Its own inverse.
+__device__ __forceinline__ void transpose_4(uint32_t (&u)[4][8], int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & d) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? u[j][i] : u[j + d][i], d);
+        u[j][i] = upper ? got : u[j][i];
+        u[j + d][i] = upper ? u[j + d][i] : got;
+      }
+    }
+  }
+}
+
+struct Rows {
+  uint8_t* at;      // the lane's 32 bytes of the first of its four rows
+  int64_t stride;   // bytes of a row
+  int rows;         // of the four, how many exist
+  int left;         // bytes of the row from `at` on (a multiple of 16; may be negative)
+  bool wide;        // rows begin on 32-byte boundaries
+};
+
+// 128 bytes from byte `col` on of the rows of this warp (32 rows from r0 on).
+__device__ __forceinline__ Rows rows_at(void* base, int64_t row, int64_t stride, int64_t col, int rows, int lane) {
+  Rows r;
+  const int64_t byte = col + (lane & 3) * 32;
+  r.at = static_cast<uint8_t*>(base) + (row + (lane & ~3)) * stride + byte;
+  r.stride = stride;
+  r.rows = rows - (lane & ~3);
+  const int64_t left = stride - byte;
+  r.left = left > 32 ? 32 : static_cast<int>(left);
+  r.wide = ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(stride) | static_cast<uintptr_t>(col)) & 31) == 0;
+  return r;
+}
+
+__device__ __forceinline__ void store_rows(const Rows& r, uint32_t (&u)[4][8], int lane) {
+  transpose_4(u, lane);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k >= r.rows) continue;
+    uint8_t* to = r.at + k * r.stride;
+    const uint4 q0 = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+    const uint4 q1 = make_uint4(u[k][4], u[k][5], u[k][6], u[k][7]);
+    if (r.wide && r.left >= 32) {
+      tc::st_v8(to, q0, q1);
+    } else {
+      if (r.left >= 16) ptx::st_v4(to, q0);
+      if (r.left >= 32) ptx::st_v4(to + 16, q1);
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 ld_v4(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void load_rows(const Rows& r, uint32_t (&u)[4][8], int lane) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
+    if (k < r.rows) {
+      const uint8_t* from = r.at + k * r.stride;
+      if (r.left >= 16) q0 = ld_v4(from);
+      if (r.left >= 32) q1 = ld_v4(from + 16);
+    }
+    u[k][0] = q0.x, u[k][1] = q0.y, u[k][2] = q0.z, u[k][3] = q0.w;
+    u[k][4] = q1.x, u[k][5] = q1.y, u[k][6] = q1.z, u[k][7] = q1.w;
+  }
+  transpose_4(u, lane);
+}
+
+// 64 float32 columns of a row out as bf16 or float32.
+__device__ __forceinline__ void store_bf16(const Rows& r, const float (&v)[kUnit], int lane) {
+  uint32_t u[4][8];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) u[i / 8][i & 7] = bf16x2(v[2 * i], v[2 * i + 1]);
+  store_rows(r, u, lane);
+}
+__device__ __forceinline__ void store_f32(Rows r, const float (&v)[kUnit], int lane, int64_t bytes_left) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[4][8];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i / 8][i & 7] = __float_as_uint(v[h * 32 + i]);
+    const int64_t left = bytes_left - h * 128 - (lane & 3) * 32;
+    r.left = left > 32 ? 32 : static_cast<int>(left);
+    store_rows(r, u, lane);
+    r.at += 128;
+  }
+}
+__device__ __forceinline__ void load_bf16(const Rows& r, float (&v)[kUnit], int lane) {
+  uint32_t u[4][8];
+  load_rows(r, u, lane);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[2 * i] = bf_lo(u[i / 8][i & 7]);
+    v[2 * i + 1] = bf_hi(u[i / 8][i & 7]);
+  }
+}
+__device__ __forceinline__ void load_f32(Rows r, float (&v)[kUnit], int lane, int64_t bytes_left) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[4][8];
+    const int64_t left = bytes_left - h * 128 - (lane & 3) * 32;
+    r.left = left > 32 ? 32 : static_cast<int>(left);
+    load_rows(r, u, lane);
+    r.at += 128;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[h * 32 + i] = __uint_as_float(u[i / 8][i & 7]);
+  }
+}
+
+// ---- activations ------------------------------------------------------------------
+// Quotients by a denominator beyond 2^126 become 0; they are below 2^-119 of the numerator there.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + expf(-v)); }
+__device__ __forceinline__ float silu_slope(float v) {
+  const float s = sigmoid(v);
+  return s * fmaf(v, 1.0f - s, 1.0f);
+}
+constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+
+__device__ __forceinline__ void activate(int act, float (&v)[kUnit]) {
+  if (act == MOE_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = v[i] > 0.0f || v[i] != v[i] ? v[i] : 0.0f;
+  } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * kSqrtHalf));
+  } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = silu(v[i]);
+  }
+}
+// g times the derivative at v.
+__device__ __forceinline__ void through(int act, float (&g)[kUnit], const float (&v)[kUnit]) {
+  if (act == MOE_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) g[i] = v[i] > 0.0f ? g[i] : 0.0f;
+  } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const float density = kInvSqrt2Pi * expf(-0.5f * v[i] * v[i]);
+      g[i] *= fmaf(v[i], density, 0.5f * (1.0f + erff(v[i] * kSqrtHalf)));
+    }
+  } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) g[i] *= silu_slope(v[i]);
+  }
+}
+
+// 64 columns of this warp's lanes.  The last columns of a matrix may be
+// missing in the tile's operand: they are zeros.
+__device__ __forceinline__ void load_acc(uint32_t from, float (&v)[kUnit]) {
+  tc::tmem_load_32(from, reinterpret_cast<uint32_t*>(v));
+  tc::tmem_load_32(from + 32, reinterpret_cast<uint32_t*>(v) + 32);
+  tc::wait_loads();
+}
+
+// bias[col .. col + 63] added, the same for every lane.
+__device__ __forceinline__ void add_bias(const LinearParams& p, int64_t first, int col, float (&v)[kUnit]) {
+  if (p.bias_f32) {
+    const float* b = static_cast<const float*>(p.bias) + first + col;
+#pragma unroll
+    for (int i = 0; i < kUnit; i += 4)
+      if (col + i < p.bias_cols) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(b + i));
+        v[i] += q.x, v[i + 1] += q.y, v[i + 2] += q.z, v[i + 3] += q.w;
+      }
+  } else {
+    const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.bias) + first + col;
+#pragma unroll
+    for (int i = 0; i < kUnit; i += 8)
+      if (col + i < p.bias_cols) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(b + i));
+        v[i] += bf_lo(q.x), v[i + 1] += bf_hi(q.x), v[i + 2] += bf_lo(q.y), v[i + 3] += bf_hi(q.y);
+        v[i + 4] += bf_lo(q.z), v[i + 5] += bf_hi(q.z), v[i + 6] += bf_lo(q.w), v[i + 7] += bf_hi(q.w);
+      }
+  }
+}
+
+template <Mode kMode, bool kGlu, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid_constant__ LinearParams p) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ Shared s;
+  uint8_t* stages = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
+  Groups g;
+  g.lo = reinterpret_cast<int32_t*>(stages + kStages * kStageBytes);
+  g.hi = g.lo + p.E;
+  g.start = g.hi + p.E;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const bool bias_grad = kMode == kWeight && p.db;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&s.full[i], 1);
+      ptx::mbar_init(&s.empty[i], bias_grad ? 3 : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&s.acc_full[i], 1);
+      ptx::mbar_init(&s.acc_empty[i], kEpilogueWarps);
+    }
+    ptx::mbar_init(&s.drained, 1);
+    ptx::mbar_fence_init();
+    s.gave_up = 0;
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, kTmemColumns);
+  if (threadIdx.x == kTmaWarp * 32) {
+    tc::tma_prefetch_map(&p.a);
+    tc::tma_prefetch_map(&p.b);
+  }
+  ptx::wait_prerequisites();
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    const int rows = static_cast<int>(p.rows);
+    int lo = 0, hi = rows;
+    if (p.offsets) {  // clamped: a damaged table cannot lead outside the buffers
+      lo = min(max(p.offsets[e], 0), rows);
+      hi = min(max(p.offsets[e + 1], lo), rows);
+    }
+    g.lo[e] = lo;
+    g.hi[e] = hi;
+  }
+  __syncthreads();
+  if (kMode != kWeight && warp == 0) {
+    int before = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int own = e < p.E ? (g.hi[e] - g.lo[e] + kTileM - 1) / kTileM : 0;
+      int sum = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      if (e < p.E) g.start[e] = before + sum - own;
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) g.start[p.E] = before;
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const int64_t tiles = tile_count<kMode>(g, p);
+  const uint32_t tmem = s.tmem, tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+
+  if (warp == kTmaWarp) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const Tile tile = find_tile<kMode>(g, p, t);
+      const int kblocks = blocks_of(tile.kc);
+      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const int st = it % kStages;
+        ok = it < kStages || tc::wait(&s.empty[st], (it / kStages - 1) & 1, &s.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t *a = stages + st * kStageBytes, *b = a + kABytes;
+        if (tc::elect() && it != p.test_drop) {
+          ptx::mbar_arrive_expect_tx(&s.full[st], kStageBytes);
+          const int k = tile.k0 + kb * kBlockK;
+          if (kMode == kWeight) {
+#pragma unroll
+            for (int q = 0; q < kTileM / 64; ++q)
+              tc::tma_load_2d(a + q * kChunkBytes, &p.a, tile.row0 + q * 64, k, &s.full[st]);
+#pragma unroll
+            for (int q = 0; q < kTileN / 64; ++q)
+              tc::tma_load_2d(b + q * kChunkBytes, &p.b, tile.n * kTileN + q * 64, k, &s.full[st]);
+          } else {
+            tc::tma_load_2d(a, &p.a, k, tile.row0, &s.full[st]);
+            if (kMode == kForward) {
+              const int n0 = tile.n * (kGlu ? kTileN / 2 : kTileN);
+              tc::tma_load_3d(b, &p.b, k, n0, tile.e, &s.full[st]);
+              tc::tma_load_3d(b + kBBytes / 2, &p.b, k, n0 + (kGlu ? p.N : kTileN / 2), tile.e, &s.full[st]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < kTileN / 64; ++q)
+                tc::tma_load_3d(b + q * kChunkBytes, &p.b, tile.n * kTileN + q * 64, k, tile.e, &s.full[st]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // Loads in flight write to this CTA's shared memory: it does not end before
+    // them, whichever warp gave up.
+    const unsigned long long start = tc::now_ns();
+    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+      if (j != p.test_drop) tc::settle(&s.full[j % kStages], (j / kStages) & 1, start);
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t kInstr = tc::instr_desc_bf16(kTileM, kTileN, kMode == kWeight, kMode != kForward);
+    uint32_t it = 0, round = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const Tile tile = find_tile<kMode>(g, p, t);
+      const int kblocks = blocks_of(tile.kc);
+      if (kblocks == 0) continue;
+      const int buf = round & 1;
+      ok = round < 2 || tc::wait(&s.acc_empty[buf], (round / 2 - 1) & 1, &s.gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const int st = it % kStages;
+        ok = tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* a_tile = stages + st * kStageBytes;
+        if (kMode == kWeight && kb == kblocks - 1 && tile.kc % kBlockK != 0) {
+          // Rows of the next expert: zeros in both operands (0 x infinity is no zero).
+          const int first = tile.kc % kBlockK;
+#pragma unroll 1
+          for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
+            for (int i = first * 8 + lane; i < kBlockK * 8; i += 32)
+              *reinterpret_cast<uint4*>(a_tile + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_async_shared();
+          __syncwarp();
+        }
+        tc::fence_after();
+        const uint64_t a = kMode == kWeight ? tc::smem_desc_mn(a_tile) : tc::smem_desc(a_tile);
+        const uint64_t b = kMode != kForward ? tc::smem_desc_mn(a_tile + kABytes) : tc::smem_desc(a_tile + kABytes);
+        // 16 further along the summed axis: 32 bytes, or 16 rows of 128.
+        constexpr uint64_t kStepA = (kMode == kWeight ? 2048 : 32) >> 4;
+        constexpr uint64_t kStepB = (kMode != kForward ? 2048 : 32) >> 4;
+        if (tc::elect()) {
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            tc::mma_f16(tmem_u + buf * kTileN, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
+          tc::commit(&s.empty[st]);
+          if (kb == kblocks - 1) tc::commit(&s.acc_full[buf]);
+        }
+        __syncwarp();
+      }
+      ++round;
+    }
+    // Nothing may be in flight when the tensor memory is freed.
+    if (tc::elect()) tc::commit(&s.drained);
+    __syncwarp();
+    tc::settle(&s.drained, 0, tc::now_ns());
+  } else if (warp >= kBiasWarp) {
+    if (bias_grad) {
+      const int c = warp - kBiasWarp;  // 64 columns of dy
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const Tile tile = find_tile<kMode>(g, p, t);
+        const int kblocks = blocks_of(tile.kc);
+        float sum0 = 0.0f, sum1 = 0.0f;
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+          const int st = it % kStages;
+          ok = tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (tile.n == 0) {
+            const uint8_t* a = stages + st * kStageBytes + c * kChunkBytes;
+            const int rows = min(kBlockK, tile.kc - kb * kBlockK);
+            float part0 = 0.0f, part1 = 0.0f;
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r) {
+              const uint32_t v =
+                  *reinterpret_cast<const uint32_t*>(a + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+              part0 += bf_lo(v);
+              part1 += bf_hi(v);
+            }
+            sum0 += part0;
+            sum1 += part1;
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.empty[st]);
+        }
+        const int col = tile.row0 + c * 64 + lane * 2;
+        if (ok && tile.n == 0 && col < p.M) {  // M is a multiple of 8
+          float2* to = reinterpret_cast<float2*>(p.db + static_cast<int64_t>(tile.e) * p.M + col);
+          float2 v = make_float2(sum0, sum1);
+          if (p.accumulate) {
+            const float2 old = *to;
+            v.x += old.x;
+            v.y += old.y;
+          }
+          *to = v;
+        }
+      }
+    }
+  } else {
+    const int half = warp >> 2, sub = (warp & 3) * 32;  // this warp's rows begin at sub
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(sub) << 16);
+    uint32_t round = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const Tile tile = find_tile<kMode>(g, p, t);
+      const bool some = sub < tile.rows;
+      const bool sums = blocks_of(tile.kc) > 0;
+      const int buf = round & 1;
+      if (sums) {
+        ok = tc::wait(&s.acc_full[buf], (round / 2) & 1, &s.gave_up);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        ++round;
+      }
+      const uint32_t acc = lanes + buf * kTileN;
+      // A warp none of whose rows exist only passes the buffer on.
+      const int rows = tile.rows - sub;
+      const int64_t row = tile.row0 + sub;
+      if constexpr (kMode == kForward && kGlu) {
+        if (some) {
+          const int col = tile.n * (kTileN / 2) + half * kUnit;
+          const int64_t first = static_cast<int64_t>(tile.e) * p.bias_cols;
+          float v[kUnit], up[kUnit];
+          load_acc(acc + half * kUnit, v);
+          load_acc(acc + kTileN / 2 + half * kUnit, up);
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+          if (p.bias) {
+            add_bias(p, first, col, v);
+            add_bias(p, first, p.N + col, up);
+          }
+          if (p.pre) {
+            const int64_t stride = static_cast<int64_t>(p.N) * 4;
+            Rows r = rows_at(p.pre, row, stride, static_cast<int64_t>(col) * 2, rows, lane);
+            const int left = min(32, (p.N - col) * 2 - (lane & 3) * 32);
+            r.left = left;
+            store_bf16(r, v, lane);
+            r = rows_at(p.pre, row, stride, static_cast<int64_t>(p.N + col) * 2, rows, lane);
+            r.left = left;
+            store_bf16(r, up, lane);
+          }
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) v[i] = silu(v[i]) * up[i];
+          if (p.residual) {
+            load_bf16(rows_at(p.residual, row, static_cast<int64_t>(p.N) * 2, static_cast<int64_t>(col) * 2, rows, lane),
+                      up, lane);
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) v[i] += up[i];
+          }
+          const int size = kF32 ? 4 : 2;
+          const Rows r = rows_at(p.out, row, static_cast<int64_t>(p.N) * size, static_cast<int64_t>(col) * size, rows, lane);
+          if (kF32) store_f32(r, v, lane, static_cast<int64_t>(p.N - col) * 4);
+          else store_bf16(r, v, lane);
+        } else {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+        }
+        continue;
+      }
+#pragma unroll 1
+      for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
+        const int col = tile.n * kTileN + half * (kTileN / 2) + q * kUnit;
+        float v[kUnit];
+        if (sums && some) {
+          load_acc(acc + half * (kTileN / 2) + q * kUnit, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) v[i] = 0.0f;
+        }
+        if (sums && q == kTileN / 2 / kUnit - 1) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+        }
+        if (!some || col >= p.N) continue;
+        const int64_t byte = static_cast<int64_t>(col) * 2, stride = static_cast<int64_t>(p.N) * 2;
+        if (kMode == kForward) {
+          if (p.bias) add_bias(p, static_cast<int64_t>(tile.e) * p.bias_cols, col, v);
+          if (p.pre) store_bf16(rows_at(p.pre, row, stride, byte, rows, lane), v, lane);
+          activate(p.act, v);
+          if (p.residual) {
+            float more[kUnit];
+            load_bf16(rows_at(p.residual, row, stride, byte, rows, lane), more, lane);
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) v[i] += more[i];
+          }
+          if (kF32) store_f32(rows_at(p.out, row, 2 * stride, 2 * byte, rows, lane), v, lane, 2 * (stride - byte));
+          else store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
+        } else if (kMode == kInput && !kGlu) {
+          if (p.act != MOE_ACT_NONE) {
+            float pre[kUnit];
+            load_bf16(rows_at(p.pre, row, stride, byte, rows, lane), pre, lane);
+            through(p.act, v, pre);
+          }
+          store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
+        } else if (kMode == kInput) {
+          Rows at = rows_at(p.pre, row, 2 * stride, byte, rows, lane);
+          Rows at_up = rows_at(p.pre, row, 2 * stride, stride + byte, rows, lane);
+          at.left = at_up.left;  // the row's first half ends where the second begins
+          float gate[kUnit], up[kUnit];
+          load_bf16(at, gate, lane);
+          load_bf16(at_up, up, lane);
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) {
+            const float sig = sigmoid(gate[i]);
+            const float d_up = v[i] * (gate[i] * sig);
+            gate[i] = v[i] * up[i] * (sig * fmaf(gate[i], 1.0f - sig, 1.0f));
+            up[i] = d_up;
+          }
+          Rows to = rows_at(p.out, row, 2 * stride, byte, rows, lane);
+          to.left = at.left;
+          store_bf16(to, gate, lane);
+          store_bf16(rows_at(p.out, row, 2 * stride, stride + byte, rows, lane), up, lane);
+        } else {
+          if (p.accumulate && !sums) continue;
+          const int64_t out_row = static_cast<int64_t>(tile.e) * p.M + row;
+          if (kF32) {
+            const Rows at = rows_at(p.out, out_row, 2 * stride, 2 * byte, rows, lane);
+            if (p.accumulate) {
+              float old[kUnit];
+              load_f32(at, old, lane, 2 * (stride - byte));
+#pragma unroll
+              for (int i = 0; i < kUnit; ++i) v[i] += old[i];
+            }
+            store_f32(at, v, lane, 2 * (stride - byte));
+          } else {
+            const Rows at = rows_at(p.out, out_row, stride, byte, rows, lane);
+            if (p.accumulate) {
+              float old[kUnit];
+              load_bf16(at, old, lane);
+#pragma unroll
+              for (int i = 0; i < kUnit; ++i) v[i] += old[i];
+            }
+            store_bf16(at, v, lane);
+          }
+        }
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (threadIdx.x == 0 && s.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
+  if (warp == kMmaWarp) tc::tmem_free(tmem, kTmemColumns);
+}
+
+template <Mode kMode, bool kGlu, bool kF32>
+cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
+  const size_t smem = 1024 + kStages * kStageBytes + (3 * static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
+  auto* kernel = expert_linear_kernel<kMode, kGlu, kF32>;
+  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
+  if (err != cudaSuccess) return err;
+  // Every expert may add one partly filled row tile.
+  int64_t most = kMode == kWeight ? static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles
+                                  : ((p.rows + kTileM - 1) / kTileM + (p.offsets ? p.E : 0)) * p.n_tiles;
+  if (most > sms) most = sms;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(most)), dim3(kThreads), smem, stream, true, p);
+}
+
+}  // namespace
+
+int linear_n_tile(bool glu) { return glu ? kTileN / 2 : kTileN; }
+int linear_m_tile() { return kTileM; }
+
+cudaError_t launch_linear(const LinearParams& p, bool glu, bool f32, int sms, cudaStream_t stream) {
+  if (glu) return f32 ? launch<kForward, true, true>(p, sms, stream) : launch<kForward, true, false>(p, sms, stream);
+  return f32 ? launch<kForward, false, true>(p, sms, stream) : launch<kForward, false, false>(p, sms, stream);
+}
+
+cudaError_t launch_linear_input(const LinearParams& p, bool glu, int sms, cudaStream_t stream) {
+  return glu ? launch<kInput, true, false>(p, sms, stream) : launch<kInput, false, false>(p, sms, stream);
+}
+
+cudaError_t launch_linear_weight(const LinearParams& p, bool f32, int sms, cudaStream_t stream) {
+  return f32 ? launch<kWeight, false, true>(p, sms, stream) : launch<kWeight, false, false>(p, sms, stream);
+}
+
+}  // namespace moe

@@ -4,7 +4,6 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <atomic>
@@ -12,89 +11,28 @@
 #include <cmath>
 #include <cstdint>
 
+#include "abi_host.cuh"
 #include "ffn_kernels.cuh"
 #include "moe_ffn.h"
 
 namespace {
 
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// SM count of the current device, asked once per device (0: the query failed).
-int sm_count() {
-  static int known[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) {
-    const int n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED);
-    if (n > 0) return n;
-  }
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
-  return n;
-}
+using moe::aligned;
+using moe::guarded;
+using moe::launched;
+using moe::NvtxRange;
+using moe::sm_count;
+using moe::test_drop;
 
 // moe_ffn_test_drop_load's.
 std::atomic<int32_t> g_test_drop{-1};
 
-uint32_t test_drop() { return static_cast<uint32_t>(g_test_drop.load(std::memory_order_relaxed)); }
-
-template <class F>
-int guarded(F&& f) {
-  try {
-    return f();
-  } catch (...) {
-    return MOE_ECUDA;
-  }
-}
-
-int launched(cudaError_t err) {
-  if (err == cudaSuccess) return MOE_OK;
-  cudaGetLastError();  // a refused launch is reported here, not by a later call
-  return MOE_ECUDA;
-}
-
-// E4M3 matrix [rows, cols] as a tensor map of box_rows x 128 boxes, 128-byte
-// swizzle, zeros outside.  The encoder is the driver's, found through the
-// runtime (no link against libcuda).
+// E4M3 matrix [rows, cols] as a tensor map of box_rows x 128 boxes.
 bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows = 128) {
-  using Encode = decltype(&cuTensorMapEncodeTiled);
-  static std::atomic<Encode> known{nullptr};
-  Encode encode = known.load(std::memory_order_acquire);
-  if (!encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess ||
-        found != cudaDriverEntryPointSuccess || !fn)
-      return false;
-    encode = reinterpret_cast<Encode>(fn);
-    known.store(encode, std::memory_order_release);
-  }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
-  auto call = [&] {
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  };
-  CUresult r = call();
-  if (r == CUDA_ERROR_INVALID_CONTEXT) {
-    // The thread's first CUDA work: the runtime makes its device's context
-    // current when it needs one, the driver's encoder does not.
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
-    r = call();
-  }
-  return r == CUDA_SUCCESS;
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  return moe::encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 2, dims, strides, box);
 }
 
 // Which kernel a product takes.  The tile kernel (expert_gemm.cu) gives 128
@@ -235,6 +173,8 @@ size_t decode_workspace(const moe_config* c, int32_t inter) {
 }
 
 }  // namespace
+
+uint32_t moe::test_drop() { return static_cast<uint32_t>(g_test_drop.load(std::memory_order_relaxed)); }
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
 

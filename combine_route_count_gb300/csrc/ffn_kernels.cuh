@@ -16,6 +16,9 @@ namespace moe {
 // scale is taken, so that 1 / scale stays finite.
 constexpr float kTinyAmax = 0x1p-100f;
 
+// The load that moe_ffn_test_drop_load names; UINT32_MAX: none.
+uint32_t test_drop();
+
 // A load that stays where it is written, behind the grid's dependency wait: for
 // data that the kernel before this one may have written.
 __device__ __forceinline__ float ld_f32(const float* p) {

@@ -74,6 +74,14 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       "l"(map), "r"(ptx::smem_addr(bar)), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(ptx::smem_addr(smem_dst)),
+      "l"(map), "r"(ptx::smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 // Columns x.. of four rows, one after the other in shared memory (the map's box is one row high).
 __device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, int x, int r0, int r1, int r2,
                                             int r3, uint64_t* bar) {
@@ -165,6 +173,34 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
+}
+// The same for an operand whose summed axis is not the contiguous one (MN-major):
+// boxes of 64 columns (128 bytes) x 64 summed rows, one after the other 8192 bytes
+// apart, groups of 8 summed rows 1024 bytes apart.  16 summed rows further add 128
+// to the descriptor.
+__device__ __forceinline__ uint64_t smem_desc_mn(const void* tile) {
+  constexpr uint64_t kRest = (static_cast<uint64_t>(8192 >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+                             (1ull << 46) | (2ull << 61);
+  return kRest | ((ptx::smem_addr(tile) & 0x3ffff) >> 4);
+}
+// bf16 x bf16 -> float32; a_mn, b_mn: the operand is MN-major.
+__host__ __device__ constexpr uint32_t instr_desc_bf16(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// D[tmem] = A * B (+ D): one thread, K = 16.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+// What this thread has written to shared memory is seen by matrix instructions and bulk copies.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 // One arrival on `bar` when all matrix instructions this thread has issued are done.
 __device__ __forceinline__ void commit(uint64_t* bar) {

@@ -1,0 +1,272 @@
+// The C ABI of the training operators (declared in include/moe_train.h):
+// argument checks and launches.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "abi_host.cuh"
+#include "ffn_kernels.cuh"
+#include "moe_train.h"
+#include "train_kernels.cuh"
+
+namespace {
+
+using moe::aligned;
+using moe::guarded;
+using moe::launched;
+using moe::NvtxRange;
+using moe::sm_count;
+
+constexpr int32_t kMaxSize = 1 << 30;  // of n and k: a tile's end past the last column, and twice that, are int32
+
+bool type_ok(int type) { return type == MOE_TYPE_BF16 || type == MOE_TYPE_F32; }
+
+bool router_ok(int logits_type, int64_t T, int32_t E, int32_t K, int score, float scale) {
+  return type_ok(logits_type) && T >= 0 && T <= INT_MAX && E >= 1 && E <= MOE_MAX_EXPERTS && K >= 1 &&
+         K <= MOE_MAX_TOP_K && K <= E && (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID) &&
+         std::isfinite(scale);
+}
+
+bool moves_ok(int64_t T, int32_t H, int32_t K, int64_t rows) {
+  return T >= 0 && H > 0 && H % 8 == 0 && K >= 1 && K <= MOE_MAX_TOP_K && T * K <= INT_MAX && T <= INT_MAX &&
+         rows >= 0 && rows <= INT_MAX;
+}
+
+// bf16 matrix [rows, cols] as a tensor map of box_rows x 64 boxes.
+bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  return moe::encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box);
+}
+
+// bf16 weights [E, n, k] as a tensor map of box_rows x 64 boxes of one expert.
+bool encode_weights(CUtensorMap* map, const void* base, int32_t E, int32_t n, int32_t k, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(E)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(k) * 2, static_cast<cuuint64_t>(k) * 2 * n};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  return moe::encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box);
+}
+
+bool product_ok(int64_t rows, int32_t n, int32_t k, int32_t E, const int32_t* offsets, const int32_t* status) {
+  return rows >= 0 && rows <= INT_MAX - 256 && n > 0 && n % 8 == 0 && n <= kMaxSize && k > 0 && k % 8 == 0 &&
+         k <= kMaxSize && E >= 1 && E <= MOE_MAX_EXPERTS && (offsets || E == 1) && aligned(offsets, 4) &&
+         aligned(status, 4);
+}
+
+int32_t tiles(int32_t n, int32_t tile) { return (n + tile - 1) / tile; }
+
+}  // namespace
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+MOE_API int moe_router_topk(const void* logits, int logits_type, const float* bias, int64_t num_tokens,
+                            int32_t num_experts, int32_t top_k, int score, int normalize, float scale,
+                            int32_t* topk_idx, float* topk_w, void* stream) {
+  NvtxRange nvtx_range("moe_router_topk");
+  if (!router_ok(logits_type, num_tokens, num_experts, top_k, score, scale)) return MOE_EINVAL;
+  if (bias && score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
+  if (num_tokens == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_w) return MOE_EINVAL;
+  if (!aligned(logits, logits_type == MOE_TYPE_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+      !aligned(topk_w, 4))
+    return MOE_EINVAL;
+  return guarded([&] {
+    moe::RouterParams p = {};
+    p.logits = logits;
+    p.bias = bias;
+    p.idx = topk_idx;
+    p.w = topk_w;
+    p.T = num_tokens;
+    p.E = num_experts;
+    p.K = top_k;
+    p.scale = scale;
+    return launched(moe::launch_router(p, logits_type == MOE_TYPE_F32, score == MOE_SCORE_SIGMOID, normalize != 0,
+                                       false, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+MOE_API int moe_router_topk_backward(const void* logits, int logits_type, const int32_t* topk_idx,
+                                     const float* d_topk_w, int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                                     int score, int normalize, float scale, void* d_logits, void* stream) {
+  NvtxRange nvtx_range("moe_router_topk_backward");
+  if (!router_ok(logits_type, num_tokens, num_experts, top_k, score, scale)) return MOE_EINVAL;
+  if (num_tokens == 0) return MOE_OK;
+  if (!logits || !topk_idx || !d_topk_w || !d_logits) return MOE_EINVAL;
+  const size_t size = logits_type == MOE_TYPE_F32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(topk_idx, 4) || !aligned(d_topk_w, 4) || !aligned(d_logits, size))
+    return MOE_EINVAL;
+  return guarded([&] {
+    moe::RouterParams p = {};
+    p.logits = logits;
+    p.idx = const_cast<int32_t*>(topk_idx);  // read only by the gradient
+    p.dw = d_topk_w;
+    p.d_logits = d_logits;
+    p.T = num_tokens;
+    p.E = num_experts;
+    p.K = top_k;
+    p.scale = scale;
+    return launched(moe::launch_router(p, logits_type == MOE_TYPE_F32, score == MOE_SCORE_SIGMOID, normalize != 0,
+                                       true, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+MOE_API int moe_combine_backward(const void* d_out, const void* expert_y, const float* topk_w,
+                                 const int32_t* slot_row, int64_t num_tokens, int32_t hidden, int32_t top_k,
+                                 int64_t rows, void* d_expert_y, float* d_topk_w, void* stream) {
+  NvtxRange nvtx_range("moe_combine_backward");
+  if (!moves_ok(num_tokens, hidden, top_k, rows)) return MOE_EINVAL;
+  if (num_tokens == 0) return MOE_OK;
+  if (!d_out || !topk_w || !slot_row || !d_expert_y || !expert_y != !d_topk_w) return MOE_EINVAL;
+  if (!aligned(d_out, 16) || !aligned(expert_y, 16) || !aligned(topk_w, 4) || !aligned(slot_row, 4) ||
+      !aligned(d_expert_y, 16) || !aligned(d_topk_w, 4))
+    return MOE_EINVAL;
+  return guarded([&] {
+    moe::CombineGradParams p = {};
+    p.d_out = static_cast<const uint8_t*>(d_out);
+    p.y = static_cast<const uint8_t*>(expert_y);
+    p.w = topk_w;
+    p.slot_row = slot_row;
+    p.dy = static_cast<uint8_t*>(d_expert_y);
+    p.dw = d_topk_w;
+    p.T = num_tokens;
+    p.rows = rows;
+    p.H = hidden;
+    p.K = top_k;
+    return launched(moe::launch_combine_grad(p, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+MOE_API int moe_dispatch_backward(const void* d_expert_x, const int32_t* slot_row, const void* add,
+                                  int64_t num_tokens, int32_t hidden, int32_t top_k, int64_t rows, void* d_x,
+                                  void* stream) {
+  NvtxRange nvtx_range("moe_dispatch_backward");
+  if (!moves_ok(num_tokens, hidden, top_k, rows)) return MOE_EINVAL;
+  if (num_tokens == 0) return MOE_OK;
+  if ((!d_expert_x && rows > 0) || !slot_row || !d_x) return MOE_EINVAL;
+  if (!aligned(d_expert_x, 16) || !aligned(slot_row, 4) || !aligned(add, 16) || !aligned(d_x, 16)) return MOE_EINVAL;
+  return guarded([&] {
+    moe::DispatchGradParams p = {};
+    p.de = static_cast<const uint8_t*>(d_expert_x);
+    p.slot_row = slot_row;
+    p.add = static_cast<const uint8_t*>(add);
+    p.dx = static_cast<uint8_t*>(d_x);
+    p.T = num_tokens;
+    p.rows = rows;
+    p.H = hidden;
+    p.K = top_k;
+    return launched(moe::launch_dispatch_grad(p, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+MOE_API int moe_expert_linear(const void* a, int64_t rows, int32_t k, const void* w, int32_t n, int32_t num_experts,
+                              const int32_t* expert_offsets, const void* bias, int bias_type, int activation,
+                              const void* residual, void* pre, void* out, int out_type, int32_t* status,
+                              void* stream) {
+  NvtxRange nvtx_range("moe_expert_linear");
+  const bool glu = activation == MOE_ACT_SWIGLU;
+  if (!product_ok(rows, n, k, num_experts, expert_offsets, status)) return MOE_EINVAL;
+  if (activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU || (glu && n % 16 != 0) || !type_ok(out_type) ||
+      (bias && !type_ok(bias_type)))
+    return MOE_EINVAL;
+  if (rows == 0) return MOE_OK;
+  if (!a || !w || !out) return MOE_EINVAL;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(pre, 16) ||
+      !aligned(out, 16))
+    return MOE_EINVAL;
+  if (residual == out && out_type != MOE_TYPE_BF16) return MOE_EINVAL;
+  return guarded([&] {
+    const int sms = sm_count();
+    if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    moe::LinearParams p = {};
+    if (!encode_rows(&p.a, a, rows, k, 128) || !encode_weights(&p.b, w, num_experts, n, k, 128))
+      return static_cast<int>(MOE_ECUDA);
+    p.offsets = expert_offsets;
+    p.bias = bias;
+    p.residual = const_cast<void*>(residual);
+    p.pre = pre;
+    p.out = out;
+    p.status = status;
+    p.rows = rows;
+    p.N = glu ? n / 2 : n;
+    p.n_tiles = tiles(p.N, moe::linear_n_tile(glu));
+    p.kc = k;
+    p.E = num_experts;
+    p.act = activation;
+    p.bias_cols = n;
+    p.bias_f32 = bias_type == MOE_TYPE_F32;
+    p.test_drop = moe::test_drop();
+    return launched(moe::launch_linear(p, glu, out_type == MOE_TYPE_F32, sms, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+MOE_API int moe_expert_linear_backward_input(const void* dy, int64_t rows, int32_t n, const void* w, int32_t k,
+                                             int32_t num_experts, const int32_t* expert_offsets, int activation,
+                                             const void* pre, void* dx, int32_t* status, void* stream) {
+  NvtxRange nvtx_range("moe_expert_linear_backward_input");
+  if (!product_ok(rows, n, k, num_experts, expert_offsets, status)) return MOE_EINVAL;
+  if (activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU) return MOE_EINVAL;
+  if (rows == 0) return MOE_OK;
+  if (!dy || !w || !dx || !pre != (activation == MOE_ACT_NONE)) return MOE_EINVAL;
+  if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(pre, 16) || !aligned(dx, 16)) return MOE_EINVAL;
+  return guarded([&] {
+    const int sms = sm_count();
+    if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    moe::LinearParams p = {};
+    if (!encode_rows(&p.a, dy, rows, n, 128) || !encode_weights(&p.b, w, num_experts, n, k, 64))
+      return static_cast<int>(MOE_ECUDA);
+    p.offsets = expert_offsets;
+    p.pre = const_cast<void*>(pre);
+    p.out = dx;
+    p.status = status;
+    p.rows = rows;
+    p.N = k;
+    p.n_tiles = tiles(k, moe::linear_n_tile(false));
+    p.kc = n;
+    p.E = num_experts;
+    p.act = activation;
+    p.test_drop = moe::test_drop();
+    return launched(moe::launch_linear_input(p, activation == MOE_ACT_SWIGLU, sms, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+MOE_API int moe_expert_linear_backward_weight(const void* dy, int64_t rows, int32_t n, const void* a, int32_t k,
+                                              int32_t num_experts, const int32_t* expert_offsets, void* dw,
+                                              int dw_type, float* db, int accumulate, int32_t* status, void* stream) {
+  NvtxRange nvtx_range("moe_expert_linear_backward_weight");
+  if (!product_ok(rows, n, k, num_experts, expert_offsets, status) || !type_ok(dw_type) || !dw || !aligned(dw, 16) ||
+      !aligned(db, 16))
+    return MOE_EINVAL;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (accumulate) return MOE_OK;
+    const size_t elements = static_cast<size_t>(num_experts) * n;
+    cudaError_t err = cudaMemsetAsync(dw, 0, elements * k * (dw_type == MOE_TYPE_F32 ? 4 : 2), on);
+    if (err == cudaSuccess && db) err = cudaMemsetAsync(db, 0, elements * sizeof(float), on);
+    return launched(err);
+  }
+  if (!dy || !a || !aligned(dy, 16) || !aligned(a, 16)) return MOE_EINVAL;
+  return guarded([&] {
+    const int sms = sm_count();
+    if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    moe::LinearParams p = {};
+    if (!encode_rows(&p.a, dy, rows, n, 64) || !encode_rows(&p.b, a, rows, k, 64)) return static_cast<int>(MOE_ECUDA);
+    p.offsets = expert_offsets;
+    p.out = dw;
+    p.db = db;
+    p.status = status;
+    p.rows = rows;
+    p.N = k;
+    p.n_tiles = tiles(k, moe::linear_n_tile(false));
+    p.M = n;
+    p.m_tiles = tiles(n, moe::linear_m_tile());
+    p.E = num_experts;
+    p.accumulate = accumulate != 0;
+    p.test_drop = moe::test_drop();
+    return launched(moe::launch_linear_weight(p, dw_type == MOE_TYPE_F32, sms, on));
+  });
+}

@@ -40,7 +40,7 @@ MOE_OPT_COMBINE_SCHEDULE = 21
 MOE_OPT_ROUTE_VARIANT_FP8 = 22  # read only: the routing moe_dispatch_send_fp8 takes
 PACK_BULK, PACK_VECTOR = 0, 1
 
-# Every entry point of include/moe.h and include/moe_ffn.h.
+# Every entry point of include/moe.h, include/moe_ffn.h and include/moe_train.h.
 EXPORTS = ("moe_validate_config", "moe_workspace_bytes", "moe_recv_bound_rows", "moe_ctx_create",
            "moe_ctx_destroy", "moe_ctx_set_option", "moe_ctx_get_option", "moe_dispatch_send", "moe_dispatch_recv",
            "moe_combine_send", "moe_combine_recv", "moe_get_error", "moe_strerror",
@@ -49,7 +49,10 @@ EXPORTS = ("moe_validate_config", "moe_workspace_bytes", "moe_recv_bound_rows", 
            "moe_dense_capacity", "moe_dispatch_send_dense", "moe_combine_recv_dense",
            # include/moe_ffn.h
            "moe_add_rms_norm_fp8", "moe_expert_gemm_fp8", "moe_expert_glu_fp8",
-           "moe_decode_workspace_bytes", "moe_decode_layer_fp8", "moe_ffn_test_drop_load")
+           "moe_decode_workspace_bytes", "moe_decode_layer_fp8", "moe_ffn_test_drop_load",
+           # include/moe_train.h
+           "moe_router_topk", "moe_router_topk_backward", "moe_combine_backward", "moe_dispatch_backward",
+           "moe_expert_linear", "moe_expert_linear_backward_input", "moe_expert_linear_backward_weight")
 
 
 class moe_config(ctypes.Structure):
@@ -84,6 +87,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "or python combine_route_count_gb300/build.py")
     lib = ctypes.CDLL(path)
     P, I, I64, C = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.POINTER(moe_config)
+    i32 = ctypes.c_int32
     sig = {
         "moe_validate_config": ([C], I),
         "moe_workspace_bytes": ([C, ctypes.POINTER(ctypes.c_size_t)], I),
@@ -113,6 +117,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_ffn_test_drop_load": ([ctypes.c_int32], I),
         "moe_expert_gemm_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, I, P, P], I),
         "moe_expert_glu_fp8": ([P, P, I64, ctypes.c_int32, P, P, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P], I),
+        "moe_router_topk": ([P, I, P, I64, i32, i32, I, I, ctypes.c_float, P, P, P], I),
+        "moe_router_topk_backward": ([P, I, P, P, I64, i32, i32, I, I, ctypes.c_float, P, P], I),
+        "moe_combine_backward": ([P, P, P, P, I64, i32, i32, I64, P, P, P], I),
+        "moe_dispatch_backward": ([P, P, P, I64, i32, i32, I64, P, P], I),
+        "moe_expert_linear": ([P, I64, i32, P, i32, i32, P, P, I, I, P, P, P, I, P, P], I),
+        "moe_expert_linear_backward_input": ([P, I64, i32, P, i32, i32, P, I, P, P, P, P], I),
+        "moe_expert_linear_backward_weight": ([P, I64, i32, P, i32, i32, P, P, I, P, I, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -344,6 +355,66 @@ def moe_decode_layer_fp8(cfg: moe_config, inter: int, xq: Any, x_scales: Any, to
 
 def moe_ffn_test_drop_load(load: int) -> None:
     _check(load_library().moe_ffn_test_drop_load(load), "moe_ffn_test_drop_load")
+
+
+# ---- training operators (include/moe_train.h); train.py calls them on tensors ----
+
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_SILU, MOE_ACT_SWIGLU = range(5)
+
+
+def moe_router_topk(logits: Any, logits_type: int, bias: Any, num_tokens: int, num_experts: int, top_k: int,
+                    score: int, normalize: bool, scale: float, topk_idx: Any, topk_w: Any, stream: Any = None) -> None:
+    _check(load_library().moe_router_topk(_ptr(logits), logits_type, _ptr(bias), num_tokens, num_experts, top_k, score,
+                                          int(normalize), scale, _ptr(topk_idx), _ptr(topk_w), _stream(stream)),
+           "moe_router_topk")
+
+
+def moe_router_topk_backward(logits: Any, logits_type: int, topk_idx: Any, d_topk_w: Any, num_tokens: int,
+                             num_experts: int, top_k: int, score: int, normalize: bool, scale: float, d_logits: Any,
+                             stream: Any = None) -> None:
+    _check(load_library().moe_router_topk_backward(_ptr(logits), logits_type, _ptr(topk_idx), _ptr(d_topk_w),
+                                                   num_tokens, num_experts, top_k, score, int(normalize), scale,
+                                                   _ptr(d_logits), _stream(stream)), "moe_router_topk_backward")
+
+
+def moe_combine_backward(d_out: Any, expert_y: Any, topk_w: Any, slot_row: Any, num_tokens: int, hidden: int,
+                         top_k: int, rows: int, d_expert_y: Any, d_topk_w: Any, stream: Any = None) -> None:
+    _check(load_library().moe_combine_backward(_ptr(d_out), _ptr(expert_y), _ptr(topk_w), _ptr(slot_row), num_tokens,
+                                               hidden, top_k, rows, _ptr(d_expert_y), _ptr(d_topk_w),
+                                               _stream(stream)), "moe_combine_backward")
+
+
+def moe_dispatch_backward(d_expert_x: Any, slot_row: Any, add: Any, num_tokens: int, hidden: int, top_k: int,
+                          rows: int, d_x: Any, stream: Any = None) -> None:
+    _check(load_library().moe_dispatch_backward(_ptr(d_expert_x), _ptr(slot_row), _ptr(add), num_tokens, hidden, top_k,
+                                                rows, _ptr(d_x), _stream(stream)), "moe_dispatch_backward")
+
+
+def moe_expert_linear(a: Any, rows: int, k: int, w: Any, n: int, num_experts: int, expert_offsets: Any, bias: Any,
+                      bias_type: int, activation: int, residual: Any, pre: Any, out: Any, out_type: int,
+                      status: Any = None, stream: Any = None) -> None:
+    _check(load_library().moe_expert_linear(_ptr(a), rows, k, _ptr(w), n, num_experts, _ptr(expert_offsets),
+                                            _ptr(bias), bias_type, activation, _ptr(residual), _ptr(pre), _ptr(out),
+                                            out_type, _ptr(status), _stream(stream)), "moe_expert_linear")
+
+
+def moe_expert_linear_backward_input(dy: Any, rows: int, n: int, w: Any, k: int, num_experts: int,
+                                     expert_offsets: Any, activation: int, pre: Any, dx: Any, status: Any = None,
+                                     stream: Any = None) -> None:
+    _check(load_library().moe_expert_linear_backward_input(_ptr(dy), rows, n, _ptr(w), k, num_experts,
+                                                           _ptr(expert_offsets), activation, _ptr(pre), _ptr(dx),
+                                                           _ptr(status), _stream(stream)),
+           "moe_expert_linear_backward_input")
+
+
+def moe_expert_linear_backward_weight(dy: Any, rows: int, n: int, a: Any, k: int, num_experts: int,
+                                      expert_offsets: Any, dw: Any, dw_type: int, db: Any, accumulate: bool,
+                                      status: Any = None, stream: Any = None) -> None:
+    _check(load_library().moe_expert_linear_backward_weight(_ptr(dy), rows, n, _ptr(a), k, num_experts,
+                                                            _ptr(expert_offsets), _ptr(dw), dw_type, _ptr(db),
+                                                            int(accumulate), _ptr(status), _stream(stream)),
+           "moe_expert_linear_backward_weight")
 
 
 # ---- convenience: one context with a torch-allocated workspace ---------------
