@@ -25,7 +25,7 @@ LIB_FFN = os.path.join(PKG, "_ffn.so")
 STAMP_FFN = os.path.join(BUILD, "ffn.stamp")
 SOURCES = ["route_count.cu", "route_split.cu", "route_cluster.cu", "route_pack.cu", "route_pack_fp8.cu", "dispatch_pack.cu", "dispatch_fp8.cu", "dispatch_staged.cu", "dense_a2a.cu", "combine.cu", "combine_two_level.cu", "moe_abi.cu", "moe_noalloc.cu",
            "add_norm_fp8.cu", "expert_gemm.cu", "decode_layer.cu", "ffn_abi.cu",
-           "router.cu", "route_grad.cu", "expert_linear.cu", "train_abi.cu"]
+           "router.cu", "route_grad.cu", "expert_linear.cu", "expert_linear_few.cu", "train_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -11,7 +11,10 @@
 // columns x 64 summed rows, no transposition anywhere.
 //
 // One CTA per SM, tile 128 x 256, 64 of the summed axis a stage, 4 stages of 48
-// KiB by tiled TMA (128-byte swizzle).  12 warps: eight for the epilogue (two
+// KiB by tiled TMA (128-byte swizzle).  With many rows an expert two CTAs (a cluster)
+// share a tile of 256 x 256: one issues the products of both (cta_group::2), each
+// holds half of either operand, 6 stages of 32 KiB, so that a product of 256 x 256 x 64
+// takes 64 KiB out of L2 instead of 96.  12 warps: eight for the epilogue (two
 // groups of four, each with half of the columns), one for TMA, one for the matrix
 // instructions, two for the bias gradient.  A tile's sum stays in tensor memory:
 // two buffers of 256 columns, so that one tile's epilogue runs under the next
@@ -23,13 +26,22 @@
 // expert); rows past the end of an expert belong to the next one, and the matrix
 // warp overwrites them with zeros in the last stage.
 //
+// What bounds it: at many rows the tensor cores.  8192 rows, N = K = 4096: forward 143
+// us, 1923 TFLOP/s, what a library's plain product takes in a burst (single CTAs 162);
+// by rows 153, by weights 165.  At few rows an expert the weights' bytes.
+//
 // Tiles are dealt out statically (tile b, b+G, ...).  Waits are bounded (2 s) and
 // report MOE_ETIMEDOUT.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <map>
+#include <mutex>
+#include <utility>
+
 #include "ffn_kernels.cuh"
+#include "linear_math.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 #include "train_kernels.cuh"
@@ -37,13 +49,18 @@
 namespace moe {
 namespace {
 
+using namespace lin;
+
 enum Mode { kForward, kInput, kWeight };
 
-constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
-constexpr int kStages = 4;
-constexpr int kABytes = kTileM * kBlockK * 2, kBBytes = kTileN * kBlockK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;  // kTileM: rows of one CTA
+constexpr int kABytes = kTileM * kBlockK * 2;
 constexpr int kChunkBytes = 64 * kBlockK * 2;  // a box of 64 x 64
+// Of one CTA: alone it holds all of B's columns, in a pair half of them.
+__host__ __device__ constexpr int b_columns(bool pair) { return pair ? kTileN / 2 : kTileN; }
+__host__ __device__ constexpr int stage_bytes(bool pair) { return kABytes + b_columns(pair) * kBlockK * 2; }
+__host__ __device__ constexpr int stage_count(bool pair) { return pair ? 6 : 4; }
+constexpr int kMaxStages = 6;
 constexpr int kEpilogueWarps = 8;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kBiasWarp = 10;
 constexpr int kThreads = 384;
@@ -51,7 +68,10 @@ constexpr uint32_t kTmemColumns = 512;
 constexpr int kUnit = 64;  // columns that an epilogue warp works on at a time
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t consumed[kMaxStages];   // bias gradient: the products have read the stage
+  uint64_t tail_full[kMaxStages];  // pair, second CTA: its half of an expert's last stage is there
+  uint64_t tail_clear[kMaxStages]; // pair, first CTA: and ends in zeros
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drained;
   uint32_t tmem;
@@ -76,16 +96,32 @@ __device__ __forceinline__ int64_t tile_count(const Groups& g, const LinearParam
   return static_cast<int64_t>(g.start[p.E]) * p.n_tiles;
 }
 
-template <Mode kMode>
-__device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p, int64_t t) {
+// Row tile (returned) and column tile of an expert's tile number t.  Bands of 2048
+// rows, inside a band rows fastest: the tiles at work at one time cover about as many
+// rows as columns, which share the operands in L2.  (All of 8192 rows first: 203 us
+// instead of 153 for the gradient by rows, N = K = 4096, whose weights were then read in
+// strips of a few hundred bytes.)
+template <int kRows>
+__device__ __forceinline__ int place(int64_t t, int m_tiles, int n_tiles, int& n) {
+  constexpr int kBand = 2048 / kRows;
+  const int band = static_cast<int>(t / (static_cast<int64_t>(kBand) * n_tiles));
+  const int height = min(kBand, m_tiles - band * kBand);
+  const int in_band = static_cast<int>(t - static_cast<int64_t>(band) * kBand * n_tiles);
+  n = in_band / height;
+  return band * kBand + in_band - n * height;
+}
+
+// What CTA `rank` of a pair has of tile t (rank 0: of a CTA alone).  Rows may be none.
+template <Mode kMode, bool kPair>
+__device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p, int64_t t, int rank) {
+  constexpr int kRows = kPair ? 2 * kTileM : kTileM;
   Tile r;
   if (kMode == kWeight) {
     const int64_t per = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
     r.e = static_cast<int>(t / per);
     const int64_t local = t - r.e * per;
-    const int m = static_cast<int>(local / p.n_tiles);
-    r.n = static_cast<int>(local - static_cast<int64_t>(m) * p.n_tiles);
-    r.row0 = m * kTileM;
+    const int m = place<kRows>(local, p.m_tiles, p.n_tiles, r.n);
+    r.row0 = m * kRows + rank * kTileM;
     r.rows = min(kTileM, p.M - r.row0);
     r.k0 = g.lo[r.e];
     r.kc = g.hi[r.e] - r.k0;
@@ -100,8 +136,7 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p
   const int m_tiles = g.start[lo + 1] - g.start[lo];
   const int64_t local = t - static_cast<int64_t>(g.start[lo]) * p.n_tiles;
   r.e = lo;
-  r.n = static_cast<int>(local / m_tiles);
-  r.row0 = g.lo[lo] + static_cast<int>(local - static_cast<int64_t>(r.n) * m_tiles) * kTileM;
+  r.row0 = g.lo[lo] + place<kRows>(local, m_tiles, p.n_tiles, r.n) * kRows + rank * kTileM;
   r.rows = min(kTileM, g.hi[lo] - r.row0);
   r.k0 = 0;
   r.kc = p.kc;
@@ -109,13 +144,6 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p
 }
 
 __device__ __forceinline__ int blocks_of(int kc) { return (kc + kBlockK - 1) / kBlockK; }
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // ---- rows in and out of the epilogue ------------------------------------------
 // A lane holds 128 bytes of its own row; four lanes move 128 bytes of one row
@@ -242,23 +270,14 @@ __device__ __forceinline__ void load_f32(Rows r, float (&v)[kUnit], int lane, in
   }
 }
 
-// ---- activations ------------------------------------------------------------------
-// Quotients by a denominator beyond 2^126 become 0; they are below 2^-119 of the numerator there.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + expf(-v)); }
-__device__ __forceinline__ float silu_slope(float v) {
-  const float s = sigmoid(v);
-  return s * fmaf(v, 1.0f - s, 1.0f);
-}
-constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
-
+// The kind of activation is asked for once for all 64 columns.
 __device__ __forceinline__ void activate(int act, float (&v)[kUnit]) {
   if (act == MOE_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[i] = v[i] > 0.0f || v[i] != v[i] ? v[i] : 0.0f;
+    for (int i = 0; i < kUnit; ++i) v[i] = relu(v[i]);
   } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * kSqrtHalf));
+    for (int i = 0; i < kUnit; ++i) v[i] = gelu(v[i]);
   } else if (act == MOE_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) v[i] = silu(v[i]);
@@ -268,16 +287,13 @@ __device__ __forceinline__ void activate(int act, float (&v)[kUnit]) {
 __device__ __forceinline__ void through(int act, float (&g)[kUnit], const float (&v)[kUnit]) {
   if (act == MOE_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) g[i] = v[i] > 0.0f ? g[i] : 0.0f;
+    for (int i = 0; i < kUnit; ++i) g[i] = act_through(MOE_ACT_RELU, g[i], v[i]);
   } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
-      const float density = kInvSqrt2Pi * expf(-0.5f * v[i] * v[i]);
-      g[i] *= fmaf(v[i], density, 0.5f * (1.0f + erff(v[i] * kSqrtHalf)));
-    }
+    for (int i = 0; i < kUnit; ++i) g[i] = act_through(MOE_ACT_GELU, g[i], v[i]);
   } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) g[i] *= silu_slope(v[i]);
+    for (int i = 0; i < kUnit; ++i) g[i] = act_through(MOE_ACT_SILU, g[i], v[i]);
   }
 }
 
@@ -311,8 +327,38 @@ __device__ __forceinline__ void add_bias(const LinearParams& p, int64_t first, i
   }
 }
 
-template <Mode kMode, bool kGlu, bool kF32>
+template <bool kPair>
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (kPair) tc::tma_load_2d_pair(dst, map, x, y, bar);
+  else tc::tma_load_2d(dst, map, x, y, bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if (kPair) tc::tma_load_3d_pair(dst, map, x, y, z, bar);
+  else tc::tma_load_3d(dst, map, x, y, z, bar);
+}
+
+// An accumulator buffer is read: the CTA that issues the products may have it again.
+template <bool kPair>
+__device__ __forceinline__ void release(uint64_t* acc_empty) {
+  if (kPair) tc::mbar_arrive_at(tc::at_rank(acc_empty, 0));
+  else tc::mbar_arrive(acc_empty);
+}
+
+// Rows from `first` on of a stage's boxes, which belong to the next expert, become
+// zeros in both operands (0 x infinity is no zero).  Whole warp.
+__device__ __forceinline__ void clear_rows(uint8_t* stage, int bytes, int first, int lane) {
+#pragma unroll 1
+  for (int c = 0; c < bytes; c += kChunkBytes)
+    for (int i = first * 8 + lane; i < kBlockK * 8; i += 32)
+      *reinterpret_cast<uint4*>(stage + c + i * 16) = make_uint4(0, 0, 0, 0);
+  tc::fence_async_shared();
+  __syncwarp();
+}
+
+template <Mode kMode, bool kGlu, bool kF32, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid_constant__ LinearParams p) {
+  constexpr int kStages = stage_count(kPair), kStageBytes = stage_bytes(kPair), kBColumns = b_columns(kPair);
   extern __shared__ uint8_t s_raw[];
   __shared__ Shared s;
   uint8_t* stages = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
@@ -322,26 +368,35 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   g.start = g.hi + p.E;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool bias_grad = kMode == kWeight && p.db;
+  const int rank = kPair ? tc::cluster_rank() : 0;
+  const int64_t first_tile = kPair ? blockIdx.x / 2 : blockIdx.x, tile_step = kPair ? gridDim.x / 2 : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
-      ptx::mbar_init(&s.empty[i], bias_grad ? 3 : 1);
+      ptx::mbar_init(&s.empty[i], bias_grad ? 2 : 1);
+      ptx::mbar_init(&s.consumed[i], 1);
+      ptx::mbar_init(&s.tail_full[i], 1);
+      ptx::mbar_init(&s.tail_clear[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s.acc_full[i], 1);
-      ptx::mbar_init(&s.acc_empty[i], kEpilogueWarps);
+      ptx::mbar_init(&s.acc_empty[i], kPair ? 2 * kEpilogueWarps : kEpilogueWarps);
     }
     ptx::mbar_init(&s.drained, 1);
     ptx::mbar_fence_init();
     s.gave_up = 0;
   }
-  if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, kTmemColumns);
+  if (warp == kMmaWarp) {
+    if (kPair) tc::tmem_alloc_pair(&s.tmem, kTmemColumns);
+    else tc::tmem_alloc(&s.tmem, kTmemColumns);
+  }
   if (threadIdx.x == kTmaWarp * 32) {
     tc::tma_prefetch_map(&p.a);
     tc::tma_prefetch_map(&p.b);
   }
   ptx::wait_prerequisites();
+  ptx::launch_dependents();
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
     const int rows = static_cast<int>(p.rows);
     int lo = 0, hi = rows;
@@ -354,10 +409,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   }
   __syncthreads();
   if (kMode != kWeight && warp == 0) {
+    constexpr int kRows = kPair ? 2 * kTileM : kTileM;
     int before = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int own = e < p.E ? (g.hi[e] - g.lo[e] + kTileM - 1) / kTileM : 0;
+      const int own = e < p.E ? (g.hi[e] - g.lo[e] + kRows - 1) / kRows : 0;
       int sum = own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -370,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     if (lane == 0) g.start[p.E] = before;
   }
   tc::fence_before();
-  __syncthreads();
+  if (kPair) tc::cluster_sync();  // the other CTA's barriers are ready too
+  else __syncthreads();
   tc::fence_after();
   const int64_t tiles = tile_count<kMode>(g, p);
   const uint32_t tmem = s.tmem, tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
@@ -378,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   if (warp == kTmaWarp) {
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = find_tile<kMode>(g, p, t);
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
       const int kblocks = blocks_of(tile.kc);
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const int st = it % kStages;
@@ -387,26 +444,31 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t *a = stages + st * kStageBytes, *b = a + kABytes;
+        // A pair's loads are all counted by the first CTA, which issues the products;
+        // but the second one's part of a stage that it has to clear by itself.
+        const bool own = kPair && kMode == kWeight && kb == kblocks - 1 && tile.kc % kBlockK != 0;
+        uint64_t* expects = own && rank == 1 ? &s.tail_full[st] : &s.full[st];
+        const uint32_t bar = kPair && !own ? tc::at_rank(expects, 0) : ptx::smem_addr(expects);
         if (tc::elect() && it != p.test_drop) {
-          ptx::mbar_arrive_expect_tx(&s.full[st], kStageBytes);
+          if (rank == 0 || own) ptx::mbar_arrive_expect_tx(expects, kPair && !own ? 2 * kStageBytes : kStageBytes);
           const int k = tile.k0 + kb * kBlockK;
           if (kMode == kWeight) {
 #pragma unroll
-            for (int q = 0; q < kTileM / 64; ++q)
-              tc::tma_load_2d(a + q * kChunkBytes, &p.a, tile.row0 + q * 64, k, &s.full[st]);
+            for (int q = 0; q < kTileM / 64; ++q) load_2d<kPair>(a + q * kChunkBytes, &p.a, tile.row0 + q * 64, k, bar);
 #pragma unroll
-            for (int q = 0; q < kTileN / 64; ++q)
-              tc::tma_load_2d(b + q * kChunkBytes, &p.b, tile.n * kTileN + q * 64, k, &s.full[st]);
+            for (int q = 0; q < kBColumns / 64; ++q)
+              load_2d<kPair>(b + q * kChunkBytes, &p.b, tile.n * kTileN + rank * kBColumns + q * 64, k, bar);
           } else {
-            tc::tma_load_2d(a, &p.a, k, tile.row0, &s.full[st]);
+            load_2d<kPair>(a, &p.a, k, tile.row0, bar);
             if (kMode == kForward) {
-              const int n0 = tile.n * (kGlu ? kTileN / 2 : kTileN);
-              tc::tma_load_3d(b, &p.b, k, n0, tile.e, &s.full[st]);
-              tc::tma_load_3d(b + kBBytes / 2, &p.b, k, n0 + (kGlu ? p.N : kTileN / 2), tile.e, &s.full[st]);
+              // Boxes of 128: the first and the second half of the columns (glu: gate, up).
+              const int n0 = tile.n * (kGlu ? kTileN / 2 : kTileN), n1 = n0 + (kGlu ? p.N : kTileN / 2);
+              load_3d<kPair>(b, &p.b, k, rank == 0 ? n0 : n1, tile.e, bar);
+              if (!kPair) load_3d<kPair>(b + 128 * kBlockK * 2, &p.b, k, n1, tile.e, bar);
             } else {
 #pragma unroll
-              for (int q = 0; q < kTileN / 64; ++q)
-                tc::tma_load_3d(b + q * kChunkBytes, &p.b, tile.n * kTileN + q * 64, k, tile.e, &s.full[st]);
+              for (int q = 0; q < kBColumns / 64; ++q)
+                load_3d<kPair>(b + q * kChunkBytes, &p.b, tile.n * kTileN + rank * kBColumns + q * 64, k, tile.e, bar);
             }
           }
         }
@@ -416,14 +478,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     // Loads in flight write to this CTA's shared memory: it does not end before
     // them, whichever warp gave up.
     const unsigned long long start = tc::now_ns();
-    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-      if (j != p.test_drop) tc::settle(&s.full[j % kStages], (j / kStages) & 1, start);
-  } else if (warp == kMmaWarp) {
-    constexpr uint32_t kInstr = tc::instr_desc_bf16(kTileM, kTileN, kMode == kWeight, kMode != kForward);
-    uint32_t it = 0, round = 0;
+    if (rank == 0)
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+        if (j != p.test_drop) tc::settle(&s.full[j % kStages], (j / kStages) & 1, start);
+    // A pair's second CTA knows its loads by their stages being free again, and
+    // that is an arrival from afar in either.
+    if (kPair)
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+        tc::settle(&s.empty[j % kStages], (j / kStages) & 1, start);
+  } else if (warp == kMmaWarp && rank == 0) {
+    constexpr uint32_t kInstr =
+        tc::instr_desc_bf16(kPair ? 2 * kTileM : kTileM, kTileN, kMode == kWeight, kMode != kForward);
+    uint32_t it = 0, round = 0, tails = 0;  // tails: parity of tail_clear, a bit a stage
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = find_tile<kMode>(g, p, t);
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
       const int kblocks = blocks_of(tile.kc);
       if (kblocks == 0) continue;
       const int buf = round & 1;
@@ -437,14 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         if (!ok) break;
         uint8_t* a_tile = stages + st * kStageBytes;
         if (kMode == kWeight && kb == kblocks - 1 && tile.kc % kBlockK != 0) {
-          // Rows of the next expert: zeros in both operands (0 x infinity is no zero).
-          const int first = tile.kc % kBlockK;
-#pragma unroll 1
-          for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
-            for (int i = first * 8 + lane; i < kBlockK * 8; i += 32)
-              *reinterpret_cast<uint4*>(a_tile + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
-          tc::fence_async_shared();
-          __syncwarp();
+          clear_rows(a_tile, kStageBytes, tile.kc % kBlockK, lane);
+          if (kPair) {
+            ok = tc::wait_cluster(&s.tail_clear[st], (tails >> st) & 1, &s.gave_up);
+            tails ^= 1u << st;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
         }
         tc::fence_after();
         const uint64_t a = kMode == kWeight ? tc::smem_desc_mn(a_tile) : tc::smem_desc(a_tile);
@@ -454,52 +522,93 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         constexpr uint64_t kStepB = (kMode != kForward ? 2048 : 32) >> 4;
         if (tc::elect()) {
 #pragma unroll
-          for (int k = 0; k < kBlockK / 16; ++k)
-            tc::mma_f16(tmem_u + buf * kTileN, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
-          tc::commit(&s.empty[st]);
-          if (kb == kblocks - 1) tc::commit(&s.acc_full[buf]);
+          for (int k = 0; k < kBlockK / 16; ++k) {
+            const uint32_t d = tmem_u + buf * kTileN;
+            if (kPair) tc::mma_f16_pair(d, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
+            else tc::mma_f16(d, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
+          }
+          // A stage is free when the products have read it, in the first column tile when the
+          // bias warps have after them; else their two arrivals are made here.
+          const bool bias_next = bias_grad && tile.n == 0;
+          for (int i = 0; i < (bias_grad && !bias_next ? 2 : 1); ++i) {
+            uint64_t* read = bias_next ? &s.consumed[st] : &s.empty[st];
+            if (kPair) tc::commit_pair(read);
+            else tc::commit(read);
+          }
+          if (kb == kblocks - 1) {
+            if (kPair) tc::commit_pair(&s.acc_full[buf]);
+            else tc::commit(&s.acc_full[buf]);
+          }
         }
         __syncwarp();
       }
       ++round;
     }
     // Nothing may be in flight when the tensor memory is freed.
-    if (tc::elect()) tc::commit(&s.drained);
+    if (tc::elect()) {
+      if (kPair) tc::commit_pair(&s.drained);
+      else tc::commit(&s.drained);
+    }
     __syncwarp();
+    tc::settle(&s.drained, 0, tc::now_ns());
+  } else if (warp == kMmaWarp) {
+    // The second CTA of a pair clears its half of an expert's last stage.
+    if (kMode == kWeight) {
+      uint32_t it = 0, tails = 0;
+      bool ok = true;
+      for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+        const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
+        it += blocks_of(tile.kc);
+        if (tile.kc % kBlockK == 0) continue;
+        const int st = (it - 1) % kStages;
+        ok = tc::wait(&s.tail_full[st], (tails >> st) & 1, &s.gave_up);
+        tails ^= 1u << st;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        clear_rows(stages + st * kStageBytes, kStageBytes, tile.kc % kBlockK, lane);
+        if (lane == 0) tc::mbar_release_at(tc::at_rank(&s.tail_clear[st], 0));
+        __syncwarp();
+      }
+    }
     tc::settle(&s.drained, 0, tc::now_ns());
   } else if (warp >= kBiasWarp) {
     if (bias_grad) {
       const int c = warp - kBiasWarp;  // 64 columns of dy
-      uint32_t it = 0;
+      uint32_t it = 0, reads = 0;      // reads: parity of consumed, a bit a stage
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const Tile tile = find_tile<kMode>(g, p, t);
+      for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+        const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
         const int kblocks = blocks_of(tile.kc);
+        if (tile.n != 0) {
+          it += kblocks;
+          continue;
+        }
         float sum0 = 0.0f, sum1 = 0.0f;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int st = it % kStages;
-          ok = tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up);
+          // A pair's second CTA is not told that its loads are there, but that they were read.
+          ok = kPair ? tc::wait_cluster(&s.consumed[st], (reads >> st) & 1, &s.gave_up)
+                     : tc::wait(&s.consumed[st], (reads >> st) & 1, &s.gave_up);
+          reads ^= 1u << st;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (tile.n == 0) {
-            const uint8_t* a = stages + st * kStageBytes + c * kChunkBytes;
-            const int rows = min(kBlockK, tile.kc - kb * kBlockK);
-            float part0 = 0.0f, part1 = 0.0f;
+          const uint8_t* a = stages + st * kStageBytes + c * kChunkBytes;
+          const int rows = min(kBlockK, tile.kc - kb * kBlockK);
+          float part0 = 0.0f, part1 = 0.0f;
 #pragma unroll 8
-            for (int r = 0; r < rows; ++r) {
-              const uint32_t v =
-                  *reinterpret_cast<const uint32_t*>(a + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-              part0 += bf_lo(v);
-              part1 += bf_hi(v);
-            }
-            sum0 += part0;
-            sum1 += part1;
+          for (int r = 0; r < rows; ++r) {
+            const uint32_t v =
+                *reinterpret_cast<const uint32_t*>(a + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+            part0 += bf_lo(v);
+            part1 += bf_hi(v);
           }
+          sum0 += part0;
+          sum1 += part1;
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&s.empty[st]);
         }
         const int col = tile.row0 + c * 64 + lane * 2;
-        if (ok && tile.n == 0 && col < p.M) {  // M is a multiple of 8
+        if (ok && col < p.M) {  // M is a multiple of 8
           float2* to = reinterpret_cast<float2*>(p.db + static_cast<int64_t>(tile.e) * p.M + col);
           float2 v = make_float2(sum0, sum1);
           if (p.accumulate) {
@@ -516,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     const uint32_t lanes = tmem + (static_cast<uint32_t>(sub) << 16);
     uint32_t round = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = find_tile<kMode>(g, p, t);
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
       const bool some = sub < tile.rows;
       const bool sums = blocks_of(tile.kc) > 0;
       const int buf = round & 1;
@@ -543,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
           load_acc(acc + kTileN / 2 + half * kUnit, up);
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+          if (lane == 0) release<kPair>(&s.acc_empty[buf]);
           if (p.bias) {
             add_bias(p, first, col, v);
             add_bias(p, first, p.N + col, up);
@@ -572,10 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
           else store_bf16(r, v, lane);
         } else {
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+          if (lane == 0) release<kPair>(&s.acc_empty[buf]);
         }
-        continue;
-      }
+      } else {
 #pragma unroll 1
       for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
         const int col = tile.n * kTileN + half * (kTileN / 2) + q * kUnit;
@@ -589,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         if (sums && q == kTileN / 2 / kUnit - 1) {
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.acc_empty[buf]);
+          if (lane == 0) release<kPair>(&s.acc_empty[buf]);
         }
         if (!some || col >= p.N) continue;
         const int64_t byte = static_cast<int64_t>(col) * 2, stride = static_cast<int64_t>(p.N) * 2;
@@ -620,12 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
           load_bf16(at, gate, lane);
           load_bf16(at_up, up, lane);
 #pragma unroll
-          for (int i = 0; i < kUnit; ++i) {
-            const float sig = sigmoid(gate[i]);
-            const float d_up = v[i] * (gate[i] * sig);
-            gate[i] = v[i] * up[i] * (sig * fmaf(gate[i], 1.0f - sig, 1.0f));
-            up[i] = d_up;
-          }
+          for (int i = 0; i < kUnit; ++i) swiglu_through(v[i], gate[i], up[i]);
           Rows to = rows_at(p.out, row, 2 * stride, byte, rows, lane);
           to.left = at.left;
           store_bf16(to, gate, lane);
@@ -654,44 +757,105 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
           }
         }
       }
+      }
     }
   }
   tc::fence_before();
   __syncthreads();
+  if (kPair) tc::cluster_sync();  // products read the other CTA's shared memory, arrivals reach it
   tc::fence_after();
   if (threadIdx.x == 0 && s.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
-  if (warp == kMmaWarp) tc::tmem_free(tmem, kTmemColumns);
+  if (warp == kMmaWarp) {
+    if (kPair) tc::tmem_free_pair(tmem, kTmemColumns);
+    else tc::tmem_free(tmem, kTmemColumns);
+  }
+  if (kPair) tc::cluster_sync();
 }
 
-template <Mode kMode, bool kGlu, bool kF32>
+// Pairs of CTAs that are resident at a time (a pair's two share a GPC, so not every
+// SM need be used), asked for once per device and kernel; 0: the query failed.
+int resident_pairs(const void* kernel, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, int> known;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = known.find({dev, kernel});
+  if (it != known.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[{dev, kernel}] = n;
+  return n;
+}
+
+template <Mode kMode, bool kGlu, bool kF32, bool kPair>
 cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
-  const size_t smem = 1024 + kStages * kStageBytes + (3 * static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
-  auto* kernel = expert_linear_kernel<kMode, kGlu, kF32>;
+  // The most tables that any call has, so that what fits is the same for all.
+  const size_t smem = 1024 + stage_count(kPair) * stage_bytes(kPair) + (3 * MOE_MAX_EXPERTS + 1) * sizeof(int32_t);
+  auto* kernel = expert_linear_kernel<kMode, kGlu, kF32, kPair>;
   cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
   if (err != cudaSuccess) return err;
   // Every expert may add one partly filled row tile.
-  int64_t most = kMode == kWeight ? static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles
-                                  : ((p.rows + kTileM - 1) / kTileM + (p.offsets ? p.E : 0)) * p.n_tiles;
-  if (most > sms) most = sms;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(most)), dim3(kThreads), smem, stream, true, p);
+  constexpr int kRows = kPair ? 2 * kTileM : kTileM;
+  const int64_t m_tiles = kMode == kWeight ? static_cast<int64_t>(p.E) * p.m_tiles
+                                           : (p.rows + kRows - 1) / kRows + (p.offsets ? p.E : 0);
+  const int64_t tiles = m_tiles * p.n_tiles;
+  if (!kPair)
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads), smem, stream,
+                         true, p);
+  const int pairs = resident_pairs(reinterpret_cast<const void*>(kernel), smem);
+  if (pairs <= 0) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <Mode kMode, bool kGlu, bool kF32>
+cudaError_t launch(const LinearParams& p, bool pair, int sms, cudaStream_t stream) {
+  return pair ? launch<kMode, kGlu, kF32, true>(p, sms, stream) : launch<kMode, kGlu, kF32, false>(p, sms, stream);
 }
 
 }  // namespace
 
 int linear_n_tile(bool glu) { return glu ? kTileN / 2 : kTileN; }
-int linear_m_tile() { return kTileM; }
+int linear_m_tile(bool pair) { return pair ? 2 * kTileM : kTileM; }
 
-cudaError_t launch_linear(const LinearParams& p, bool glu, bool f32, int sms, cudaStream_t stream) {
-  if (glu) return f32 ? launch<kForward, true, true>(p, sms, stream) : launch<kForward, true, false>(p, sms, stream);
-  return f32 ? launch<kForward, false, true>(p, sms, stream) : launch<kForward, false, false>(p, sms, stream);
+cudaError_t launch_linear(const LinearParams& p, bool glu, bool f32, bool pair, int sms, cudaStream_t stream) {
+  if (glu)
+    return f32 ? launch<kForward, true, true>(p, pair, sms, stream) : launch<kForward, true, false>(p, pair, sms, stream);
+  return f32 ? launch<kForward, false, true>(p, pair, sms, stream) : launch<kForward, false, false>(p, pair, sms, stream);
 }
 
-cudaError_t launch_linear_input(const LinearParams& p, bool glu, int sms, cudaStream_t stream) {
-  return glu ? launch<kInput, true, false>(p, sms, stream) : launch<kInput, false, false>(p, sms, stream);
+cudaError_t launch_linear_input(const LinearParams& p, bool glu, bool pair, int sms, cudaStream_t stream) {
+  return glu ? launch<kInput, true, false>(p, pair, sms, stream) : launch<kInput, false, false>(p, pair, sms, stream);
 }
 
-cudaError_t launch_linear_weight(const LinearParams& p, bool f32, int sms, cudaStream_t stream) {
-  return f32 ? launch<kWeight, false, true>(p, sms, stream) : launch<kWeight, false, false>(p, sms, stream);
+cudaError_t launch_linear_weight(const LinearParams& p, bool f32, bool pair, int sms, cudaStream_t stream) {
+  return f32 ? launch<kWeight, false, true>(p, pair, sms, stream) : launch<kWeight, false, false>(p, pair, sms, stream);
 }
 
 }  // namespace moe

@@ -1,0 +1,325 @@
+// The products of expert_linear.cu for few rows: forward and input.
+//
+// Bound by memory: the weights are read once for a few rows, so what counts is to
+// have every SM load from the start.  A tile of expert_linear.cu is 256 columns of
+// out and all of the summed axis, 28 tiles of N = 7168: 28 SMs at work.  Here 128
+// weight rows (input: columns) are the 128 rows of the matrix instruction and up
+// to 32 rows of the expert its columns, and the summed axis is split over a
+// cluster of up to 8 CTAs, whose sums are exchanged through distributed shared
+// memory and added in rank order.  Two CTAs share an SM.
+//
+// A thread of the epilogue owns one column of out.  Operands, bounds of the summed
+// axis and waits as in expert_linear.cu.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ffn_kernels.cuh"
+#include "linear_math.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+#include "train_kernels.cuh"
+
+namespace moe {
+namespace {
+
+using namespace lin;
+
+constexpr int kCols = 128, kBlockK = 64;  // columns of out a CTA, summed axis a stage
+constexpr int kRows = kFewLinearRows;     // rows of an expert a CTA
+constexpr int kWBytes = kCols * kBlockK * 2, kABytes = kRows * kBlockK * 2;
+constexpr int kChunkBytes = 64 * kBlockK * 2;  // a box of 64 x 64
+constexpr int kMaxStages = 8;
+constexpr int kThreads = 192;  // warps 0-3: epilogue
+constexpr int kTmaWarp = 4, kMmaWarp = 5;
+constexpr int kMaxRanks = 8;
+constexpr int kPitch = kCols + 4;  // floats from one row's sums to the next
+
+__host__ __device__ constexpr int stage_bytes(bool two) { return (two ? 2 : 1) * kWBytes + kABytes; }
+__host__ __device__ constexpr int stage_count(bool two) { return two ? 3 : 5; }
+
+// Four floats of CTA `rank`'s shared memory, at the place that `p` has in this CTA's.
+__device__ __forceinline__ float4 ld_rank_v4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(tc::at_rank(p, rank))
+               : "memory");
+  return v;
+}
+
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full;
+  uint32_t tmem;
+  int gave_up;
+  int unit[3];  // expert, first row, rows
+};
+
+// kGate: forward with MOE_ACT_SWIGLU, gate and up columns side by side.
+template <bool kInput, bool kGate>
+__global__ void __launch_bounds__(kThreads, 2) few_linear_kernel(const __grid_constant__ LinearParams p, int ranks) {
+  constexpr int kStages = stage_count(kGate), kStageBytes = stage_bytes(kGate);
+  constexpr uint32_t kTmemColumns = kGate ? 2 * kRows : kRows;
+  extern __shared__ uint8_t s_raw[];
+  __shared__ Shared s;
+  uint8_t* stages = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
+  float* sums = reinterpret_cast<float*>(stages);  // [gate, up][row][column], when the stages are done with
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = ranks > 1 ? static_cast<int>(tc::cluster_rank()) : 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&s.full[i], 1);
+      ptx::mbar_init(&s.empty[i], 1);
+    }
+    ptx::mbar_init(&s.acc_full, 1);
+    ptx::mbar_fence_init();
+    s.gave_up = 0;
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, kTmemColumns);
+  if (threadIdx.x == kTmaWarp * 32) {
+    tc::tma_prefetch_map(&p.a);
+    tc::tma_prefetch_map(&p.b);
+  }
+  ptx::wait_prerequisites();
+  ptx::launch_dependents();
+  // Unit (expert, 32 of its rows) number u: the experts' rows are counted off until it is reached.
+  const unsigned cluster = blockIdx.x / ranks;
+  const int tile = static_cast<int>(cluster % p.n_tiles), u = static_cast<int>(cluster / p.n_tiles);
+  if (warp == 0) {
+    const int rows = static_cast<int>(p.rows);
+    int e_found = -1, lo_found = 0, hi_found = 0, before = 0;
+    for (int e0 = 0; e0 < p.E && e_found < 0; e0 += 32) {
+      const int e = e0 + lane;
+      int lo = 0, hi = e < p.E ? rows : 0;
+      if (p.offsets && e < p.E) {  // clamped: a damaged table cannot lead outside the buffers
+        lo = min(max(p.offsets[e], 0), rows);
+        hi = min(max(p.offsets[e + 1], lo), rows);
+      }
+      const int own = (hi - lo + kRows - 1) / kRows;
+      int sum = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      const int first = before + sum - own;
+      const unsigned here = __ballot_sync(0xffffffffu, u >= first && u < first + own);
+      if (here) {
+        const int from = __ffs(here) - 1;
+        e_found = e0 + from;
+        lo_found = __shfl_sync(0xffffffffu, lo + (u - first) * kRows, from);
+        hi_found = __shfl_sync(0xffffffffu, hi, from);
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+      s.unit[0] = e_found;
+      s.unit[1] = lo_found;
+      s.unit[2] = min(kRows, hi_found - lo_found);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const int e = s.unit[0], row0 = s.unit[1], rows = s.unit[2];
+  const uint32_t tmem = s.tmem, tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+  // This rank's part of the summed axis (the same in every CTA of the cluster whether there is a unit).
+  const int kblocks = (p.kc + kBlockK - 1) / kBlockK;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / ranks);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / ranks);
+  const int col0 = tile * kCols;
+
+  if (e >= 0) {
+    if (warp == kTmaWarp) {
+      bool ok = true;
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int st = it % kStages;
+        ok = it < kStages || tc::wait(&s.empty[st], (it / kStages - 1) & 1, &s.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t *w = stages + st * kStageBytes, *a = w + kStageBytes - kABytes;
+        if (tc::elect() && static_cast<uint32_t>(it) != p.test_drop) {
+          ptx::mbar_arrive_expect_tx(&s.full[st], kStageBytes);
+          const uint32_t bar = ptx::smem_addr(&s.full[st]);
+          const int k = kb * kBlockK;
+          if (kInput) {
+            tc::tma_load_3d(w, &p.b, col0, k, e, bar);
+            tc::tma_load_3d(w + kChunkBytes, &p.b, col0 + 64, k, e, bar);
+          } else {
+            tc::tma_load_3d(w, &p.b, k, col0, e, bar);
+            if (kGate) tc::tma_load_3d(w + kWBytes, &p.b, k, p.N + col0, e, bar);
+          }
+          tc::tma_load_2d(a, &p.a, k, row0, bar);
+        }
+        __syncwarp();
+      }
+      // Loads in flight write to this CTA's shared memory: it does not end before them.
+      const unsigned long long start = tc::now_ns();
+      for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
+        if (static_cast<uint32_t>(j) != p.test_drop) tc::settle(&s.full[j % kStages], (j / kStages) & 1, start);
+    } else if (warp == kMmaWarp) {
+      constexpr uint32_t kInstr = tc::instr_desc_bf16(kCols, kRows, kInput, false);
+      constexpr uint64_t kStepW = (kInput ? 2048 : 32) >> 4;
+      bool ok = true;
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int st = it % kStages;
+        ok = tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after();
+        const uint8_t* w_tile = stages + st * kStageBytes;
+        const uint64_t w = kInput ? tc::smem_desc_mn(w_tile) : tc::smem_desc(w_tile);
+        const uint64_t up = tc::smem_desc(w_tile + kWBytes);
+        const uint64_t a = tc::smem_desc(w_tile + kStageBytes - kABytes);
+        if (tc::elect()) {
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k) {
+            tc::mma_f16(tmem_u, w + kStepW * k, a + 2 * k, kInstr, kb > kb0 || k > 0);
+            if (kGate) tc::mma_f16(tmem_u + kRows, up + kStepW * k, a + 2 * k, kInstr, kb > kb0 || k > 0);
+          }
+          tc::commit(&s.empty[st]);
+        }
+        __syncwarp();
+      }
+      // Also where a wait gave up: nothing may be in flight when the CTA ends.
+      if (tc::elect()) tc::commit(&s.acc_full);
+      __syncwarp();
+      tc::settle(&s.acc_full, 0, tc::now_ns());
+    }
+  }
+  __syncthreads();
+  // Every load and product of this CTA is over.
+  tc::fence_after();
+  constexpr int kSums = kGate ? 2 : 1;
+  if (e >= 0 && warp < 4) {
+    float v[kSums][kRows];
+#pragma unroll
+    for (int h = 0; h < kSums; ++h)
+      tc::tmem_load_32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + h * kRows, reinterpret_cast<uint32_t*>(v[h]));
+    tc::wait_loads();
+#pragma unroll
+    for (int h = 0; h < kSums; ++h)
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (r < rows) sums[(h * kRows + r) * kPitch + threadIdx.x] = v[h][r];
+  }
+  tc::fence_before();
+  if (ranks > 1) tc::cluster_sync();
+  else __syncthreads();
+  tc::fence_after();
+  if (warp == kMmaWarp) tc::tmem_free(tmem, kTmemColumns);
+  if (threadIdx.x == 0 && s.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
+
+  if (e >= 0) {
+    // Column c, row r of out from its sum x (gate: and the up column's y).
+    const int64_t wide = static_cast<int64_t>(p.N);
+    auto finish = [&](int c, int r, float x, float y) {
+      const int64_t row = row0 + r, at = row * wide + c;
+      if (kInput) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+        const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(p.pre);
+        if (p.act == MOE_ACT_SWIGLU) {
+          const int64_t gate_at = row * 2 * wide + c, up_at = gate_at + wide;
+          float gate = __bfloat162float(pre[gate_at]), up = __bfloat162float(pre[up_at]);
+          swiglu_through(x, gate, up);
+          out[gate_at] = __float2bfloat16_rn(gate);
+          out[up_at] = __float2bfloat16_rn(up);
+        } else {
+          out[at] = __float2bfloat16_rn(
+              p.act == MOE_ACT_NONE ? x : act_through(p.act, x, __bfloat162float(pre[at])));
+        }
+        return;
+      }
+      if (p.bias) {
+        const int64_t b = static_cast<int64_t>(e) * p.bias_cols + c;
+        auto bias = [&](int64_t i) {
+          return p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + i)
+                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[i]);
+        };
+        x += bias(b);
+        if (kGate) y += bias(b + p.N);
+      }
+      if (p.pre) {
+        __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(p.pre);
+        if (kGate) {
+          pre[row * 2 * wide + c] = __float2bfloat16_rn(x);
+          pre[row * 2 * wide + wide + c] = __float2bfloat16_rn(y);
+        } else {
+          pre[at] = __float2bfloat16_rn(x);
+        }
+      }
+      x = kGate ? silu(x) * y : act_value(p.act, x);
+      if (p.residual) x += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[at]);
+      if (p.out_f32) static_cast<float*>(p.out)[at] = x;
+      else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+    };
+    // A rank's share: 128 / ranks columns of every row, four at a time.  (One loop for
+    // all: 32 rows unrolled were more code than the instruction cache takes, 4 us.)
+    const int part = kCols / ranks / 4;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < part * rows; i += kThreads) {
+      const int r = i / part, c = rank * (kCols / ranks) + i % part * 4;
+      float4 x[kSums][kMaxRanks];
+#pragma unroll
+      for (int h = 0; h < kSums; ++h) {
+        const float* from = sums + (h * kRows + r) * kPitch + c;
+#pragma unroll
+        for (int q = 0; q < kMaxRanks; ++q)
+          if (q < ranks)
+            x[h][q] = ranks > 1 ? ld_rank_v4(from, q) : *reinterpret_cast<const float4*>(from);
+      }
+#pragma unroll
+      for (int h = 0; h < kSums; ++h)
+#pragma unroll
+        for (int q = 1; q < kMaxRanks; ++q)
+          if (q < ranks) {
+            x[h][0].x += x[h][q].x;
+            x[h][0].y += x[h][q].y;
+            x[h][0].z += x[h][q].z;
+            x[h][0].w += x[h][q].w;
+          }
+      if (col0 + c >= p.N) continue;  // N is a multiple of 8
+      const float4 g = x[0][0], u = x[kSums - 1][0];
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j)
+        finish(col0 + c + j, r, j == 0 ? g.x : j == 1 ? g.y : j == 2 ? g.z : g.w,
+               j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w);
+    }
+  }
+  if (ranks > 1) tc::cluster_sync();  // no CTA leaves while its shared memory is being read
+}
+
+template <bool kInput, bool kGate>
+cudaError_t launch(const LinearParams& p, int ranks, cudaStream_t stream) {
+  const size_t smem = 1024 + static_cast<size_t>(stage_count(kGate)) * stage_bytes(kGate);
+  auto* kernel = few_linear_kernel<kInput, kGate>;
+  cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(few_linear_units(p.rows, p.E) * p.n_tiles * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ranks);
+}
+
+}  // namespace
+
+cudaError_t launch_few_linear(const LinearParams& p, bool input, bool gate, int ranks, cudaStream_t stream) {
+  if (input) return launch<true, false>(p, ranks, stream);
+  return gate ? launch<false, true>(p, ranks, stream) : launch<false, false>(p, ranks, stream);
+}
+
+}  // namespace moe

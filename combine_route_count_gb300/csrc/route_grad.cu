@@ -54,6 +54,7 @@ template <int KMAX, bool kDots>
 __global__ void __launch_bounds__(kMaxWarps * 32) combine_grad_kernel(CombineGradParams p, int group) {
   __shared__ float s_dot[kMaxWarps][KMAX];
   ptx::wait_prerequisites();
+  ptx::launch_dependents();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / group) + threadIdx.x / group;
   const int K = p.K, at = threadIdx.x % group;
   if (t >= p.T) return;  // only in blocks of several tokens: one-warp groups
@@ -136,6 +137,7 @@ constexpr int kSumThreads = 256;
 template <int KMAX>
 __global__ void __launch_bounds__(kSumThreads) dispatch_grad_kernel(DispatchGradParams p) {
   ptx::wait_prerequisites();
+  ptx::launch_dependents();
   const int K = p.K;
   const int64_t chunks = p.H / 8;
   const int64_t g = static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x;

@@ -95,6 +95,7 @@ __device__ __forceinline__ void softmax_stats(const float (&z)[N], int lane, int
 template <class T, int N, bool kSigmoid, bool kNormalize, bool kBias>
 __global__ void __launch_bounds__(kWarps * 32) router_kernel(RouterParams p) {
   ptx::wait_prerequisites();
+  ptx::launch_dependents();
   const int lane = threadIdx.x & 31, E = p.E, K = p.K;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= p.T) return;
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32) router_kernel(RouterParams p) {
 template <class T, int N, bool kSigmoid, bool kNormalize>
 __global__ void __launch_bounds__(kWarps * 32) router_grad_kernel(RouterParams p) {
   ptx::wait_prerequisites();
+  ptx::launch_dependents();
   const int lane = threadIdx.x & 31, E = p.E, K = p.K;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= p.T) return;

@@ -60,6 +60,35 @@ bool product_ok(int64_t rows, int32_t n, int32_t k, int32_t E, const int32_t* of
 
 int32_t tiles(int32_t n, int32_t tile) { return (n + tile - 1) / tile; }
 
+// Which kernel a product takes, from what the host knows: the mean of the experts' rows.
+//
+// Tiles by pairs of CTAs (256 x 256, half the operand traffic of two tiles of 128 x
+// 256) from a mean of 256 rows an expert on; below it half of such a tile is empty.  us,
+// single CTAs / pairs, N = K = 4096 but where said:
+//   forward  8 experts: 50.1 / 53.5 at a mean of 128, 62.5 / 56.4 at 256, 173 / 149 at
+//            1024; 64 experts, N 2816, K 2048, swiglu: 125 / 136 at 128, 159 / 147 at
+//            256, under a skewed router 186 / 188; 1 expert: 162 / 143 at 8192 rows
+//   by rows  8 experts 65.7 / 58.0 at 256; K 8192, swiglu: 414 / 343 at 1024
+//   by weights  1 expert: 11.2 / 12.1 at 128 rows, 29.2 / 26.6 at 1024, 227 / 165 at
+//            8192; 256 experts, N = K = 2048: 363 / 446 at 128 (bound by what it writes)
+bool takes_pairs(int64_t rows, int32_t E) { return rows >= 256 * static_cast<int64_t>(E); }
+
+// CTAs that share a tile of the few-row kernel; 0: not the few-row kernel.  It is
+// for calls whose tiles leave most SMs without work: two or more of its CTAs a tile fit on
+// the GPU at once.  us, tile kernel / 1 / 2 / 4 / 8 CTAs a tile of 128 columns (56 of them
+// for N 7168; few_linear_units times that many for the rows):
+//   N 7168, K 2048: 15.8 / 11.6 / 10.8 / 10.3 / 14.4 at 1 row (224 CTAs of 4), 15.8 / 15.9 /
+//   12.9 / 12.8 / 19.0 at 32, 15.8 / 16.0 / 13.4 / 18.9 / 29 at 64, 16.4 / 16.6 / 24 / 32 /
+//   46 at 128; N 2048, K 7168: 41 / 27 / 17.6 / 12.6 / 11.2 at 16; N 512, K 8192: 43 / 30 /
+//   18 / 12.0 / 9.1 at 32; E 8, N = K = 1024: 10.9 / 9.5 / 8.7 / 8.6 / 13.7 at 64 rows,
+//   10.9 / 13.3 / 11.7 / 18 / 30 at 512; E 64, N 2816, K 2048: 115 / 112 / 116 / 123 at 256
+int few_ranks(int64_t rows, int32_t E, int32_t cols, int32_t kc, int sms) {
+  const int64_t all = moe::few_linear_units(rows, E) * tiles(cols, 128);
+  int ranks = 1;
+  while (ranks < 8 && all * ranks * 2 <= 2 * sms && ranks * 2 <= tiles(kc, 64)) ranks *= 2;
+  return all * 4 <= 2 * sms || ranks > 1 ? ranks : 0;
+}
+
 }  // namespace
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -182,8 +211,9 @@ MOE_API int moe_expert_linear(const void* a, int64_t rows, int32_t k, const void
   return guarded([&] {
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    const int ranks = few_ranks(rows, num_experts, glu ? n / 2 : n, k, sms);
     moe::LinearParams p = {};
-    if (!encode_rows(&p.a, a, rows, k, 128) || !encode_weights(&p.b, w, num_experts, n, k, 128))
+    if (!encode_rows(&p.a, a, rows, k, ranks > 0 ? moe::kFewLinearRows : 128) || !encode_weights(&p.b, w, num_experts, n, k, 128))
       return static_cast<int>(MOE_ECUDA);
     p.offsets = expert_offsets;
     p.bias = bias;
@@ -193,14 +223,16 @@ MOE_API int moe_expert_linear(const void* a, int64_t rows, int32_t k, const void
     p.status = status;
     p.rows = rows;
     p.N = glu ? n / 2 : n;
-    p.n_tiles = tiles(p.N, moe::linear_n_tile(glu));
+    p.n_tiles = tiles(p.N, ranks > 0 ? 128 : moe::linear_n_tile(glu));
     p.kc = k;
     p.E = num_experts;
     p.act = activation;
     p.bias_cols = n;
     p.bias_f32 = bias_type == MOE_TYPE_F32;
+    p.out_f32 = out_type == MOE_TYPE_F32;
     p.test_drop = moe::test_drop();
-    return launched(moe::launch_linear(p, glu, out_type == MOE_TYPE_F32, sms, static_cast<cudaStream_t>(stream)));
+    if (ranks > 0) return launched(moe::launch_few_linear(p, false, glu, ranks, static_cast<cudaStream_t>(stream)));
+    return launched(moe::launch_linear(p, glu, out_type == MOE_TYPE_F32, takes_pairs(rows, num_experts), sms, static_cast<cudaStream_t>(stream)));
   });
 }
 
@@ -216,8 +248,9 @@ MOE_API int moe_expert_linear_backward_input(const void* dy, int64_t rows, int32
   return guarded([&] {
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
+    const int ranks = few_ranks(rows, num_experts, k, n, sms);
     moe::LinearParams p = {};
-    if (!encode_rows(&p.a, dy, rows, n, 128) || !encode_weights(&p.b, w, num_experts, n, k, 64))
+    if (!encode_rows(&p.a, dy, rows, n, ranks > 0 ? moe::kFewLinearRows : 128) || !encode_weights(&p.b, w, num_experts, n, k, 64))
       return static_cast<int>(MOE_ECUDA);
     p.offsets = expert_offsets;
     p.pre = const_cast<void*>(pre);
@@ -225,12 +258,13 @@ MOE_API int moe_expert_linear_backward_input(const void* dy, int64_t rows, int32
     p.status = status;
     p.rows = rows;
     p.N = k;
-    p.n_tiles = tiles(k, moe::linear_n_tile(false));
+    p.n_tiles = tiles(k, ranks > 0 ? 128 : moe::linear_n_tile(false));
     p.kc = n;
     p.E = num_experts;
     p.act = activation;
     p.test_drop = moe::test_drop();
-    return launched(moe::launch_linear_input(p, activation == MOE_ACT_SWIGLU, sms, static_cast<cudaStream_t>(stream)));
+    if (ranks > 0) return launched(moe::launch_few_linear(p, true, false, ranks, static_cast<cudaStream_t>(stream)));
+    return launched(moe::launch_linear_input(p, activation == MOE_ACT_SWIGLU, takes_pairs(rows, num_experts), sms, static_cast<cudaStream_t>(stream)));
   });
 }
 
@@ -256,6 +290,7 @@ MOE_API int moe_expert_linear_backward_weight(const void* dy, int64_t rows, int3
     moe::LinearParams p = {};
     if (!encode_rows(&p.a, dy, rows, n, 64) || !encode_rows(&p.b, a, rows, k, 64)) return static_cast<int>(MOE_ECUDA);
     p.offsets = expert_offsets;
+    const bool pair = takes_pairs(rows, num_experts);
     p.out = dw;
     p.db = db;
     p.status = status;
@@ -263,10 +298,10 @@ MOE_API int moe_expert_linear_backward_weight(const void* dy, int64_t rows, int3
     p.N = k;
     p.n_tiles = tiles(k, moe::linear_n_tile(false));
     p.M = n;
-    p.m_tiles = tiles(n, moe::linear_m_tile());
+    p.m_tiles = tiles(n, moe::linear_m_tile(pair));
     p.E = num_experts;
     p.accumulate = accumulate != 0;
     p.test_drop = moe::test_drop();
-    return launched(moe::launch_linear_weight(p, dw_type == MOE_TYPE_F32, sms, on));
+    return launched(moe::launch_linear_weight(p, dw_type == MOE_TYPE_F32, pair, sms, on));
   });
 }

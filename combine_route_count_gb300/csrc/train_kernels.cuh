@@ -66,13 +66,22 @@ struct LinearParams {
   int32_t M, m_tiles;        // weight: rows of an expert's matrix
   int32_t kc;                // length of the summed axis (weight: the expert's rows instead)
   int32_t E, act, bias_cols;
-  bool bias_f32, accumulate;
+  bool bias_f32, out_f32, accumulate;
   uint32_t test_drop;        // the number of a load that each CTA leaves out; UINT32_MAX: none
 };
 int linear_n_tile(bool glu);  // columns of out that one tile covers
-int linear_m_tile();
-cudaError_t launch_linear(const LinearParams& p, bool glu, bool f32, int sms, cudaStream_t stream);
-cudaError_t launch_linear_input(const LinearParams& p, bool glu, int sms, cudaStream_t stream);
-cudaError_t launch_linear_weight(const LinearParams& p, bool f32, int sms, cudaStream_t stream);
+int linear_m_tile(bool pair);
+cudaError_t launch_linear(const LinearParams& p, bool glu, bool f32, bool pair, int sms, cudaStream_t stream);
+cudaError_t launch_linear_input(const LinearParams& p, bool glu, bool pair, int sms, cudaStream_t stream);
+cudaError_t launch_linear_weight(const LinearParams& p, bool f32, bool pair, int sms, cudaStream_t stream);
+
+// The same for few rows (forward, input): a in boxes of 64 x kFewLinearRows, n_tiles
+// of 128 columns, the summed axis split over `ranks` CTAs (1, 2, 4 or 8).
+constexpr int kFewLinearRows = 32;
+// The most groups of up to kFewLinearRows rows that E experts' rows can make.
+inline int64_t few_linear_units(int64_t rows, int32_t E) {
+  return (rows < E ? rows : E) + rows / kFewLinearRows;
+}
+cudaError_t launch_few_linear(const LinearParams& p, bool input, bool gate, int ranks, cudaStream_t stream);
 
 }  // namespace moe
