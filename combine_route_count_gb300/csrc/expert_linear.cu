@@ -16,7 +16,8 @@
 // holds half of either operand, 6 stages of 32 KiB, so that a product of 256 x 256 x 64
 // takes 64 KiB out of L2 instead of 96.  12 warps: eight for the epilogue (two
 // groups of four, each with half of the columns), one for TMA, one for the matrix
-// instructions, two for the bias gradient.  A tile's sum stays in tensor memory:
+// instructions, two for the bias gradient, which they sum from memory (from L2: the
+// tiles read the same rows; 3 % more time than without).  A tile's sum stays in tensor memory:
 // two buffers of 256 columns, so that one tile's epilogue runs under the next
 // one's products.
 //
@@ -28,7 +29,9 @@
 //
 // What bounds it: at many rows the tensor cores.  8192 rows, N = K = 4096: forward 143
 // us, 1923 TFLOP/s, what a library's plain product takes in a burst (single CTAs 162);
-// by rows 153, by weights 165.  At few rows an expert the weights' bytes.
+// by rows 142, by weights 157.  Call after call the power limit holds the SMs at 1350 to
+// 1700 MHz, and these times grow by a tenth to a fifth.  At few rows an expert the bytes
+// of the weights.
 //
 // Tiles are dealt out statically (tile b, b+G, ...).  Waits are bounded (2 s) and
 // report MOE_ETIMEDOUT.
@@ -36,6 +39,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -64,12 +68,12 @@ constexpr int kMaxStages = 6;
 constexpr int kEpilogueWarps = 8;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kBiasWarp = 10;
 constexpr int kThreads = 384;
+constexpr int kLoads = 24;  // of a lane of the bias warps on their way: under load one takes microseconds
 constexpr uint32_t kTmemColumns = 512;
 constexpr int kUnit = 64;  // columns that an epilogue warp works on at a time
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t consumed[kMaxStages];   // bias gradient: the products have read the stage
   uint64_t tail_full[kMaxStages];  // pair, second CTA: its half of an expert's last stage is there
   uint64_t tail_clear[kMaxStages]; // pair, first CTA: and ends in zeros
   uint64_t acc_full[2], acc_empty[2];
@@ -90,37 +94,43 @@ struct Tile {
   int k0, kc;      // the summed axis: where it begins, how long it is
 };
 
+// Tiles are counted in 32 bits (the host refuses calls with more): with 64-bit
+// divisions, finding a tile took the loading and the issuing warp about 1000 cycles.
 template <Mode kMode>
-__device__ __forceinline__ int64_t tile_count(const Groups& g, const LinearParams& p) {
-  if (kMode == kWeight) return static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles;
-  return static_cast<int64_t>(g.start[p.E]) * p.n_tiles;
+__device__ __forceinline__ uint32_t tile_count(const Groups& g, const LinearParams& p) {
+  if (kMode == kWeight) return static_cast<uint32_t>(p.E) * p.m_tiles * p.n_tiles;
+  return static_cast<uint32_t>(g.start[p.E]) * p.n_tiles;
 }
 
 // Row tile (returned) and column tile of an expert's tile number t.  Bands of 2048
 // rows, inside a band rows fastest: the tiles at work at one time cover about as many
 // rows as columns, which share the operands in L2.  (All of 8192 rows first: 203 us
 // instead of 153 for the gradient by rows, N = K = 4096, whose weights were then read in
-// strips of a few hundred bytes.)
+// strips of a few hundred bytes.)  The gradient by weights has its bands along the
+// columns, so that whole rows of dw are written at a time: 170 us / 157 with N = K = 4096,
+// 440 / 370 where the writes are all (256 experts of 128 rows, N = K = 2048).
 template <int kRows>
-__device__ __forceinline__ int place(int64_t t, int m_tiles, int n_tiles, int& n) {
-  constexpr int kBand = 2048 / kRows;
-  const int band = static_cast<int>(t / (static_cast<int64_t>(kBand) * n_tiles));
-  const int height = min(kBand, m_tiles - band * kBand);
-  const int in_band = static_cast<int>(t - static_cast<int64_t>(band) * kBand * n_tiles);
-  n = in_band / height;
-  return band * kBand + in_band - n * height;
+__device__ __forceinline__ int place(uint32_t t, uint32_t m_tiles, uint32_t n_tiles, int& n) {
+  constexpr uint32_t kBand = 2048 / kRows;
+  const uint32_t band = t / kBand / n_tiles;
+  const uint32_t height = min(kBand, m_tiles - band * kBand);
+  const uint32_t in_band = t - band * kBand * n_tiles;
+  const uint32_t column = height == kBand ? in_band / kBand : in_band / height;
+  n = static_cast<int>(column);
+  return static_cast<int>(band * kBand + in_band - column * height);
 }
 
 // What CTA `rank` of a pair has of tile t (rank 0: of a CTA alone).  Rows may be none.
 template <Mode kMode, bool kPair>
-__device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p, int64_t t, int rank) {
+__device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p, uint32_t t, int rank) {
   constexpr int kRows = kPair ? 2 * kTileM : kTileM;
   Tile r;
   if (kMode == kWeight) {
-    const int64_t per = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+    const uint32_t per = static_cast<uint32_t>(p.m_tiles) * p.n_tiles;
     r.e = static_cast<int>(t / per);
-    const int64_t local = t - r.e * per;
-    const int m = place<kRows>(local, p.m_tiles, p.n_tiles, r.n);
+    const uint32_t local = t - r.e * per;
+    int m;
+    r.n = place<kTileN>(local, p.n_tiles, p.m_tiles, m);  // bands of 2048 columns, columns fastest
     r.row0 = m * kRows + rank * kTileM;
     r.rows = min(kTileM, p.M - r.row0);
     r.k0 = g.lo[r.e];
@@ -130,11 +140,11 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p
   int lo = 0, hi = p.E;  // largest e with start[e] * n_tiles <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(g.start[mid]) * p.n_tiles <= t) lo = mid;
+    if (static_cast<uint32_t>(g.start[mid]) * p.n_tiles <= t) lo = mid;
     else hi = mid;
   }
   const int m_tiles = g.start[lo + 1] - g.start[lo];
-  const int64_t local = t - static_cast<int64_t>(g.start[lo]) * p.n_tiles;
+  const uint32_t local = t - static_cast<uint32_t>(g.start[lo]) * p.n_tiles;
   r.e = lo;
   r.row0 = g.lo[lo] + place<kRows>(local, m_tiles, p.n_tiles, r.n) * kRows + rank * kTileM;
   r.rows = min(kTileM, g.hi[lo] - r.row0);
@@ -367,15 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   g.hi = g.lo + p.E;
   g.start = g.hi + p.E;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const bool bias_grad = kMode == kWeight && p.db;
   const int rank = kPair ? tc::cluster_rank() : 0;
-  const int64_t first_tile = kPair ? blockIdx.x / 2 : blockIdx.x, tile_step = kPair ? gridDim.x / 2 : gridDim.x;
+  const uint32_t first_tile = kPair ? blockIdx.x / 2 : blockIdx.x, tile_step = kPair ? gridDim.x / 2 : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
-      ptx::mbar_init(&s.empty[i], bias_grad ? 2 : 1);
-      ptx::mbar_init(&s.consumed[i], 1);
+      ptx::mbar_init(&s.empty[i], 1);
       ptx::mbar_init(&s.tail_full[i], 1);
       ptx::mbar_init(&s.tail_clear[i], 1);
     }
@@ -429,16 +437,22 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   if (kPair) tc::cluster_sync();  // the other CTA's barriers are ready too
   else __syncthreads();
   tc::fence_after();
-  const int64_t tiles = tile_count<kMode>(g, p);
+  const uint32_t tiles = tile_count<kMode>(g, p);
   const uint32_t tmem = s.tmem, tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
 
   if (warp == kTmaWarp) {
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-      const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
+    Tile next;
+    if (first_tile < tiles) next = find_tile<kMode, kPair>(g, p, first_tile, rank);
+    for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const Tile tile = next;
       const int kblocks = blocks_of(tile.kc);
+      // The next tile is looked for while this one's first loads are on their way.
+      const int look = min(1, kblocks - 1);
+      if (kblocks == 0 && t + tile_step < tiles) next = find_tile<kMode, kPair>(g, p, t + tile_step, rank);
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        if (kb == look && t + tile_step < tiles) next = find_tile<kMode, kPair>(g, p, t + tile_step, rank);
         const int st = it % kStages;
         ok = it < kStages || tc::wait(&s.empty[st], (it / kStages - 1) & 1, &s.gave_up);
         ok = __all_sync(0xffffffffu, ok);
@@ -491,8 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         tc::instr_desc_bf16(kPair ? 2 * kTileM : kTileM, kTileN, kMode == kWeight, kMode != kForward);
     uint32_t it = 0, round = 0, tails = 0;  // tails: parity of tail_clear, a bit a stage
     bool ok = true;
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-      const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
+    for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
+      Tile tile;
+      tile.kc = p.kc;
+      if (kMode == kWeight) tile = find_tile<kMode, kPair>(g, p, t, rank);
       const int kblocks = blocks_of(tile.kc);
       if (kblocks == 0) continue;
       const int buf = round & 1;
@@ -527,14 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
             if (kPair) tc::mma_f16_pair(d, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
             else tc::mma_f16(d, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
           }
-          // A stage is free when the products have read it, in the first column tile when the
-          // bias warps have after them; else their two arrivals are made here.
-          const bool bias_next = bias_grad && tile.n == 0;
-          for (int i = 0; i < (bias_grad && !bias_next ? 2 : 1); ++i) {
-            uint64_t* read = bias_next ? &s.consumed[st] : &s.empty[st];
-            if (kPair) tc::commit_pair(read);
-            else tc::commit(read);
-          }
+          if (kPair) tc::commit_pair(&s.empty[st]);
+          else tc::commit(&s.empty[st]);
           if (kb == kblocks - 1) {
             if (kPair) tc::commit_pair(&s.acc_full[buf]);
             else tc::commit(&s.acc_full[buf]);
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     if (kMode == kWeight) {
       uint32_t it = 0, tails = 0;
       bool ok = true;
-      for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
         const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
         it += blocks_of(tile.kc);
         if (tile.kc % kBlockK == 0) continue;
@@ -572,51 +582,52 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     }
     tc::settle(&s.drained, 0, tc::now_ns());
   } else if (warp >= kBiasWarp) {
-    if (bias_grad) {
-      const int c = warp - kBiasWarp;  // 64 columns of dy
-      uint32_t it = 0, reads = 0;      // reads: parity of consumed, a bit a stage
-      bool ok = true;
-      for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-        const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
-        const int kblocks = blocks_of(tile.kc);
-        if (tile.n != 0) {
-          it += kblocks;
-          continue;
-        }
-        float sum0 = 0.0f, sum1 = 0.0f;
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
-          const int st = it % kStages;
-          // A pair's second CTA is not told that its loads are there, but that they were read.
-          ok = kPair ? tc::wait_cluster(&s.consumed[st], (reads >> st) & 1, &s.gave_up)
-                     : tc::wait(&s.consumed[st], (reads >> st) & 1, &s.gave_up);
-          reads ^= 1u << st;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint8_t* a = stages + st * kStageBytes + c * kChunkBytes;
-          const int rows = min(kBlockK, tile.kc - kb * kBlockK);
-          float part0 = 0.0f, part1 = 0.0f;
-#pragma unroll 8
-          for (int r = 0; r < rows; ++r) {
-            const uint32_t v =
-                *reinterpret_cast<const uint32_t*>(a + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-            part0 += bf_lo(v);
-            part1 += bf_hi(v);
+    if (kMode == kWeight && p.db) {
+      // An expert's 128 columns of dy a CTA at a time, 64 a warp, a lane 8 of them in
+      // every fourth row.
+      const int piece = lane & 7, first = lane >> 3;
+      const uint32_t blocks = (p.M + 127) / 128, units = blocks * p.E;
+      for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int e = static_cast<int>(u / blocks);
+        const int col = static_cast<int>(u - e * blocks) * 128 + (warp - kBiasWarp) * 64 + piece * 8;
+        const int rows = g.hi[e] - g.lo[e];
+        if (p.accumulate && rows == 0) continue;
+        const uint8_t* from = p.dy + (static_cast<int64_t>(g.lo[e]) * p.M + col) * 2;
+        const int64_t stride = static_cast<int64_t>(p.M) * 2;
+        const bool some = col < p.M;  // M is a multiple of 8
+        float sum[8] = {};
+        for (int r0 = 0; r0 < rows; r0 += 4 * kLoads) {
+          uint4 v[kLoads];
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            const int r = r0 + 4 * i + first;
+            v[i] = some && r < rows ? ptx::ld_stream_v4(from + r * stride) : make_uint4(0, 0, 0, 0);
           }
-          sum0 += part0;
-          sum1 += part1;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.empty[st]);
-        }
-        const int col = tile.row0 + c * 64 + lane * 2;
-        if (ok && col < p.M) {  // M is a multiple of 8
-          float2* to = reinterpret_cast<float2*>(p.db + static_cast<int64_t>(tile.e) * p.M + col);
-          float2 v = make_float2(sum0, sum1);
-          if (p.accumulate) {
-            const float2 old = *to;
-            v.x += old.x;
-            v.y += old.y;
+          float part[8] = {};
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            part[0] += bf_lo(v[i].x), part[1] += bf_hi(v[i].x), part[2] += bf_lo(v[i].y), part[3] += bf_hi(v[i].y);
+            part[4] += bf_lo(v[i].z), part[5] += bf_hi(v[i].z), part[6] += bf_lo(v[i].w), part[7] += bf_hi(v[i].w);
           }
-          *to = v;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] += part[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
+        }
+        if (first == 0 && some) {
+          float4* to = reinterpret_cast<float4*>(p.db + static_cast<int64_t>(e) * p.M + col);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float4 v = make_float4(sum[4 * h], sum[4 * h + 1], sum[4 * h + 2], sum[4 * h + 3]);
+            if (p.accumulate) {
+              const float4 old = to[h];
+              v.x += old.x, v.y += old.y, v.z += old.z, v.w += old.w;
+            }
+            to[h] = v;
+          }
         }
       }
     }
@@ -625,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     const uint32_t lanes = tmem + (static_cast<uint32_t>(sub) << 16);
     uint32_t round = 0;
     bool ok = true;
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+    for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
       const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
       const bool some = sub < tile.rows;
       const bool sums = blocks_of(tile.kc) > 0;
@@ -813,6 +824,7 @@ cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
   const int64_t m_tiles = kMode == kWeight ? static_cast<int64_t>(p.E) * p.m_tiles
                                            : (p.rows + kRows - 1) / kRows + (p.offsets ? p.E : 0);
   const int64_t tiles = m_tiles * p.n_tiles;
+  if (tiles > INT_MAX) return cudaErrorInvalidValue;
   if (!kPair)
     return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads), smem, stream,
                          true, p);

@@ -69,7 +69,7 @@ int32_t tiles(int32_t n, int32_t tile) { return (n + tile - 1) / tile; }
 //            1024; 64 experts, N 2816, K 2048, swiglu: 125 / 136 at 128, 159 / 147 at
 //            256, under a skewed router 186 / 188; 1 expert: 162 / 143 at 8192 rows
 //   by rows  8 experts 65.7 / 58.0 at 256; K 8192, swiglu: 414 / 343 at 1024
-//   by weights  1 expert: 11.2 / 12.1 at 128 rows, 29.2 / 26.6 at 1024, 227 / 165 at
+//   by weights  1 expert: 11.2 / 12.1 at 128 rows, 29.2 / 26.6 at 1024, 183 / 160 at
 //            8192; 256 experts, N = K = 2048: 363 / 446 at 128 (bound by what it writes)
 bool takes_pairs(int64_t rows, int32_t E) { return rows >= 256 * static_cast<int64_t>(E); }
 
@@ -292,6 +292,7 @@ MOE_API int moe_expert_linear_backward_weight(const void* dy, int64_t rows, int3
     p.offsets = expert_offsets;
     const bool pair = takes_pairs(rows, num_experts);
     p.out = dw;
+    p.dy = static_cast<const uint8_t*>(dy);
     p.db = db;
     p.status = status;
     p.rows = rows;

@@ -59,6 +59,7 @@ struct LinearParams {
   void* residual;            // forward: bf16 [rows, N] or null
   void* pre;                 // forward: bf16 [rows, N], glu [rows, 2N], written, or null; input: read
   void* out;                 // forward: [rows, N]; input: bf16 [rows, N], glu [rows, 2N]; weight: [E, M, N]
+  const uint8_t* dy;         // weight: as in a, for db
   float* db;                 // weight: [E, M] or null
   int32_t* status;           // may be null
   int64_t rows;
