@@ -14,7 +14,9 @@
 // KiB by tiled TMA (128-byte swizzle).  With many rows an expert two CTAs (a cluster)
 // share a tile of 256 x 256: one issues the products of both (cta_group::2), each
 // holds half of either operand, 6 stages of 32 KiB, so that a product of 256 x 256 x 64
-// takes 64 KiB out of L2 instead of 96.  12 warps: eight for the epilogue (two
+// takes 64 KiB out of L2 instead of 96.  Where there are few tiles and a long summed axis,
+// up to 8 CTAs (a cluster) split the axis of one tile, read one another's sums through
+// distributed shared memory and each finish a part of the tile.  12 warps: eight for the epilogue (two
 // groups of four, each with half of the columns), one for TMA, one for the matrix
 // instructions, two for the bias gradient, which they sum from memory (from L2: the
 // tiles read the same rows; 3 % more time than without).  A tile's sum stays in tensor memory:
@@ -56,6 +58,8 @@ namespace {
 using namespace lin;
 
 enum Mode { kForward, kInput, kWeight };
+// Who works on a tile: one CTA, a pair of them, or several that split the summed axis.
+enum Team { kAlone, kPairs, kSplit };
 
 constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;  // kTileM: rows of one CTA
 constexpr int kABytes = kTileM * kBlockK * 2;
@@ -71,6 +75,8 @@ constexpr int kThreads = 384;
 constexpr int kLoads = 24;  // of a lane of the bias warps on their way: under load one takes microseconds
 constexpr uint32_t kTmemColumns = 512;
 constexpr int kUnit = 64;  // columns that an epilogue warp works on at a time
+constexpr int kMaxSplit = 8;
+constexpr int kPitch = kTileN + 4;  // floats from one row's sums to the next, where they are split
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -154,6 +160,10 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p
 }
 
 __device__ __forceinline__ int blocks_of(int kc) { return (kc + kBlockK - 1) / kBlockK; }
+// Where share `part` of `parts` of them begins.
+__device__ __forceinline__ int share(int kblocks, int part, int parts) {
+  return parts == 1 ? part * kblocks : static_cast<int>(static_cast<int64_t>(kblocks) * part / parts);
+}
 
 // ---- rows in and out of the epilogue ------------------------------------------
 // A lane holds 128 bytes of its own row; four lanes move 128 bytes of one row
@@ -337,6 +347,116 @@ __device__ __forceinline__ void add_bias(const LinearParams& p, int64_t first, i
   }
 }
 
+// What becomes of a tile's sums: this warp's 32 rows (from sub on) and half of the
+// columns.  load(column, v, last) gets 64 of them; it is called for all of them even where
+// the warp has no rows (some is false), but not where there are no sums (any is false:
+// zeros).
+template <Mode kMode, bool kGlu, bool kF32, class Load>
+__device__ __forceinline__ void epilogue(const LinearParams& p, const Tile& tile, int half, int sub, int lane, bool any,
+                                         bool some, Load&& load) {
+  const int rows = tile.rows - sub;
+  const int64_t row = tile.row0 + sub;
+  if constexpr (kMode == kForward && kGlu) {
+    const int col = tile.n * (kTileN / 2) + half * kUnit;
+    const int64_t first = static_cast<int64_t>(tile.e) * p.bias_cols;
+    float v[kUnit], up[kUnit];
+    load(half * kUnit, v, false);
+    load(kTileN / 2 + half * kUnit, up, true);
+    if (!some || col >= p.N) return;
+    if (p.bias) {
+      add_bias(p, first, col, v);
+      add_bias(p, first, p.N + col, up);
+    }
+    if (p.pre) {
+      const int64_t stride = static_cast<int64_t>(p.N) * 4;
+      Rows r = rows_at(p.pre, row, stride, static_cast<int64_t>(col) * 2, rows, lane);
+      const int left = min(32, (p.N - col) * 2 - (lane & 3) * 32);  // the first half ends where the second begins
+      r.left = left;
+      store_bf16(r, v, lane);
+      r = rows_at(p.pre, row, stride, static_cast<int64_t>(p.N + col) * 2, rows, lane);
+      r.left = left;
+      store_bf16(r, up, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = silu(v[i]) * up[i];
+    if (p.residual) {
+      load_bf16(rows_at(p.residual, row, static_cast<int64_t>(p.N) * 2, static_cast<int64_t>(col) * 2, rows, lane), up,
+                lane);
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) v[i] += up[i];
+    }
+    constexpr int kSize = kF32 ? 4 : 2;
+    const Rows r =
+        rows_at(p.out, row, static_cast<int64_t>(p.N) * kSize, static_cast<int64_t>(col) * kSize, rows, lane);
+    if (kF32) store_f32(r, v, lane, static_cast<int64_t>(p.N - col) * 4);
+    else store_bf16(r, v, lane);
+  } else {
+#pragma unroll 1
+    for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
+      const int col = tile.n * kTileN + half * (kTileN / 2) + q * kUnit;
+      float v[kUnit] = {};
+      if (any) load(half * (kTileN / 2) + q * kUnit, v, q == kTileN / 2 / kUnit - 1);
+      if (!some || col >= p.N) continue;
+      const int64_t byte = static_cast<int64_t>(col) * 2, stride = static_cast<int64_t>(p.N) * 2;
+      if (kMode == kForward) {
+        if (p.bias) add_bias(p, static_cast<int64_t>(tile.e) * p.bias_cols, col, v);
+        if (p.pre) store_bf16(rows_at(p.pre, row, stride, byte, rows, lane), v, lane);
+        activate(p.act, v);
+        if (p.residual) {
+          float more[kUnit];
+          load_bf16(rows_at(p.residual, row, stride, byte, rows, lane), more, lane);
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) v[i] += more[i];
+        }
+        if (kF32) store_f32(rows_at(p.out, row, 2 * stride, 2 * byte, rows, lane), v, lane, 2 * (stride - byte));
+        else store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
+      } else if (kMode == kInput && !kGlu) {
+        if (p.act != MOE_ACT_NONE) {
+          float pre[kUnit];
+          load_bf16(rows_at(p.pre, row, stride, byte, rows, lane), pre, lane);
+          through(p.act, v, pre);
+        }
+        store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
+      } else if (kMode == kInput) {
+        Rows at = rows_at(p.pre, row, 2 * stride, byte, rows, lane);
+        const Rows at_up = rows_at(p.pre, row, 2 * stride, stride + byte, rows, lane);
+        at.left = at_up.left;  // the row's first half ends where the second begins
+        float gate[kUnit], up[kUnit];
+        load_bf16(at, gate, lane);
+        load_bf16(at_up, up, lane);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) swiglu_through(v[i], gate[i], up[i]);
+        Rows to = rows_at(p.out, row, 2 * stride, byte, rows, lane);
+        to.left = at.left;
+        store_bf16(to, gate, lane);
+        store_bf16(rows_at(p.out, row, 2 * stride, stride + byte, rows, lane), up, lane);
+      } else {
+        if (p.accumulate && !any) continue;
+        const int64_t out_row = static_cast<int64_t>(tile.e) * p.M + row;
+        if (kF32) {
+          const Rows at = rows_at(p.out, out_row, 2 * stride, 2 * byte, rows, lane);
+          if (p.accumulate) {
+            float old[kUnit];
+            load_f32(at, old, lane, 2 * (stride - byte));
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) v[i] += old[i];
+          }
+          store_f32(at, v, lane, 2 * (stride - byte));
+        } else {
+          const Rows at = rows_at(p.out, out_row, stride, byte, rows, lane);
+          if (p.accumulate) {
+            float old[kUnit];
+            load_bf16(at, old, lane);
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) v[i] += old[i];
+          }
+          store_bf16(at, v, lane);
+        }
+      }
+    }
+  }
+}
+
 template <bool kPair>
 __device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   if (kPair) tc::tma_load_2d_pair(dst, map, x, y, bar);
@@ -366,19 +486,24 @@ __device__ __forceinline__ void clear_rows(uint8_t* stage, int bytes, int first,
   __syncwarp();
 }
 
-template <Mode kMode, bool kGlu, bool kF32, bool kPair>
+template <Mode kMode, bool kGlu, bool kF32, Team kTeam>
 __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid_constant__ LinearParams p) {
+  constexpr bool kPair = kTeam == kPairs;
   constexpr int kStages = stage_count(kPair), kStageBytes = stage_bytes(kPair), kBColumns = b_columns(kPair);
   extern __shared__ uint8_t s_raw[];
   __shared__ Shared s;
   uint8_t* stages = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
+  float* parts_at = reinterpret_cast<float*>(stages);  // split: the tile's sums, when the stages are done with
   Groups g;
   g.lo = reinterpret_cast<int32_t*>(stages + kStages * kStageBytes);
   g.hi = g.lo + p.E;
   g.start = g.hi + p.E;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = kPair ? tc::cluster_rank() : 0;
-  const uint32_t first_tile = kPair ? blockIdx.x / 2 : blockIdx.x, tile_step = kPair ? gridDim.x / 2 : gridDim.x;
+  // Split: one tile a cluster, whose CTA number `part` sums part / parts of the axis.
+  const int part = kTeam == kSplit ? tc::cluster_rank() : 0, parts = kTeam == kSplit ? p.split : 1;
+  const int team = kPair ? 2 : parts;
+  const uint32_t first_tile = blockIdx.x / team, tile_step = gridDim.x / team;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -447,12 +572,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     if (first_tile < tiles) next = find_tile<kMode, kPair>(g, p, first_tile, rank);
     for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
       const Tile tile = next;
-      const int kblocks = blocks_of(tile.kc);
+      const int kblocks = blocks_of(tile.kc), kb0 = share(kblocks, part, parts), kb1 = share(kblocks, part + 1, parts);
       // The next tile is looked for while this one's first loads are on their way.
       const int look = min(1, kblocks - 1);
       if (kblocks == 0 && t + tile_step < tiles) next = find_tile<kMode, kPair>(g, p, t + tile_step, rank);
-      for (int kb = 0; kb < kblocks; ++kb, ++it) {
-        if (kb == look && t + tile_step < tiles) next = find_tile<kMode, kPair>(g, p, t + tile_step, rank);
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        if (kTeam != kSplit && kb == look && t + tile_step < tiles) next = find_tile<kMode, kPair>(g, p, t + tile_step, rank);
         const int st = it % kStages;
         ok = it < kStages || tc::wait(&s.empty[st], (it / kStages - 1) & 1, &s.gave_up);
         ok = __all_sync(0xffffffffu, ok);
@@ -509,13 +634,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
       Tile tile;
       tile.kc = p.kc;
       if (kMode == kWeight) tile = find_tile<kMode, kPair>(g, p, t, rank);
-      const int kblocks = blocks_of(tile.kc);
-      if (kblocks == 0) continue;
+      const int kblocks = blocks_of(tile.kc), kb0 = share(kblocks, part, parts), kb1 = share(kblocks, part + 1, parts);
+      if (kb0 == kb1) continue;
       const int buf = round & 1;
       ok = round < 2 || tc::wait(&s.acc_empty[buf], (round / 2 - 1) & 1, &s.gave_up);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const int st = it % kStages;
         ok = tc::wait(&s.full[st], (it / kStages) & 1, &s.gave_up);
         ok = __all_sync(0xffffffffu, ok);
@@ -540,12 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k) {
             const uint32_t d = tmem_u + buf * kTileN;
-            if (kPair) tc::mma_f16_pair(d, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
-            else tc::mma_f16(d, a + kStepA * k, b + kStepB * k, kInstr, kb > 0 || k > 0);
+            if (kPair) tc::mma_f16_pair(d, a + kStepA * k, b + kStepB * k, kInstr, kb > kb0 || k > 0);
+            else tc::mma_f16(d, a + kStepA * k, b + kStepB * k, kInstr, kb > kb0 || k > 0);
           }
           if (kPair) tc::commit_pair(&s.empty[st]);
           else tc::commit(&s.empty[st]);
-          if (kb == kblocks - 1) {
+          if (kb == kb1 - 1) {
             if (kPair) tc::commit_pair(&s.acc_full[buf]);
             else tc::commit(&s.acc_full[buf]);
           }
@@ -638,8 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     bool ok = true;
     for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
       const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
-      const bool some = sub < tile.rows;
-      const bool sums = blocks_of(tile.kc) > 0;
+      const int kblocks = blocks_of(tile.kc);
+      const bool any = kblocks > 0;  // whether there is a sum at all (weight: the expert has rows)
+      const bool sums = share(kblocks, part, parts) < share(kblocks, part + 1, parts);
       const int buf = round & 1;
       if (sums) {
         ok = tc::wait(&s.acc_full[buf], (round / 2) & 1, &s.gave_up);
@@ -651,129 +777,81 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         ++round;
       }
       const uint32_t acc = lanes + buf * kTileN;
-      // A warp none of whose rows exist only passes the buffer on.
-      const int rows = tile.rows - sub;
-      const int64_t row = tile.row0 + sub;
-      if constexpr (kMode == kForward && kGlu) {
-        if (some) {
-          const int col = tile.n * (kTileN / 2) + half * kUnit;
-          const int64_t first = static_cast<int64_t>(tile.e) * p.bias_cols;
-          float v[kUnit], up[kUnit];
-          load_acc(acc + half * kUnit, v);
-          load_acc(acc + kTileN / 2 + half * kUnit, up);
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) release<kPair>(&s.acc_empty[buf]);
-          if (p.bias) {
-            add_bias(p, first, col, v);
-            add_bias(p, first, p.N + col, up);
-          }
-          if (p.pre) {
-            const int64_t stride = static_cast<int64_t>(p.N) * 4;
-            Rows r = rows_at(p.pre, row, stride, static_cast<int64_t>(col) * 2, rows, lane);
-            const int left = min(32, (p.N - col) * 2 - (lane & 3) * 32);
-            r.left = left;
-            store_bf16(r, v, lane);
-            r = rows_at(p.pre, row, stride, static_cast<int64_t>(p.N + col) * 2, rows, lane);
-            r.left = left;
-            store_bf16(r, up, lane);
-          }
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i) v[i] = silu(v[i]) * up[i];
-          if (p.residual) {
-            load_bf16(rows_at(p.residual, row, static_cast<int64_t>(p.N) * 2, static_cast<int64_t>(col) * 2, rows, lane),
-                      up, lane);
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) v[i] += up[i];
-          }
-          const int size = kF32 ? 4 : 2;
-          const Rows r = rows_at(p.out, row, static_cast<int64_t>(p.N) * size, static_cast<int64_t>(col) * size, rows, lane);
-          if (kF32) store_f32(r, v, lane, static_cast<int64_t>(p.N - col) * 4);
-          else store_bf16(r, v, lane);
-        } else {
-          __syncwarp();
-          if (lane == 0) release<kPair>(&s.acc_empty[buf]);
-        }
-      } else {
+      if (kTeam == kSplit) {
+        // This CTA's part of the sums, for the others to read.
+        float* to = parts_at + (sub + lane) * kPitch + half * (kTileN / 2);
+        if (any) {
 #pragma unroll 1
-      for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
-        const int col = tile.n * kTileN + half * (kTileN / 2) + q * kUnit;
-        float v[kUnit];
-        if (sums && some) {
-          load_acc(acc + half * (kTileN / 2) + q * kUnit, v);
-        } else {
+          for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
+            float v[kUnit] = {};
+            if (sums) load_acc(acc + half * (kTileN / 2) + q * kUnit, v);
 #pragma unroll
-          for (int i = 0; i < kUnit; ++i) v[i] = 0.0f;
+            for (int i = 0; i < kUnit; i += 4)
+              *reinterpret_cast<float4*>(to + q * kUnit + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
         }
-        if (sums && q == kTileN / 2 / kUnit - 1) {
+        break;
+      }
+      // A warp none of whose rows exist only passes the buffer on.
+      epilogue<kMode, kGlu, kF32>(p, tile, half, sub, lane, any, sub < tile.rows, [&](int column, float(&v)[kUnit], bool last) {
+        if (sub < tile.rows) load_acc(acc + column, v);
+        if (last) {
           tc::fence_before();
           __syncwarp();
           if (lane == 0) release<kPair>(&s.acc_empty[buf]);
         }
-        if (!some || col >= p.N) continue;
-        const int64_t byte = static_cast<int64_t>(col) * 2, stride = static_cast<int64_t>(p.N) * 2;
-        if (kMode == kForward) {
-          if (p.bias) add_bias(p, static_cast<int64_t>(tile.e) * p.bias_cols, col, v);
-          if (p.pre) store_bf16(rows_at(p.pre, row, stride, byte, rows, lane), v, lane);
-          activate(p.act, v);
-          if (p.residual) {
-            float more[kUnit];
-            load_bf16(rows_at(p.residual, row, stride, byte, rows, lane), more, lane);
+      });
+    }
+  }
+  if (kTeam == kSplit) {
+    tc::fence_before();
+    tc::cluster_sync();
+    if (warp < kEpilogueWarps && first_tile < tiles) {
+      // Every CTA finishes the blocks of 32 rows x half of the columns whose warp's number
+      // falls to it: adds the parts in order, the eight warps together, then writes them out.
+      const Tile tile = find_tile<kMode, kPair>(g, p, first_tile, rank);
+      const bool any = tile.kc > 0;
+      if (any) {
+        const int mine = kEpilogueWarps / parts;  // 1 to 4 blocks, part, part + parts, ...
+        for (int i = threadIdx.x; i < mine * 32 * 32; i += kEpilogueWarps * 32) {
+          const int block = part + (i >> 10) * parts, r = (block & 3) * 32 + ((i >> 5) & 31);
+          // Glu: 64 gate columns and the 64 up columns that belong to them.
+          const int quad = (i & 31) * 4, h = block >> 2;
+          const int c = kMode == kForward && kGlu ? (quad >> 6) * (kTileN / 2) + h * kUnit + (quad & 63)
+                                                  : h * (kTileN / 2) + quad;
+          float* at = parts_at + r * kPitch + c;
+          float4 v[kMaxSplit];
 #pragma unroll
-            for (int i = 0; i < kUnit; ++i) v[i] += more[i];
-          }
-          if (kF32) store_f32(rows_at(p.out, row, 2 * stride, 2 * byte, rows, lane), v, lane, 2 * (stride - byte));
-          else store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
-        } else if (kMode == kInput && !kGlu) {
-          if (p.act != MOE_ACT_NONE) {
-            float pre[kUnit];
-            load_bf16(rows_at(p.pre, row, stride, byte, rows, lane), pre, lane);
-            through(p.act, v, pre);
-          }
-          store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
-        } else if (kMode == kInput) {
-          Rows at = rows_at(p.pre, row, 2 * stride, byte, rows, lane);
-          Rows at_up = rows_at(p.pre, row, 2 * stride, stride + byte, rows, lane);
-          at.left = at_up.left;  // the row's first half ends where the second begins
-          float gate[kUnit], up[kUnit];
-          load_bf16(at, gate, lane);
-          load_bf16(at_up, up, lane);
+          for (int q = 0; q < kMaxSplit; ++q)
+            if (q < parts) v[q] = tc::ld_cluster_v4(tc::at_rank(at, q));
 #pragma unroll
-          for (int i = 0; i < kUnit; ++i) swiglu_through(v[i], gate[i], up[i]);
-          Rows to = rows_at(p.out, row, 2 * stride, byte, rows, lane);
-          to.left = at.left;
-          store_bf16(to, gate, lane);
-          store_bf16(rows_at(p.out, row, 2 * stride, stride + byte, rows, lane), up, lane);
-        } else {
-          if (p.accumulate && !sums) continue;
-          const int64_t out_row = static_cast<int64_t>(tile.e) * p.M + row;
-          if (kF32) {
-            const Rows at = rows_at(p.out, out_row, 2 * stride, 2 * byte, rows, lane);
-            if (p.accumulate) {
-              float old[kUnit];
-              load_f32(at, old, lane, 2 * (stride - byte));
-#pragma unroll
-              for (int i = 0; i < kUnit; ++i) v[i] += old[i];
+          for (int q = 1; q < kMaxSplit; ++q)
+            if (q < parts) {
+              v[0].x += v[q].x;
+              v[0].y += v[q].y;
+              v[0].z += v[q].z;
+              v[0].w += v[q].w;
             }
-            store_f32(at, v, lane, 2 * (stride - byte));
-          } else {
-            const Rows at = rows_at(p.out, out_row, stride, byte, rows, lane);
-            if (p.accumulate) {
-              float old[kUnit];
-              load_bf16(at, old, lane);
-#pragma unroll
-              for (int i = 0; i < kUnit; ++i) v[i] += old[i];
-            }
-            store_bf16(at, v, lane);
-          }
+          *reinterpret_cast<float4*>(at) = v[0];
         }
       }
-      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+      const int half = warp >> 2, sub = (warp & 3) * 32;
+      if (warp % parts == part)
+        epilogue<kMode, kGlu, kF32>(p, tile, half, sub, lane, any, sub < tile.rows, [&](int column, float(&v)[kUnit], bool) {
+          const float* from = parts_at + (sub + lane) * kPitch + column;
+#pragma unroll
+          for (int i = 0; i < kUnit; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(from + i);
+            v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+          }
+        });
     }
   }
   tc::fence_before();
   __syncthreads();
-  if (kPair) tc::cluster_sync();  // products read the other CTA's shared memory, arrivals reach it
+  // Pair: products read the other CTA's shared memory, arrivals reach it; split: sums are read.
+  if (kTeam != kAlone) tc::cluster_sync();
   tc::fence_after();
   if (threadIdx.x == 0 && s.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
   if (warp == kMmaWarp) {
@@ -812,11 +890,12 @@ int resident_pairs(const void* kernel, size_t smem) {
   return n;
 }
 
-template <Mode kMode, bool kGlu, bool kF32, bool kPair>
+template <Mode kMode, bool kGlu, bool kF32, Team kTeam>
 cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
+  constexpr bool kPair = kTeam == kPairs;
   // The most tables that any call has, so that what fits is the same for all.
   const size_t smem = 1024 + stage_count(kPair) * stage_bytes(kPair) + (3 * MOE_MAX_EXPERTS + 1) * sizeof(int32_t);
-  auto* kernel = expert_linear_kernel<kMode, kGlu, kF32, kPair>;
+  auto* kernel = expert_linear_kernel<kMode, kGlu, kF32, kTeam>;
   cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
   if (err != cudaSuccess) return err;
   // Every expert may add one partly filled row tile.
@@ -824,14 +903,20 @@ cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
   const int64_t m_tiles = kMode == kWeight ? static_cast<int64_t>(p.E) * p.m_tiles
                                            : (p.rows + kRows - 1) / kRows + (p.offsets ? p.E : 0);
   const int64_t tiles = m_tiles * p.n_tiles;
-  if (tiles > INT_MAX) return cudaErrorInvalidValue;
-  if (!kPair)
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads), smem, stream,
-                         true, p);
-  const int pairs = resident_pairs(reinterpret_cast<const void*>(kernel), smem);
-  if (pairs <= 0) return cudaErrorInvalidConfiguration;
+  if (tiles > INT_MAX / kMaxSplit) return cudaErrorInvalidValue;
+  int64_t teams = tiles, team = 1;  // split: a cluster for each tile there may be
+  if (kTeam == kAlone) {
+    teams = tiles < sms ? tiles : sms;
+  } else if (kTeam == kPairs) {
+    const int pairs = resident_pairs(reinterpret_cast<const void*>(kernel), smem);
+    if (pairs <= 0) return cudaErrorInvalidConfiguration;
+    teams = tiles < pairs ? tiles : pairs;
+    team = 2;
+  } else {
+    team = p.split;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs));
+  cfg.gridDim = dim3(static_cast<unsigned>(teams * team));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -839,16 +924,17 @@ cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(team);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = kTeam == kAlone ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <Mode kMode, bool kGlu, bool kF32>
 cudaError_t launch(const LinearParams& p, bool pair, int sms, cudaStream_t stream) {
-  return pair ? launch<kMode, kGlu, kF32, true>(p, sms, stream) : launch<kMode, kGlu, kF32, false>(p, sms, stream);
+  if (p.split > 1) return launch<kMode, kGlu, kF32, kSplit>(p, sms, stream);
+  return pair ? launch<kMode, kGlu, kF32, kPairs>(p, sms, stream) : launch<kMode, kGlu, kF32, kAlone>(p, sms, stream);
 }
 
 }  // namespace

@@ -38,16 +38,6 @@ constexpr int kPitch = kCols + 4;  // floats from one row's sums to the next
 __host__ __device__ constexpr int stage_bytes(bool two) { return (two ? 2 : 1) * kWBytes + kABytes; }
 __host__ __device__ constexpr int stage_count(bool two) { return two ? 3 : 5; }
 
-// Four floats of CTA `rank`'s shared memory, at the place that `p` has in this CTA's.
-__device__ __forceinline__ float4 ld_rank_v4(const float* p, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(tc::at_rank(p, rank))
-               : "memory");
-  return v;
-}
-
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full;
@@ -270,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_linear_kernel(const __grid_co
 #pragma unroll
         for (int q = 0; q < kMaxRanks; ++q)
           if (q < ranks)
-            x[h][q] = ranks > 1 ? ld_rank_v4(from, q) : *reinterpret_cast<const float4*>(from);
+            x[h][q] = ranks > 1 ? tc::ld_cluster_v4(tc::at_rank(from, q)) : *reinterpret_cast<const float4*>(from);
       }
 #pragma unroll
       for (int h = 0; h < kSums; ++h)

@@ -93,6 +93,14 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
   return at;
 }
 
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
 // One arrival on another CTA's barrier (an address of at_rank).  What this thread
 // wrote before is seen by who waits there with wait_cluster; the plain form, for
 // arrivals that pass no data of ordinary memory, costs no such fence (a microsecond).

@@ -86,7 +86,27 @@ int few_ranks(int64_t rows, int32_t E, int32_t cols, int32_t kc, int sms) {
   const int64_t all = moe::few_linear_units(rows, E) * tiles(cols, 128);
   int ranks = 1;
   while (ranks < 8 && all * ranks * 2 <= 2 * sms && ranks * 2 <= tiles(kc, 64)) ranks *= 2;
-  return all * 4 <= 2 * sms || ranks > 1 ? ranks : 0;
+  return all <= sms ? ranks : 0;
+}
+
+// The most row tiles that `ragged` experts' rows make (0: one matrix).
+int64_t row_tiles(int64_t rows, int32_t ragged) {
+  return (rows + moe::linear_m_tile(false) - 1) / moe::linear_m_tile(false) + ragged;
+}
+
+// CTAs that share the sum of a tile, for calls with few tiles and a long summed axis
+// (kc; by weights the mean of the experts' rows).  Sharing costs about 8 us, so a CTA keeps
+// 12 blocks of 64 or more, and at most 128 CTAs take part (of clusters of 8, 96: more
+// are not resident at once).  us, 1 / 2 / 4 / 8 CTAs a tile:
+//   forward  N = K = 4096: 26.4 / 22.2 / 17.8 / 28.5 at 128 rows (16 tiles), 24.0 / 22.8 /
+//            33 / 64 at 512; 2048 rows, N = K = 1024: 15.0 / 17.7 / 31 / 71
+//   by rows  256 rows, N = K = 4096: 23.3 / 21.1 / 17.7 / 38
+//   by weights  16384 rows, N = K = 512: 73 / 44 / 26.5 / 19.9; 8192 rows, N = K = 1024: 39 /
+//            27 / 20.3 / 43, 2048: 104 / 119 / 122 / 142; 1024 rows, 1024: 9.9 / 12.2 / 11.4 / 30
+int split_of(int64_t most_tiles, int64_t kc) {
+  int split = 1;
+  while (split < 8 && most_tiles * split * 2 <= (split == 4 ? 96 : 128) && kc / 64 >= 12 * split * 2) split *= 2;
+  return split;
 }
 
 }  // namespace
@@ -228,6 +248,7 @@ MOE_API int moe_expert_linear(const void* a, int64_t rows, int32_t k, const void
     p.E = num_experts;
     p.act = activation;
     p.bias_cols = n;
+    p.split = split_of(row_tiles(rows, expert_offsets ? num_experts : 0) * p.n_tiles, k);
     p.bias_f32 = bias_type == MOE_TYPE_F32;
     p.out_f32 = out_type == MOE_TYPE_F32;
     p.test_drop = moe::test_drop();
@@ -262,6 +283,7 @@ MOE_API int moe_expert_linear_backward_input(const void* dy, int64_t rows, int32
     p.kc = n;
     p.E = num_experts;
     p.act = activation;
+    p.split = split_of(row_tiles(rows, expert_offsets ? num_experts : 0) * p.n_tiles, n);
     p.test_drop = moe::test_drop();
     if (ranks > 0) return launched(moe::launch_few_linear(p, true, false, ranks, static_cast<cudaStream_t>(stream)));
     return launched(moe::launch_linear_input(p, activation == MOE_ACT_SWIGLU, takes_pairs(rows, num_experts), sms, static_cast<cudaStream_t>(stream)));
@@ -290,18 +312,22 @@ MOE_API int moe_expert_linear_backward_weight(const void* dy, int64_t rows, int3
     moe::LinearParams p = {};
     if (!encode_rows(&p.a, dy, rows, n, 64) || !encode_rows(&p.b, a, rows, k, 64)) return static_cast<int>(MOE_ECUDA);
     p.offsets = expert_offsets;
-    const bool pair = takes_pairs(rows, num_experts);
+    const int32_t n_tiles = tiles(k, moe::linear_n_tile(false));
+    const int split = split_of(static_cast<int64_t>(num_experts) * tiles(n, moe::linear_m_tile(false)) * n_tiles,
+                               rows / num_experts);
+    const bool pair = split == 1 && takes_pairs(rows, num_experts);
     p.out = dw;
     p.dy = static_cast<const uint8_t*>(dy);
     p.db = db;
     p.status = status;
     p.rows = rows;
     p.N = k;
-    p.n_tiles = tiles(k, moe::linear_n_tile(false));
+    p.n_tiles = n_tiles;
     p.M = n;
     p.m_tiles = tiles(n, moe::linear_m_tile(pair));
     p.E = num_experts;
     p.accumulate = accumulate != 0;
+    p.split = split;
     p.test_drop = moe::test_drop();
     return launched(moe::launch_linear_weight(p, dw_type == MOE_TYPE_F32, pair, sms, on));
   });

@@ -67,6 +67,7 @@ struct LinearParams {
   int32_t M, m_tiles;        // weight: rows of an expert's matrix
   int32_t kc;                // length of the summed axis (weight: the expert's rows instead)
   int32_t E, act, bias_cols;
+  int32_t split;             // CTAs that share a tile's sum: 1, 2, 4 or 8
   bool bias_f32, out_f32, accumulate;
   uint32_t test_drop;        // the number of a load that each CTA leaves out; UINT32_MAX: none
 };
