@@ -79,6 +79,7 @@ constexpr int kMaxSplit = 8;
 constexpr int kPitch = kTileN + 4;  // floats from one row's sums to the next, where they are split
 
 struct Shared {
+  float bias[kEpilogueWarps][2 * kUnit];  // of each epilogue warp's columns
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tail_full[kMaxStages];  // pair, second CTA: its half of an expert's last stage is there
   uint64_t tail_clear[kMaxStages]; // pair, first CTA: and ends in zeros
@@ -234,19 +235,23 @@ __device__ __forceinline__ uint4 ld_v4(const uint8_t* p) {
   return v;
 }
 
-__device__ __forceinline__ void load_rows(const Rows& r, uint32_t (&u)[4][8], int lane) {
+// The loads alone; transpose_4 then gives every lane its own row.
+__device__ __forceinline__ void fetch_rows(const Rows& r, uint32_t (&u)[4][8]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
     if (k < r.rows) {
       const uint8_t* from = r.at + k * r.stride;
-      if (r.left >= 16) q0 = ld_v4(from);
-      if (r.left >= 32) q1 = ld_v4(from + 16);
+      if (r.wide && r.left >= 32) {
+        tc::ld_v8(from, q0, q1);
+      } else {
+        if (r.left >= 16) q0 = ld_v4(from);
+        if (r.left >= 32) q1 = ld_v4(from + 16);
+      }
     }
     u[k][0] = q0.x, u[k][1] = q0.y, u[k][2] = q0.z, u[k][3] = q0.w;
     u[k][4] = q1.x, u[k][5] = q1.y, u[k][6] = q1.z, u[k][7] = q1.w;
   }
-  transpose_4(u, lane);
 }
 
 // 64 float32 columns of a row out as bf16 or float32.
@@ -268,13 +273,11 @@ __device__ __forceinline__ void store_f32(Rows r, const float (&v)[kUnit], int l
     r.at += 128;
   }
 }
-__device__ __forceinline__ void load_bf16(const Rows& r, float (&v)[kUnit], int lane) {
-  uint32_t u[4][8];
-  load_rows(r, u, lane);
+__device__ __forceinline__ void add_packed(const uint32_t (&u)[4][8], float (&v)[kUnit]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    v[2 * i] = bf_lo(u[i / 8][i & 7]);
-    v[2 * i + 1] = bf_hi(u[i / 8][i & 7]);
+    v[2 * i] += bf_lo(u[i / 8][i & 7]);
+    v[2 * i + 1] += bf_hi(u[i / 8][i & 7]);
   }
 }
 __device__ __forceinline__ void load_f32(Rows r, float (&v)[kUnit], int lane, int64_t bytes_left) {
@@ -283,7 +286,8 @@ __device__ __forceinline__ void load_f32(Rows r, float (&v)[kUnit], int lane, in
     uint32_t u[4][8];
     const int64_t left = bytes_left - h * 128 - (lane & 3) * 32;
     r.left = left > 32 ? 32 : static_cast<int>(left);
-    load_rows(r, u, lane);
+    fetch_rows(r, u);
+    transpose_4(u, lane);
     r.at += 128;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[h * 32 + i] = __uint_as_float(u[i / 8][i & 7]);
@@ -291,30 +295,34 @@ __device__ __forceinline__ void load_f32(Rows r, float (&v)[kUnit], int lane, in
 }
 
 // The kind of activation is asked for once for all 64 columns.
-__device__ __forceinline__ void activate(int act, float (&v)[kUnit]) {
-  if (act == MOE_ACT_RELU) {
+template <int kAct>
+__device__ __forceinline__ void activate_all(float (&v)[kUnit]) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[i] = relu(v[i]);
-  } else if (act == MOE_ACT_GELU) {
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[i] = gelu(v[i]);
-  } else if (act == MOE_ACT_SILU) {
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[i] = silu(v[i]);
+  for (int i = 0; i < kUnit; i += 2) {
+    const Two r = act_value(kAct, Two(v[i], v[i + 1]));
+    v[i] = r.lo();
+    v[i + 1] = r.hi();
   }
 }
-// g times the derivative at v.
-__device__ __forceinline__ void through(int act, float (&g)[kUnit], const float (&v)[kUnit]) {
-  if (act == MOE_ACT_RELU) {
+__device__ __forceinline__ void activate(int act, float (&v)[kUnit]) {
+  if (act == MOE_ACT_RELU) activate_all<MOE_ACT_RELU>(v);
+  else if (act == MOE_ACT_GELU) activate_all<MOE_ACT_GELU>(v);
+  else if (act == MOE_ACT_SILU) activate_all<MOE_ACT_SILU>(v);
+}
+// g times the derivative at the packed values.
+template <int kAct>
+__device__ __forceinline__ void through_one(float (&g)[kUnit], const uint32_t (&u)[4][8]) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) g[i] = act_through(MOE_ACT_RELU, g[i], v[i]);
-  } else if (act == MOE_ACT_GELU) {
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) g[i] = act_through(MOE_ACT_GELU, g[i], v[i]);
-  } else if (act == MOE_ACT_SILU) {
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) g[i] = act_through(MOE_ACT_SILU, g[i], v[i]);
+  for (int i = 0; i < 32; ++i) {
+    const Two r = act_through(kAct, Two(g[2 * i], g[2 * i + 1]), Two(bf_lo(u[i / 8][i & 7]), bf_hi(u[i / 8][i & 7])));
+    g[2 * i] = r.lo();
+    g[2 * i + 1] = r.hi();
   }
+}
+__device__ __forceinline__ void through(int act, float (&g)[kUnit], const uint32_t (&u)[4][8]) {
+  if (act == MOE_ACT_RELU) through_one<MOE_ACT_RELU>(g, u);
+  else if (act == MOE_ACT_GELU) through_one<MOE_ACT_GELU>(g, u);
+  else if (act == MOE_ACT_SILU) through_one<MOE_ACT_SILU>(g, u);
 }
 
 // 64 columns of this warp's lanes.  The last columns of a matrix may be
@@ -325,136 +333,200 @@ __device__ __forceinline__ void load_acc(uint32_t from, float (&v)[kUnit]) {
   tc::wait_loads();
 }
 
-// bias[col .. col + 63] added, the same for every lane.
-__device__ __forceinline__ void add_bias(const LinearParams& p, int64_t first, int col, float (&v)[kUnit]) {
-  if (p.bias_f32) {
-    const float* b = static_cast<const float*>(p.bias) + first + col;
+// Four columns of the bias from `col` on (0 past the last).
+__device__ __forceinline__ float4 bias_at(const LinearParams& p, int e, int col) {
+  if (col >= p.bias_cols) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // bias_cols is a multiple of 8
+  const int64_t at = static_cast<int64_t>(e) * p.bias_cols + col;
+  if (p.bias_f32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + at));
+  const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.bias) + at));
+  return make_float4(bf_lo(q.x), bf_hi(q.x), bf_lo(q.y), bf_hi(q.y));
+}
+// 64 columns of it added, from shared memory: the same for every lane.
+__device__ __forceinline__ void add_bias(const float* bias, float (&v)[kUnit]) {
 #pragma unroll
-    for (int i = 0; i < kUnit; i += 4)
-      if (col + i < p.bias_cols) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(b + i));
-        v[i] += q.x, v[i + 1] += q.y, v[i + 2] += q.z, v[i + 3] += q.w;
-      }
-  } else {
-    const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.bias) + first + col;
-#pragma unroll
-    for (int i = 0; i < kUnit; i += 8)
-      if (col + i < p.bias_cols) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(b + i));
-        v[i] += bf_lo(q.x), v[i + 1] += bf_hi(q.x), v[i + 2] += bf_lo(q.y), v[i + 3] += bf_hi(q.y);
-        v[i + 4] += bf_lo(q.z), v[i + 5] += bf_hi(q.z), v[i + 6] += bf_lo(q.w), v[i + 7] += bf_hi(q.w);
-      }
+  for (int i = 0; i < kUnit; i += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(bias + i);
+    v[i] += q.x, v[i + 1] += q.y, v[i + 2] += q.z, v[i + 3] += q.w;
   }
 }
 
+// Asks L2 for what epilogue will read of this warp's rows (residual, pre), a tile
+// ahead.
+template <Mode kMode, bool kGlu>
+__device__ __forceinline__ void prefetch_rows(const LinearParams& p, const Tile& tile, int half, int sub, int lane) {
+  const void* base = kMode == kForward ? p.residual : p.pre;
+  if (lane >= tile.rows - sub) return;
+  // Glu: forward 64 columns of h, input both halves of pre.
+  constexpr bool kWide = kMode == kInput && kGlu;
+  const int col = tile.n * (kMode == kForward && kGlu ? kTileN / 2 : kTileN) +
+                  half * (kMode == kForward && kGlu ? kUnit : kTileN / 2);
+  const uint8_t* row = static_cast<const uint8_t*>(base) +
+                       static_cast<int64_t>(tile.row0 + sub + lane) * p.N * (kWide ? 4 : 2) + static_cast<int64_t>(col) * 2;
+  // Rows need not begin with a line: the last element's line is asked for too.
+  constexpr int kColumns = kMode == kForward && kGlu ? kUnit : kTileN / 2;
+#pragma unroll
+  for (int i = 0; i <= kColumns; i += 64) {
+    const int c = min(min(i, kColumns - 1), p.N - 1 - col);
+    if (c < 0) break;
+    ptx::prefetch_l2(row + c * 2);
+    if (kWide) ptx::prefetch_l2(row + (static_cast<int64_t>(p.N) + c) * 2);
+  }
+}
+
+// Whether epilogue reads rows 64 columns at a time, the next ones while it works on these.
+template <Mode kMode, bool kGlu>
+__device__ __forceinline__ bool reads_ahead(const LinearParams& p) {
+  return !kGlu && ((kMode == kForward && p.residual) || (kMode == kInput && p.act != MOE_ACT_NONE));
+}
+// Columns 64 q .. of a tile's part of them, if this warp has any.
+template <Mode kMode>
+__device__ __forceinline__ void fetch_unit(const LinearParams& p, const Tile& tile, int half, int sub, int lane, int q,
+                                           uint32_t (&raw)[4][8]) {
+  const int col = tile.n * kTileN + half * (kTileN / 2) + q * kUnit, rows = tile.rows - sub;
+  if (rows > 0 && col < p.N)
+    fetch_rows(rows_at(kMode == kForward ? p.residual : p.pre, tile.row0 + sub, static_cast<int64_t>(p.N) * 2,
+                       static_cast<int64_t>(col) * 2, rows, lane),
+               raw);
+}
+
 // What becomes of a tile's sums: this warp's 32 rows (from sub on) and half of the
-// columns.  load(column, v, last) gets 64 of them; it is called for all of them even where
-// the warp has no rows (some is false), but not where there are no sums (any is false:
-// zeros).
+// columns.  load(column, v, last) waits for the sums and gets 64 of them; it is called
+// for all of them even where the warp has no rows (some is false), but not where there
+// are no sums (any is false: zeros).  False: the wait gave up.  raw: what fetch_unit gave
+// for the first columns, and with `more` in the end for those of `next`; bias: this
+// warp's 128 floats of shared memory.
 template <Mode kMode, bool kGlu, bool kF32, class Load>
-__device__ __forceinline__ void epilogue(const LinearParams& p, const Tile& tile, int half, int sub, int lane, bool any,
-                                         bool some, Load&& load) {
+__device__ __forceinline__ bool epilogue(const LinearParams& p, const Tile& tile, const Tile& next, bool more, int half,
+                                         int sub, int lane, bool any, bool some, uint32_t (&raw)[4][8], float* bias,
+                                         Load&& load) {
   const int rows = tile.rows - sub;
   const int64_t row = tile.row0 + sub;
-  if constexpr (kMode == kForward && kGlu) {
-    const int col = tile.n * (kTileN / 2) + half * kUnit;
-    const int64_t first = static_cast<int64_t>(tile.e) * p.bias_cols;
+  constexpr bool kGate = kMode == kForward && kGlu;  // 64 columns of h: 64 of the gate, 64 up
+  const int col0 = kGate ? tile.n * (kTileN / 2) + half * kUnit : tile.n * kTileN + half * (kTileN / 2);
+  const int64_t stride = static_cast<int64_t>(p.N) * 2;
+  some = some && col0 < p.N;
+  const bool adds = kMode == kForward && p.residual, turns = kMode == kInput && !kGlu && p.act != MOE_ACT_NONE;
+  if (kMode == kForward && p.bias) {
+    __syncwarp();
+    const int c = kGate ? (lane < 16 ? 0 : p.N - kUnit) + col0 + lane * 4 : col0 + lane * 4;
+    *reinterpret_cast<float4*>(bias + lane * 4) = bias_at(p, tile.e, c);
+    __syncwarp();
+  }
+  if constexpr (kGate) {
     float v[kUnit], up[kUnit];
-    load(half * kUnit, v, false);
-    load(kTileN / 2 + half * kUnit, up, true);
-    if (!some || col >= p.N) return;
+    if (!load(half * kUnit, v, false) || !load(kTileN / 2 + half * kUnit, up, true)) return false;
+    if (!some) return true;
     if (p.bias) {
-      add_bias(p, first, col, v);
-      add_bias(p, first, p.N + col, up);
+      add_bias(bias, v);
+      add_bias(bias + kUnit, up);
     }
     if (p.pre) {
-      const int64_t stride = static_cast<int64_t>(p.N) * 4;
-      Rows r = rows_at(p.pre, row, stride, static_cast<int64_t>(col) * 2, rows, lane);
-      const int left = min(32, (p.N - col) * 2 - (lane & 3) * 32);  // the first half ends where the second begins
+      Rows r = rows_at(p.pre, row, 2 * stride, static_cast<int64_t>(col0) * 2, rows, lane);
+      const int left = min(32, (p.N - col0) * 2 - (lane & 3) * 32);  // the first half ends where the second begins
       r.left = left;
       store_bf16(r, v, lane);
-      r = rows_at(p.pre, row, stride, static_cast<int64_t>(p.N + col) * 2, rows, lane);
+      r = rows_at(p.pre, row, 2 * stride, stride + static_cast<int64_t>(col0) * 2, rows, lane);
       r.left = left;
       store_bf16(r, up, lane);
     }
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[i] = silu(v[i]) * up[i];
-    if (p.residual) {
-      load_bf16(rows_at(p.residual, row, static_cast<int64_t>(p.N) * 2, static_cast<int64_t>(col) * 2, rows, lane), up,
-                lane);
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) v[i] += up[i];
+    for (int i = 0; i < kUnit; i += 2) {
+      const Two r = act_value(MOE_ACT_SILU, Two(v[i], v[i + 1])) * Two(up[i], up[i + 1]);
+      v[i] = r.lo();
+      v[i + 1] = r.hi();
+    }
+    if (adds) {
+      fetch_rows(rows_at(p.residual, row, stride, static_cast<int64_t>(col0) * 2, rows, lane), raw);
+      transpose_4(raw, lane);
+      add_packed(raw, v);
     }
     constexpr int kSize = kF32 ? 4 : 2;
     const Rows r =
-        rows_at(p.out, row, static_cast<int64_t>(p.N) * kSize, static_cast<int64_t>(col) * kSize, rows, lane);
-    if (kF32) store_f32(r, v, lane, static_cast<int64_t>(p.N - col) * 4);
+        rows_at(p.out, row, static_cast<int64_t>(p.N) * kSize, static_cast<int64_t>(col0) * kSize, rows, lane);
+    if (kF32) store_f32(r, v, lane, static_cast<int64_t>(p.N - col0) * 4);
     else store_bf16(r, v, lane);
+  } else if constexpr (kMode == kInput && kGlu) {
+#pragma unroll 1
+    for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
+      const int64_t byte = static_cast<int64_t>(col0 + q * kUnit) * 2;
+      const bool here = some && col0 + q * kUnit < p.N;
+      Rows at = rows_at(p.pre, row, 2 * stride, byte, rows, lane);
+      const Rows at_up = rows_at(p.pre, row, 2 * stride, stride + byte, rows, lane);
+      at.left = at_up.left;  // the row's first half ends where the second begins
+      uint32_t up[4][8];     // gate: raw
+      if (here) {
+        fetch_rows(at, raw);
+        fetch_rows(at_up, up);
+      }
+      float v[kUnit] = {};
+      if (any && !load(half * (kTileN / 2) + q * kUnit, v, q == kTileN / 2 / kUnit - 1)) return false;
+      if (!here) continue;
+      transpose_4(raw, lane);
+      transpose_4(up, lane);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        uint32_t &g2 = raw[i / 8][i & 7], &u2 = up[i / 8][i & 7];
+        Two gate(bf_lo(g2), bf_hi(g2)), u(bf_lo(u2), bf_hi(u2));
+        swiglu_through(Two(v[2 * i], v[2 * i + 1]), gate, u);
+        g2 = bf16x2(gate.lo(), gate.hi());
+        u2 = bf16x2(u.lo(), u.hi());
+      }
+      Rows to = rows_at(p.out, row, 2 * stride, byte, rows, lane);
+      to.left = at.left;
+      store_rows(to, raw, lane);
+      store_rows(rows_at(p.out, row, 2 * stride, stride + byte, rows, lane), up, lane);
+    }
   } else {
 #pragma unroll 1
     for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
-      const int col = tile.n * kTileN + half * (kTileN / 2) + q * kUnit;
+      const int col = col0 + q * kUnit;
       float v[kUnit] = {};
-      if (any) load(half * (kTileN / 2) + q * kUnit, v, q == kTileN / 2 / kUnit - 1);
-      if (!some || col >= p.N) continue;
-      const int64_t byte = static_cast<int64_t>(col) * 2, stride = static_cast<int64_t>(p.N) * 2;
-      if (kMode == kForward) {
-        if (p.bias) add_bias(p, static_cast<int64_t>(tile.e) * p.bias_cols, col, v);
-        if (p.pre) store_bf16(rows_at(p.pre, row, stride, byte, rows, lane), v, lane);
-        activate(p.act, v);
-        if (p.residual) {
-          float more[kUnit];
-          load_bf16(rows_at(p.residual, row, stride, byte, rows, lane), more, lane);
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i) v[i] += more[i];
+      if (any && !load(half * (kTileN / 2) + q * kUnit, v, q == kTileN / 2 / kUnit - 1)) return false;
+      const bool here = some && col < p.N;
+      const int64_t byte = static_cast<int64_t>(col) * 2;
+      if (here) {
+        if (kMode == kForward) {
+          if (p.bias) add_bias(bias + q * kUnit, v);
+          if (p.pre) store_bf16(rows_at(p.pre, row, stride, byte, rows, lane), v, lane);
+          activate(p.act, v);
         }
+        if (adds || turns) transpose_4(raw, lane);
+        if (adds) add_packed(raw, v);
+        if (turns) through(p.act, v, raw);
+      }
+      if (adds || turns) {
+        if (q == 0) fetch_unit<kMode>(p, tile, half, sub, lane, 1, raw);
+        else if (more) fetch_unit<kMode>(p, next, half, sub, lane, 0, raw);
+      }
+      if (!here) continue;
+      if (kMode != kWeight) {
         if (kF32) store_f32(rows_at(p.out, row, 2 * stride, 2 * byte, rows, lane), v, lane, 2 * (stride - byte));
         else store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
-      } else if (kMode == kInput && !kGlu) {
-        if (p.act != MOE_ACT_NONE) {
-          float pre[kUnit];
-          load_bf16(rows_at(p.pre, row, stride, byte, rows, lane), pre, lane);
-          through(p.act, v, pre);
-        }
-        store_bf16(rows_at(p.out, row, stride, byte, rows, lane), v, lane);
-      } else if (kMode == kInput) {
-        Rows at = rows_at(p.pre, row, 2 * stride, byte, rows, lane);
-        const Rows at_up = rows_at(p.pre, row, 2 * stride, stride + byte, rows, lane);
-        at.left = at_up.left;  // the row's first half ends where the second begins
-        float gate[kUnit], up[kUnit];
-        load_bf16(at, gate, lane);
-        load_bf16(at_up, up, lane);
+        continue;
+      }
+      if (p.accumulate && !any) continue;
+      const int64_t out_row = static_cast<int64_t>(tile.e) * p.M + row;
+      if (kF32) {
+        const Rows at = rows_at(p.out, out_row, 2 * stride, 2 * byte, rows, lane);
+        if (p.accumulate) {
+          float old[kUnit];
+          load_f32(at, old, lane, 2 * (stride - byte));
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) swiglu_through(v[i], gate[i], up[i]);
-        Rows to = rows_at(p.out, row, 2 * stride, byte, rows, lane);
-        to.left = at.left;
-        store_bf16(to, gate, lane);
-        store_bf16(rows_at(p.out, row, 2 * stride, stride + byte, rows, lane), up, lane);
+          for (int i = 0; i < kUnit; ++i) v[i] += old[i];
+        }
+        store_f32(at, v, lane, 2 * (stride - byte));
       } else {
-        if (p.accumulate && !any) continue;
-        const int64_t out_row = static_cast<int64_t>(tile.e) * p.M + row;
-        if (kF32) {
-          const Rows at = rows_at(p.out, out_row, 2 * stride, 2 * byte, rows, lane);
-          if (p.accumulate) {
-            float old[kUnit];
-            load_f32(at, old, lane, 2 * (stride - byte));
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) v[i] += old[i];
-          }
-          store_f32(at, v, lane, 2 * (stride - byte));
-        } else {
-          const Rows at = rows_at(p.out, out_row, stride, byte, rows, lane);
-          if (p.accumulate) {
-            float old[kUnit];
-            load_bf16(at, old, lane);
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) v[i] += old[i];
-          }
-          store_bf16(at, v, lane);
+        const Rows at = rows_at(p.out, out_row, stride, byte, rows, lane);
+        if (p.accumulate) {
+          fetch_rows(at, raw);
+          transpose_4(raw, lane);
+          add_packed(raw, v);
         }
+        store_bf16(at, v, lane);
       }
     }
   }
+  return true;
 }
 
 template <bool kPair>
@@ -759,28 +831,36 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   } else {
     const int half = warp >> 2, sub = (warp & 3) * 32;  // this warp's rows begin at sub
     const uint32_t lanes = tmem + (static_cast<uint32_t>(sub) << 16);
-    uint32_t round = 0;
+    uint32_t round = 0, raw[4][8];
     bool ok = true;
+    const bool ahead = reads_ahead<kMode, kGlu>(p);
+    const bool reads = kMode == kForward ? p.residual : kMode == kInput ? p.pre : nullptr;
+    Tile next;
+    if (first_tile < tiles) next = find_tile<kMode, kPair>(g, p, first_tile, rank);
+    if (ahead && kTeam != kSplit && first_tile < tiles) fetch_unit<kMode>(p, next, half, sub, lane, 0, raw);
     for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
-      const Tile tile = find_tile<kMode, kPair>(g, p, t, rank);
+      const Tile tile = next;
+      const bool more = kTeam != kSplit && t + tile_step < tiles;
+      if (more) next = find_tile<kMode, kPair>(g, p, t + tile_step, rank);
       const int kblocks = blocks_of(tile.kc);
       const bool any = kblocks > 0;  // whether there is a sum at all (weight: the expert has rows)
       const bool sums = share(kblocks, part, parts) < share(kblocks, part + 1, parts);
       const int buf = round & 1;
-      if (sums) {
-        ok = tc::wait(&s.acc_full[buf], (round / 2) & 1, &s.gave_up);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after();
-        ++round;
-      }
       const uint32_t acc = lanes + buf * kTileN;
+      bool waits = sums;
+      auto sums_are_there = [&] {
+        if (waits) {
+          waits = false;
+          ok = __all_sync(0xffffffffu, tc::wait(&s.acc_full[buf], (round / 2) & 1, &s.gave_up));
+          tc::fence_after();
+          ++round;
+        }
+        return ok;
+      };
       if (kTeam == kSplit) {
         // This CTA's part of the sums, for the others to read.
         float* to = parts_at + (sub + lane) * kPitch + half * (kTileN / 2);
-        if (any) {
+        if (any && sums_are_there()) {
 #pragma unroll 1
           for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
             float v[kUnit] = {};
@@ -792,15 +872,19 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         }
         break;
       }
+      if (reads && more) prefetch_rows<kMode, kGlu>(p, next, half, sub, lane);
       // A warp none of whose rows exist only passes the buffer on.
-      epilogue<kMode, kGlu, kF32>(p, tile, half, sub, lane, any, sub < tile.rows, [&](int column, float(&v)[kUnit], bool last) {
-        if (sub < tile.rows) load_acc(acc + column, v);
-        if (last) {
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) release<kPair>(&s.acc_empty[buf]);
-        }
-      });
+      epilogue<kMode, kGlu, kF32>(p, tile, next, more, half, sub, lane, any, sub < tile.rows, raw, s.bias[warp],
+                                  [&](int column, float(&v)[kUnit], bool last) {
+                                    if (!sums_are_there()) return false;
+                                    if (sub < tile.rows) load_acc(acc + column, v);
+                                    if (last) {
+                                      tc::fence_before();
+                                      __syncwarp();
+                                      if (lane == 0) release<kPair>(&s.acc_empty[buf]);
+                                    }
+                                    return true;
+                                  });
     }
   }
   if (kTeam == kSplit) {
@@ -837,15 +921,20 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
       const int half = warp >> 2, sub = (warp & 3) * 32;
-      if (warp % parts == part)
-        epilogue<kMode, kGlu, kF32>(p, tile, half, sub, lane, any, sub < tile.rows, [&](int column, float(&v)[kUnit], bool) {
-          const float* from = parts_at + (sub + lane) * kPitch + column;
+      if (warp % parts == part) {
+        uint32_t raw[4][8];
+        if (reads_ahead<kMode, kGlu>(p)) fetch_unit<kMode>(p, tile, half, sub, lane, 0, raw);
+        epilogue<kMode, kGlu, kF32>(p, tile, tile, false, half, sub, lane, any, sub < tile.rows, raw, s.bias[warp],
+                                    [&](int column, float(&v)[kUnit], bool) {
+                                      const float* from = parts_at + (sub + lane) * kPitch + column;
 #pragma unroll
-          for (int i = 0; i < kUnit; i += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(from + i);
-            v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-          }
-        });
+                                      for (int i = 0; i < kUnit; i += 4) {
+                                        const float4 q = *reinterpret_cast<const float4*>(from + i);
+                                        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+                                      }
+                                      return true;
+                                    });
+      }
     }
   }
   tc::fence_before();

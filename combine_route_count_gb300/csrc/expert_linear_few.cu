@@ -214,10 +214,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_linear_kernel(const __grid_co
         const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(p.pre);
         if (p.act == MOE_ACT_SWIGLU) {
           const int64_t gate_at = row * 2 * wide + c, up_at = gate_at + wide;
-          float gate = __bfloat162float(pre[gate_at]), up = __bfloat162float(pre[up_at]);
-          swiglu_through(x, gate, up);
-          out[gate_at] = __float2bfloat16_rn(gate);
-          out[up_at] = __float2bfloat16_rn(up);
+          Two gate(__bfloat162float(pre[gate_at]), 0.0f), up(__bfloat162float(pre[up_at]), 0.0f);
+          swiglu_through(Two(x, 0.0f), gate, up);
+          out[gate_at] = __float2bfloat16_rn(gate.lo());
+          out[up_at] = __float2bfloat16_rn(up.lo());
         } else {
           out[at] = __float2bfloat16_rn(
               p.act == MOE_ACT_NONE ? x : act_through(p.act, x, __bfloat162float(pre[at])));

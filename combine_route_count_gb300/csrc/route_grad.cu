@@ -154,8 +154,9 @@ cudaError_t launch_combine_grad_k(const CombineGradParams& p, cudaStream_t strea
   }
   // A block a token.  us with blocks of up to 64 / 128 / 256 threads: 4096 tokens of 8 x 7168
   // 157 / 153 / 152, 16384 tokens 599 / 592 / 587, 1024 tokens 45.1 / 47.0 / 43.3.
+  // With few tokens every thread has one chunk, or as few as there are threads for.
   int threads = 64;
-  while (threads < kMaxWarps * 32 && threads * 4 < chunks) threads *= 2;
+  while (threads < kMaxWarps * 32 && threads * (p.T <= 256 ? 1 : 4) < chunks) threads *= 2;
   return launch_kernel(combine_grad_kernel<KMAX, kDots, 0>, dim3(static_cast<unsigned>(p.T)), dim3(threads), 0, stream,
                        true, p);
 }

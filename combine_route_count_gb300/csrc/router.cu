@@ -36,22 +36,62 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 4;
 
-__device__ __forceinline__ float load(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load(const __nv_bfloat16* p) {
-  return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p))) << 16);
+// Logit i of the call, of either type.
+__device__ __forceinline__ float load(const RouterParams& p, int64_t i) {
+  if (p.f32) return __ldg(static_cast<const float*>(p.logits) + i);
+  return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const unsigned short*>(p.logits) + i)) << 16);
 }
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store(const RouterParams& p, int64_t i, float v) {
+  if (p.f32) static_cast<float*>(p.d_logits)[i] = v;
+  else static_cast<__nv_bfloat16*>(p.d_logits)[i] = __float2bfloat16_rn(v);
+}
+// A lane's logits of the token whose first one is number `row`: every G-th.
+template <int G, int N>
+__device__ __forceinline__ void load_row(const RouterParams& p, int64_t row, int lane, float (&z)[N]) {
+  if (p.f32) {
+    const float* from = static_cast<const float*>(p.logits) + row;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = i * G + lane < p.E ? __ldg(from + i * G + lane) : -INFINITY;
+  } else {
+    const unsigned short* from = static_cast<const unsigned short*>(p.logits) + row;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      z[i] = i * G + lane < p.E ? __uint_as_float(static_cast<uint32_t>(__ldg(from + i * G + lane)) << 16) : -INFINITY;
+  }
+}
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the G lanes of a token; the whole warp calls them together.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  for (int d = G / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  for (int d = G / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
   return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (G == 32) {
+    return __reduce_max_sync(kAll, v);
+  } else {
+#pragma unroll
+    for (int d = G / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+  }
+}
+template <int G>
+__device__ __forceinline__ int group_min(int v) {
+  if constexpr (G == 32) {
+    return __reduce_min_sync(kAll, v);
+  } else {
+#pragma unroll
+    for (int d = G / 2; d > 0; d >>= 1) v = min(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+  }
 }
 
 // Floats as integers in the same order; -0 as 0, NaN as -inf, nothing at 0 (which
@@ -78,25 +118,25 @@ __device__ __forceinline__ float exp_from(float a, float b) { return a == -INFIN
 
 // The scores of the chosen experts, up to a common factor where they are going
 // to be normalised.  z: the logit of the lane's choice (lanes < K).
-template <bool kSigmoid>
+template <bool kSigmoid, int G>
 __device__ __forceinline__ float share(float z, bool chosen) {
   const float e = kSigmoid ? fminf(z, 0.0f) : z;
-  const float top = warp_max(chosen ? e : -INFINITY);
+  const float top = group_max<G>(chosen ? e : -INFINITY);
   float s = chosen ? exp_from(e, top) : 0.0f;
   if (kSigmoid) s = __fdiv_rn(s, 1.0f + expf(-fabsf(z)));
-  const float sum = warp_sum(chosen ? s : 0.0f);
+  const float sum = group_sum<G>(chosen ? s : 0.0f);
   return sum > 0.0f ? __fdiv_rn(s, sum) : (sum == 0.0f ? 0.0f : sum);
 }
 
 // z becomes exp(z - top); 1 / their sum, 0 in a row without a finite logit.  The
 // product with log2(e) is off by 2^-24 of itself, so a term by 2^-24 (1.5 (top - z) + 4)
 // of itself: nothing in the sum, where such terms are small.
-template <int N>
+template <int G, int N>
 __device__ __forceinline__ float softmax_terms(float (&z)[N], float& top) {
   top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < N; ++i) top = fmaxf(top, z[i]);
-  top = warp_max(top);
+  top = group_max<G>(top);
   const float from = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
 #pragma unroll
@@ -104,7 +144,7 @@ __device__ __forceinline__ float softmax_terms(float (&z)[N], float& top) {
     z[i] = exp2_fast((z[i] - from) * kLog2e);
     sum += z[i];
   }
-  sum = warp_sum(sum);
+  sum = group_sum<G>(sum);
   return sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
 }
 
@@ -132,48 +172,49 @@ __device__ __forceinline__ float key_error(float m) { return 0x1p-19f + 0x1p-21f
 
 // Lane k's choice k where float32 keys lie too close together: of the keys near the
 // largest the largest in 64 bits.
-template <class T, int N>
-__device__ __noinline__ int choose_exactly(const T* row, const float* bias, int E, int K) {
-  const int lane = threadIdx.x & 31;
+template <int G, int N>
+__device__ __noinline__ int choose_exactly(const RouterParams& p, int64_t row, int lane) {
+  float z[N];
+  load_row<G>(p, row, lane, z);
   uint32_t key[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < E ? ordered(sigmoid(load(row + e)) + __ldg(bias + e)) : 0;
+    const int e = i * G + lane;
+    key[i] = e < p.E ? ordered(sigmoid(z[i]) + __ldg(p.bias + e)) : 0;
   }
   int mine = 0;
-  for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < p.K; ++k) {
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(kAll, best);
+    best = group_max<G>(best);
     int e = 0x7fffffff;
 #pragma unroll
     for (int i = N - 1; i >= 0; --i)
-      if (key[i] == best) e = i * 32 + lane;
-    e = __reduce_min_sync(kAll, e);
+      if (key[i] == best) e = i * G + lane;
+    e = group_min<G>(e);
     const float m = from_ordered(best), near = m - key_error(m);
     const uint32_t from = isfinite(near) ? ordered(near) : best;
-    int close = 0;
+    uint32_t close = 0;  // a bit for each of the lane's keys near the largest
 #pragma unroll
-    for (int i = 0; i < N; ++i) close += key[i] >= from;
+    for (int i = 0; i < N; ++i) close |= static_cast<uint32_t>(key[i] >= from) << i;
     // 64 bits only where there is something to tell apart: they take a microsecond.
-    if (__reduce_add_sync(kAll, close) > 1) {
+    if (__any_sync(kAll, group_sum<G>(static_cast<float>(__popc(close))) > 1.0f)) {
       double top = -INFINITY;
       int at = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = i * 32 + lane;
-        if (key[i] >= from && c < E) {
-          const double exact = 1.0 / (1.0 + exp(-static_cast<double>(load(row + c)))) + __ldg(bias + c);
+      for (; close; close &= close - 1) {
+        const int c = (__ffs(close) - 1) * G + lane;
+        if (c < p.E) {
+          const double exact = 1.0 / (1.0 + exp(-static_cast<double>(load(p, row + c)))) + __ldg(p.bias + c);
           if (exact > top) {
             top = exact;
             at = c;
           }
         }
       }
+      __syncwarp();
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
+      for (int d = G / 2; d > 0; d >>= 1) {
         const double other = __shfl_xor_sync(kAll, top, d);
         const int other_at = __shfl_xor_sync(kAll, at, d);
         if (other > top || (other == top && other_at < at)) {
@@ -181,31 +222,46 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
           at = other_at;
         }
       }
-      if (at < E) e = at;  // else all of them are NaN
+      if (at < p.E) e = at;  // else all of them are NaN
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (e == i * 32 + lane) key[i] = 0;
+      if (e == i * G + lane) key[i] = 0;
     if (lane == k) mine = e;
   }
   return mine;
 }
 
-template <class T, int N, bool kSigmoid, bool kNormalize, bool kBias>
-__global__ void __launch_bounds__(kWarps * 32) router_kernel(RouterParams p) {
+// This lane's token and place among its G lanes; behind the last token a group does the
+// last one again and keeps it to itself.
+template <int G>
+struct Place {
+  int lane, base;
+  int64_t t;
+  bool here;
+  __device__ __forceinline__ explicit Place(int64_t T) {
+    lane = threadIdx.x % G;
+    base = (threadIdx.x & 31) - lane;
+    t = (static_cast<int64_t>(blockIdx.x) * (kWarps * 32) + threadIdx.x) / G;
+    here = t < T;
+    if (!here) t = T - 1;
+  }
+};
+
+// G lanes a token, N logits a lane, K <= G.
+template <int G, int N, bool kSigmoid, bool kNormalize, bool kBias>
+__global__ void __launch_bounds__(kWarps * 32) router_kernel(const __grid_constant__ RouterParams p) {
   ptx::wait_prerequisites();
   ptx::launch_dependents();
-  const int lane = threadIdx.x & 31, E = p.E, K = p.K;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  const T* row = static_cast<const T*>(p.logits) + t * E;
+  const Place<G> at(p.T);
+  const int lane = at.lane, E = p.E, K = p.K;
+  const int64_t row = at.t * E;
   float z[N];
+  load_row<G>(p, row, lane, z);
   uint32_t key[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) z[i] = i * 32 + lane < E ? load(row + i * 32 + lane) : -INFINITY;
-#pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int e = i * 32 + lane;
+    const int e = i * G + lane;
     key[i] = 0;
     if (e < E)
       key[i] = ordered(kBias ? __fdividef(1.0f, 1.0f + exp2_fast(-z[i] * kLog2e)) + __ldg(p.bias + e) : z[i]);
@@ -218,19 +274,23 @@ __global__ void __launch_bounds__(kWarps * 32) router_kernel(RouterParams p) {
   bool close = false;
   float before = 0.0f;
   for (int k = 0; k < (kBias ? K + 1 : K); ++k) {
-    const uint32_t best = __reduce_max_sync(kAll, k1);
+    const uint32_t best = group_max<G>(k1);
     if (kBias) {
       const float m = from_ordered(best);  // after the last expert there is nothing (0)
       close |= k > 0 && best > 0 && !(before - m > key_error(before));
       before = m;
       if (k == K) break;
     }
-    const unsigned lanes = __ballot_sync(kAll, k1 == best);
-    int e = i1 * 32 + lane;
-    if (lanes & (lanes - 1)) e = __reduce_min_sync(kAll, k1 == best ? e : 0x7fffffff);
-    else e = __shfl_sync(kAll, e, __ffs(lanes) - 1);
+    int e = i1 * G + lane;
+    if (G == 32) {
+      const unsigned lanes = __ballot_sync(kAll, k1 == best);
+      if (lanes & (lanes - 1)) e = group_min<G>(k1 == best ? e : 0x7fffffff);
+      else e = __shfl_sync(kAll, e, __ffs(lanes) - 1);
+    } else {
+      e = group_min<G>(k1 == best ? e : 0x7fffffff);
+    }
     if (lane == k) mine = e;
-    if (k1 == best && e == i1 * 32 + lane) {
+    if (k1 == best && e == i1 * G + lane) {
       taken |= 1u << i1;
       k1 = k2;
       i1 = i2;
@@ -238,108 +298,103 @@ __global__ void __launch_bounds__(kWarps * 32) router_kernel(RouterParams p) {
       second = !second;
     }
   }
-  if (kBias && close) mine = choose_exactly<T, N>(row, p.bias, E, K);
+  if (kBias && __any_sync(kAll, close)) mine = choose_exactly<G, N>(p, row, lane);
   const bool chosen = lane < K;
-  const float zk = chosen ? load(row + mine) : 0.0f;
+  const float zk = chosen ? load(p, row + mine) : 0.0f;
   float w;
   if (kNormalize) {
-    w = share<kSigmoid>(zk, chosen);
+    w = share<kSigmoid, G>(zk, chosen);
   } else if (kSigmoid) {
     w = sigmoid(zk);
   } else {
     float top;
-    const float inv = softmax_terms(z, top);
+    const float inv = softmax_terms<G>(z, top);
     w = exp_from(zk, top) * inv;
   }
-  if (chosen) {
-    p.idx[t * K + lane] = mine;
-    p.w[t * K + lane] = p.scale * w;
+  if (chosen && at.here) {
+    p.idx[at.t * K + lane] = mine;
+    p.w[at.t * K + lane] = p.scale * w;
   }
 }
 
-template <class T, int N, bool kSigmoid, bool kNormalize>
-__global__ void __launch_bounds__(kWarps * 32) router_grad_kernel(RouterParams p) {
+template <int G, int N, bool kSigmoid, bool kNormalize>
+__global__ void __launch_bounds__(kWarps * 32) router_grad_kernel(const __grid_constant__ RouterParams p) {
   ptx::wait_prerequisites();
   ptx::launch_dependents();
-  const int lane = threadIdx.x & 31, E = p.E, K = p.K;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  const T* row = static_cast<const T*>(p.logits) + t * E;
-  T* out = static_cast<T*>(p.d_logits) + t * E;
+  const Place<G> at(p.T);
+  const int lane = at.lane, E = p.E, K = p.K;
+  const int64_t row = at.t * E;
   constexpr bool kDense = !kSigmoid && !kNormalize;
   float z[kDense ? N : 1], top = 0.0f, inv = 0.0f;
   if constexpr (kDense) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = i * 32 + lane < E ? load(row + i * 32 + lane) : -INFINITY;
-    inv = softmax_terms(z, top);
+    load_row<G>(p, row, lane, z);
+    inv = softmax_terms<G>(z, top);
   }
-  const int e = lane < K ? __ldg(p.idx + t * K + lane) : -1;
+  const int e = lane < K ? __ldg(p.idx + at.t * K + lane) : -1;
   const bool chosen = e >= 0 && e < E;
-  const float zk = chosen ? load(row + e) : 0.0f;
-  const float dw = chosen ? p.scale * __ldg(p.dw + t * K + lane) : 0.0f;
+  const float zk = chosen ? load(p, row + e) : 0.0f;
+  const float dw = chosen ? p.scale * __ldg(p.dw + at.t * K + lane) : 0.0f;
   float u;
   if (kNormalize) {
-    const float w = share<kSigmoid>(zk, chosen);
-    u = w * (dw - warp_sum(w * dw));
+    const float w = share<kSigmoid, G>(zk, chosen);
+    u = w * (dw - group_sum<G>(w * dw));
   } else {
     u = dw * (kSigmoid ? sigmoid(zk) : exp_from(zk, top) * inv);
   }
   if (!chosen) u = 0.0f;
   float d = u;
-  const unsigned same = __match_any_sync(kAll, chosen ? e : -1 - lane);
+  const unsigned same = __match_any_sync(kAll, chosen ? e + at.base * MOE_MAX_EXPERTS : -1 - lane - at.base);
   if (__any_sync(kAll, (same & (same - 1)) != 0)) {  // the same expert named twice counts twice
     d = 0.0f;
     for (int k = 0; k < K; ++k) {
-      const float v = __shfl_sync(kAll, u, k);
-      if ((same >> k) & 1) d += v;
+      const float v = __shfl_sync(kAll, u, k, G);
+      if ((same >> (at.base + k)) & 1) d += v;
     }
   }
   if (kSigmoid) d *= sigmoid(-zk);
   if constexpr (kDense) {
-    const float all = warp_sum(u);
+    const float all = group_sum<G>(u);
     d -= exp_from(zk, top) * inv * all;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i * 32 + lane < E) store(out + i * 32 + lane, -(z[i] * inv) * all);
+      if (at.here && i * G + lane < E) store(p, row + i * G + lane, -(z[i] * inv) * all);
   } else {
-    for (int i = lane; i < E; i += 32) store(out + i, 0.0f);
+    for (int i = lane; at.here && i < E; i += G) store(p, row + i, 0.0f);
   }
   __syncwarp();  // the chosen ones' values come last
-  if (chosen) store(out + e, d);
+  if (chosen && at.here) store(p, row + e, d);
 }
 
-template <class T, int N>
+template <int G, int N>
 cudaError_t launch_n(const RouterParams& p, bool sigmoid, bool normalize, bool backward, cudaStream_t stream) {
-  void (*kernel)(RouterParams);
+  void (*kernel)(const RouterParams);
   if (backward)
-    kernel = sigmoid ? (normalize ? router_grad_kernel<T, N, true, true> : router_grad_kernel<T, N, true, false>)
-                     : (normalize ? router_grad_kernel<T, N, false, true> : router_grad_kernel<T, N, false, false>);
+    kernel = sigmoid ? (normalize ? router_grad_kernel<G, N, true, true> : router_grad_kernel<G, N, true, false>)
+                     : (normalize ? router_grad_kernel<G, N, false, true> : router_grad_kernel<G, N, false, false>);
   else if (!sigmoid)
-    kernel = normalize ? router_kernel<T, N, false, true, false> : router_kernel<T, N, false, false, false>;
+    kernel = normalize ? router_kernel<G, N, false, true, false> : router_kernel<G, N, false, false, false>;
   else if (p.bias)
-    kernel = normalize ? router_kernel<T, N, true, true, true> : router_kernel<T, N, true, false, true>;
+    kernel = normalize ? router_kernel<G, N, true, true, true> : router_kernel<G, N, true, false, true>;
   else
-    kernel = normalize ? router_kernel<T, N, true, true, false> : router_kernel<T, N, true, false, false>;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, stream,
+    kernel = normalize ? router_kernel<G, N, true, true, false> : router_kernel<G, N, true, false, false>;
+  const int64_t tokens = kWarps * 32 / G;  // a block
+  return launch_kernel(kernel, dim3(static_cast<unsigned>((p.T + tokens - 1) / tokens)), dim3(kWarps * 32), 0, stream,
                        true, p);
-}
-
-template <class T>
-cudaError_t launch_t(const RouterParams& p, bool sigmoid, bool normalize, bool backward, cudaStream_t stream) {
-  if (p.E <= 64) return launch_n<T, 2>(p, sigmoid, normalize, backward, stream);
-  if (p.E <= 128) return launch_n<T, 4>(p, sigmoid, normalize, backward, stream);
-  if (p.E <= 256) return launch_n<T, 8>(p, sigmoid, normalize, backward, stream);
-  if (p.E <= 384) return launch_n<T, 12>(p, sigmoid, normalize, backward, stream);
-  if (p.E <= 512) return launch_n<T, 16>(p, sigmoid, normalize, backward, stream);
-  return launch_n<T, 32>(p, sigmoid, normalize, backward, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_router(const RouterParams& p, bool f32, bool sigmoid, bool normalize, bool backward,
-                          cudaStream_t stream) {
-  return f32 ? launch_t<float>(p, sigmoid, normalize, backward, stream)
-             : launch_t<__nv_bfloat16>(p, sigmoid, normalize, backward, stream);
+// Up to 64 experts do not fill a warp: 8 or 16 lanes a token.  15503 tokens, 34 experts, 14
+// chosen, with gradient: 18.4 us, a warp each 21.0; 16384 tokens, 64 experts, 6 chosen: 8.1 forward.
+cudaError_t launch_router(const RouterParams& p, bool sigmoid, bool normalize, bool backward, cudaStream_t stream) {
+  if (p.E <= 16 && p.K <= 8) return launch_n<8, 2>(p, sigmoid, normalize, backward, stream);
+  if (p.E <= 64 && p.K <= 8) return launch_n<8, 8>(p, sigmoid, normalize, backward, stream);
+  if (p.E <= 64) return launch_n<16, 4>(p, sigmoid, normalize, backward, stream);
+  if (p.E <= 128) return launch_n<32, 4>(p, sigmoid, normalize, backward, stream);
+  if (p.E <= 256) return launch_n<32, 8>(p, sigmoid, normalize, backward, stream);
+  if (p.E <= 384) return launch_n<32, 12>(p, sigmoid, normalize, backward, stream);
+  if (p.E <= 512) return launch_n<32, 16>(p, sigmoid, normalize, backward, stream);
+  return launch_n<32, 32>(p, sigmoid, normalize, backward, stream);
 }
 
 }  // namespace moe

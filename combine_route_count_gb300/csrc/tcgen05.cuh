@@ -310,6 +310,14 @@ __device__ __forceinline__ void st_v8(void* p, uint4 a, uint4 b) {
                : "memory");
 }
 
+// 32 bytes in one load; 32-byte aligned.
+__device__ __forceinline__ void ld_v8(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+
 // Two float32 operations in one instruction.
 __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
   return static_cast<unsigned long long>(__float_as_uint(lo)) |

@@ -74,19 +74,22 @@ int32_t tiles(int32_t n, int32_t tile) { return (n + tile - 1) / tile; }
 bool takes_pairs(int64_t rows, int32_t E) { return rows >= 256 * static_cast<int64_t>(E); }
 
 // CTAs that share a tile of the few-row kernel; 0: not the few-row kernel.  It is
-// for calls whose tiles leave most SMs without work: two or more of its CTAs a tile fit on
-// the GPU at once.  us, tile kernel / 1 / 2 / 4 / 8 CTAs a tile of 128 columns (56 of them
+// for a mean of up to 4 rows an expert, and for calls whose tiles leave most SMs without
+// work: two or more of its CTAs a tile fit on the GPU at once.  us, tile kernel / 1 / 2 / 4 / 8 CTAs a tile of 128 columns (56 of them
 // for N 7168; few_linear_units times that many for the rows):
 //   N 7168, K 2048: 15.8 / 11.6 / 10.8 / 10.3 / 14.4 at 1 row (224 CTAs of 4), 15.8 / 15.9 /
 //   12.9 / 12.8 / 19.0 at 32, 15.8 / 16.0 / 13.4 / 18.9 / 29 at 64, 16.4 / 16.6 / 24 / 32 /
 //   46 at 128; N 2048, K 7168: 41 / 27 / 17.6 / 12.6 / 11.2 at 16; N 512, K 8192: 43 / 30 /
 //   18 / 12.0 / 9.1 at 32; E 8, N = K = 1024: 10.9 / 9.5 / 8.7 / 8.6 / 13.7 at 64 rows,
 //   10.9 / 13.3 / 11.7 / 18 / 30 at 512; E 64, N 2816, K 2048: 115 / 112 / 116 / 123 at 256
+// and, tile kernel / 1 CTA a tile, by the mean of the rows, E 64, N 2816, K 2048, swiglu: 119 /
+//   111 at 2, 118 / 112 at 4 (skewed router 96 / 90), 118 / 114 at 8 (98 / 98); N 2048, K 1408:
+//   63 / 65 at 8 (51 / 55), 64 / 69 at 16; E 194, N 4464, K 408, gelu, 14 rows: 22.0 / 15.7
 int few_ranks(int64_t rows, int32_t E, int32_t cols, int32_t kc, int sms) {
   const int64_t all = moe::few_linear_units(rows, E) * tiles(cols, 128);
   int ranks = 1;
   while (ranks < 8 && all * ranks * 2 <= 2 * sms && ranks * 2 <= tiles(kc, 64)) ranks *= 2;
-  return all <= sms ? ranks : 0;
+  return all <= sms || rows <= 4 * static_cast<int64_t>(E) ? ranks : 0;
 }
 
 // The most row tiles that `ragged` experts' rows make (0: one matrix).
@@ -134,8 +137,9 @@ MOE_API int moe_router_topk(const void* logits, int logits_type, const float* bi
     p.E = num_experts;
     p.K = top_k;
     p.scale = scale;
-    return launched(moe::launch_router(p, logits_type == MOE_TYPE_F32, score == MOE_SCORE_SIGMOID, normalize != 0,
-                                       false, static_cast<cudaStream_t>(stream)));
+    p.f32 = logits_type == MOE_TYPE_F32;
+    return launched(moe::launch_router(p, score == MOE_SCORE_SIGMOID, normalize != 0, false,
+                                       static_cast<cudaStream_t>(stream)));
   });
 }
 
@@ -159,8 +163,9 @@ MOE_API int moe_router_topk_backward(const void* logits, int logits_type, const 
     p.E = num_experts;
     p.K = top_k;
     p.scale = scale;
-    return launched(moe::launch_router(p, logits_type == MOE_TYPE_F32, score == MOE_SCORE_SIGMOID, normalize != 0,
-                                       true, static_cast<cudaStream_t>(stream)));
+    p.f32 = logits_type == MOE_TYPE_F32;
+    return launched(moe::launch_router(p, score == MOE_SCORE_SIGMOID, normalize != 0, true,
+                                       static_cast<cudaStream_t>(stream)));
   });
 }
 

@@ -23,9 +23,9 @@ struct RouterParams {
   int64_t T;
   int32_t E, K;
   float scale;
+  bool f32;                  // the logits' type
 };
-cudaError_t launch_router(const RouterParams& p, bool f32, bool sigmoid, bool normalize, bool backward,
-                          cudaStream_t stream);
+cudaError_t launch_router(const RouterParams& p, bool sigmoid, bool normalize, bool backward, cudaStream_t stream);
 
 // ---- gradients of combine and dispatch ----------------------------------------
 struct CombineGradParams {
