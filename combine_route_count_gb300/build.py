@@ -19,10 +19,12 @@ LIB = os.path.join(PKG, "libmoe.so")
 # its buffer before use (MOE_ECORRUPT); a separate library and object folder.
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libmoe_checked.so")
-# The CPython module of ffn.py and train.py: argument checks on torch tensors, calls into
-# libmoe.so next to it.  Built against the installed torch, with the host compiler.
+# The CPython modules of ffn.py and train.py: argument checks on torch tensors, calls into
+# libmoe.so next to them.  Built against the installed torch, with the host compiler.
 LIB_FFN = os.path.join(PKG, "_ffn.so")
 STAMP_FFN = os.path.join(BUILD, "ffn.stamp")
+LIB_TRAIN = os.path.join(PKG, "_train.so")
+STAMP_TRAIN = os.path.join(BUILD, "train.stamp")
 SOURCES = ["route_count.cu", "route_split.cu", "route_cluster.cu", "route_pack.cu", "route_pack_fp8.cu", "dispatch_pack.cu", "dispatch_fp8.cu", "dispatch_staged.cu", "dense_a2a.cu", "combine.cu", "combine_two_level.cu", "moe_abi.cu", "moe_noalloc.cu",
            "add_norm_fp8.cu", "expert_gemm.cu", "decode_layer.cu", "ffn_abi.cu",
            "router.cu", "route_grad.cu", "expert_linear.cu", "expert_linear_few.cu", "train_abi.cu"]
@@ -91,37 +93,47 @@ def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List
     return lib
 
 
-def build_ffn(force: bool = False) -> str:
-    """Compile csrc/ffn_py.cc into _ffn.so next to libmoe.so; returns its path."""
+def _build_module(source: str, lib: str, stamp: str, force: bool) -> str:
     import sysconfig
 
     import torch
-    src = [os.path.join(CSRC, "ffn_py.cc"), os.path.join(CSRC, "train_py.cc")]
+    src = os.path.join(CSRC, source)
     troot = os.path.dirname(torch.__file__)
     # What the module was compiled against: another torch or Python needs another module.
     against = f"torch {torch.__version__} in {troot}, {sysconfig.get_config_var('SOABI')}\n"
-    if not force and os.path.exists(LIB_FFN) and os.path.getmtime(LIB_FFN) >= _newest_input() and _read(STAMP_FFN) == against:
-        return LIB_FFN
+    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _newest_input() and _read(stamp) == against:
+        return lib
     build()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = LIB_FFN + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", *src, "-o", tmp]
+    tmp = lib + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
     for inc in (INCLUDE, os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
         cmd += ["-I", inc]
-    lib = os.path.join(troot, "lib")
-    cmd += [LIB, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", os.path.join(cuda, "lib64"), "-lcudart",
-            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}", f"-Wl,-rpath,{os.path.join(cuda, 'lib64')}"]
+    tlib = os.path.join(troot, "lib")
+    cmd += [LIB, "-L", tlib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", os.path.join(cuda, "lib64"), "-lcudart",
+            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{tlib}", f"-Wl,-rpath,{os.path.join(cuda, 'lib64')}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on _ffn.so:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_FFN)
+        raise RuntimeError(f"{cmd[0]} failed on {source}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, lib)
     os.makedirs(BUILD, exist_ok=True)
-    with open(STAMP_FFN, "w") as f:
+    with open(stamp, "w") as f:
         f.write(against)
-    return LIB_FFN
+    return lib
+
+
+def build_ffn(force: bool = False) -> str:
+    """Compile csrc/ffn_py.cc into _ffn.so next to libmoe.so; returns its path."""
+    return _build_module("ffn_py.cc", LIB_FFN, STAMP_FFN, force)
+
+
+def build_train(force: bool = False) -> str:
+    """Compile csrc/train_py.cc into _train.so next to libmoe.so; returns its path."""
+    return _build_module("train_py.cc", LIB_TRAIN, STAMP_TRAIN, force)
 
 
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
     print(build_ffn(force=True))
+    print(build_train(force=True))

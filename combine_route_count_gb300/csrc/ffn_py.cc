@@ -1,5 +1,5 @@
 // CPython module _ffn: the argument checks of ffn.py on torch tensors and the
-// calls into libmoe.so (include/moe_ffn.h); train_py.cc has those of train.py.
+// calls into libmoe.so (include/moe_ffn.h).
 //
 // A feed-forward call on a few tokens takes a few microseconds on the GPU; the
 // same checks in Python (type, shape, contiguity, device and address of five to
@@ -12,7 +12,6 @@
 
 #include "moe_ffn.h"
 #include "py_args.h"
-#include "train_py.h"
 
 namespace {
 
@@ -159,12 +158,6 @@ PyObject* check_weights(PyObject*, PyObject* const* v, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-PyObject* init(PyObject*, PyObject* error) {
-  Py_INCREF(error);
-  Py_XSETREF(g_error, error);
-  Py_RETURN_NONE;
-}
-
 PyMethodDef kMethods[] = {
     {"init", init, METH_O, "Sets the error class."},
     {"add_rms_norm_fp8", fast<add_rms_norm_fp8>(), METH_FASTCALL, nullptr},
@@ -173,12 +166,8 @@ PyMethodDef kMethods[] = {
     {"check_weights", fast<check_weights>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ffn", "Argument checks and calls of ffn.py and train.py.", -1, kMethods};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ffn", "Argument checks and calls of ffn.py.", -1, kMethods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ffn() {
-  PyObject* module = PyModule_Create(&kModule);
-  if (module && PyModule_AddFunctions(module, train_methods()) != 0) Py_CLEAR(module);
-  return module;
-}
+PyMODINIT_FUNC PyInit__ffn() { return PyModule_Create(&kModule); }

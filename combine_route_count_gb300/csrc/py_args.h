@@ -1,4 +1,4 @@
-// What the files of the CPython module _ffn have in common: the checks of a
+// What the CPython modules _ffn and _train have in common: the checks of a
 // call's torch tensors and the call into libmoe.so.
 #pragma once
 
@@ -137,6 +137,12 @@ inline bool fits(const char* name, int64_t v) {
   if (v <= INT32_MAX) return true;
   fail(MOE_EINVAL, "%s is too large", name);
   return false;
+}
+
+inline PyObject* init(PyObject*, PyObject* error) {
+  Py_INCREF(error);
+  Py_XSETREF(g_error, error);
+  Py_RETURN_NONE;
 }
 
 // C++ exceptions of the tensor library do not leave a call.

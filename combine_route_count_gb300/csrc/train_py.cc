@@ -1,7 +1,5 @@
-// The argument checks of train.py on torch tensors and the calls into libmoe.so
-// (include/moe_train.h): part of the CPython module _ffn.
-
-#include "train_py.h"
+// CPython module _train: the argument checks of train.py on torch tensors and the
+// calls into libmoe.so (include/moe_train.h), as ffn_py.cc's for ffn.py.
 
 #include "moe_train.h"
 #include "py_args.h"
@@ -236,6 +234,7 @@ PyObject* expert_linear_backward_weight(PyObject*, PyObject* const* v, Py_ssize_
 }
 
 PyMethodDef kMethods[] = {
+    {"init", init, METH_O, "Sets the error class."},
     {"router_topk", fast<router_topk>(), METH_FASTCALL, nullptr},
     {"router_topk_backward", fast<router_topk_backward>(), METH_FASTCALL, nullptr},
     {"combine_backward", fast<combine_backward>(), METH_FASTCALL, nullptr},
@@ -245,6 +244,8 @@ PyMethodDef kMethods[] = {
     {"expert_linear_backward_weight", fast<expert_linear_backward_weight>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_train", "Argument checks and calls of train.py.", -1, kMethods};
+
 }  // namespace
 
-PyMethodDef* train_methods() { return kMethods; }
+PyMODINIT_FUNC PyInit__train() { return PyModule_Create(&kModule); }

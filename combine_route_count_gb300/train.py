@@ -23,9 +23,14 @@ A training step of one layer, with ``lay = layer.dispatch_recv()``:
     dispatch_backward(d_expert_x, lay["slot_row"], d_x);  router_topk_backward(logits, idx, d_w, d_logits)
 
 The layout's arrays live in the layer's workspace until its next dispatch_send.
+
+The checks run in the CPython module ``_train`` (csrc/train_py.cc), built next to
+libmoe.so; there is no fallback: if it is missing, every call raises.
 """
 from __future__ import annotations
 
+import importlib
+import os
 from typing import Any, Optional
 
 import torch
@@ -35,6 +40,23 @@ from . import ffn, moe
 SCORES = {"softmax": moe.MOE_SCORE_SOFTMAX, "sigmoid": moe.MOE_SCORE_SIGMOID}
 ACTIVATIONS = {"none": moe.MOE_ACT_NONE, "relu": moe.MOE_ACT_RELU, "gelu": moe.MOE_ACT_GELU,
                "silu": moe.MOE_ACT_SILU, "swiglu": moe.MOE_ACT_SWIGLU}
+
+
+_module: Any = None
+
+
+def _native() -> Any:
+    global _module
+    if _module is None:
+        path = os.path.join(moe.PKG, "_train.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_train.so is not built ({path}); run __graft_entry__.build() "
+                               "or python combine_route_count_gb300/build.py")
+        moe.load_library()
+        module = importlib.import_module("._train", __package__)
+        module.init(moe.MoEError)
+        _module = module
+    return _module
 
 
 def _named(what: str, names: dict, name: str) -> int:
@@ -53,7 +75,7 @@ def router_topk(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
     with the largest score (plus bias float32 [E], which only "sigmoid" takes),
     the lower index first among equals, and topk_w float32 [T, K] = scale *
     score, with normalize divided by the sum over the token's choices."""
-    (ffn._module or ffn._native()).router_topk(logits, topk_idx, topk_w, bias, _named("score", SCORES, score),
+    (_module or _native()).router_topk(logits, topk_idx, topk_w, bias, _named("score", SCORES, score),
                                                normalize, scale, ffn._stream(stream, logits))
 
 
@@ -63,7 +85,7 @@ def router_topk_backward(logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w:
     """Gradient of router_topk's weights by the logits, the choice held fixed.
 
     d_topk_w float32 [T, K]; writes d_logits [T, E] of the logits' type, all of it."""
-    (ffn._module or ffn._native()).router_topk_backward(logits, topk_idx, d_topk_w, d_logits,
+    (_module or _native()).router_topk_backward(logits, topk_idx, d_topk_w, d_logits,
                                                         _named("score", SCORES, score), normalize, scale,
                                                         ffn._stream(stream, logits))
 
@@ -77,7 +99,7 @@ def combine_backward(d_out: torch.Tensor, slot_row: torch.Tensor, topk_w: torch.
     float32 [T, K]; writes the rows of d_expert_y bf16 [rows, H] that slot_row
     names (may be expert_y itself) and, from expert_y bf16 [rows, H], d_topk_w
     float32 [T, K] (both or neither)."""
-    (ffn._module or ffn._native()).combine_backward(d_out, slot_row, topk_w, d_expert_y, expert_y, d_topk_w,
+    (_module or _native()).combine_backward(d_out, slot_row, topk_w, d_expert_y, expert_y, d_topk_w,
                                                     ffn._stream(stream, d_out))
 
 
@@ -86,7 +108,7 @@ def dispatch_backward(d_expert_x: torch.Tensor, slot_row: torch.Tensor, d_x: tor
     """Gradient of ``MoELayer.dispatch_send``: d_x[t] = sum_k d_expert_x[slot_row[t, k]] (+ add[t]).
 
     d_expert_x bf16 [rows, H], d_x and add bf16 [T, H] (add may be d_x)."""
-    (ffn._module or ffn._native()).dispatch_backward(d_expert_x, slot_row, d_x, add, ffn._stream(stream, d_expert_x))
+    (_module or _native()).dispatch_backward(d_expert_x, slot_row, d_x, add, ffn._stream(stream, d_expert_x))
 
 
 def expert_linear(a: torch.Tensor, w: torch.Tensor, out: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
@@ -101,7 +123,7 @@ def expert_linear(a: torch.Tensor, w: torch.Tensor, out: torch.Tensor, *, bias: 
     [rows, N] (swiglu: [rows, N/2]), pre bf16 [rows, N]: what the activation was
     taken of.  expert_offsets int32 [E+1], None for one expert with all rows.
     K % 8 == 0, N % 8 == 0.  status as for ``ffn.expert_gemm_fp8``."""
-    (ffn._module or ffn._native()).expert_linear(a, w, out, bias, _named("activation", ACTIVATIONS, activation),
+    (_module or _native()).expert_linear(a, w, out, bias, _named("activation", ACTIVATIONS, activation),
                                                  residual, pre, expert_offsets, status, ffn._stream(stream, a))
 
 
@@ -112,7 +134,7 @@ def expert_linear_backward_input(dy: torch.Tensor, w: torch.Tensor, dx: torch.Te
 
     dy bf16 [rows, N], w bf16 [E, N, K], dx and pre bf16 [rows, K] ("swiglu":
     [rows, 2K], gate and up); dx may be pre.  "none" (without pre): dx = dy . w."""
-    (ffn._module or ffn._native()).expert_linear_backward_input(
+    (_module or _native()).expert_linear_backward_input(
         dy, w, dx, _named("activation", ACTIVATIONS, activation), pre, expert_offsets, status, ffn._stream(stream, dy))
 
 
@@ -123,5 +145,5 @@ def expert_linear_backward_weight(dy: torch.Tensor, a: torch.Tensor, dw: torch.T
     """dw[e] = dy_e^T . a_e and db[e] = the sum of dy_e over expert e's rows; added to them with accumulate.
 
     dy bf16 [rows, N], a bf16 [rows, K], dw bf16 or float32 [E, N, K], db float32 [E, N]."""
-    (ffn._module or ffn._native()).expert_linear_backward_weight(dy, a, dw, db, accumulate, expert_offsets, status,
+    (_module or _native()).expert_linear_backward_weight(dy, a, dw, db, accumulate, expert_offsets, status,
                                                                  ffn._stream(stream, dy))

@@ -21,7 +21,7 @@ def train():
         pytest.skip("no CUDA device")
     from combine_route_count_gb300 import build, moe, train as t
     build.build()
-    build.build_ffn()
+    build.build_train()
     moe.load_library()
     return t
 
@@ -53,7 +53,10 @@ def untouched(buf):
 # (rows of each expert or rows, N, K)
 SHAPES = [(1, 8, 8), (1, 256, 64), (3, 264, 72), (128, 256, 128), (129, 128, 200), (300, 1000, 520),
           ([0, 5, 0, 128, 1], 256, 136), ([130, 0, 0], 520, 64), ([1] * 40, 72, 328), ([257, 3, 64, 65], 768, 1032),
-          ([0, 0], 64, 64), (2048, 512, 64)]
+          ([0, 0], 64, 64), (2048, 512, 64),
+          # pairs of CTAs over ragged groups; sums split over 2, 4 and 8 CTAs, of each product in turn; few rows
+          ([300, 0, 700, 513], 264, 136), (600, 1032, 1544), (600, 1544, 1032), (600, 520, 6152), (16400, 72, 72),
+          (20, 264, 1032)]
 
 
 def split(shape):

@@ -17,7 +17,7 @@ def train():
         pytest.skip("no CUDA device")
     from combine_route_count_gb300 import build, moe, train as t
     build.build()
-    build.build_ffn()
+    build.build_train()
     moe.load_library()
     return t
 
