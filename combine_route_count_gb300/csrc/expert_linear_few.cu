@@ -34,6 +34,7 @@ constexpr int kThreads = 192;  // warps 0-3: epilogue
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
 constexpr int kMaxRanks = 8;
 constexpr int kPitch = kCols + 4;  // floats from one row's sums to the next
+static_assert(MOE_MAX_EXPERTS * sizeof(int2) <= kWBytes, "the table of the experts' rows fits in a stage");
 
 __host__ __device__ constexpr int stage_bytes(bool two) { return (two ? 2 : 1) * kWBytes + kABytes; }
 __host__ __device__ constexpr int stage_count(bool two) { return two ? 3 : 5; }
@@ -77,17 +78,23 @@ __global__ void __launch_bounds__(kThreads, 2) few_linear_kernel(const __grid_co
   // Unit (expert, 32 of its rows) number u: the experts' rows are counted off until it is reached.
   const unsigned cluster = blockIdx.x / ranks;
   const int tile = static_cast<int>(cluster % p.n_tiles), u = static_cast<int>(cluster / p.n_tiles);
-  if (warp == 0) {
+  // (The table lies where the first stage will: the threads that use it say so to the loads.)
+  int2* table = reinterpret_cast<int2*>(stages);
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
     const int rows = static_cast<int>(p.rows);
+    int2 r = make_int2(0, rows);
+    if (p.offsets) {  // clamped: a damaged table cannot lead outside the buffers
+      r.x = min(max(p.offsets[e], 0), rows);
+      r.y = min(max(p.offsets[e + 1], r.x), rows);
+    }
+    table[e] = r;
+  }
+  __syncthreads();
+  if (warp == 0) {
     int e_found = -1, lo_found = 0, hi_found = 0, before = 0;
     for (int e0 = 0; e0 < p.E && e_found < 0; e0 += 32) {
-      const int e = e0 + lane;
-      int lo = 0, hi = e < p.E ? rows : 0;
-      if (p.offsets && e < p.E) {  // clamped: a damaged table cannot lead outside the buffers
-        lo = min(max(p.offsets[e], 0), rows);
-        hi = min(max(p.offsets[e + 1], lo), rows);
-      }
-      const int own = (hi - lo + kRows - 1) / kRows;
+      const int2 r = e0 + lane < p.E ? table[e0 + lane] : make_int2(0, 0);
+      const int own = (r.y - r.x + kRows - 1) / kRows;
       int sum = own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -99,8 +106,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_linear_kernel(const __grid_co
       if (here) {
         const int from = __ffs(here) - 1;
         e_found = e0 + from;
-        lo_found = __shfl_sync(0xffffffffu, lo + (u - first) * kRows, from);
-        hi_found = __shfl_sync(0xffffffffu, hi, from);
+        lo_found = __shfl_sync(0xffffffffu, r.x + (u - first) * kRows, from);
+        hi_found = __shfl_sync(0xffffffffu, r.y, from);
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
@@ -110,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_linear_kernel(const __grid_co
       s.unit[2] = min(kRows, hi_found - lo_found);
     }
   }
+  tc::fence_async_shared();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();

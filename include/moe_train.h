@@ -80,7 +80,8 @@ int moe_router_topk_backward(const void* logits, int logits_type, const int32_t*
  *   topk_w      device float32 [num_tokens, top_k], top_k 1..MOE_MAX_TOP_K
  *   slot_row    device int32 [num_tokens, top_k], of the dispatch's layout.  A
  *               row outside [0, rows) (after a routing error: -1) is neither
- *               read nor written, its d_topk_w is 0
+ *               read nor written, its d_topk_w is 0; a row that two
+ *               slots name (no dispatch makes that) may hold either's gradient
  *   rows        rows of expert_y and d_expert_y, < 2^31
  *   d_expert_y  device bf16 [rows, hidden], rows that no slot names are left
  *               untouched.  May be expert_y itself
