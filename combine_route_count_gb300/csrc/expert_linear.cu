@@ -79,7 +79,7 @@ constexpr int kMaxSplit = 8;
 constexpr int kPitch = kTileN + 4;  // floats from one row's sums to the next, where they are split
 
 struct Shared {
-  float bias[kEpilogueWarps][2 * kUnit];  // of each epilogue warp's columns
+  alignas(16) float bias[kEpilogueWarps][2 * kUnit];  // of each epilogue warp's columns
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tail_full[kMaxStages];  // pair, second CTA: its half of an expert's last stage is there
   uint64_t tail_clear[kMaxStages]; // pair, first CTA: and ends in zeros

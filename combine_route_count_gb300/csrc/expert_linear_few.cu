@@ -39,6 +39,26 @@ static_assert(MOE_MAX_EXPERTS * sizeof(int2) <= kWBytes, "the table of the exper
 __host__ __device__ constexpr int stage_bytes(bool two) { return (two ? 2 : 1) * kWBytes + kABytes; }
 __host__ __device__ constexpr int stage_count(bool two) { return two ? 3 : 5; }
 
+// Four neighbouring columns.
+struct Four {
+  float v[4];
+  __device__ __forceinline__ explicit Four(float a) : v{a, a, a, a} {}
+  __device__ __forceinline__ explicit Four(float4 q) : v{q.x, q.y, q.z, q.w} {}
+  static __device__ __forceinline__ Four f32(const void* p, int64_t i) {
+    return Four(*reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+  }
+  static __device__ __forceinline__ Four bf16(const void* p, int64_t i) {
+    const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    return Four(make_float4(bf_lo(q.x), bf_hi(q.x), bf_lo(q.y), bf_hi(q.y)));
+  }
+  __device__ __forceinline__ void store_bf16(void* p, int64_t i) const {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+  }
+  __device__ __forceinline__ Four operator+(const Four& o) const {
+    return Four(make_float4(v[0] + o.v[0], v[1] + o.v[1], v[2] + o.v[2], v[3] + o.v[3]));
+  }
+};
+
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full;
@@ -213,79 +233,74 @@ __global__ void __launch_bounds__(kThreads, 2) few_linear_kernel(const __grid_co
   if (threadIdx.x == 0 && s.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
 
   if (e >= 0) {
-    // Column c, row r of out from its sum x (gate: and the up column's y).
-    const int64_t wide = static_cast<int64_t>(p.N);
-    auto finish = [&](int c, int r, float x, float y) {
-      const int64_t row = row0 + r, at = row * wide + c;
-      if (kInput) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-        const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(p.pre);
-        if (p.act == MOE_ACT_SWIGLU) {
-          const int64_t gate_at = row * 2 * wide + c, up_at = gate_at + wide;
-          Two gate(__bfloat162float(pre[gate_at]), 0.0f), up(__bfloat162float(pre[up_at]), 0.0f);
-          swiglu_through(Two(x, 0.0f), gate, up);
-          out[gate_at] = __float2bfloat16_rn(gate.lo());
-          out[up_at] = __float2bfloat16_rn(up.lo());
-        } else {
-          out[at] = __float2bfloat16_rn(
-              p.act == MOE_ACT_NONE ? x : act_through(p.act, x, __bfloat162float(pre[at])));
-        }
-        return;
-      }
-      if (p.bias) {
-        const int64_t b = static_cast<int64_t>(e) * p.bias_cols + c;
-        auto bias = [&](int64_t i) {
-          return p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + i)
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[i]);
-        };
-        x += bias(b);
-        if (kGate) y += bias(b + p.N);
-      }
-      if (p.pre) {
-        __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(p.pre);
-        if (kGate) {
-          pre[row * 2 * wide + c] = __float2bfloat16_rn(x);
-          pre[row * 2 * wide + wide + c] = __float2bfloat16_rn(y);
-        } else {
-          pre[at] = __float2bfloat16_rn(x);
-        }
-      }
-      x = kGate ? silu(x) * y : act_value(p.act, x);
-      if (p.residual) x += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[at]);
-      if (p.out_f32) static_cast<float*>(p.out)[at] = x;
-      else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
-    };
-    // A rank's share: 128 / ranks columns of every row, four at a time.  (One loop for
-    // all: 32 rows unrolled were more code than the instruction cache takes, 4 us.)
-    const int part = kCols / ranks / 4;
+    // A rank's share: 128 / ranks columns of every row, four at a time; what else they need
+    // is on its way while the sums are read.  (One loop for all: 32 rows unrolled were more
+    // code than the instruction cache takes, 4 us.  us, N 7168, K 2048, one token with bias
+    // and residual, and 32 rows: four columns one after the other 9.6, 12.7; one column at a
+    // time 9.0, 14.7; so 8.9, 11.6.)
+    const int quads = kCols / ranks / 4;
+    const int64_t wide = p.N;
+    const bool halves = kGate || (kInput && p.act == MOE_ACT_SWIGLU);
 #pragma unroll 1
-    for (int i = threadIdx.x; i < part * rows; i += kThreads) {
-      const int r = i / part, c = rank * (kCols / ranks) + i % part * 4;
-      float4 x[kSums][kMaxRanks];
+    for (int i = threadIdx.x; i < quads * rows; i += kThreads) {
+      const int r = i / quads, c = rank * (kCols / ranks) + i % quads * 4, col = col0 + c;
+      if (col >= p.N) continue;  // N is a multiple of 8
+      const int64_t row = row0 + r, at = row * wide + col;
+      const int64_t at_pre = halves ? row * 2 * wide + col : at;
+      const Four none(0.0f);
+      Four b0 = none, b1 = none, more = none, pre0 = none, pre1 = none;
+      if (kInput) {
+        if (p.pre) pre0 = Four::bf16(p.pre, at_pre);
+        if (halves) pre1 = Four::bf16(p.pre, at_pre + wide);
+      } else {
+        const int64_t b = static_cast<int64_t>(e) * p.bias_cols + col;
+        if (p.bias) b0 = p.bias_f32 ? Four::f32(p.bias, b) : Four::bf16(p.bias, b);
+        if (kGate && p.bias) b1 = p.bias_f32 ? Four::f32(p.bias, b + p.N) : Four::bf16(p.bias, b + p.N);
+        if (p.residual) more = Four::bf16(p.residual, at);
+      }
+      Four x = none, y = none;
 #pragma unroll
       for (int h = 0; h < kSums; ++h) {
         const float* from = sums + (h * kRows + r) * kPitch + c;
+        float4 v[kMaxRanks];
 #pragma unroll
         for (int q = 0; q < kMaxRanks; ++q)
-          if (q < ranks)
-            x[h][q] = ranks > 1 ? tc::ld_cluster_v4(tc::at_rank(from, q)) : *reinterpret_cast<const float4*>(from);
+          if (q < ranks) v[q] = ranks > 1 ? tc::ld_cluster_v4(tc::at_rank(from, q)) : *reinterpret_cast<const float4*>(from);
+        Four& to = h ? y : x;
+#pragma unroll
+        for (int q = 0; q < kMaxRanks; ++q)
+          if (q < ranks) to = q ? to + Four(v[q]) : Four(v[0]);
+      }
+      if (kInput) {
+        if (halves) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            Two gate(pre0.v[2 * j], pre0.v[2 * j + 1]), up(pre1.v[2 * j], pre1.v[2 * j + 1]);
+            swiglu_through(Two(x.v[2 * j], x.v[2 * j + 1]), gate, up);
+            x.v[2 * j] = gate.lo(), x.v[2 * j + 1] = gate.hi();
+            y.v[2 * j] = up.lo(), y.v[2 * j + 1] = up.hi();
+          }
+          y.store_bf16(p.out, at_pre + wide);
+        } else if (p.act != MOE_ACT_NONE) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x.v[j] = act_through(p.act, x.v[j], pre0.v[j]);
+        }
+        x.store_bf16(p.out, at_pre);
+        continue;
+      }
+      if (p.bias) {
+        x = x + b0;
+        y = y + b1;
+      }
+      if (p.pre) {
+        x.store_bf16(p.pre, at_pre);
+        if (kGate) y.store_bf16(p.pre, at_pre + wide);
       }
 #pragma unroll
-      for (int h = 0; h < kSums; ++h)
-#pragma unroll
-        for (int q = 1; q < kMaxRanks; ++q)
-          if (q < ranks) {
-            x[h][0].x += x[h][q].x;
-            x[h][0].y += x[h][q].y;
-            x[h][0].z += x[h][q].z;
-            x[h][0].w += x[h][q].w;
-          }
-      if (col0 + c >= p.N) continue;  // N is a multiple of 8
-      const float4 g = x[0][0], u = x[kSums - 1][0];
-#pragma unroll 1
-      for (int j = 0; j < 4; ++j)
-        finish(col0 + c + j, r, j == 0 ? g.x : j == 1 ? g.y : j == 2 ? g.z : g.w,
-               j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w);
+      for (int j = 0; j < 4; ++j) x.v[j] = kGate ? silu(x.v[j]) * y.v[j] : act_value(p.act, x.v[j]);
+      if (p.residual) x = x + more;
+      if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+      else x.store_bf16(p.out, at);
     }
   }
   if (ranks > 1) tc::cluster_sync();  // no CTA leaves while its shared memory is being read
@@ -298,7 +313,7 @@ cudaError_t launch(const LinearParams& p, int ranks, cudaStream_t stream) {
   cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(few_linear_units(p.rows, p.E) * p.n_tiles * ranks));
+  cfg.gridDim = dim3(static_cast<unsigned>(few_linear_units(p.rows, p.offsets ? p.E : 0) * p.n_tiles * ranks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

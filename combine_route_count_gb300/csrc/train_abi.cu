@@ -85,11 +85,11 @@ bool takes_pairs(int64_t rows, int32_t E) { return rows >= 256 * static_cast<int
 // and, tile kernel / 1 CTA a tile, by the mean of the rows, E 64, N 2816, K 2048, swiglu: 119 /
 //   111 at 2, 118 / 112 at 4 (skewed router 96 / 90), 118 / 114 at 8 (98 / 98); N 2048, K 1408:
 //   63 / 65 at 8 (51 / 55), 64 / 69 at 16; E 194, N 4464, K 408, gelu, 14 rows: 22.0 / 15.7
-int few_ranks(int64_t rows, int32_t E, int32_t cols, int32_t kc, int sms) {
-  const int64_t all = moe::few_linear_units(rows, E) * tiles(cols, 128);
+int few_ranks(int64_t rows, int32_t ragged, int32_t cols, int32_t kc, int sms) {
+  const int64_t all = moe::few_linear_units(rows, ragged) * tiles(cols, 128);
   int ranks = 1;
   while (ranks < 8 && all * ranks * 2 <= 2 * sms && ranks * 2 <= tiles(kc, 64)) ranks *= 2;
-  return all <= sms || rows <= 4 * static_cast<int64_t>(E) ? ranks : 0;
+  return all <= sms || rows <= 4 * static_cast<int64_t>(ragged) ? ranks : 0;
 }
 
 // The most row tiles that `ragged` experts' rows make (0: one matrix).
@@ -236,7 +236,7 @@ MOE_API int moe_expert_linear(const void* a, int64_t rows, int32_t k, const void
   return guarded([&] {
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
-    const int ranks = few_ranks(rows, num_experts, glu ? n / 2 : n, k, sms);
+    const int ranks = few_ranks(rows, expert_offsets ? num_experts : 0, glu ? n / 2 : n, k, sms);
     moe::LinearParams p = {};
     if (!encode_rows(&p.a, a, rows, k, ranks > 0 ? moe::kFewLinearRows : 128) || !encode_weights(&p.b, w, num_experts, n, k, 128))
       return static_cast<int>(MOE_ECUDA);
@@ -274,7 +274,7 @@ MOE_API int moe_expert_linear_backward_input(const void* dy, int64_t rows, int32
   return guarded([&] {
     const int sms = sm_count();
     if (sms <= 0) return static_cast<int>(MOE_ECUDA);
-    const int ranks = few_ranks(rows, num_experts, k, n, sms);
+    const int ranks = few_ranks(rows, expert_offsets ? num_experts : 0, k, n, sms);
     moe::LinearParams p = {};
     if (!encode_rows(&p.a, dy, rows, n, ranks > 0 ? moe::kFewLinearRows : 128) || !encode_weights(&p.b, w, num_experts, n, k, 64))
       return static_cast<int>(MOE_ECUDA);

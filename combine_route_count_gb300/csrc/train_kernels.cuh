@@ -80,9 +80,11 @@ cudaError_t launch_linear_weight(const LinearParams& p, bool f32, bool pair, int
 // The same for few rows (forward, input): a in boxes of 64 x kFewLinearRows, n_tiles
 // of 128 columns, the summed axis split over `ranks` CTAs (1, 2, 4 or 8).
 constexpr int kFewLinearRows = 32;
-// The most groups of up to kFewLinearRows rows that E experts' rows can make.
-inline int64_t few_linear_units(int64_t rows, int32_t E) {
-  return (rows < E ? rows : E) + rows / kFewLinearRows;
+// The most groups of up to kFewLinearRows rows that the rows of `ragged` experts can make (0:
+// one matrix, all rows).
+inline int64_t few_linear_units(int64_t rows, int32_t ragged) {
+  if (ragged == 0) return (rows + kFewLinearRows - 1) / kFewLinearRows;
+  return (rows < ragged ? rows : ragged) + rows / kFewLinearRows;
 }
 cudaError_t launch_few_linear(const LinearParams& p, bool input, bool gate, int ranks, cudaStream_t stream);
 
