@@ -65,31 +65,33 @@ int32_t tiles(int32_t n, int32_t tile) { return (n + tile - 1) / tile; }
 // Tiles by pairs of CTAs (256 x 256, half the operand traffic of two tiles of 128 x
 // 256) from a mean of 256 rows an expert on; below it half of such a tile is empty.  us,
 // single CTAs / pairs, N = K = 4096 but where said:
-//   forward  8 experts: 50.1 / 53.5 at a mean of 128, 62.5 / 56.4 at 256, 173 / 149 at
-//            1024; 64 experts, N 2816, K 2048, swiglu: 125 / 136 at 128, 159 / 147 at
-//            256, under a skewed router 186 / 188; 1 expert: 162 / 143 at 8192 rows
-//   by rows  8 experts 65.7 / 58.0 at 256; K 8192, swiglu: 414 / 343 at 1024
-//   by weights  1 expert: 11.2 / 12.1 at 128 rows, 29.2 / 26.6 at 1024, 183 / 160 at
-//            8192; 256 experts, N = K = 2048: 363 / 446 at 128 (bound by what it writes)
+//   forward  8 experts: 50.6 / 53.9 at a mean of 128, 63.3 / 56.5 at 256, 173 / 149 at
+//            1024; 64 experts, N 2816, K 2048, swiglu: 126 / 136 at 128, 158 / 142 at
+//            256, under a skewed router 176 / 178; 1 expert: 161 / 141 at 8192 rows
+//   by rows  8 experts 60.7 / 53.9 at 256; K 8192, swiglu: 381 / 332 at 1024
+//   by weights  1 expert: 10.5 / 11.7 at 128 rows, 27.1 / 24.8 at 1024, 176 / 156 at
+//            8192; 256 experts, N = K = 2048: 371 / 442 at 128 (bound by what it writes)
 bool takes_pairs(int64_t rows, int32_t E) { return rows >= 256 * static_cast<int64_t>(E); }
 
 // CTAs that share a tile of the few-row kernel; 0: not the few-row kernel.  It is
 // for a mean of up to 4 rows an expert, and for calls whose tiles leave most SMs without
-// work: two or more of its CTAs a tile fit on the GPU at once.  us, tile kernel / 1 / 2 / 4 / 8 CTAs a tile of 128 columns (56 of them
-// for N 7168; few_linear_units times that many for the rows):
-//   N 7168, K 2048: 15.8 / 11.6 / 10.8 / 10.3 / 14.4 at 1 row (224 CTAs of 4), 15.8 / 15.9 /
-//   12.9 / 12.8 / 19.0 at 32, 15.8 / 16.0 / 13.4 / 18.9 / 29 at 64, 16.4 / 16.6 / 24 / 32 /
-//   46 at 128; N 2048, K 7168: 41 / 27 / 17.6 / 12.6 / 11.2 at 16; N 512, K 8192: 43 / 30 /
-//   18 / 12.0 / 9.1 at 32; E 8, N = K = 1024: 10.9 / 9.5 / 8.7 / 8.6 / 13.7 at 64 rows,
-//   10.9 / 13.3 / 11.7 / 18 / 30 at 512; E 64, N 2816, K 2048: 115 / 112 / 116 / 123 at 256
-// and, tile kernel / 1 CTA a tile, by the mean of the rows, E 64, N 2816, K 2048, swiglu: 119 /
-//   111 at 2, 118 / 112 at 4 (skewed router 96 / 90), 118 / 114 at 8 (98 / 98); N 2048, K 1408:
-//   63 / 65 at 8 (51 / 55), 64 / 69 at 16; E 194, N 4464, K 408, gelu, 14 rows: 22.0 / 15.7
+// work: three of its CTAs on two SMs take all of its tiles.  us, tile kernel / 1 / 2 / 4 / 8
+// CTAs a tile of 128 columns (56 of them for N 7168; few_linear_units times that many for
+// the rows):
+//   N 7168, K 2048: 16.1 / 11.7 / 10.7 / 10.1 / 14.3 at 1 row, 16.1 / 13.3 / 11.7 / 11.4 /
+//   17.2 at 32, 16.2 / 13.5 / 12.0 / 17.4 / 29 at 64, 16.6 / 13.8 / 19.5 / 29 / 48 at 128
+//   (224 tiles), 15.8 / 24 / 30 / 48 / - at 256; N 2048, K 7168: 42 / 27 / 17.3 / 12.5 / 11.2 at
+//   16; N = K = 4096: 17.8 (a split sum) / 18.3 / 14.9 / 21 / - at 128, 18.3 / 20.3 / 26 / 38 / -
+//   at 256 (256 tiles); 8 experts, N = K = 1024: 11.3 / 8.9 / 8.6 / 8.8 / 13.7 at 64 rows,
+//   11.2 / 10.5 / 11.1 / 16.8 / 30 at 512 (192 tiles)
+// and, tile kernel / 1 CTA a tile, by the mean of the rows, 64 experts, N 2816, K 2048, swiglu:
+//   116 / 112 at 2, 116 / 111 at 4 (skewed router 94.5 / 90), 116 / 113 at 8 (97 / 98); N 2048, K
+//   1408: 63 / 63 at 8 (52 / 54), 64 / 65 at 16; 194 experts, N 4464, K 408, gelu, 14 rows: 22 / 15
 int few_ranks(int64_t rows, int32_t ragged, int32_t cols, int32_t kc, int sms) {
   const int64_t all = moe::few_linear_units(rows, ragged) * tiles(cols, 128);
   int ranks = 1;
   while (ranks < 8 && all * ranks * 2 <= 2 * sms && ranks * 2 <= tiles(kc, 64)) ranks *= 2;
-  return all <= sms || rows <= 4 * static_cast<int64_t>(ragged) ? ranks : 0;
+  return 2 * all <= 3 * sms || rows <= 4 * static_cast<int64_t>(ragged) ? ranks : 0;
 }
 
 // The most row tiles that `ragged` experts' rows make (0: one matrix).
@@ -101,11 +103,11 @@ int64_t row_tiles(int64_t rows, int32_t ragged) {
 // (kc; by weights the mean of the experts' rows).  Sharing costs about 8 us, so a CTA keeps
 // 12 blocks of 64 or more, and at most 128 CTAs take part (of clusters of 8, 96: more
 // are not resident at once).  us, 1 / 2 / 4 / 8 CTAs a tile:
-//   forward  N = K = 4096: 26.4 / 22.2 / 17.8 / 28.5 at 128 rows (16 tiles), 24.0 / 22.8 /
-//            33 / 64 at 512; 2048 rows, N = K = 1024: 15.0 / 17.7 / 31 / 71
-//   by rows  256 rows, N = K = 4096: 23.3 / 21.1 / 17.7 / 38
-//   by weights  16384 rows, N = K = 512: 73 / 44 / 26.5 / 19.9; 8192 rows, N = K = 1024: 39 /
-//            27 / 20.3 / 43, 2048: 104 / 119 / 122 / 142; 1024 rows, 1024: 9.9 / 12.2 / 11.4 / 30
+//   forward  N = K = 4096: 26.8 / 22.2 / 17.8 / 28.3 at 128 rows (16 tiles), 26.9 / 22.7 /
+//            33 / 64 at 512; 2048 rows, N = K = 1024: 9.9 / 13.1 / 22.7 / 52
+//   by rows  256 rows, N = K = 4096: 25.6 / 21.3 / 17.6 / 38
+//   by weights  16384 rows, N = K = 512: 72 / 44 / 26.3 / 19.2; 8192 rows, N = K = 1024: 38.5 /
+//            27 / 19.8 / 42, 2048: 45 / 58 / 77 / 128; 1024 rows, 1024: 8.9 / 12.1 / 11.2 / 29
 int split_of(int64_t most_tiles, int64_t kc) {
   int split = 1;
   while (split < 8 && most_tiles * split * 2 <= (split == 4 ? 96 : 128) && kc / 64 >= 12 * split * 2) split *= 2;
