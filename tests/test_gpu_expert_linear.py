@@ -262,3 +262,60 @@ def test_graph_replay_and_streams(train):
     again = torch.empty_like(out)
     train.expert_linear(a, w, again, expert_offsets=off)
     assert torch.equal(again, out) and not torch.equal(again, first[0])
+
+
+def test_offsets_past_32_bits(train):
+    """Weights, gradients and rows beyond 2^31 elements from their buffers' start."""
+    g = gen(8)
+    E, N, K = 70, 8192, 4096
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    w[69, -64:] = bf(g, 64, K, integers=True)
+    for rows in (8, 900):  # few rows, and tiles
+        counts = [3] + [0] * 68 + [rows - 3]
+        off = offsets_of(counts)
+        a, dy = bf(g, rows, K, integers=True), torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+        dy[:, -64:] = bf(g, rows, 64, integers=True)
+        out = torch.full((rows, N), -7.25, device="cuda")
+        train.expert_linear(a, w, out, expert_offsets=off)
+        assert torch.equal(out[3:, -64:].double(), a[3:].double() @ w[69, -64:].double().t())
+        assert not bool(out[:3].any()) and not bool(out[3:, :-64].any())
+        dx = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+        train.expert_linear_backward_input(dy, w, dx, expert_offsets=off)
+        assert torch.equal(dx[3:], (dy[3:, -64:].double() @ w[69, -64:].double()).to(torch.bfloat16))
+        assert not bool(dx[:3].any())
+        dw = torch.full_like(w, -7.25)
+        train.expert_linear_backward_weight(dy, a, dw, expert_offsets=off)
+        assert torch.equal(dw[69, -64:], (dy[3:, -64:].double().t() @ a[3:].double()).to(torch.bfloat16))
+        assert not bool(dw[1:69].any()) and not bool(dw[69, :-64].any())
+    del w, dw
+    rows, N, K = 2 ** 31 // 8192 + 300, 8192, 64
+    a, w = bf(g, rows, K, integers=True), bf(g, N, K, integers=True)
+    r = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    r[-400:] = 1.0
+    train.expert_linear(a, w, r, residual=r)
+    want = a[-400:].double() @ w.double().t() + 1.0
+    assert torch.equal(r[-400:], want.to(torch.bfloat16))
+    assert torch.equal(r[:10], (a[:10].double() @ w.double().t()).to(torch.bfloat16))
+
+
+def test_many_shapes(train):
+    """Shapes over the range in which a call changes its kernel, all three products of each."""
+    import random
+    rng = random.Random(12)
+    size = lambda hi: 8 * max(1, int(2 ** rng.uniform(0, np.log2(hi / 8))))  # noqa: E731
+    for i in range(60):
+        g = gen(1000 + i)
+        E = rng.choice([1, 1, 2, 5, 40])
+        N, K, rows = size(1200), size(2000), int(2 ** rng.uniform(0, 11))
+        cuts = sorted(rng.randint(0, rows) for _ in range(E - 1))
+        off = None if E == 1 else torch.tensor([0, *cuts, rows], dtype=torch.int32, device="cuda")
+        a, w, dy = bf(g, rows, K, integers=True), bf(g, E, N, K, integers=True), bf(g, rows, N, integers=True)
+        out, dx = torch.empty(rows, N, device="cuda"), torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+        dw, db = torch.empty(E, N, K, device="cuda"), torch.empty(E, N, device="cuda")
+        train.expert_linear(a, w, out, expert_offsets=off)
+        train.expert_linear_backward_input(dy, w, dx, expert_offsets=off)
+        train.expert_linear_backward_weight(dy, a, dw, db=db, expert_offsets=off)
+        want, _, want_b, _ = ref.by_weights(dy, a, off, E)
+        assert torch.equal(out.double(), ref.forward(a, w, off)[0]), (rows, E, N, K)
+        assert torch.equal(dx, ref.by_rows(dy, w, off)[0].to(torch.bfloat16)), (rows, E, N, K)
+        assert torch.equal(dw.double(), want) and torch.equal(db.double(), want_b), (rows, E, N, K)
