@@ -14,7 +14,8 @@
 // KiB by tiled TMA (128-byte swizzle).  With many rows an expert two CTAs (a cluster)
 // share a tile of 256 x 256: one issues the products of both (cta_group::2), each
 // holds half of either operand, 6 stages of 32 KiB, so that a product of 256 x 256 x 64
-// takes 64 KiB out of L2 instead of 96.  Where there are few tiles and a long summed axis,
+// takes 64 KiB out of L2 instead of 96.  Where there are few tiles, they have 128 columns
+// and 6 stages of 32 KiB; where the summed axis is long as well,
 // up to 8 CTAs (a cluster) split the axis of one tile, read one another's sums through
 // distributed shared memory and each finish a part of the tile.  12 warps: eight for the epilogue (two
 // groups of four, each with half of the columns), one for TMA, one for the matrix
@@ -58,16 +59,18 @@ namespace {
 using namespace lin;
 
 enum Mode { kForward, kInput, kWeight };
-// Who works on a tile: one CTA, a pair of them, or several that split the summed axis.
-enum Team { kAlone, kPairs, kSplit };
+// Who works on a tile: one CTA (on half as many columns: kNarrow), a pair of them, or
+// several that split the summed axis.
+enum Team { kAlone, kNarrow, kPairs, kSplit };
 
-constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;  // kTileM: rows of one CTA
+constexpr int kTileM = 128, kBlockK = 64;  // kTileM: rows of one CTA
+__host__ __device__ constexpr int tile_n(Team team) { return team == kNarrow ? 128 : 256; }
 constexpr int kABytes = kTileM * kBlockK * 2;
 constexpr int kChunkBytes = 64 * kBlockK * 2;  // a box of 64 x 64
 // Of one CTA: alone it holds all of B's columns, in a pair half of them.
-__host__ __device__ constexpr int b_columns(bool pair) { return pair ? kTileN / 2 : kTileN; }
-__host__ __device__ constexpr int stage_bytes(bool pair) { return kABytes + b_columns(pair) * kBlockK * 2; }
-__host__ __device__ constexpr int stage_count(bool pair) { return pair ? 6 : 4; }
+__host__ __device__ constexpr int b_columns(Team team) { return team == kPairs ? tile_n(team) / 2 : tile_n(team); }
+__host__ __device__ constexpr int stage_bytes(Team team) { return kABytes + b_columns(team) * kBlockK * 2; }
+__host__ __device__ constexpr int stage_count(Team team) { return b_columns(team) == 128 ? 6 : 4; }
 constexpr int kMaxStages = 6;
 constexpr int kEpilogueWarps = 8;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kBiasWarp = 10;
@@ -76,7 +79,7 @@ constexpr int kLoads = 24;  // of a lane of the bias warps on their way: under l
 constexpr uint32_t kTmemColumns = 512;
 constexpr int kUnit = 64;  // columns that an epilogue warp works on at a time
 constexpr int kMaxSplit = 8;
-constexpr int kPitch = kTileN + 4;  // floats from one row's sums to the next, where they are split
+constexpr int kPitch = tile_n(kSplit) + 4;  // floats from one row's sums to the next, where they are split
 
 struct Shared {
   alignas(16) float bias[kEpilogueWarps][2 * kUnit];  // of each epilogue warp's columns
@@ -127,7 +130,7 @@ __device__ __forceinline__ int place(uint32_t t, uint32_t m_tiles, uint32_t n_ti
 }
 
 // What CTA `rank` of a pair has of tile t (rank 0: of a CTA alone).  Rows may be none.
-template <Mode kMode, bool kPair>
+template <Mode kMode, bool kPair, int kN>
 __device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p, uint32_t t, int rank) {
   constexpr int kRows = kPair ? 2 * kTileM : kTileM;
   Tile r;
@@ -136,7 +139,7 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p
     r.e = static_cast<int>(t / per);
     const uint32_t local = t - r.e * per;
     int m;
-    r.n = place<kTileN>(local, p.n_tiles, p.m_tiles, m);  // bands of 2048 columns, columns fastest
+    r.n = place<kN>(local, p.n_tiles, p.m_tiles, m);  // bands of 2048 columns, columns fastest
     r.row0 = m * kRows + rank * kTileM;
     r.rows = min(kTileM, p.M - r.row0);
     r.k0 = g.lo[r.e];
@@ -162,7 +165,7 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, const LinearParams& p
 // The tiles of a CTA one after the other, for a whole warp: every lane looks for one of
 // the next 32, which are then handed round.  (Looked for one at a time: through 8
 // experts' gate, N 4096, K 8192, 340 us instead of 334; 256 experts' dw, 381 instead of 369.)
-template <Mode kMode, bool kPair>
+template <Mode kMode, bool kPair, int kN>
 struct Walk {
   uint32_t first, step, tiles;
   int rank;
@@ -170,7 +173,7 @@ struct Walk {
 
   // Number i; i goes up by one from call to call, first + i * step < tiles.
   __device__ __forceinline__ Tile get(const Groups& g, const LinearParams& p, uint32_t i, int lane) {
-    if (i % 32 == 0) mine = find_tile<kMode, kPair>(g, p, min(first + (i + lane) * step, tiles - 1), rank);
+    if (i % 32 == 0) mine = find_tile<kMode, kPair, kN>(g, p, min(first + (i + lane) * step, tiles - 1), rank);
     const int from = i % 32;
     Tile r;
     r.e = __shfl_sync(0xffffffffu, mine.e, from);
@@ -375,18 +378,18 @@ __device__ __forceinline__ void add_bias(const float* bias, float (&v)[kUnit]) {
 
 // Asks L2 for what epilogue will read of this warp's rows (residual, pre), a tile
 // ahead.
-template <Mode kMode, bool kGlu>
+template <Mode kMode, bool kGlu, int kN>
 __device__ __forceinline__ void prefetch_rows(const LinearParams& p, const Tile& tile, int half, int sub, int lane) {
   const void* base = kMode == kForward ? p.residual : p.pre;
   if (lane >= tile.rows - sub) return;
   // Glu: forward 64 columns of h, input both halves of pre.
   constexpr bool kWide = kMode == kInput && kGlu;
-  const int col = tile.n * (kMode == kForward && kGlu ? kTileN / 2 : kTileN) +
-                  half * (kMode == kForward && kGlu ? kUnit : kTileN / 2);
+  const int col = tile.n * (kMode == kForward && kGlu ? kN / 2 : kN) +
+                  half * (kMode == kForward && kGlu ? kUnit : kN / 2);
   const uint8_t* row = static_cast<const uint8_t*>(base) +
                        static_cast<int64_t>(tile.row0 + sub + lane) * p.N * (kWide ? 4 : 2) + static_cast<int64_t>(col) * 2;
   // Rows need not begin with a line: the last element's line is asked for too.
-  constexpr int kColumns = kMode == kForward && kGlu ? kUnit : kTileN / 2;
+  constexpr int kColumns = kMode == kForward && kGlu ? kUnit : kN / 2;
 #pragma unroll
   for (int i = 0; i <= kColumns; i += 64) {
     const int c = min(min(i, kColumns - 1), p.N - 1 - col);
@@ -402,10 +405,10 @@ __device__ __forceinline__ bool reads_ahead(const LinearParams& p) {
   return !kGlu && ((kMode == kForward && p.residual) || (kMode == kInput && p.act != MOE_ACT_NONE));
 }
 // Columns 64 q .. of a tile's part of them, if this warp has any.
-template <Mode kMode>
+template <Mode kMode, int kN>
 __device__ __forceinline__ void fetch_unit(const LinearParams& p, const Tile& tile, int half, int sub, int lane, int q,
                                            uint32_t (&raw)[4][8]) {
-  const int col = tile.n * kTileN + half * (kTileN / 2) + q * kUnit, rows = tile.rows - sub;
+  const int col = tile.n * kN + half * (kN / 2) + q * kUnit, rows = tile.rows - sub;
   if (rows > 0 && col < p.N)
     fetch_rows(rows_at(kMode == kForward ? p.residual : p.pre, tile.row0 + sub, static_cast<int64_t>(p.N) * 2,
                        static_cast<int64_t>(col) * 2, rows, lane),
@@ -418,14 +421,14 @@ __device__ __forceinline__ void fetch_unit(const LinearParams& p, const Tile& ti
 // are no sums (any is false: zeros).  False: the wait gave up.  raw: what fetch_unit gave
 // for the first columns, and with `more` in the end for those of `next`; bias: this
 // warp's 128 floats of shared memory.
-template <Mode kMode, bool kGlu, bool kF32, class Load>
+template <Mode kMode, bool kGlu, bool kF32, int kN, class Load>
 __device__ __forceinline__ bool epilogue(const LinearParams& p, const Tile& tile, const Tile& next, bool more, int half,
                                          int sub, int lane, bool any, bool some, uint32_t (&raw)[4][8], float* bias,
                                          Load&& load) {
   const int rows = tile.rows - sub;
   const int64_t row = tile.row0 + sub;
   constexpr bool kGate = kMode == kForward && kGlu;  // 64 columns of h: 64 of the gate, 64 up
-  const int col0 = kGate ? tile.n * (kTileN / 2) + half * kUnit : tile.n * kTileN + half * (kTileN / 2);
+  const int col0 = kGate ? tile.n * (kN / 2) + half * kUnit : tile.n * kN + half * (kN / 2);
   const int64_t stride = static_cast<int64_t>(p.N) * 2;
   some = some && col0 < p.N;
   const bool adds = kMode == kForward && p.residual, turns = kMode == kInput && !kGlu && p.act != MOE_ACT_NONE;
@@ -437,7 +440,7 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, const Tile& tile
   }
   if constexpr (kGate) {
     float v[kUnit], up[kUnit];
-    if (!load(half * kUnit, v, false) || !load(kTileN / 2 + half * kUnit, up, true)) return false;
+    if (!load(half * kUnit, v, false) || !load(kN / 2 + half * kUnit, up, true)) return false;
     if (!some) return true;
     if (p.bias) {
       add_bias(bias, v);
@@ -470,7 +473,7 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, const Tile& tile
     else store_bf16(r, v, lane);
   } else if constexpr (kMode == kInput && kGlu) {
 #pragma unroll 1
-    for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
+    for (int q = 0; q < kN / 2 / kUnit; ++q) {
       const int64_t byte = static_cast<int64_t>(col0 + q * kUnit) * 2;
       const bool here = some && col0 + q * kUnit < p.N;
       Rows at = rows_at(p.pre, row, 2 * stride, byte, rows, lane);
@@ -482,7 +485,7 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, const Tile& tile
         fetch_rows(at_up, up);
       }
       float v[kUnit] = {};
-      if (any && !load(half * (kTileN / 2) + q * kUnit, v, q == kTileN / 2 / kUnit - 1)) return false;
+      if (any && !load(half * (kN / 2) + q * kUnit, v, q == kN / 2 / kUnit - 1)) return false;
       if (!here) continue;
       transpose_4(raw, lane);
       transpose_4(up, lane);
@@ -501,10 +504,10 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, const Tile& tile
     }
   } else {
 #pragma unroll 1
-    for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
+    for (int q = 0; q < kN / 2 / kUnit; ++q) {
       const int col = col0 + q * kUnit;
       float v[kUnit] = {};
-      if (any && !load(half * (kTileN / 2) + q * kUnit, v, q == kTileN / 2 / kUnit - 1)) return false;
+      if (any && !load(half * (kN / 2) + q * kUnit, v, q == kN / 2 / kUnit - 1)) return false;
       const bool here = some && col < p.N;
       const int64_t byte = static_cast<int64_t>(col) * 2;
       if (here) {
@@ -518,8 +521,8 @@ __device__ __forceinline__ bool epilogue(const LinearParams& p, const Tile& tile
         if (turns) through(p.act, v, raw);
       }
       if (adds || turns) {
-        if (q == 0) fetch_unit<kMode>(p, tile, half, sub, lane, 1, raw);
-        else if (more) fetch_unit<kMode>(p, next, half, sub, lane, 0, raw);
+        if (q + 1 < kN / 2 / kUnit) fetch_unit<kMode, kN>(p, tile, half, sub, lane, q + 1, raw);
+        else if (more) fetch_unit<kMode, kN>(p, next, half, sub, lane, 0, raw);
       }
       if (!here) continue;
       if (kMode != kWeight) {
@@ -584,7 +587,8 @@ __device__ __forceinline__ void clear_rows(uint8_t* stage, int bytes, int first,
 template <Mode kMode, bool kGlu, bool kF32, Team kTeam>
 __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid_constant__ LinearParams p) {
   constexpr bool kPair = kTeam == kPairs;
-  constexpr int kStages = stage_count(kPair), kStageBytes = stage_bytes(kPair), kBColumns = b_columns(kPair);
+  constexpr int kStages = stage_count(kTeam), kStageBytes = stage_bytes(kTeam), kBColumns = b_columns(kTeam);
+  constexpr int kN = tile_n(kTeam);
   extern __shared__ uint8_t s_raw[];
   __shared__ Shared s;
   uint8_t* stages = s_raw + ((1024 - (ptx::smem_addr(s_raw) & 1023)) & 1023);
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   else __syncthreads();
   tc::fence_after();
   const uint32_t tiles = tile_count<kMode>(g, p);
-  Walk<kMode, kPair> walk = {first_tile, tile_step, tiles, rank};
+  Walk<kMode, kPair, kN> walk = {first_tile, tile_step, tiles, rank};
   const uint32_t tmem = s.tmem, tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
 
   if (warp == kTmaWarp) {
@@ -687,18 +691,18 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
             for (int q = 0; q < kTileM / 64; ++q) load_2d<kPair>(a + q * kChunkBytes, &p.a, tile.row0 + q * 64, k, bar);
 #pragma unroll
             for (int q = 0; q < kBColumns / 64; ++q)
-              load_2d<kPair>(b + q * kChunkBytes, &p.b, tile.n * kTileN + rank * kBColumns + q * 64, k, bar);
+              load_2d<kPair>(b + q * kChunkBytes, &p.b, tile.n * kN + rank * kBColumns + q * 64, k, bar);
           } else {
             load_2d<kPair>(a, &p.a, k, tile.row0, bar);
             if (kMode == kForward) {
               // Boxes of 128: the first and the second half of the columns (glu: gate, up).
-              const int n0 = tile.n * (kGlu ? kTileN / 2 : kTileN), n1 = n0 + (kGlu ? p.N : kTileN / 2);
+              const int n0 = tile.n * (kGlu ? kN / 2 : kN), n1 = n0 + (kGlu ? p.N : kN / 2);
               load_3d<kPair>(b, &p.b, k, rank == 0 ? n0 : n1, tile.e, bar);
-              if (!kPair) load_3d<kPair>(b + 128 * kBlockK * 2, &p.b, k, n1, tile.e, bar);
+              if (kBColumns == 256) load_3d<kPair>(b + 128 * kBlockK * 2, &p.b, k, n1, tile.e, bar);
             } else {
 #pragma unroll
               for (int q = 0; q < kBColumns / 64; ++q)
-                load_3d<kPair>(b + q * kChunkBytes, &p.b, tile.n * kTileN + rank * kBColumns + q * 64, k, tile.e, bar);
+                load_3d<kPair>(b + q * kChunkBytes, &p.b, tile.n * kN + rank * kBColumns + q * 64, k, tile.e, bar);
             }
           }
         }
@@ -718,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         tc::settle(&s.empty[j % kStages], (j / kStages) & 1, start);
   } else if (warp == kMmaWarp && rank == 0) {
     constexpr uint32_t kInstr =
-        tc::instr_desc_bf16(kPair ? 2 * kTileM : kTileM, kTileN, kMode == kWeight, kMode != kForward);
+        tc::instr_desc_bf16(kPair ? 2 * kTileM : kTileM, kN, kMode == kWeight, kMode != kForward);
     uint32_t i = 0, it = 0, round = 0, tails = 0;  // tails: parity of tail_clear, a bit a stage
     bool ok = true;
     for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
@@ -755,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         if (tc::elect()) {
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k) {
-            const uint32_t d = tmem_u + buf * kTileN;
+            const uint32_t d = tmem_u + buf * kN;
             if (kPair) tc::mma_f16_pair(d, a + kStepA * k, b + kStepB * k, kInstr, kb > kb0 || k > 0);
             else tc::mma_f16(d, a + kStepA * k, b + kStepB * k, kInstr, kb > kb0 || k > 0);
           }
@@ -860,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     Tile next;
     uint32_t number = 0;
     if (first_tile < tiles) next = walk.get(g, p, number++, lane);
-    if (ahead && kTeam != kSplit && first_tile < tiles) fetch_unit<kMode>(p, next, half, sub, lane, 0, raw);
+    if (ahead && kTeam != kSplit && first_tile < tiles) fetch_unit<kMode, kN>(p, next, half, sub, lane, 0, raw);
     for (uint32_t t = first_tile; ok && t < tiles; t += tile_step) {
       const Tile tile = next;
       const bool more = kTeam != kSplit && t + tile_step < tiles;
@@ -869,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
       const bool any = kblocks > 0;  // whether there is a sum at all (weight: the expert has rows)
       const bool sums = share(kblocks, part, parts) < share(kblocks, part + 1, parts);
       const int buf = round & 1;
-      const uint32_t acc = lanes + buf * kTileN;
+      const uint32_t acc = lanes + buf * kN;
       bool waits = sums;
       auto sums_are_there = [&] {
         if (waits) {
@@ -882,12 +886,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
       };
       if (kTeam == kSplit) {
         // This CTA's part of the sums, for the others to read.
-        float* to = parts_at + (sub + lane) * kPitch + half * (kTileN / 2);
+        float* to = parts_at + (sub + lane) * kPitch + half * (kN / 2);
         if (any && sums_are_there()) {
 #pragma unroll 1
-          for (int q = 0; q < kTileN / 2 / kUnit; ++q) {
+          for (int q = 0; q < kN / 2 / kUnit; ++q) {
             float v[kUnit] = {};
-            if (sums) load_acc(acc + half * (kTileN / 2) + q * kUnit, v);
+            if (sums) load_acc(acc + half * (kN / 2) + q * kUnit, v);
 #pragma unroll
             for (int i = 0; i < kUnit; i += 4)
               *reinterpret_cast<float4*>(to + q * kUnit + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -895,9 +899,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
         }
         break;
       }
-      if (reads && more) prefetch_rows<kMode, kGlu>(p, next, half, sub, lane);
+      if (reads && more) prefetch_rows<kMode, kGlu, kN>(p, next, half, sub, lane);
       // A warp none of whose rows exist only passes the buffer on.
-      epilogue<kMode, kGlu, kF32>(p, tile, next, more, half, sub, lane, any, sub < tile.rows, raw, s.bias[warp],
+      epilogue<kMode, kGlu, kF32, kN>(p, tile, next, more, half, sub, lane, any, sub < tile.rows, raw, s.bias[warp],
                                   [&](int column, float(&v)[kUnit], bool last) {
                                     if (!sums_are_there()) return false;
                                     if (sub < tile.rows) load_acc(acc + column, v);
@@ -916,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
     if (warp < kEpilogueWarps && first_tile < tiles) {
       // Every CTA finishes the blocks of 32 rows x half of the columns whose warp's number
       // falls to it: adds the parts in order, the eight warps together, then writes them out.
-      const Tile tile = find_tile<kMode, kPair>(g, p, first_tile, rank);
+      const Tile tile = find_tile<kMode, kPair, kN>(g, p, first_tile, rank);
       const bool any = tile.kc > 0;
       if (any) {
         const int mine = kEpilogueWarps / parts;  // 1 to 4 blocks, part, part + parts, ...
@@ -924,8 +928,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
           const int block = part + (i >> 10) * parts, r = (block & 3) * 32 + ((i >> 5) & 31);
           // Glu: 64 gate columns and the 64 up columns that belong to them.
           const int quad = (i & 31) * 4, h = block >> 2;
-          const int c = kMode == kForward && kGlu ? (quad >> 6) * (kTileN / 2) + h * kUnit + (quad & 63)
-                                                  : h * (kTileN / 2) + quad;
+          const int c = kMode == kForward && kGlu ? (quad >> 6) * (kN / 2) + h * kUnit + (quad & 63)
+                                                  : h * (kN / 2) + quad;
           float* at = parts_at + r * kPitch + c;
           float4 v[kMaxSplit];
 #pragma unroll
@@ -946,8 +950,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
       const int half = warp >> 2, sub = (warp & 3) * 32;
       if (warp % parts == part) {
         uint32_t raw[4][8];
-        if (reads_ahead<kMode, kGlu>(p)) fetch_unit<kMode>(p, tile, half, sub, lane, 0, raw);
-        epilogue<kMode, kGlu, kF32>(p, tile, tile, false, half, sub, lane, any, sub < tile.rows, raw, s.bias[warp],
+        if (reads_ahead<kMode, kGlu>(p)) fetch_unit<kMode, kN>(p, tile, half, sub, lane, 0, raw);
+        epilogue<kMode, kGlu, kF32, kN>(p, tile, tile, false, half, sub, lane, any, sub < tile.rows, raw, s.bias[warp],
                                     [&](int column, float(&v)[kUnit], bool) {
                                       const float* from = parts_at + (sub + lane) * kPitch + column;
 #pragma unroll
@@ -963,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_linear_kernel(const __grid
   tc::fence_before();
   __syncthreads();
   // Pair: products read the other CTA's shared memory, arrivals reach it; split: sums are read.
-  if (kTeam != kAlone) tc::cluster_sync();
+  if (kTeam == kPairs || kTeam == kSplit) tc::cluster_sync();
   tc::fence_after();
   if (threadIdx.x == 0 && s.gave_up && p.status) atomicCAS(p.status, MOE_OK, MOE_ETIMEDOUT);
   if (warp == kMmaWarp) {
@@ -1006,7 +1010,7 @@ template <Mode kMode, bool kGlu, bool kF32, Team kTeam>
 cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
   constexpr bool kPair = kTeam == kPairs;
   // The most tables that any call has, so that what fits is the same for all.
-  const size_t smem = 1024 + stage_count(kPair) * stage_bytes(kPair) + (3 * MOE_MAX_EXPERTS + 1) * sizeof(int32_t);
+  const size_t smem = 1024 + stage_count(kTeam) * stage_bytes(kTeam) + (3 * MOE_MAX_EXPERTS + 1) * sizeof(int32_t);
   auto* kernel = expert_linear_kernel<kMode, kGlu, kF32, kTeam>;
   cudaError_t err = set_kernel_limits(reinterpret_cast<const void*>(kernel), smem);
   if (err != cudaSuccess) return err;
@@ -1017,7 +1021,7 @@ cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
   const int64_t tiles = m_tiles * p.n_tiles;
   if (tiles > INT_MAX / kMaxSplit) return cudaErrorInvalidValue;
   int64_t teams = tiles, team = 1;  // split: a cluster for each tile there may be
-  if (kTeam == kAlone) {
+  if (kTeam == kAlone || kTeam == kNarrow) {
     teams = tiles < sms ? tiles : sms;
   } else if (kTeam == kPairs) {
     const int pairs = resident_pairs(reinterpret_cast<const void*>(kernel), smem);
@@ -1039,19 +1043,21 @@ cudaError_t launch(const LinearParams& p, int sms, cudaStream_t stream) {
   attr[1].val.clusterDim.x = static_cast<unsigned>(team);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kTeam == kAlone ? 1 : 2;
+  cfg.numAttrs = kTeam == kAlone || kTeam == kNarrow ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <Mode kMode, bool kGlu, bool kF32>
 cudaError_t launch(const LinearParams& p, bool pair, int sms, cudaStream_t stream) {
   if (p.split > 1) return launch<kMode, kGlu, kF32, kSplit>(p, sms, stream);
+  if constexpr (kMode != kForward || !kGlu)  // (64 gate and 64 up columns would be half units)
+    if (p.narrow) return launch<kMode, kGlu, kF32, kNarrow>(p, sms, stream);
   return pair ? launch<kMode, kGlu, kF32, kPairs>(p, sms, stream) : launch<kMode, kGlu, kF32, kAlone>(p, sms, stream);
 }
 
 }  // namespace
 
-int linear_n_tile(bool glu) { return glu ? kTileN / 2 : kTileN; }
+int linear_n_tile(bool glu, bool narrow) { return glu || narrow ? 128 : 256; }
 int linear_m_tile(bool pair) { return pair ? 2 * kTileM : kTileM; }
 
 cudaError_t launch_linear(const LinearParams& p, bool glu, bool f32, bool pair, int sms, cudaStream_t stream) {

@@ -114,6 +114,33 @@ int split_of(int64_t most_tiles, int64_t kc) {
   return split;
 }
 
+// What tiles of which shape a product of `most_row_tiles` x cols takes, into p; whether by pairs.
+//
+// Tiles of 128 columns (narrow) where all of them fit on the SMs at once: twice the CTAs, and six
+// stages on their way instead of four, which is what a call without other work on its SMs waits
+// for; two CTAs to a sum gain less.  us, one CTA a tile of 256 columns / of 128 / pairs / a sum
+// split over 2 / 4:
+//   forward  N = K = 4096, 256 rows: 27.2 / 18.2 / 23.8 / 22.4 / 18.6, 512: 27.2 / 18.9 / 24.0 /
+//            23.1 / 33; 2048 rows, N = K = 1024: 9.9 / 7.9 / 10.7 / 13.3 / 22.8
+//   by rows  589 rows, 2400 x 408: 22.1 / 14.6 / 17.2 / 18.7 / 14.1
+//   by weights  1024 rows, N = K = 1024: 8.9 / 7.3 / 9.9 / 12.1 / 11.2; 6758 rows, 1376 x 280: 54 /
+//            34.5 / 37 / 34.5 / 22.5
+// and with several rounds of tiles: 40 experts' 3003 rows, 1416 x 2320, gelu: 62.8 / 70.1; 256
+// experts' dw, 128 rows, N = K = 2048: 388 / 448; forward 256 experts, 8192 rows: 324 / 322.
+bool choose_tiles(moe::LinearParams& p, int64_t most_row_tiles, int32_t cols, int64_t kc, bool glu, bool pairs, int sms) {
+  p.n_tiles = tiles(cols, moe::linear_n_tile(glu, false));
+  const int64_t most = most_row_tiles * p.n_tiles;
+  p.split = split_of(most, kc);
+  if (p.split > (glu ? 1 : 2)) return false;
+  if (!glu) p.split = 1;
+  if (!glu && 2 * most <= sms) {
+    p.narrow = true;
+    p.n_tiles = tiles(cols, moe::linear_n_tile(false, true));
+    return false;
+  }
+  return pairs;
+}
+
 }  // namespace
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -250,17 +277,21 @@ MOE_API int moe_expert_linear(const void* a, int64_t rows, int32_t k, const void
     p.status = status;
     p.rows = rows;
     p.N = glu ? n / 2 : n;
-    p.n_tiles = tiles(p.N, ranks > 0 ? 128 : moe::linear_n_tile(glu));
     p.kc = k;
     p.E = num_experts;
     p.act = activation;
     p.bias_cols = n;
-    p.split = split_of(row_tiles(rows, expert_offsets ? num_experts : 0) * p.n_tiles, k);
     p.bias_f32 = bias_type == MOE_TYPE_F32;
     p.out_f32 = out_type == MOE_TYPE_F32;
     p.test_drop = moe::test_drop();
-    if (ranks > 0) return launched(moe::launch_few_linear(p, false, glu, ranks, static_cast<cudaStream_t>(stream)));
-    return launched(moe::launch_linear(p, glu, out_type == MOE_TYPE_F32, takes_pairs(rows, num_experts), sms, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t on = static_cast<cudaStream_t>(stream);
+    if (ranks > 0) {
+      p.n_tiles = tiles(p.N, 128);
+      return launched(moe::launch_few_linear(p, false, glu, ranks, on));
+    }
+    const bool pair = choose_tiles(p, row_tiles(rows, expert_offsets ? num_experts : 0), p.N, k, glu,
+                                   takes_pairs(rows, num_experts), sms);
+    return launched(moe::launch_linear(p, glu, out_type == MOE_TYPE_F32, pair, sms, on));
   });
 }
 
@@ -286,14 +317,18 @@ MOE_API int moe_expert_linear_backward_input(const void* dy, int64_t rows, int32
     p.status = status;
     p.rows = rows;
     p.N = k;
-    p.n_tiles = tiles(k, ranks > 0 ? 128 : moe::linear_n_tile(false));
     p.kc = n;
     p.E = num_experts;
     p.act = activation;
-    p.split = split_of(row_tiles(rows, expert_offsets ? num_experts : 0) * p.n_tiles, n);
     p.test_drop = moe::test_drop();
-    if (ranks > 0) return launched(moe::launch_few_linear(p, true, false, ranks, static_cast<cudaStream_t>(stream)));
-    return launched(moe::launch_linear_input(p, activation == MOE_ACT_SWIGLU, takes_pairs(rows, num_experts), sms, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t on = static_cast<cudaStream_t>(stream);
+    if (ranks > 0) {
+      p.n_tiles = tiles(k, 128);
+      return launched(moe::launch_few_linear(p, true, false, ranks, on));
+    }
+    const bool pair = choose_tiles(p, row_tiles(rows, expert_offsets ? num_experts : 0), k, n, false,
+                                   takes_pairs(rows, num_experts), sms);
+    return launched(moe::launch_linear_input(p, activation == MOE_ACT_SWIGLU, pair, sms, on));
   });
 }
 
@@ -319,23 +354,19 @@ MOE_API int moe_expert_linear_backward_weight(const void* dy, int64_t rows, int3
     moe::LinearParams p = {};
     if (!encode_rows(&p.a, dy, rows, n, 64) || !encode_rows(&p.b, a, rows, k, 64)) return static_cast<int>(MOE_ECUDA);
     p.offsets = expert_offsets;
-    const int32_t n_tiles = tiles(k, moe::linear_n_tile(false));
-    const int split = split_of(static_cast<int64_t>(num_experts) * tiles(n, moe::linear_m_tile(false)) * n_tiles,
-                               rows / num_experts);
-    const bool pair = split == 1 && takes_pairs(rows, num_experts);
     p.out = dw;
     p.dy = static_cast<const uint8_t*>(dy);
     p.db = db;
     p.status = status;
     p.rows = rows;
     p.N = k;
-    p.n_tiles = n_tiles;
     p.M = n;
-    p.m_tiles = tiles(n, moe::linear_m_tile(pair));
     p.E = num_experts;
     p.accumulate = accumulate != 0;
-    p.split = split;
     p.test_drop = moe::test_drop();
+    const bool pair = choose_tiles(p, static_cast<int64_t>(num_experts) * tiles(n, moe::linear_m_tile(false)), k,
+                                   rows / num_experts, false, takes_pairs(rows, num_experts), sms);
+    p.m_tiles = tiles(n, moe::linear_m_tile(pair));
     return launched(moe::launch_linear_weight(p, dw_type == MOE_TYPE_F32, pair, sms, on));
   });
 }

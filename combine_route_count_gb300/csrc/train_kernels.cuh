@@ -68,10 +68,11 @@ struct LinearParams {
   int32_t kc;                // length of the summed axis (weight: the expert's rows instead)
   int32_t E, act, bias_cols;
   int32_t split;             // CTAs that share a tile's sum: 1, 2, 4 or 8
+  bool narrow;               // tiles of 128 columns (not glu forward; split 1, no pairs)
   bool bias_f32, out_f32, accumulate;
   uint32_t test_drop;        // the number of a load that each CTA leaves out; UINT32_MAX: none
 };
-int linear_n_tile(bool glu);  // columns of out that one tile covers
+int linear_n_tile(bool glu, bool narrow);  // columns of out that one tile covers (glu: forward)
 int linear_m_tile(bool pair);
 cudaError_t launch_linear(const LinearParams& p, bool glu, bool f32, bool pair, int sms, cudaStream_t stream);
 cudaError_t launch_linear_input(const LinearParams& p, bool glu, bool pair, int sms, cudaStream_t stream);
