@@ -75,15 +75,17 @@ bool takes_pairs(int64_t rows, int32_t E) { return rows >= 256 * static_cast<int
 
 // CTAs that share a tile of the few-row kernel; 0: not the few-row kernel.  It is
 // for a mean of up to 4 rows an expert, and for calls whose tiles leave most SMs without
-// work: three of its CTAs on two SMs take all of its tiles.  us, tile kernel / 1 / 2 / 4 / 8
-// CTAs a tile of 128 columns (56 of them for N 7168; few_linear_units times that many for
-// the rows):
+// work: two or more of its CTAs a tile fit on the GPU at once, whatever the rows.  (With one
+// each, a long axis and many rows it reads the weights for every 32 of them: 5925 rows, N 176,
+// K 6952, swiglu: 115 instead of 44.)  us, tile kernel / 1 / 2 / 4 / 8 CTAs a tile of 128
+// columns (56 of them for N 7168; few_linear_units times that many for the rows):
 //   N 7168, K 2048: 16.1 / 11.7 / 10.7 / 10.1 / 14.3 at 1 row, 16.1 / 13.3 / 11.7 / 11.4 /
 //   17.2 at 32, 16.2 / 13.5 / 12.0 / 17.4 / 29 at 64, 16.6 / 13.8 / 19.5 / 29 / 48 at 128
 //   (224 tiles), 15.8 / 24 / 30 / 48 / - at 256; N 2048, K 7168: 42 / 27 / 17.3 / 12.5 / 11.2 at
 //   16; N = K = 4096: 17.8 (a split sum) / 18.3 / 14.9 / 21 / - at 128, 18.3 / 20.3 / 26 / 38 / -
 //   at 256 (256 tiles); 8 experts, N = K = 1024: 11.3 / 8.9 / 8.6 / 8.8 / 13.7 at 64 rows,
-//   11.2 / 10.5 / 11.1 / 16.8 / 30 at 512 (192 tiles)
+//   11.2 / 10.5 / 11.1 / 16.8 / 30 at 512 (192 tiles); N 128, K 4096, 4096 rows (128 tiles): 15.2 (a
+//   split sum) / 17.0 / 12.6 / 17.4 / -
 // and, tile kernel / 1 CTA a tile, by the mean of the rows, 64 experts, N 2816, K 2048, swiglu:
 //   116 / 112 at 2, 116 / 111 at 4 (skewed router 94.5 / 90), 116 / 113 at 8 (97 / 98); N 2048, K
 //   1408: 63 / 63 at 8 (52 / 54), 64 / 65 at 16; 194 experts, N 4464, K 408, gelu, 14 rows: 22 / 15
@@ -91,7 +93,7 @@ int few_ranks(int64_t rows, int32_t ragged, int32_t cols, int32_t kc, int sms) {
   const int64_t all = moe::few_linear_units(rows, ragged) * tiles(cols, 128);
   int ranks = 1;
   while (ranks < 8 && all * ranks * 2 <= 2 * sms && ranks * 2 <= tiles(kc, 64)) ranks *= 2;
-  return 2 * all <= 3 * sms || rows <= 4 * static_cast<int64_t>(ragged) ? ranks : 0;
+  return all <= sms || rows <= 4 * static_cast<int64_t>(ragged) ? ranks : 0;
 }
 
 // The most row tiles that `ragged` experts' rows make (0: one matrix).
